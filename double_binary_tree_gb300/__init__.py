@@ -47,6 +47,7 @@ class vr_tree_t(ctypes.Structure):
 
 
 P, I, S, VP = ctypes.POINTER, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+F = ctypes.c_float
 PP = P(VP)
 _SIGNATURES = {
     "vr_build_ring": (I, [I, I, P(I), P(I)]),
@@ -64,6 +65,8 @@ _SIGNATURES = {
     "vr_ring_stepwise_scratch_bytes": (S, [S, I]),
     "vr_allreduce_ring_stepwise": (I, [PP, PP, I, S, I, I, I, S, VP, S, VP]),
     "vr_allreduce_ring_stepwise_noalloc": (I, [PP, PP, I, S, I, I, I, S, VP]),
+    "vr_balance_loss_workspace_bytes": (I, [I, S, I, P(S)]),
+    "vr_balance_loss": (I, [PP, S, PP, I, S, I, I, I, F, F, VP, VP, PP, PP, VP, S, VP]),
     "vr_predict_us": (I, [I, I, I, S, P(vr_cost_model_t), P(ctypes.c_double)]),
     "vr_select_algo": (I, [I, I, S, P(vr_cost_model_t), P(I)]),
     "vr_set_cost_model": (I, [P(vr_cost_model_t)]),
@@ -270,6 +273,29 @@ def vr_allreduce_ring_stepwise_noalloc(sendbufs, recvbufs, R, count, dtype, op, 
            "vr_allreduce_ring_stepwise_noalloc")
 
 
+# ------------------------------------------- operators of a training step
+def _size(fn, where, *args):
+    n = ctypes.c_size_t()
+    _check(fn(*args, ctypes.byref(n)), where)
+    return n.value
+
+
+def vr_balance_loss_workspace_bytes(R, tokens, experts):
+    return _size(_L().vr_balance_loss_workspace_bytes, "vr_balance_loss_workspace_bytes", R,
+                 tokens, experts)
+
+
+def vr_balance_loss(logits, rowStride, masks, R, tokens, experts, topK, dtype, coef, gradScale,
+                    loss, counts, chosen, dlogits, workspace, workspaceBytes, stream=None):
+    """logits / masks / chosen / dlogits: sequences of R buffers (all but
+    logits may be None, as may single masks and chosen)."""
+    _check(_L().vr_balance_loss(_ptrs(logits), rowStride, _ptrs(masks), R, tokens, experts, topK,
+                                dtype, coef, gradScale, _ptr(loss), _ptr(counts), _ptrs(chosen),
+                                _ptrs(dlogits), _ptr(workspace), workspaceBytes,
+                                _stream(stream)), "vr_balance_loss")
+
+
+# ------------------------------------------------------------- cost model
 def _model(m):
     """None, a vr_cost_model_t, or ((alpha_ring, alpha_tree), (b_ring, b_tree))."""
     if m is None or isinstance(m, vr_cost_model_t):

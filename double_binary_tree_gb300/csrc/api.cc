@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "host.h"
+#include "ops.h"
 
 namespace vr {
 namespace {
@@ -667,6 +668,46 @@ vr_result_t host_pipe(int device, HostPipe** out) {
 }
 
 }  // namespace
+
+vr_result_t op_device(OpDevice* out) {
+  try {
+    DeviceInfo di;
+    int device = 0;
+    const vr_result_t e = device_info(&di, &device);
+    if (e != VR_SUCCESS) return e;
+    *out = OpDevice{device, di.sms, di.status, wait_timeout_ns()};
+    return VR_SUCCESS;
+  } catch (...) {  // no host memory for the device's entry
+    return VR_ERR_INTERNAL;
+  }
+}
+
+vr_result_t op_launch(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
+                      void* stream, int cluster) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (option(kOptPdl)) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) return VR_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return VR_SUCCESS;
+}
+
 }  // namespace vr
 
 using namespace vr;

@@ -1,0 +1,43 @@
+// Host-side helpers shared by the training operators (internal): device
+// properties, launches and buffer checks (ops.cc).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/vr.h"
+
+namespace vr {
+
+struct OpDevice {
+  int device;
+  int sms;
+  unsigned* status;              // this device's status word
+  unsigned long long timeoutNs;  // limit of every bounded wait
+};
+
+// The current device's properties (api.cc).
+vr_result_t op_device(OpDevice* out);
+// One kernel launch on the caller's stream (api.cc), counted in
+// vr_launch_count.  Every kernel launched this way calls pdl_wait before it
+// touches memory: it may start while the previous one on the stream drains.
+vr_result_t op_launch(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
+                      void* stream, int cluster = 1);
+
+inline size_t op_elem_size(int dtype) {
+  return dtype == VR_FLOAT32 ? 4 : dtype == VR_FLOAT16 || dtype == VR_BFLOAT16 ? 2 : 0;
+}
+
+// A buffer of `rows` rows of rowBytes bytes, strideBytes apart.
+struct OpBuffer {
+  const void* p;
+  size_t rows, rowBytes, strideBytes;
+  bool write;
+};
+// No written buffer may touch another one, except an identical input listed
+// directly before it (in place).  Rows of equal stride may interleave.
+bool op_buffers_ok(const OpBuffer* b, int n);
+
+// Bytes rounded up to the alignment of a workspace's parts.
+inline size_t op_round(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace vr

@@ -421,6 +421,51 @@ vr_result_t vr_allreduce_ring_stepwise_noalloc(const void* const* sendbufs, void
                                                int R, size_t count, vr_dtype_t dtype, vr_op_t op,
                                                int nChannels, size_t chunkBytes, void* stream);
 
+/* ------------------------------------------- operators of a training step
+ * What stands directly before and after the AllReduce of a data-parallel
+ * step: the losses whose gradients it sums, and the update made of the sum.
+ * The pages stop at the collective; these have no counterpart there.  The
+ * conventions at the top of this header hold: asynchronous on `stream`,
+ * arguments checked before anything is enqueued, no device memory allocated
+ * (each call takes a workspace of the caller's, at least as large as its
+ * ..._workspace_bytes says and 16-byte aligned, whose contents need no
+ * initial value and are overwritten; calls that run at the same time need
+ * one each), the same bits on every run.  A written buffer may overlap no
+ * other buffer of the call unless stated. */
+
+/* Balance loss of R ranks' expert routers over the whole batch, with its
+ * gradients.  logits[r]: `tokens` rows of `experts` router logits (fp32,
+ * fp16 or bf16), rowStride elements apart.  Over the N valid tokens of all
+ * ranks, with p_t the softmax of a token's logits and c_e the number of
+ * tokens whose topK largest logits include expert e (equal logits: the lower
+ * expert first; NaN above +inf):
+ *   f_e = c_e / (N topK),  P_e = sum_t p_te / N,
+ *   *loss = coef * experts * sum_e f_e P_e
+ *   dlogits_te = gradScale * coef * experts / N * p_te (f_e - sum_j f_j p_tj)
+ * f is held constant in the gradient (the choice has none).
+ *   masks: NULL, or R pointers (each may be NULL: every token counts) to
+ *     `tokens` bytes, 0 where a token does not count.  A token whose logits
+ *     are all -inf does not count either.  Such tokens choose -1 and get a
+ *     gradient of zero whatever their logits hold.  A NaN or +inf logit of
+ *     a token that counts makes the loss NaN.
+ *   counts: `experts` ints, c_e.  loss: one float.
+ *   chosen: NULL, or R pointers (each may be NULL) to tokens * topK ints:
+ *     each token's experts, the largest logit first.
+ *   dlogits: NULL (no gradients), or R buffers laid out as the logits;
+ *     dlogits[r] may be logits[r].  Elements between rows are not touched.
+ * Softmax and sums are fp32; the gradient is rounded once to dtype (fp16:
+ * scale it into range with gradScale).  N = 0 gives loss 0, counts 0.
+ * Errors: VR_ERR_INVALID_ARGUMENT for R outside [1, VR_MAX_RANKS], experts
+ * outside [1, 1024], topK outside [1, min(experts, 32)], rowStride <
+ * experts, R * tokens above 2^31 - 1, a NULL or misaligned buffer, a bad
+ * overlap or a short workspace. */
+vr_result_t vr_balance_loss_workspace_bytes(int R, size_t tokens, int experts, size_t* bytes);
+vr_result_t vr_balance_loss(const void* const* logits, size_t rowStride,
+                            const unsigned char* const* masks, int R, size_t tokens, int experts,
+                            int topK, vr_dtype_t dtype, float coef, float gradScale, float* loss,
+                            int* counts, int* const* chosen, void* const* dlogits,
+                            void* workspace, size_t workspaceBytes, void* stream);
+
 /* ---------------------------------------------------------- cost model
  * The pages' alpha-beta model ([Course13] "理想成本模型"; [Interview]
  * "推导 / 关键公式"), with N ranks, tree depth D (the deeper of the two

@@ -1,0 +1,69 @@
+"""The training operators in 64 bits on the CPU, from their definitions, and
+bounds on what 32-bit arithmetic may differ by.  Shares no code with the
+package."""
+
+import math
+
+import torch
+
+U32 = 2.0 ** -24
+U_T = {torch.float32: U32, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+MIN_T = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
+
+
+def balance(logits, masks, topk, coef, grad_scale):
+    """logits: R CPU tensors (T, E); masks: R CPU tensors (T,) or None.
+    Returns loss, counts, chosen, dlogits and, for each gradient, a bound of
+    the fp32 evaluation's error before its final rounding."""
+    R = len(logits)
+    T, E = logits[0].shape
+    x = torch.stack(logits).double()
+    valid = torch.ones(R, T, dtype=torch.bool)
+    if masks is not None:
+        for r, m in enumerate(masks):
+            if m is not None:
+                valid[r] = m != 0
+    valid &= ~(x == -math.inf).all(2)
+    chosen = torch.full((R, T, topk), -1, dtype=torch.int64)
+    counts = torch.zeros(E, dtype=torch.int64)
+    for r in range(R):
+        for t in range(T):
+            if valid[r, t]:
+                row = x[r, t].tolist()
+                # NaN above +inf, equal values: the lower index first
+                order = sorted(range(E), key=lambda e: (0, 0.0, e) if row[e] != row[e]
+                               else (1, -row[e], e))[:topk]
+                chosen[r, t] = torch.tensor(order)
+                for e in order:
+                    counts[e] += 1
+    n = int(valid.sum())
+    p = torch.zeros_like(x)
+    if n:
+        p[valid] = torch.softmax(x[valid], 1)
+    f = counts.double() / max(1, n * topk)
+    mean = p.sum((0, 1)) / max(1, n)
+    loss = coef * E * float((f * mean).sum())
+    factor = grad_scale * coef * E / max(1, n)
+    dot = (p * f).sum(2, keepdim=True)
+    grads = factor * p * (f - dot)
+    # exp in fp32: the exponent x - lse is rounded to |x - lse| 2^-23 (the
+    # difference, its product with log2 e, lse itself), ex2 to 2 ulp
+    gap = torch.where(p > 0, -torch.log(p.clamp(min=1e-300)), torch.zeros_like(p))
+    top = x.abs().where(x.abs() < math.inf, torch.zeros_like(x)).amax(2, keepdim=True)
+    rel = (2 * gap + 2 * top + 8) * 2 * U32
+    # p (f - dot): p's relative error twice over, dot's E-term sum
+    bound = abs(factor) * p * (f + dot) * (2 * rel + (E + 8) * U32)
+    worst = float(rel[valid].max()) if n else 0.0
+    loss_bound = abs(loss) * (worst + (T * R + E + 16) * U32)
+    return dict(loss=loss, loss_bound=loss_bound, counts=counts, chosen=chosen, grads=grads,
+                bound=bound, n=n)
+
+
+def assert_close(got, want, bound, dtype, what=""):
+    """|got - want| within `bound`, widened by one rounding to dtype."""
+    got = got.double()
+    limit = bound + (want.abs() + bound) * U_T[dtype] + MIN_T[dtype]
+    bad = ~((got - want).abs() <= limit)
+    assert not bool(bad.any()), "%s: %d of %d outside, first got %r want %r limit %r" % (
+        what, int(bad.sum()), bad.numel(), float(got[bad][0]), float(want[bad][0]),
+        float(limit.expand_as(want)[bad][0]))

@@ -1,0 +1,50 @@
+"""Refusals of the training operators: argument errors are reported on the
+host, before anything is enqueued.  The pointers are never dereferenced."""
+
+import pytest
+
+import double_binary_tree_gb300 as vr
+
+INV, UNS = vr.VR_ERR_INVALID_ARGUMENT, vr.VR_ERR_UNSUPPORTED
+A = 0x10000000   # distinct buffers, far apart
+STEP = 0x1000000
+
+
+def code(fn, *args):
+    before = vr.vr_launch_count()
+    with pytest.raises(vr.VrError) as ei:
+        fn(*args)
+    assert vr.vr_launch_count() == before
+    return ei.value.code
+
+
+def balance_args(**kw):
+    a = dict(logits=[A, A + STEP], rowStride=16, masks=None, R=2, tokens=10, experts=16, topK=2,
+             dtype=vr.VR_FLOAT32, coef=1.0, gradScale=1.0, loss=A + 2 * STEP, counts=A + 3 * STEP,
+             chosen=[A + 4 * STEP, A + 5 * STEP], dlogits=[A + 6 * STEP, A + 7 * STEP],
+             workspace=A + 8 * STEP, workspaceBytes=4 << 20)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(R=0), dict(R=65), dict(experts=0), dict(experts=1025, rowStride=1025), dict(topK=0),
+    dict(topK=17), dict(experts=64, rowStride=64, topK=33), dict(rowStride=15), dict(dtype=3),
+    dict(tokens=1 << 31), dict(tokens=1 << 62), dict(rowStride=1 << 62), dict(logits=None),
+    dict(logits=[A, 0]), dict(dlogits=[0, A]), dict(loss=0), dict(counts=0), dict(workspace=0),
+    dict(workspaceBytes=16), dict(workspace=A + 8 * STEP + 4), dict(loss=A + 2 * STEP + 2),
+    dict(logits=[A + 2, A + STEP]), dict(chosen=[A + 4 * STEP + 2, 0]),
+    dict(dlogits=[A + 6 * STEP, A + 6 * STEP + 64]),       # two ranks' gradients overlap
+    dict(dlogits=[A + STEP, A + 7 * STEP]),                # over another rank's logits
+    dict(dlogits=[A + 16, A + 7 * STEP]),                  # partly over its own
+    dict(loss=A + 8 * STEP), dict(counts=A + 64),
+])
+def test_balance_refusals(bad):
+    assert code(vr.vr_balance_loss, *balance_args(**bad)) == INV
+
+
+def test_balance_workspace():
+    assert code(vr.vr_balance_loss_workspace_bytes, 0, 1, 1) == INV
+    assert code(vr.vr_balance_loss_workspace_bytes, 1, 1, 1025) == INV
+    small = vr.vr_balance_loss_workspace_bytes(1, 1, 8)
+    assert 0 < small <= vr.vr_balance_loss_workspace_bytes(8, 1 << 20, 1024)
