@@ -47,7 +47,7 @@ class vr_tree_t(ctypes.Structure):
 
 
 P, I, S, VP = ctypes.POINTER, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
-F = ctypes.c_float
+F, LL = ctypes.c_float, ctypes.c_longlong
 PP = P(VP)
 _SIGNATURES = {
     "vr_build_ring": (I, [I, I, P(I), P(I)]),
@@ -65,6 +65,9 @@ _SIGNATURES = {
     "vr_ring_stepwise_scratch_bytes": (S, [S, I]),
     "vr_allreduce_ring_stepwise": (I, [PP, PP, I, S, I, I, I, S, VP, S, VP]),
     "vr_allreduce_ring_stepwise_noalloc": (I, [PP, PP, I, S, I, I, I, S, VP]),
+    "vr_linear_xent_workspace_bytes": (I, [VP, S, VP, S, S, S, S, I, I, P(S)]),
+    "vr_linear_xent": (I, [VP, S, VP, S, VP, S, S, S, I, LL, I, F, VP, VP, VP, VP, VP, VP, S,
+                           VP]),
     "vr_balance_loss_workspace_bytes": (I, [I, S, I, P(S)]),
     "vr_balance_loss": (I, [PP, S, PP, I, S, I, I, I, F, F, VP, VP, PP, PP, VP, S, VP]),
     "vr_predict_us": (I, [I, I, I, S, P(vr_cost_model_t), P(ctypes.c_double)]),
@@ -278,6 +281,24 @@ def _size(fn, where, *args):
     n = ctypes.c_size_t()
     _check(fn(*args, ctypes.byref(n)), where)
     return n.value
+
+
+def vr_linear_xent_workspace_bytes(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab,
+                                   dtype, grads):
+    return _size(_L().vr_linear_xent_workspace_bytes, "vr_linear_xent_workspace_bytes",
+                 _ptr(hidden), hiddenStride, _ptr(weight), weightStride, tokens, dim, vocab, dtype,
+                 int(grads))
+
+
+def vr_linear_xent(hidden, hiddenStride, weight, weightStride, targets, tokens, dim, vocab, dtype,
+                   ignoreIndex, mean, gradScale, losses, lse, loss, dHidden, dWeight, workspace,
+                   workspaceBytes, stream=None):
+    """dHidden / dWeight may be None (that gradient is not computed)."""
+    _check(_L().vr_linear_xent(_ptr(hidden), hiddenStride, _ptr(weight), weightStride,
+                               _ptr(targets), tokens, dim, vocab, dtype, ignoreIndex, int(mean),
+                               gradScale, _ptr(losses), _ptr(lse), _ptr(loss), _ptr(dHidden),
+                               _ptr(dWeight), _ptr(workspace), workspaceBytes, _stream(stream)),
+           "vr_linear_xent")
 
 
 def vr_balance_loss_workspace_bytes(R, tokens, experts):

@@ -1,0 +1,634 @@
+// Softmax cross entropy of a linear layer over a large vocabulary
+// (vr_linear_xent).
+//
+//   l_tv = h_t . w_v;  lse_t = log sum_v exp l_tv;  loss_t = lse_t - l_t,y(t)
+//   g_tv = s (exp(l_tv - lse_t) - [v = y(t)]);  dH = G W;  dW = G^T H
+//
+// The logits are never stored.  The first product (gemm.cuh) turns each
+// 128 x 256 tile of them into one maximum and one sum per row in its epilogue;
+// joining the tiles' pairs gives lse.  For the gradients the vocabulary is
+// taken piece by piece: the product runs again, its epilogue now writing
+// exp(l - lse) - [v = y] in 16 bits, and two more products multiply that
+// piece with the weight and with the hidden states while it is in L2 or
+// fresh in memory.  8 T D V operations instead of the 6 T D V of keeping T x V
+// logits.
+//
+// Only tokens that count take part in the gradients: their hidden states are
+// gathered into a packed copy first, which leaves out the products of
+// ignored tokens and whatever such tokens hold (NaN times zero is NaN).
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "gemm.cuh"
+#include "gemm_host.h"
+
+namespace vr {
+namespace {
+
+constexpr int kBN = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Device-side results of the preparation.
+struct XentState {
+  int valid;        // tokens that count
+  float lossScale;  // 1 / valid or 1
+  float gradScale;  // of the 16-bit gradient factors
+};
+
+// The gradient factors p - [v = y] lie in [-1, 1]; small p are common.  fp16
+// holds them times 2^14 (down to 2^-28 normal), bf16 as they are.
+template <typename T>
+constexpr int kShift = std::is_same<T, __half>::value ? 14 : 0;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)Ty<T>::narrow(a) | (uint32_t)Ty<T>::narrow(b) << 16;
+}
+
+// 32 consecutive 16-bit values of one row; `vec`: 16-byte stores allowed.
+template <typename T>
+__device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, bool vec) {
+  typename Ty<T>::Bits* o = reinterpret_cast<typename Ty<T>::Bits*>(out);
+  if (vec && cols >= 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint4*>(o)[i] =
+          make_uint4(pack2<T>(v[8 * i], v[8 * i + 1]), pack2<T>(v[8 * i + 2], v[8 * i + 3]),
+                     pack2<T>(v[8 * i + 4], v[8 * i + 5]), pack2<T>(v[8 * i + 6], v[8 * i + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < cols) o[i] = Ty<T>::narrow(v[i]);
+  }
+}
+
+// Row statistics of a tile of logits: the maximum (in units of log 2) and
+// the sum of exp over each half tile, and the target's logit.
+struct StatsEpilogue {
+  struct Args {
+    const int* target;  // [T], -1: none
+    float* targetLogit;
+    float2* parts;      // [T][nParts]
+    int nParts;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
+                                             int row, int col0, int cols, int M, const Acc& acc) {
+    const int t = o.m0 + row;
+    const int first = o.n0 + col0;
+    const int at = t < M ? a.target[t] - first : -1;
+    float top = -INFINITY, sum = 0.0f;
+    for (int c = 0; c < cols; c += 32) {
+      if (first + c >= g.N) break;
+      float v[32];
+      acc(col0 + c, v);
+      if (first + c + 32 > g.N) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (first + c + i >= g.N) v[i] = -INFINITY;
+      }
+      float m = v[0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
+      m *= kLog2e;
+      const float next = fmaxf(top, m);
+      // nothing but -inf so far: subtract 0, so that exp2 gives 0, not NaN
+      const float base = next == -INFINITY ? 0.0f : next;
+      sum *= exp2_fast(top - base);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum += exp2_fast(fmaf(v[i], kLog2e, -base));
+      top = next;
+    }
+    acc.pick(at >= 0 && at < cols ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
+    if (t < M) a.parts[(long long)t * a.nParts + first / (kBN / 2)] = make_float2(top, sum);
+  }
+};
+
+// Gradient factors of a tile of a piece of the vocabulary.
+template <typename T>
+struct FactorEpilogue {
+  struct Args {
+    const int* target;   // packed tokens' targets
+    const float* lse2;   // their log sums, in units of log 2
+    T* out;              // [tokens][ld]
+    long long ld;
+    int v0;              // the piece's first row of the vocabulary
+  };
+  static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
+                                             int row, int col0, int cols, int M, const Acc& acc) {
+    const int t = o.m0 + row;
+    const bool live = t < M;
+    const float sub = live ? (float)kShift<T> - a.lse2[t] : 0.0f;
+    const int at = live ? a.target[t] - a.v0 - o.n0 - col0 : -1;
+    T* out = a.out + (long long)t * a.ld + o.n0 + col0;
+    for (int c = 0; c < cols; c += 32) {
+      if (o.n0 + col0 + c >= g.N) break;
+      float v[32];
+      acc(col0 + c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = live ? exp2_fast(fmaf(v[i], kLog2e, sub)) : 0.0f;
+      store32(out + c, v, 32, true);
+    }
+    // the target's factor over the one just written by the same thread
+    acc.pick(at >= 0 && at < cols ? col0 + at : -1, [&](float x) {
+      const float p = exp2_fast(fmaf(x, kLog2e, sub)) - (float)(1 << kShift<T>);
+      reinterpret_cast<typename Ty<T>::Bits*>(out)[at] = Ty<T>::narrow(p);
+    });
+  }
+};
+
+// dH: the pieces' products added up in fp32 in piece order, rounded once.
+template <typename T>
+struct HiddenEpilogue {
+  struct Args {
+    float* sum;            // [packed tokens][ld]
+    long long ld;
+    T* out;                // [T][N]
+    const int* token;      // packed token -> token
+    const XentState* state;
+    int first, last, vec;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
+                                             int row, int col0, int cols, int M, const Acc& acc) {
+    const int t = o.m0 + row;
+    const bool live = t < M;
+    const float scale = a.last ? a.state->gradScale : 0.0f;
+    T* out = a.out + (a.last && live ? (long long)a.token[t] * g.N : 0);
+    for (int c = 0; c < cols; c += 32) {
+      const int n = o.n0 + col0 + c;
+      if (n >= g.N) break;
+      float v[32];
+      acc(col0 + c, v);
+      if (!live) continue;
+      float4* sum = reinterpret_cast<float4*>(a.sum + (long long)t * a.ld + n);
+      if (!a.first) {  // rows are padded to whole groups of 32 columns
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 s = sum[i];
+          v[4 * i] += s.x, v[4 * i + 1] += s.y, v[4 * i + 2] += s.z, v[4 * i + 3] += s.w;
+        }
+      }
+      if (a.last) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= scale;
+        store32(out + n, v, g.N - n, a.vec != 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sum[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+  }
+};
+
+// dW: rows of one piece of the vocabulary, whole sums over the tokens.
+template <typename T>
+struct WeightEpilogue {
+  struct Args {
+    T* out;  // the piece's first row, [V][N]
+    const XentState* state;
+    int vec;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
+                                             int row, int col0, int cols, int M, const Acc& acc) {
+    const int v0 = o.m0 + row;
+    const float scale = a.state->gradScale;
+    for (int c = 0; c < cols; c += 32) {
+      const int n = o.n0 + col0 + c;
+      if (n >= g.N) break;
+      float v[32];
+      acc(col0 + c, v);
+      if (v0 >= M) continue;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= scale;
+      store32(a.out + (long long)v0 * g.N + n, v, g.N - n, a.vec != 0);
+    }
+  }
+};
+
+// One CTA: the targets narrowed (-1: ignored), the tokens that count packed
+// in order, their number and the scales.  A target outside the vocabulary is
+// reported in the status word and ignored.
+struct PrepArgs {
+  const long long* targets;
+  long long ignore;
+  int T, V, mean;
+  float gradScale;
+  int shift;
+  int* target;
+  int* token;
+  XentState* state;
+  unsigned* status;
+};
+__global__ void __launch_bounds__(1024) xent_prep_kernel(const __grid_constant__ PrepArgs a) {
+  __shared__ int sWarp[32];
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int base = 0;
+  for (int t0 = 0; t0 < a.T; t0 += 1024) {
+    const int t = t0 + threadIdx.x;
+    int y = -1;
+    if (t < a.T) {
+      const long long raw = a.targets[t];
+      if (raw >= 0 && raw < a.V && raw != a.ignore) y = (int)raw;
+      else if (raw != a.ignore) atomicCAS(a.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
+      a.target[t] = y;
+    }
+    const unsigned votes = __ballot_sync(0xffffffffu, y >= 0);
+    if (lane == 0) sWarp[warp] = __popc(votes);
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int n = sWarp[w];
+      before += w < warp ? n : 0;
+      all += n;
+    }
+    if (y >= 0) a.token[base + before + __popc(votes & ((1u << lane) - 1))] = t;
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const float per = a.mean ? (base ? 1.0f / (float)base : 0.0f) : 1.0f;
+    a.state->valid = base;
+    a.state->lossScale = per;
+    a.state->gradScale = per * a.gradScale * exp2f((float)-a.shift);
+  }
+}
+
+// A warp per token joins its tiles' (maximum, sum) pairs.
+struct JoinArgs {
+  const float2* parts;
+  int nParts, T;
+  const int* target;
+  const float* targetLogit;
+  float *lse2, *lse, *losses;
+};
+__global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ JoinArgs a) {
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32;
+  for (int t = blockIdx.x * 8 + threadIdx.x / 32; t < a.T; t += gridDim.x * 8) {
+    const float2* p = a.parts + (long long)t * a.nParts;
+    float top = -INFINITY;
+    for (int i = lane; i < a.nParts; i += 32) top = fmaxf(top, p[i].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int i = lane; i < a.nParts; i += 32) sum += p[i].y * exp2f(p[i].x - base);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const float l2 = base + log2f(sum);
+      const float l = l2 * kLn2;
+      a.lse2[t] = l2;
+      a.lse[t] = l;
+      a.losses[t] = a.target[t] >= 0 ? l - a.targetLogit[t] : 0.0f;
+    }
+  }
+}
+
+// One CTA: the loss, summed in a fixed order.
+__global__ void __launch_bounds__(1024)
+    xent_loss_kernel(const float* losses, int T, const XentState* state, float* loss) {
+  __shared__ double s[32];
+  pdl_launch();
+  pdl_wait();
+  double sum = 0.0;
+  for (int t = threadIdx.x; t < T; t += 1024) sum += (double)losses[t];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.0;
+    for (int w = 0; w < 32; ++w) sum += s[w];
+    *loss = (float)(sum * (double)state->lossScale);
+  }
+}
+
+// Rows copied into a buffer whose rows are whole 16-byte units, zeros after
+// the last column.
+struct PadArgs {
+  const uint16_t* src;
+  long long stride, rows;
+  int cols, ld;
+  uint16_t* dst;
+};
+__global__ void __launch_bounds__(256) xent_pad_kernel(const __grid_constant__ PadArgs a) {
+  pdl_launch();
+  pdl_wait();
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < a.ld; c += 256)
+      a.dst[r * a.ld + c] = c < a.cols ? a.src[r * a.stride + c] : (uint16_t)0;
+}
+
+// The packed hidden states, targets and log sums of the tokens that count,
+// zero rows up to the next whole tile, and zero gradients for the others.
+struct PackArgs {
+  const uint16_t* hidden;
+  long long stride;
+  int T, D, ld, vec;
+  const int *target, *token;
+  const float* lse2;
+  const XentState* state;
+  uint16_t* packed;
+  int* packedTarget;
+  float* packedLse2;
+  uint16_t* dHidden;  // [T][D] or null
+};
+__global__ void __launch_bounds__(256) xent_pack_kernel(const __grid_constant__ PackArgs a) {
+  pdl_launch();
+  pdl_wait();
+  const int valid = a.state->valid;
+  const int rows = (valid + kTileM - 1) / kTileM * kTileM;
+  const int last = max(rows, a.T);
+  for (int r = blockIdx.x; r < last; r += gridDim.x) {
+    if (r < rows) {
+      const int t = r < valid ? a.token[r] : -1;
+      uint16_t* out = a.packed + (long long)r * a.ld;
+      const uint16_t* in = a.hidden + (t < 0 ? 0 : t * a.stride);
+      if (a.vec) {
+        for (int c = threadIdx.x * 8; c < a.ld; c += 256 * 8)
+          *reinterpret_cast<uint4*>(out + c) =
+              t < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(in + c);
+      } else {
+        for (int c = threadIdx.x; c < a.ld; c += 256)
+          out[c] = t >= 0 && c < a.D ? in[c] : (uint16_t)0;
+      }
+      if (threadIdx.x == 0 && t >= 0) {
+        a.packedTarget[r] = a.target[t];
+        a.packedLse2[r] = a.lse2[t];
+      }
+    }
+    if (a.dHidden && r < a.T && a.target[r] < 0)
+      for (int c = threadIdx.x; c < a.D; c += 256) a.dHidden[(long long)r * a.D + c] = 0;
+  }
+}
+
+// ------------------------------------------------------------- host side
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+// Rows of the vocabulary taken at a time: a piece of the gradient factors of
+// about 256 MB, so that the fp32 sums of dH, read and written once a
+// piece, stay a small part of the traffic.
+constexpr size_t kPieceBytes = (size_t)256 << 20;
+size_t piece_rows(size_t T, size_t V) {
+  const size_t fit = kPieceBytes / (2 * up(T, kTileM)) / kBN * kBN;
+  return std::min(up(V, kBN), std::max<size_t>(fit, kBN));
+}
+
+bool packed_rows(const void* p, size_t stride) {
+  return ((uintptr_t)p & 15) == 0 && stride % 8 == 0;
+}
+
+struct XentPlan {
+  bool padHidden, padWeight;
+  size_t T, D, V, Dp, T128, nParts, piece, nPieces, sumLd;
+  // offsets into the workspace
+  size_t state, target, token, lse2, targetLogit, parts, hidden, weight, packed, packedTarget,
+      packedLse2, factors, sum, bytes;
+};
+
+bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size_t weightStride,
+               size_t T, size_t D, size_t V, int dtype, bool grads, XentPlan* p) {
+  if ((dtype != VR_FLOAT16 && dtype != VR_BFLOAT16) || T > (1u << 30) || D < 1 || D > (1u << 24) ||
+      V < 1 || V > (1u << 30) || hiddenStride < D || weightStride < D ||
+      hiddenStride > (1ull << 32) || weightStride > (1ull << 32))
+    return false;
+  p->T = T, p->D = D, p->V = V;
+  p->padHidden = !packed_rows(hidden, hiddenStride);
+  p->padWeight = !packed_rows(weight, weightStride);
+  p->Dp = up(D, 8);
+  p->T128 = up(std::max<size_t>(T, 1), kTileM);
+  p->nParts = 2 * (up(V, kBN) / kBN);
+  p->piece = piece_rows(T, V);
+  p->nPieces = (V + p->piece - 1) / p->piece;
+  p->sumLd = up(D, 32);
+  size_t at = 0;
+  auto take = [&at](size_t n) {
+    const size_t here = at;
+    at += op_round(n);
+    return here;
+  };
+  p->state = take(sizeof(XentState));
+  p->target = take(T * 4);
+  p->token = take(T * 4);
+  p->lse2 = take(T * 4);
+  p->targetLogit = take(T * 4);
+  p->parts = take(T * p->nParts * sizeof(float2));
+  p->hidden = p->padHidden ? take(T * p->Dp * 2) : 0;
+  p->weight = p->padWeight ? take(V * p->Dp * 2) : 0;
+  if (grads) {
+    p->packed = take(p->T128 * p->Dp * 2);
+    p->packedTarget = take(p->T128 * 4);
+    p->packedLse2 = take(p->T128 * 4);
+    p->factors = take(p->T128 * p->piece * 2);
+    p->sum = p->nPieces > 1 ? take(p->T128 * p->sumLd * 4) : 0;
+  }
+  p->bytes = at;
+  return true;
+}
+
+// One product: the operands' extents and layouts, the launch.
+template <typename T, bool AMN, bool BMN, class Epi>
+vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* b, size_t bLd,
+                    size_t M, size_t N, size_t K, const int* dynM, const int* dynK,
+                    typename Epi::Args& epi, void* stream) {
+  using Shape = GemmShape<kBN, 1>;
+  const void* fn = (const void*)gemm_kernel<T, kBN, 1, AMN, BMN, Epi>;
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  GemmArgs g = {};
+  vr_result_t e = gemm_operand(&g.a[0], a, bf16, AMN ? M : K, AMN ? K : M, 1, aLd * 2,
+                               aLd * 2 * (AMN ? K : M), AMN ? kTileK : kTileM);
+  if (e != VR_SUCCESS) return e;
+  e = gemm_operand(&g.b[0], b, bf16, BMN ? N : K, BMN ? K : N, 1, bLd * 2,
+                   bLd * 2 * (BMN ? K : N), BMN ? kTileK : kBN);
+  if (e != VR_SUCCESS) return e;
+  if ((e = gemm_prepare(fn, dev.device, Shape::kSmem)) != VR_SUCCESS) return e;
+  g.M = (int)M;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.batch = 1;
+  g.dynM = dynM;
+  g.dynK = dynK;
+  g.status = dev.status;
+  g.timeoutNs = dev.timeoutNs;
+  const size_t tiles = (M + kTileM - 1) / kTileM * ((N + kBN - 1) / kBN);
+  void* args[] = {&g, &epi};
+  return op_launch(fn, dim3((unsigned)std::min<size_t>(tiles, dev.sms)), dim3(kGemmThreads), args,
+                   Shape::kSmem, stream);
+}
+
+template <typename T>
+vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size_t hiddenStride,
+                const void* weight, size_t weightStride, const long long* targets,
+                long long ignoreIndex, int mean, float gradScale, float* losses, float* lse,
+                float* loss, void* dHidden, void* dWeight, char* w, void* stream) {
+  XentState* state = reinterpret_cast<XentState*>(w + p.state);
+  int* target = reinterpret_cast<int*>(w + p.target);
+  int* token = reinterpret_cast<int*>(w + p.token);
+  float* lse2 = reinterpret_cast<float*>(w + p.lse2);
+  float* targetLogit = reinterpret_cast<float*>(w + p.targetLogit);
+  float2* parts = reinterpret_cast<float2*>(w + p.parts);
+  vr_result_t e;
+  {
+    PrepArgs a = {targets,   ignoreIndex, (int)p.T, (int)p.V, mean,  gradScale,
+                  kShift<T>, target,      token,    state,    dev.status};
+    void* args[] = {&a};
+    if ((e = op_launch((const void*)xent_prep_kernel, dim3(1), dim3(1024), args, 0, stream)) !=
+        VR_SUCCESS)
+      return e;
+  }
+  auto pad = [&](const void** src, size_t* stride, size_t rows, size_t at) -> vr_result_t {
+    PadArgs a = {static_cast<const uint16_t*>(*src), (long long)*stride, (long long)rows,
+                 (int)p.D, (int)p.Dp, reinterpret_cast<uint16_t*>(w + at)};
+    void* args[] = {&a};
+    *src = w + at;
+    *stride = p.Dp;
+    return op_launch((const void*)xent_pad_kernel,
+                     dim3((unsigned)std::min<size_t>(rows, (size_t)dev.sms * 8)), dim3(256), args,
+                     0, stream);
+  };
+  if (p.T && p.padHidden && (e = pad(&hidden, &hiddenStride, p.T, p.hidden)) != VR_SUCCESS) return e;
+  if (p.T && p.padWeight && (e = pad(&weight, &weightStride, p.V, p.weight)) != VR_SUCCESS) return e;
+  if (p.T) {
+    StatsEpilogue::Args epi = {target, targetLogit, parts, (int)p.nParts};
+    if ((e = product<T, false, false, StatsEpilogue>(dev, hidden, hiddenStride, weight,
+                                                     weightStride, p.T, p.V, p.D, nullptr, nullptr,
+                                                     epi, stream)) != VR_SUCCESS)
+      return e;
+    JoinArgs a = {parts, (int)p.nParts, (int)p.T, target, targetLogit, lse2, lse, losses};
+    void* args[] = {&a};
+    if ((e = op_launch((const void*)xent_join_kernel,
+                       dim3((unsigned)std::min<size_t>((p.T + 7) / 8, (size_t)dev.sms * 8)),
+                       dim3(256), args, 0, stream)) != VR_SUCCESS)
+      return e;
+  }
+  {
+    int T32 = (int)p.T;
+    const float* in = losses;
+    void* args[] = {&in, &T32, &state, &loss};
+    if ((e = op_launch((const void*)xent_loss_kernel, dim3(1), dim3(1024), args, 0, stream)) !=
+        VR_SUCCESS)
+      return e;
+  }
+  if (!dHidden && !dWeight) return VR_SUCCESS;
+  if (!p.T) {
+    if (dWeight && cudaMemsetAsync(dWeight, 0, p.V * p.D * 2, (cudaStream_t)stream) != cudaSuccess)
+      return VR_ERR_CUDA;
+    return VR_SUCCESS;
+  }
+  uint16_t* packed = reinterpret_cast<uint16_t*>(w + p.packed);
+  int* packedTarget = reinterpret_cast<int*>(w + p.packedTarget);
+  float* packedLse2 = reinterpret_cast<float*>(w + p.packedLse2);
+  T* factors = reinterpret_cast<T*>(w + p.factors);
+  {
+    PackArgs a = {static_cast<const uint16_t*>(hidden), (long long)hiddenStride, (int)p.T,
+                  (int)p.D, (int)p.Dp, p.Dp == p.D || p.padHidden, target, token, lse2, state,
+                  packed, packedTarget, packedLse2, static_cast<uint16_t*>(dHidden)};
+    void* args[] = {&a};
+    if ((e = op_launch((const void*)xent_pack_kernel,
+                       dim3((unsigned)std::min<size_t>(p.T128, (size_t)dev.sms * 8)), dim3(256),
+                       args, 0, stream)) != VR_SUCCESS)
+      return e;
+  }
+  const int vecH = p.D % 8 == 0 && ((uintptr_t)dHidden & 15) == 0;
+  const int vecW = p.D % 8 == 0 && ((uintptr_t)dWeight & 15) == 0;
+  for (size_t i = 0; i < p.nPieces; ++i) {
+    const size_t v0 = i * p.piece, rows = std::min(p.piece, p.V - v0);
+    const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
+    typename FactorEpilogue<T>::Args fa = {packedTarget, packedLse2, factors, (long long)p.piece,
+                                           (int)v0};
+    if ((e = product<T, false, false, FactorEpilogue<T>>(
+             dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
+             stream)) != VR_SUCCESS)
+      return e;
+    if (dHidden) {
+      typename HiddenEpilogue<T>::Args ha = {
+          reinterpret_cast<float*>(w + p.sum), (long long)p.sumLd, static_cast<T*>(dHidden), token,
+          state, i == 0, i + 1 == p.nPieces, vecH};
+      if ((e = product<T, false, true, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
+                                                          weightStride, p.T, p.D, rows,
+                                                          &state->valid, nullptr, ha, stream)) !=
+          VR_SUCCESS)
+        return e;
+    }
+    if (dWeight) {
+      typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, vecW};
+      if ((e = product<T, true, true, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
+                                                         p.D, p.T128, nullptr, &state->valid, wa,
+                                                         stream)) != VR_SUCCESS)
+        return e;
+    }
+  }
+  return VR_SUCCESS;
+}
+
+}  // namespace
+}  // namespace vr
+
+using namespace vr;
+
+extern "C" {
+
+vr_result_t vr_linear_xent_workspace_bytes(const void* hidden, size_t hiddenStride,
+                                           const void* weight, size_t weightStride, size_t tokens,
+                                           size_t dim, size_t vocab, vr_dtype_t dtype, int grads,
+                                           size_t* bytes) {
+  XentPlan p = {};
+  if (!bytes || !make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype,
+                           grads != 0, &p))
+    return VR_ERR_INVALID_ARGUMENT;
+  *bytes = p.bytes;
+  return VR_SUCCESS;
+}
+
+vr_result_t vr_linear_xent(const void* hidden, size_t hiddenStride, const void* weight,
+                           size_t weightStride, const long long* targets, size_t tokens,
+                           size_t dim, size_t vocab, vr_dtype_t dtype, long long ignoreIndex,
+                           int mean, float gradScale, float* losses, float* lse, float* loss,
+                           void* dHidden, void* dWeight, void* workspace, size_t workspaceBytes,
+                           void* stream) {
+  XentPlan p = {};
+  if (!make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype,
+                 dHidden || dWeight, &p) ||
+      !weight || !loss || !workspace || (tokens && (!hidden || !targets || !losses || !lse)) ||
+      workspaceBytes < p.bytes || ((uintptr_t)workspace & 15) || ((uintptr_t)targets & 7) ||
+      (((uintptr_t)losses | (uintptr_t)lse | (uintptr_t)loss) & 3) ||
+      (((uintptr_t)hidden | (uintptr_t)weight | (uintptr_t)dHidden | (uintptr_t)dWeight) & 1))
+    return VR_ERR_INVALID_ARGUMENT;
+  OpBuffer buf[9] = {
+      {hidden, tokens, dim * 2, hiddenStride * 2, false},
+      {weight, vocab, dim * 2, weightStride * 2, false},
+      {targets, 1, tokens * 8, tokens * 8, false},
+      {losses, 1, tokens * 4, tokens * 4, true},
+      {lse, 1, tokens * 4, tokens * 4, true},
+      {loss, 1, 4, 4, true},
+      {workspace, 1, workspaceBytes, workspaceBytes, true},
+  };
+  int n = 7;
+  if (dHidden) buf[n++] = {dHidden, 1, tokens * dim * 2, tokens * dim * 2, true};
+  if (dWeight) buf[n++] = {dWeight, 1, vocab * dim * 2, vocab * dim * 2, true};
+  if (!op_buffers_ok(buf, n)) return VR_ERR_INVALID_ARGUMENT;
+  OpDevice dev;
+  const vr_result_t e = op_device(&dev);
+  if (e != VR_SUCCESS) return e;
+  char* w = static_cast<char*>(workspace);
+  return dtype == VR_BFLOAT16
+             ? run<__nv_bfloat16>(p, dev, hidden, hiddenStride, weight, weightStride, targets,
+                                  ignoreIndex, mean, gradScale, losses, lse, loss, dHidden, dWeight,
+                                  w, stream)
+             : run<__half>(p, dev, hidden, hiddenStride, weight, weightStride, targets, ignoreIndex,
+                           mean, gradScale, losses, lse, loss, dHidden, dWeight, w, stream);
+}
+
+}  // extern "C"

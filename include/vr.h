@@ -433,6 +433,42 @@ vr_result_t vr_allreduce_ring_stepwise_noalloc(const void* const* sendbufs, void
  * one each), the same bits on every run.  A written buffer may overlap no
  * other buffer of the call unless stated. */
 
+/* Softmax cross entropy of a linear layer over a large vocabulary, with its
+ * gradients, without the tokens x vocab logits ever being stored.
+ *   l_tv = hidden_t . weight_v,  lse[t] = log sum_v exp l_tv,
+ *   losses[t] = lse[t] - l_t,targets[t]  (0 for a token that does not count)
+ *   *loss = s * sum_t losses[t],  s = mean ? 1 / (tokens that count) : 1
+ *   dHidden = gradScale * d*loss/dhidden,  dWeight = gradScale * d*loss/dweight
+ * hidden: `tokens` rows of dim elements, hiddenStride elements apart; weight:
+ * `vocab` rows of dim, weightStride apart; both fp16 or both bf16.  targets:
+ * 64-bit indices below vocab; ignoreIndex marks a token that does not count
+ * (its gradient is zero whatever its hidden state holds).  Any other index
+ * outside the vocabulary is ignored too and reported by vr_stream_status as
+ * VR_ERR_INVALID_ARGUMENT.  losses, lse: `tokens` floats; loss: one float.
+ * dHidden (tokens x dim), dWeight (vocab x dim): contiguous, of dtype; each
+ * may be NULL, both for the loss alone.
+ * Products are exact and summed in fp32, as are the softmax and the losses;
+ * in the gradients softmax minus one-hot is rounded to dtype once (fp16:
+ * scaled by 2^14 first) and each gradient once (fp16: scale it into range
+ * with gradScale).  When no token counts, the loss and the gradients are 0.
+ * Rows that are not 16-byte units (dim or stride not a multiple of 8, or a
+ * misaligned buffer) are copied into the workspace first; its size depends
+ * on the buffers' alignment, so vr_linear_xent_workspace_bytes takes the
+ * call's own pointers and strides (grads: whether either gradient is wanted).
+ * Errors: VR_ERR_INVALID_ARGUMENT for fp32 or a bad dtype, dim or vocab < 1,
+ * tokens or vocab above 2^30, dim above 2^24, a stride below dim or above
+ * 2^32, a NULL or misaligned buffer, an overlap or a short workspace. */
+vr_result_t vr_linear_xent_workspace_bytes(const void* hidden, size_t hiddenStride,
+                                           const void* weight, size_t weightStride, size_t tokens,
+                                           size_t dim, size_t vocab, vr_dtype_t dtype, int grads,
+                                           size_t* bytes);
+vr_result_t vr_linear_xent(const void* hidden, size_t hiddenStride, const void* weight,
+                           size_t weightStride, const long long* targets, size_t tokens,
+                           size_t dim, size_t vocab, vr_dtype_t dtype, long long ignoreIndex,
+                           int mean, float gradScale, float* losses, float* lse, float* loss,
+                           void* dHidden, void* dWeight, void* workspace, size_t workspaceBytes,
+                           void* stream);
+
 /* Balance loss of R ranks' expert routers over the whole batch, with its
  * gradients.  logits[r]: `tokens` rows of `experts` router logits (fp32,
  * fp16 or bf16), rowStride elements apart.  Over the N valid tokens of all

@@ -67,3 +67,57 @@ def assert_close(got, want, bound, dtype, what=""):
     assert not bool(bad.any()), "%s: %d of %d outside, first got %r want %r limit %r" % (
         what, int(bad.sum()), bad.numel(), float(got[bad][0]), float(want[bad][0]),
         float(limit.expand_as(want)[bad][0]))
+
+
+def xent(hidden, weight, targets, ignore, mean, grad_scale):
+    """The cross entropy and its gradients in 64 bits, with bounds on what the
+    operator's arithmetic may differ by: products exact, fp32 sums that may
+    truncate (2^-23 a term), exp and log in fp32, softmax minus one-hot
+    rounded to the type once."""
+    ty = hidden.dtype
+    h, w = hidden.double(), weight.double()
+    T, D = h.shape
+    V = w.shape[0]
+    valid = (targets != ignore) & (targets >= 0) & (targets < V)
+    rows = valid.nonzero()[:, 0]
+    l = h @ w.t()
+    el = (D + 16) * 2.0 ** -23 * (h.abs() @ w.abs().t())
+    big = l.abs().amax(1).nan_to_num(0.0)
+    lse = torch.logsumexp(l, 1)
+    # exponents rounded to 2^-22 of the logits, sums of up to 128 terms in a
+    # row, then over the tiles
+    el_row = el.amax(1)
+    b_lse = el_row + (200 + V / 2048) * U32 + big * 2.0 ** -21 + lse.abs() * U32
+    n = int(valid.sum())
+    per = (1.0 / n if n else 0.0) if mean else 1.0
+    losses = torch.zeros(T, dtype=torch.float64, device=h.device)
+    hot = targets.clone()
+    hot[~valid] = 0
+    losses[valid] = (lse - l.gather(1, hot[:, None])[:, 0])[valid]
+    b_losses = b_lse + el_row + (losses.abs() + big) * U32
+    loss = float(losses[valid].sum()) * per
+    b_loss = float(b_losses[valid].sum()) * per + abs(loss) * 4 * U32
+    # gradients over the tokens that count
+    hv, lv = h[rows], l[rows]
+    p = torch.exp(lv - lse[rows, None])
+    one = torch.zeros_like(p)
+    one[torch.arange(len(rows), device=h.device), hot[rows]] = 1.0
+    g = p - one
+    bp = p * (el[rows] + b_lse[rows, None] + big[rows, None] * 2.0 ** -21 + 8 * U32)
+    bg = bp + (g.abs() + bp) * U_T[ty] + (2.0 ** -39 if ty == torch.float16 else 2.0 ** -126)
+    s = per * grad_scale
+    dh = torch.zeros_like(h)
+    b_dh = torch.zeros_like(h)
+    dh[rows] = s * (g @ w)
+    b_dh[rows] = abs(s) * ((bg + (V + 16) * 2.0 ** -23 * (g.abs() + bg)) @ w.abs())
+    dw = s * (g.t() @ hv)
+    b_dw = abs(s) * ((bg + (n + 16) * 2.0 ** -23 * (g.abs() + bg)).t() @ hv.abs())
+    return dict(valid=valid, lse=lse, b_lse=b_lse, losses=losses, b_losses=b_losses, loss=loss,
+                b_loss=b_loss, dh=dh, b_dh=b_dh, dw=dw, b_dw=b_dw)
+
+
+def norm_error(got, want):
+    """2-norm of the difference over the 2-norm of the result."""
+    n = float(want.norm())
+    d = float((got.double() - want).norm())
+    return d / n if n else d

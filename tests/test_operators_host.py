@@ -48,3 +48,42 @@ def test_balance_workspace():
     assert code(vr.vr_balance_loss_workspace_bytes, 1, 1, 1025) == INV
     small = vr.vr_balance_loss_workspace_bytes(1, 1, 8)
     assert 0 < small <= vr.vr_balance_loss_workspace_bytes(8, 1 << 20, 1024)
+
+
+def xent_args(**kw):
+    a = dict(hidden=A, hiddenStride=64, weight=A + STEP, weightStride=64, targets=A + 2 * STEP,
+             tokens=100, dim=64, vocab=500, dtype=vr.VR_BFLOAT16, ignoreIndex=-100, mean=True,
+             gradScale=1.0, losses=A + 3 * STEP, lse=A + 4 * STEP, loss=A + 5 * STEP,
+             dHidden=A + 6 * STEP, dWeight=A + 7 * STEP, workspace=A + 8 * STEP,
+             workspaceBytes=8 << 20)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=vr.VR_FLOAT32), dict(dtype=9), dict(dim=0), dict(vocab=0), dict(tokens=1 << 31),
+    dict(tokens=1 << 62), dict(vocab=1 << 31), dict(dim=1 << 25, hiddenStride=1 << 25,
+                                                    weightStride=1 << 25),
+    dict(hiddenStride=63), dict(weightStride=63), dict(hiddenStride=1 << 40), dict(hidden=0),
+    dict(weight=0), dict(targets=0), dict(losses=0), dict(lse=0), dict(loss=0), dict(workspace=0),
+    dict(workspaceBytes=1 << 16), dict(workspace=A + 8 * STEP + 8), dict(targets=A + 2 * STEP + 4),
+    dict(losses=A + 3 * STEP + 2), dict(hidden=A + 1), dict(dWeight=A + 7 * STEP + 1),
+    dict(dHidden=A), dict(dWeight=A + STEP), dict(lse=A + 3 * STEP + 4), dict(loss=A + 2 * STEP),
+    dict(workspace=A + 7 * STEP + 256),
+])
+def test_linear_xent_refusals(bad):
+    assert code(vr.vr_linear_xent, *xent_args(**bad)) == INV
+
+
+def test_linear_xent_workspace():
+    size = vr.vr_linear_xent_workspace_bytes
+    B = vr.VR_BFLOAT16
+    assert code(size, A, 64, A, 64, 10, 64, 0, B, 1) == INV
+    loss, grads = (size(A, 64, A, 64, 1000, 64, 5000, B, g) for g in (0, 1))
+    assert 0 < loss < grads
+    # rows that are no 16-byte units need a copy
+    assert size(A, 65, A, 64, 1000, 64, 5000, B, 0) > loss
+    assert size(A + 2, 64, A, 64, 1000, 64, 5000, B, 0) > loss
+    # the gradient factors are taken in pieces: the workspace does not hold
+    # tokens x vocab of them
+    assert size(A, 64, A, 64, 1 << 16, 64, 1 << 17, B, 1) < (1 << 33)
