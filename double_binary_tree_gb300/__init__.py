@@ -68,6 +68,8 @@ _SIGNATURES = {
     "vr_linear_xent_workspace_bytes": (I, [VP, S, VP, S, S, S, S, I, I, P(S)]),
     "vr_linear_xent": (I, [VP, S, VP, S, VP, S, S, S, I, LL, I, F, VP, VP, VP, VP, VP, VP, S,
                            VP]),
+    "vr_orthogonalize_workspace_bytes": (I, [I, S, S, I, P(S)]),
+    "vr_orthogonalize": (I, [PP, PP, I, S, S, I, I, P(F), F, F, VP, S, VP]),
     "vr_balance_loss_workspace_bytes": (I, [I, S, I, P(S)]),
     "vr_balance_loss": (I, [PP, S, PP, I, S, I, I, I, F, F, VP, VP, PP, PP, VP, S, VP]),
     "vr_predict_us": (I, [I, I, I, S, P(vr_cost_model_t), P(ctypes.c_double)]),
@@ -314,6 +316,24 @@ def vr_balance_loss(logits, rowStride, masks, R, tokens, experts, topK, dtype, c
                                 dtype, coef, gradScale, _ptr(loss), _ptr(counts), _ptrs(chosen),
                                 _ptrs(dlogits), _ptr(workspace), workspaceBytes,
                                 _stream(stream)), "vr_balance_loss")
+
+
+def vr_orthogonalize_workspace_bytes(count, rows, cols, dtype):
+    return _size(_L().vr_orthogonalize_workspace_bytes, "vr_orthogonalize_workspace_bytes", count,
+                 rows, cols, dtype)
+
+
+def vr_orthogonalize(src, dst, count, rows, cols, dtype, steps, coefs, eps, scale, workspace,
+                     workspaceBytes, stream=None):
+    """coefs: None, or 3 * steps floats (a, b, c of each step)."""
+    if coefs is not None:
+        coefs = [float(c) for c in coefs]
+        if len(coefs) != 3 * steps:
+            raise VrError(VR_ERR_INVALID_ARGUMENT, "vr_orthogonalize")
+        coefs = (F * len(coefs))(*coefs)
+    _check(_L().vr_orthogonalize(_ptrs(src), _ptrs(dst), count, rows, cols, dtype, steps, coefs,
+                                 eps, scale, _ptr(workspace), workspaceBytes, _stream(stream)),
+           "vr_orthogonalize")
 
 
 # ------------------------------------------------------------- cost model

@@ -21,7 +21,7 @@ LIB_DEBUG = os.path.join(HERE, "libvr_debug.so")
 SOURCES = ["topology.cc", "api.cc", "kernels_f32.cu", "kernels_f16.cu", "kernels_bf16.cu",
            "kernels_copy.cu", "kernels_ablation.cu", "noalloc.cu", "jit.cc",
            "costmodel.cc", "options.cc", "graphlog.cc", "ops.cc", "gemm_host.cc",
-           "balance.cu", "xent.cu"]
+           "balance.cu", "xent.cu", "ortho.cu"]
 HEADERS = ["common.h", "host.h", "fold.cuh", "kernels.cuh", "staged.cuh", "ablation.cuh",
            "gather.cuh", "bounds.cuh", "ops.h", "gemm.cuh", "gemm_host.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

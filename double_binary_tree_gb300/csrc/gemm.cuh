@@ -118,9 +118,9 @@ __device__ __forceinline__ float tmem_load1(uint32_t addr) {
       : "memory");
   return __uint_as_float(r);
 }
-// A warp's rows of a finished accumulator; called by whole warps.  Without a
-// product (K = 0) the sums are zero and tensor memory is not read.
-struct Acc {
+// A warp's rows of a finished accumulator in tensor memory; called by whole
+// warps.  Without a product (K = 0) the sums are zero and it is not read.
+struct TmemAcc {
   uint32_t addr;
   bool summed;
   __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
@@ -149,6 +149,29 @@ struct Acc {
   }
 };
 
+// The same rows already in registers (N columns from `first`); the columns
+// asked for are constants once the epilogue's loops are unrolled.
+template <int N>
+struct RegAcc {
+  const float (&sum)[N];
+  int first;
+  __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = sum[c - first + i];
+  }
+  template <class F>
+  __device__ __forceinline__ void pick(int c, F f) const {
+    if (c < 0) return;
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)  // a select each: no indexed registers
+      asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, %2;\n\t@p mov.f32 %0, %3;\n\t}"
+          : "+f"(x)
+          : "r"(c - first), "r"(i), "f"(sum[i]));
+    f(x);
+  }
+};
+
 // Instruction descriptor of kind::f16 with fp32 accumulators.
 template <typename T>
 __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool aMn, bool bMn) {
@@ -162,9 +185,12 @@ struct GemmShape {
   static constexpr int kABytes = kTileM * kTileK * 2;
   static constexpr int kBBytes = BN * kTileK * 2;
   static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
+  // columns of an accumulator: with two planes the products of a low plane
+  // are summed apart (their size would not survive being added one by one)
+  static constexpr int kAcc = PARTS * BN;
   static constexpr int kStages = (kGemmSmem - 2048) / kStageBytes;
   static constexpr int kSmem = 2048 + kStages * kStageBytes;  // header, alignment
-  static_assert(kStages >= 2, "too few stages");
+  static_assert(kStages >= 2 && 2 * kAcc <= 512, "too large");
 };
 
 // Blocks of 16 tile rows are walked column by column, so that the rows' and
@@ -199,14 +225,21 @@ __device__ __forceinline__ Tile tile_of(int t, int tilesM, int tilesN, int BN, b
 
 // Epi: struct with `Args` (kernel parameter) and
 //   static __device__ void run(const Args&, const GemmArgs&, const Tile&, int row, int col0,
-//                              int cols, int M, const Acc& acc)
-// called by every thread of the epilogue warps for its accumulator row `row`
-// (of the tile) and its columns [col0, col0 + cols) of the tile; acc(c, v)
+//                              int M, const Acc& acc)
+// (templates: int COLS, class Acc) called by every thread of the epilogue warps for its accumulator row `row`
+// (of the tile) and its columns [col0, col0 + COLS) of the tile; acc(c, v)
 // fetches the 32 accumulator columns from c.
-template <typename T, int BN, int PARTS, bool AMN, bool BMN, class Epi>
+//
+// CHUNK > 0: the tensor cores truncate where they add a product to the
+// accumulator (one addition per 16 k), an error that grows with the length of
+// the sum.  Every CHUNK slices of 64 the accumulator is handed to the
+// epilogue warps, which add the partial sums in registers with rounding; the
+// next chunk is summed meanwhile in the other accumulator.
+template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ typename Epi::Args e) {
   using Shape = GemmShape<BN, PARTS>;
+  static_assert(PARTS == 1 || CHUNK > 0, "two planes are summed in the epilogue warps");
   extern __shared__ unsigned char smemRaw[];
   __shared__ alignas(8) uint64_t bars[2 * Shape::kStages + 5];
   __shared__ uint32_t tmemBase;
@@ -238,7 +271,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&tmemBase)),
-                 "r"(2 * BN)
+                 "r"(2 * Shape::kAcc)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -253,6 +286,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int K = g.dynK ? min(*g.dynK, g.K) : g.K;
   const int tilesM = (M + kTileM - 1) / kTileM, tilesN = (g.N + BN - 1) / BN;
   const int blocks = (K + kTileK - 1) / kTileK;
+  const int chunk = CHUNK ? CHUNK : max(blocks, 1);
+  constexpr int kHalf = BN / 2;  // columns of an epilogue warp
   int tiles = tilesM * tilesN;
   if (g.triangle) {
     tiles = 0;
@@ -313,32 +348,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr unsigned aStep = (AMN ? 16 * 128 : 32) >> 4, bStep = (BMN ? 16 * 128 : 32) >> 4;
     int s = 0, turn = 0, buf = 0, bufTurn = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && blocks && t < tiles; t += gridDim.x) {
-      ok = wait_phase(accEmpty(buf), bufTurn ^ 1, &abortFlag, true, g.timeoutNs);
-      if (!ok) break;
-      tmem_fence_after();
-      const uint32_t acc = tmem + (unsigned)buf * BN;
-      for (int kb = 0; kb < blocks; ++kb) {
-        ok = wait_phase(full(s), turn, &abortFlag, true, g.timeoutNs);
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (int kb0 = 0; ok && kb0 < blocks; kb0 += chunk) {
+        ok = wait_phase(accEmpty(buf), bufTurn ^ 1, &abortFlag, true, g.timeoutNs);
         if (!ok) break;
         tmem_fence_after();
-        const uint32_t base = stage0 + (unsigned)s * Shape::kStageBytes;
+        const uint32_t acc = tmem + (unsigned)buf * Shape::kAcc;
+        const int kb1 = min(kb0 + chunk, blocks);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = wait_phase(full(s), turn, &abortFlag, true, g.timeoutNs);
+          if (!ok) break;
+          tmem_fence_after();
+          const uint32_t base = stage0 + (unsigned)s * Shape::kStageBytes;
 #pragma unroll
-        for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
-          const uint32_t aAt = base + (p == 2 ? Shape::kABytes : 0);
-          const uint32_t bAt = base + PARTS * Shape::kABytes + (p == 1 ? Shape::kBBytes : 0);
-          const uint64_t aDesc = operand_desc(aAt, AMN ? kSlab : 16, 1024);
-          const uint64_t bDesc = operand_desc(bAt, BMN ? kSlab : 16, 1024);
+          for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
+            const uint32_t aAt = base + (p == 2 ? Shape::kABytes : 0);
+            const uint32_t bAt = base + PARTS * Shape::kABytes + (p == 1 ? Shape::kBBytes : 0);
+            const uint64_t aDesc = operand_desc(aAt, AMN ? kSlab : 16, 1024);
+            const uint64_t bDesc = operand_desc(bAt, BMN ? kSlab : 16, 1024);
 #pragma unroll
-          for (int k = 0; k < kTileK / 16; ++k)
-            mma_f16(acc, aDesc + k * aStep, bDesc + k * bStep, idesc, kb | p | k);
+            for (int k = 0; k < kTileK / 16; ++k)
+              mma_f16(p ? acc + BN : acc, aDesc + k * aStep, bDesc + k * bStep, idesc,
+                      (kb - kb0) | (p == 2) | k);
+          }
+          mma_commit(empty(s));
+          if (++s == Shape::kStages) s = 0, turn ^= 1;
         }
-        mma_commit(empty(s));
-        if (++s == Shape::kStages) s = 0, turn ^= 1;
+        if (!ok) break;
+        mma_commit(accFull(buf));
+        if (++buf == 2) buf = 0, bufTurn ^= 1;
       }
-      if (!ok) break;
-      mma_commit(accFull(buf));
-      if (++buf == 2) buf = 0, bufTurn ^= 1;
     }
     if (!ok) {
       raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
@@ -350,23 +389,55 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int buf = 0, bufTurn = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const Tile o = tile_of(t, tilesM, tilesN, BN, g.triangle);
-      if (blocks) {
+      const uint32_t quadBase = tmem + ((uint32_t)(quad * 32) << 16);
+      const int row = quad * 32 + lane;
+      // the next accumulator, or false when the warp has to leave
+      auto next = [&]() {
         const bool ready = wait_phase(accFull(buf), bufTurn, &abortFlag, true, g.timeoutNs);
-        if (!__all_sync(0xffffffffu, ready)) {  // the warp leaves as a whole
+        if (!__all_sync(0xffffffffu, ready)) {  // as a whole
           raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
-          break;
+          return false;
         }
         tmem_fence_after();
-      }
-      __syncwarp();
-      const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (unsigned)buf * BN;
-      const Acc load{acc, blocks != 0};
-      Epi::run(e, g, o, quad * 32 + lane, half * (BN / 2), BN / 2, M, load);
-      if (blocks) {
+        return true;
+      };
+      auto release = [&]() {
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(accEmpty(buf));
         if (++buf == 2) buf = 0, bufTurn ^= 1;
+      };
+      if (CHUNK) {
+        float sum[kHalf];
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
+        bool left = false;
+        for (int kb0 = 0; kb0 < blocks; kb0 += chunk) {
+          left = !next();
+          if (left) break;
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            float v[32];
+            const uint32_t at = quadBase + (unsigned)(buf * Shape::kAcc + half * kHalf + c);
+            tmem_load32(at, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += v[i];
+            if (PARTS == 2) {
+              tmem_load32(at + BN, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[c + i] += v[i];
+            }
+          }
+          release();
+        }
+        if (left) break;
+        Epi::template run<kHalf>(e, g, o, row, half * kHalf, M,
+                                 RegAcc<kHalf>{sum, half * kHalf});
+      } else {
+        if (blocks && !next()) break;
+        Epi::template run<kHalf>(e, g, o, row, half * kHalf, M,
+                                 TmemAcc{quadBase + (unsigned)(buf * Shape::kAcc), blocks != 0});
+        if (blocks) release();
       }
     }
   }
@@ -375,7 +446,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   if (warp == 2) {
     tmem_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(2 * Shape::kAcc));
   }
 }
 

@@ -1,7 +1,9 @@
 // Buffer checks shared by the training operators.
 #include "ops.h"
 
+#include <algorithm>
 #include <cstdint>
+#include <vector>
 
 namespace vr {
 namespace {
@@ -36,6 +38,35 @@ bool op_buffers_ok(const OpBuffer* b, int n) {
     }
   }
   return true;
+}
+
+bool op_lists_ok(const void* const* src, void* const* dst, int count, size_t bytes,
+                 const void* workspace, size_t workspaceBytes) {
+  try {
+    struct Span {
+      uintptr_t lo, hi;
+      int i;  // list index; -1: the workspace
+      bool write;
+    };
+    std::vector<Span> v;
+    v.reserve(2 * (size_t)count + 1);
+    for (int i = 0; i < count; ++i) {
+      v.push_back({(uintptr_t)dst[i], (uintptr_t)dst[i] + bytes, i, true});
+      if (src[i] != dst[i]) v.push_back({(uintptr_t)src[i], (uintptr_t)src[i] + bytes, i, false});
+    }
+    v.push_back({(uintptr_t)workspace, (uintptr_t)workspace + workspaceBytes, -1, true});
+    std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    // the furthest end so far of any span, and of a written one
+    uintptr_t any = 0, written = 0;
+    for (const Span& s : v) {
+      if (s.lo < written || (s.write && s.lo < any)) return false;
+      any = std::max(any, s.hi);
+      if (s.write) written = std::max(written, s.hi);
+    }
+    return true;
+  } catch (...) {  // no host memory for the list
+    return false;
+  }
 }
 
 }  // namespace vr

@@ -37,6 +37,11 @@ struct OpBuffer {
 // directly before it (in place).  Rows of equal stride may interleave.
 bool op_buffers_ok(const OpBuffer* b, int n);
 
+// The same for `count` inputs and outputs of one size and a workspace:
+// dst[i] may be src[i].  Any count: sorted by address.
+bool op_lists_ok(const void* const* src, void* const* dst, int count, size_t bytes,
+                 const void* workspace, size_t workspaceBytes);
+
 // Bytes rounded up to the alignment of a workspace's parts.
 inline size_t op_round(size_t n) { return (n + 255) & ~(size_t)255; }
 

@@ -1,0 +1,520 @@
+// Newton-Schulz orthogonalisation of matrices of one shape (vr_orthogonalize).
+//
+//   X = M / (|M|_F + eps)          (transposed when M has more rows than columns)
+//   steps times:  A = X X^T,  B = b A + c A A,  X <- a X + B X
+//
+// Every step is three products on the tensor cores (gemm.cuh), with the
+// polynomial's sums in their epilogues.  A and B are symmetric: only the
+// 128-blocks on and below the diagonal are computed, the others are stored
+// as their mirror images.
+//
+// Operands are fp16 planes of the values times 2^12 (the entries of X, A and
+// B stay below 16, which the entry point checks, and typical ones, of size
+// 1 / sqrt(m n) to 1, stay in fp16's normal range).  X itself is kept as a
+// high and a low plane, 22 bits: a rounding of X would be amplified by a with
+// every later step in the directions of small singular values, where a
+// rounding of an operand of B X is not (it enters between a small and a large
+// direction, which the next steps damp).  So bf16 results take one product of
+// high planes (operand roundings 2^-12, together below the result's own 2^-9),
+// fp16 and fp32 results three products of both planes, summed in chunks.
+// (Holding X in fp32 beside the planes measured 4 % slower at 4096 x 1024
+// and no more exact, but where all but a few singular values are below 1e-3:
+// 1.2e-5 against 1.5e-5, fp32 arithmetic throughout 2.2e-5.)
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "gemm.cuh"
+#include "gemm_host.h"
+
+namespace vr {
+namespace {
+
+constexpr int kMost = 64;          // matrices per launch
+constexpr float kScale = 4096.0f;  // of the planes
+constexpr int kNormCtas = 64;      // partial sums of squares per matrix, at most
+constexpr int kSplitChunk = 2;     // slices of 64 summed before rounding (two planes)
+
+struct Planes {
+  __half *hi, *lo;
+};
+
+// v as a high plane and what the rounding left.
+__device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
+  hi = __float2half_rn(v);
+  lo = __float2half_rn(v - __half2float(hi));
+}
+
+// 32 consecutive values of a row of a plane whose rows are whole groups of 32.
+__device__ __forceinline__ void store_plane(__half* out, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 q;
+    __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+    reinterpret_cast<uint4*>(out)[i] = q;
+  }
+}
+__device__ __forceinline__ void add_plane(const __half* in, float by, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 q = reinterpret_cast<const uint4*>(in)[i];
+    const __half2* h = reinterpret_cast<const __half2*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(h[j]);
+      v[8 * i + 2 * j] = fmaf(by, f.x, v[8 * i + 2 * j]);
+      v[8 * i + 2 * j + 1] = fmaf(by, f.y, v[8 * i + 2 * j + 1]);
+    }
+  }
+}
+// The low plane of v: what its high plane's rounding left.
+__device__ __forceinline__ void residue(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] -= __half2float(__float2half_rn(v[i]));
+}
+
+// A = X X^T (from = null) or B = b A + c A A, at the planes' scale; the block
+// and, below the diagonal, its mirror image.
+struct SymmetricEpilogue {
+  struct Args {
+    Planes from, to;
+    long long ld, size;  // of a row, of a matrix
+    float byFrom, byAcc;
+    float diagonal;      // subtracted from it
+    int low;             // the result's low plane is wanted
+  };
+  template <int COLS, class Acc>
+  static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
+                                             int row, int col0, int M, const Acc& acc) {
+    const int r = o.m0 + row, blockR = o.m0 / kTileM, blockC = (o.n0 + col0) / kTileM;
+    const bool live = r < M && blockC <= blockR;
+    const long long base = o.z * a.size;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+      const int n = o.n0 + col0 + c;
+      if (n >= g.N) break;
+      float v[32];
+      acc(col0 + c, v);
+      if (!live) continue;
+      const long long at = base + r * a.ld + n;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= a.byAcc;
+      if (a.from.hi) {
+        add_plane(a.from.hi + at, a.byFrom, v);
+        if (a.low) add_plane(a.from.lo + at, a.byFrom, v);
+        if (blockC == blockR) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (n + i == r) v[i] -= a.diagonal;
+        }
+      }
+      auto put = [&](__half* plane) {
+        store_plane(plane + at, v);
+        if (blockC < blockR) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (n + i < g.N) plane[base + (n + i) * a.ld + r] = __float2half_rn(v[i]);
+        }
+      };
+      put(a.to.hi);
+      if (a.low) {
+        residue(v);
+        put(a.to.lo);
+      }
+    }
+  }
+};
+
+// X <- a X + B X into the other pair of planes, or, after the last step,
+// into the result.
+template <typename T>
+struct ApplyEpilogue {
+  struct Args {
+    Planes from, to;
+    long long ld, size;
+    float byFrom, byAcc;
+    int last, tall, vec;
+    float byOut;
+    int cols;         // of X
+    T* out[kMost];
+  };
+  template <int COLS, class Acc>
+  static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
+                                             int row, int col0, int M, const Acc& acc) {
+    const int r = o.m0 + row;
+    const bool live = r < M;
+    const long long base = o.z * a.size;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+      const int n = o.n0 + col0 + c;
+      if (n >= g.N) break;
+      float v[32];
+      acc(col0 + c, v);
+      if (!live) continue;
+      const long long at = base + r * a.ld + n;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= a.byAcc;
+      add_plane(a.from.hi + at, a.byFrom, v);
+      add_plane(a.from.lo + at, a.byFrom, v);
+      if (!a.last) {
+        store_plane(a.to.hi + at, v);
+        residue(v);
+        store_plane(a.to.lo + at, v);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= a.byOut;
+      typename Ty<T>::Bits* out = reinterpret_cast<typename Ty<T>::Bits*>(a.out[o.z]);
+      if (a.tall) {  // the lanes' rows are consecutive columns of the result
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (n + i < g.N) out[(long long)(n + i) * M + r] = Ty<T>::narrow(v[i]);
+      } else if (a.vec && n + 32 <= g.N) {
+        constexpr int U = Ty<T>::U;
+        uint4* p = reinterpret_cast<uint4*>(out + (long long)r * a.cols + n);
+#pragma unroll
+        for (int i = 0; i < 32 / U; ++i) {
+          uint4 q;
+          typename Ty<T>::Bits* b = reinterpret_cast<typename Ty<T>::Bits*>(&q);
+#pragma unroll
+          for (int j = 0; j < U; ++j) b[j] = Ty<T>::narrow(v[i * U + j]);
+          p[i] = q;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (n + i < g.N) out[(long long)r * a.cols + n + i] = Ty<T>::narrow(v[i]);
+      }
+    }
+  }
+};
+
+struct LoadArgs {
+  const void* src[kMost];
+  long long rows, cols;
+  float* part;     // [matrix][kNormCtas]
+  int ctas;        // partial sums per matrix
+  float eps;
+  int tall;
+  Planes x;
+  long long ld, size;
+};
+
+// Partial sums of squares, fp32: a run of elements per thread, then a tree.
+template <typename T>
+__global__ void __launch_bounds__(256) ortho_norm_kernel(const __grid_constant__ LoadArgs a) {
+  __shared__ float s[8];
+  pdl_launch();
+  pdl_wait();
+  const typename Ty<T>::Bits* p = static_cast<const typename Ty<T>::Bits*>(a.src[blockIdx.y]);
+  const long long n = a.rows * a.cols;
+  constexpr int U = Ty<T>::U;
+  float sum = 0.0f;
+  const long long step = (long long)gridDim.x * 256;
+  const long long first = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (((uintptr_t)p & 15) == 0) {
+    const long long units = n / U;
+    for (long long i = first; i < units; i += step) {
+      const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+      const typename Ty<T>::Bits* b = reinterpret_cast<const typename Ty<T>::Bits*>(&q);
+      float t = 0.0f;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const float x = Ty<T>::widen(b[j]);
+        t = fmaf(x, x, t);
+      }
+      sum += t;
+    }
+    for (long long i = units * U + first; i < n; i += step) {
+      const float x = Ty<T>::widen(p[i]);
+      sum = fmaf(x, x, sum);
+    }
+  } else {
+    for (long long i = first; i < n; i += step) {
+      const float x = Ty<T>::widen(p[i]);
+      sum = fmaf(x, x, sum);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) sum += s[w];
+    a.part[blockIdx.y * kNormCtas + blockIdx.x] = sum;
+  }
+}
+
+// The normalised matrix into the planes of X, 32 x 32 blocks at a time
+// through shared memory when it is transposed.
+template <typename T>
+__global__ void __launch_bounds__(256) ortho_load_kernel(const __grid_constant__ LoadArgs a) {
+  __shared__ float tile[32][33];
+  pdl_launch();
+  pdl_wait();
+  const int z = blockIdx.y;
+  float sum = 0.0f;
+  for (int i = 0; i < a.ctas; ++i) sum += a.part[z * kNormCtas + i];
+  const float by = kScale / (sqrtf(sum) + a.eps);
+  const typename Ty<T>::Bits* p = static_cast<const typename Ty<T>::Bits*>(a.src[z]);
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const long long blocksC = (a.cols + 31) / 32, blocks = blocksC * ((a.rows + 31) / 32);
+  for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const long long r0 = b / blocksC * 32, c0 = b % blocksC * 32;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      const long long r = r0 + ty + i, c = c0 + tx;
+      const float v = r < a.rows && c < a.cols ? Ty<T>::widen(p[r * a.cols + c]) * by : 0.0f;
+      if (a.tall) {
+        tile[ty + i][tx] = v;
+      } else if (r < a.rows && c < a.cols) {
+        const long long at = z * a.size + r * a.ld + c;
+        split(v, a.x.hi[at], a.x.lo[at]);
+      }
+    }
+    if (a.tall) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        const long long r = c0 + ty + i, c = r0 + tx;  // of X
+        if (r < a.cols && c < a.rows) {
+          const long long at = z * a.size + r * a.ld + c;
+          split(tile[tx][ty + i], a.x.hi[at], a.x.lo[at]);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+struct OrthoPlan {
+  int parts;         // planes of the operands
+  size_t m, n;       // X: m <= n
+  size_t ldX, ldA, group;  // matrices per launch
+  size_t part, x[2][2], a[2], b[2], bytes;
+};
+
+bool make_plan(int count, size_t rows, size_t cols, int dtype, OrthoPlan* p) {
+  if (!op_elem_size(dtype) || count < 1 || rows < 1 || cols < 1 || rows > (1u << 24) ||
+      cols > (1u << 24))
+    return false;
+  p->parts = dtype == VR_BFLOAT16 ? 1 : 2;
+  p->m = std::min(rows, cols);
+  p->n = std::max(rows, cols);
+  p->ldX = up(p->n, 32);
+  p->ldA = up(p->m, 32);
+  p->group = std::min<size_t>(count, kMost);
+  size_t at = 0;
+  auto take = [&at](size_t n) {
+    const size_t here = at;
+    at += op_round(n);
+    return here;
+  };
+  p->part = take(p->group * kNormCtas * 4);
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j) p->x[i][j] = take(p->group * p->m * p->ldX * 2);
+  for (int j = 0; j < p->parts; ++j) p->a[j] = take(p->group * p->m * p->ldA * 2);
+  for (int j = 0; j < p->parts; ++j) p->b[j] = take(p->group * p->m * p->ldA * 2);
+  p->bytes = at;
+  return true;
+}
+
+// What moves from B's diagonal to the factor of X: X <- (a + d) X + (B - d I) X.
+// Near convergence A is near I and B near (b + c) I, so B - d I is small, and
+// with it what the roundings of B's and X's operands contribute (bf16 results
+// of decaying spectra: 1.7e-3 to 1.2e-3 before the last rounding, simulated
+// and measured).  Early steps keep d = 0: it would add roundings of X in the
+// small directions, which later steps amplify.
+float shift_of(const float* coefs, int steps, int k) {
+  const float at1 = coefs[3 * k + 1] + coefs[3 * k + 2];
+  return k + 1 == steps ? at1 : k + 2 == steps ? 0.5f * at1 : 0.0f;
+}
+
+// Whether every intermediate stays below what the planes hold (16) for any
+// matrix: the singular values start in [0, 1], and a step maps s to
+// a s + b s^3 + c s^5.
+bool in_range(const float* coefs, int steps) {
+  double top = 1.0;
+  for (int k = 0; k < steps; ++k) {
+    const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
+    const double reach = top * 1.01;  // roundings
+    double next = 0.0;
+    if (reach * reach > 15.0) return false;
+    for (int i = 0; i <= 512; ++i) {
+      const double s = reach * i / 512.0, q = s * s;
+      const double poly = b * q + c * q * q;
+      if (std::fabs(poly) > 15.0 || std::fabs(poly - shift_of(coefs, steps, k)) > 15.0)
+        return false;
+      next = std::max(next, std::fabs(s * (a + b * q + c * q * q)));
+    }
+    top = next;
+  }
+  return top <= 15.0;
+}
+
+constexpr float kCoefs[3] = {3.4445f, -4.7750f, 2.0315f};
+
+// The products of one step: `T` only names the result's type.
+template <int BN, int PARTS, bool BMN, class Epi>
+vr_result_t product(const OpDevice& dev, const Planes& a, size_t aLd, const Planes& b, size_t bLd,
+                    size_t M, size_t N, size_t K, size_t batch, bool triangle,
+                    typename Epi::Args& epi, void* stream) {
+  using Shape = GemmShape<BN, PARTS>;
+  const void* fn =
+      (const void*)gemm_kernel<__half, BN, PARTS, false, BMN, PARTS == 2 ? kSplitChunk : 0, Epi>;
+  GemmArgs g = {};
+  for (int i = 0; i < PARTS; ++i) {
+    vr_result_t e = gemm_operand(&g.a[i], i ? a.lo : a.hi, false, K, M, batch, aLd * 2,
+                                 aLd * 2 * M, kTileM);
+    if (e != VR_SUCCESS) return e;
+    e = gemm_operand(&g.b[i], i ? b.lo : b.hi, false, BMN ? N : K, BMN ? K : N, batch, bLd * 2,
+                     bLd * 2 * (BMN ? K : N), BMN ? kTileK : BN);
+    if (e != VR_SUCCESS) return e;
+  }
+  const vr_result_t e = gemm_prepare(fn, dev.device, Shape::kSmem);
+  if (e != VR_SUCCESS) return e;
+  g.M = (int)M;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.batch = (int)batch;
+  g.triangle = triangle;
+  g.status = dev.status;
+  g.timeoutNs = dev.timeoutNs;
+  const size_t tm = (M + kTileM - 1) / kTileM, tn = (N + BN - 1) / BN;
+  size_t tiles = tm * tn;
+  if (triangle) {
+    tiles = 0;
+    for (size_t i = 0; i < tm; ++i) tiles += i / (BN / kTileM) + 1;
+  }
+  tiles *= batch;
+  void* args[] = {&g, &epi};
+  return op_launch(fn, dim3((unsigned)std::min<size_t>(tiles, dev.sms)), dim3(kGemmThreads), args,
+                   Shape::kSmem, stream);
+}
+
+template <typename T, int PARTS>
+vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src, void* const* dst,
+                int count, size_t rows, size_t cols, int steps, const float* coefs, float eps,
+                float scale, char* w, void* stream) {
+  const bool tall = rows > cols;
+  auto plane = [w](size_t at) { return reinterpret_cast<__half*>(w + at); };
+  const Planes x[2] = {{plane(p.x[0][0]), plane(p.x[0][1])}, {plane(p.x[1][0]), plane(p.x[1][1])}};
+  const Planes A = {plane(p.a[0]), PARTS == 2 ? plane(p.a[1]) : nullptr};
+  const Planes B = {plane(p.b[0]), PARTS == 2 ? plane(p.b[1]) : nullptr};
+  const long long sizeX = (long long)(p.m * p.ldX), sizeA = (long long)(p.m * p.ldA);
+  LoadArgs la = {};
+  la.rows = (long long)rows;
+  la.cols = (long long)cols;
+  la.part = reinterpret_cast<float*>(w + p.part);
+  la.eps = eps;
+  la.tall = tall;
+  la.x = x[0];
+  la.ld = (long long)p.ldX;
+  la.size = sizeX;
+  typename ApplyEpilogue<T>::Args ap = {};
+  ap.vec = cols % Ty<T>::U == 0;
+  for (int i = 0; i < count; ++i) {
+    la.src[i] = src[i];
+    ap.out[i] = static_cast<T*>(dst[i]);
+    if ((uintptr_t)dst[i] & 15) ap.vec = 0;
+  }
+  la.ctas = (int)std::max<size_t>(1, std::min<size_t>(kNormCtas, rows * cols / 8192));
+  void* args[] = {&la};
+  vr_result_t e = op_launch((const void*)ortho_norm_kernel<T>, dim3(la.ctas, count), dim3(256),
+                            args, 0, stream);
+  if (e != VR_SUCCESS) return e;
+  const size_t blocks = (rows + 31) / 32 * ((cols + 31) / 32);
+  e = op_launch((const void*)ortho_load_kernel<T>,
+                dim3((unsigned)std::min<size_t>(blocks, (size_t)dev.sms * 8), count), dim3(256),
+                args, 0, stream);
+  if (e != VR_SUCCESS) return e;
+  for (int k = 0; k < steps; ++k) {
+    const float a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
+    const Planes& from = x[k % 2];
+    const float shift = shift_of(coefs, steps, k);
+    SymmetricEpilogue::Args ga = {{nullptr, nullptr}, A, (long long)p.ldA, sizeA, 0.0f,
+                                  1.0f / kScale, 0.0f, PARTS == 2};
+    if ((e = product<128, PARTS, false, SymmetricEpilogue>(dev, from, p.ldX, from, p.ldX, p.m, p.m,
+                                                           p.n, count, true, ga, stream)) !=
+        VR_SUCCESS)
+      return e;
+    SymmetricEpilogue::Args pa = {A, B, (long long)p.ldA, sizeA, b, c / kScale, shift * kScale,
+                                  PARTS == 2};
+    if ((e = product<128, PARTS, false, SymmetricEpilogue>(dev, A, p.ldA, A, p.ldA, p.m, p.m, p.m,
+                                                           count, true, pa, stream)) != VR_SUCCESS)
+      return e;
+    ap.from = from;
+    ap.to = x[1 - k % 2];
+    ap.ld = (long long)p.ldX;
+    ap.size = sizeX;
+    ap.byFrom = a + shift;
+    ap.byAcc = 1.0f / kScale;
+    ap.last = k + 1 == steps;
+    ap.tall = tall;
+    ap.byOut = scale / kScale;
+    ap.cols = (int)p.n;
+    if ((e = product<128, PARTS, true, ApplyEpilogue<T>>(dev, B, p.ldA, from, p.ldX, p.m, p.n, p.m,
+                                                         count, false, ap, stream)) != VR_SUCCESS)
+      return e;
+  }
+  return VR_SUCCESS;
+}
+
+}  // namespace
+}  // namespace vr
+
+using namespace vr;
+
+extern "C" {
+
+vr_result_t vr_orthogonalize_workspace_bytes(int count, size_t rows, size_t cols, vr_dtype_t dtype,
+                                             size_t* bytes) {
+  OrthoPlan p = {};
+  if (!bytes || !make_plan(count, rows, cols, dtype, &p)) return VR_ERR_INVALID_ARGUMENT;
+  *bytes = p.bytes;
+  return VR_SUCCESS;
+}
+
+vr_result_t vr_orthogonalize(const void* const* src, void* const* dst, int count, size_t rows,
+                             size_t cols, vr_dtype_t dtype, int steps, const float* coefs,
+                             float eps, float scale, void* workspace, size_t workspaceBytes,
+                             void* stream) {
+  OrthoPlan p = {};
+  if (!make_plan(count, rows, cols, dtype, &p) || !src || !dst || steps < 1 || steps > 32 ||
+      !(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(scale) || !workspace ||
+      workspaceBytes < p.bytes || ((uintptr_t)workspace & 15))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t E = op_elem_size(dtype), bytes = rows * cols * E;
+  float use[3 * 32];
+  for (int k = 0; k < 3 * steps; ++k) {
+    use[k] = coefs ? coefs[k] : kCoefs[k % 3];
+    if (!std::isfinite(use[k])) return VR_ERR_INVALID_ARGUMENT;
+  }
+  for (int i = 0; i < count; ++i)
+    if (!src[i] || !dst[i] || ((uintptr_t)src[i] | (uintptr_t)dst[i]) % E)
+      return VR_ERR_INVALID_ARGUMENT;
+  if (!op_lists_ok(src, dst, count, bytes, workspace, workspaceBytes))
+    return VR_ERR_INVALID_ARGUMENT;
+  if (!in_range(use, steps)) return VR_ERR_UNSUPPORTED;
+  OpDevice dev;
+  vr_result_t e = op_device(&dev);
+  char* w = static_cast<char*>(workspace);
+  for (int at = 0; at < count && e == VR_SUCCESS; at += kMost) {
+    const int n = std::min(kMost, count - at);
+    e = dtype == VR_FLOAT32 ? run<float, 2>(p, dev, src + at, dst + at, n, rows, cols, steps, use,
+                                            eps, scale, w, stream)
+        : dtype == VR_FLOAT16
+            ? run<__half, 2>(p, dev, src + at, dst + at, n, rows, cols, steps, use, eps, scale, w,
+                             stream)
+            : run<__nv_bfloat16, 1>(p, dev, src + at, dst + at, n, rows, cols, steps, use, eps,
+                                    scale, w, stream);
+  }
+  return e;
+}
+
+}  // extern "C"

@@ -27,6 +27,9 @@ namespace vr {
 namespace {
 
 constexpr int kBN = 256;
+// The losses are fp32 results: their logits are summed in chunks of 512.
+// (The gradients' roundings to 16 bits are far above the truncation.)
+constexpr int kStatsChunk = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Device-side results of the preparation.
@@ -78,13 +81,15 @@ struct StatsEpilogue {
     float2* parts;      // [T][nParts]
     int nParts;
   };
+  template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
-                                             int row, int col0, int cols, int M, const Acc& acc) {
+                                             int row, int col0, int M, const Acc& acc) {
     const int t = o.m0 + row;
     const int first = o.n0 + col0;
     const int at = t < M ? a.target[t] - first : -1;
     float top = -INFINITY, sum = 0.0f;
-    for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
       if (first + c >= g.N) break;
       float v[32];
       acc(col0 + c, v);
@@ -105,7 +110,7 @@ struct StatsEpilogue {
       for (int i = 0; i < 32; ++i) sum += exp2_fast(fmaf(v[i], kLog2e, -base));
       top = next;
     }
-    acc.pick(at >= 0 && at < cols ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
+    acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
     if (t < M) a.parts[(long long)t * a.nParts + first / (kBN / 2)] = make_float2(top, sum);
   }
 };
@@ -120,14 +125,16 @@ struct FactorEpilogue {
     long long ld;
     int v0;              // the piece's first row of the vocabulary
   };
+  template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
-                                             int row, int col0, int cols, int M, const Acc& acc) {
+                                             int row, int col0, int M, const Acc& acc) {
     const int t = o.m0 + row;
     const bool live = t < M;
     const float sub = live ? (float)kShift<T> - a.lse2[t] : 0.0f;
     const int at = live ? a.target[t] - a.v0 - o.n0 - col0 : -1;
     T* out = a.out + (long long)t * a.ld + o.n0 + col0;
-    for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
       if (o.n0 + col0 + c >= g.N) break;
       float v[32];
       acc(col0 + c, v);
@@ -137,7 +144,7 @@ struct FactorEpilogue {
       store32(out + c, v, 32, true);
     }
     // the target's factor over the one just written by the same thread
-    acc.pick(at >= 0 && at < cols ? col0 + at : -1, [&](float x) {
+    acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) {
       const float p = exp2_fast(fmaf(x, kLog2e, sub)) - (float)(1 << kShift<T>);
       reinterpret_cast<typename Ty<T>::Bits*>(out)[at] = Ty<T>::narrow(p);
     });
@@ -155,13 +162,15 @@ struct HiddenEpilogue {
     const XentState* state;
     int first, last, vec;
   };
+  template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
-                                             int row, int col0, int cols, int M, const Acc& acc) {
+                                             int row, int col0, int M, const Acc& acc) {
     const int t = o.m0 + row;
     const bool live = t < M;
     const float scale = a.last ? a.state->gradScale : 0.0f;
     T* out = a.out + (a.last && live ? (long long)a.token[t] * g.N : 0);
-    for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
       const int n = o.n0 + col0 + c;
       if (n >= g.N) break;
       float v[32];
@@ -196,11 +205,13 @@ struct WeightEpilogue {
     const XentState* state;
     int vec;
   };
+  template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
-                                             int row, int col0, int cols, int M, const Acc& acc) {
+                                             int row, int col0, int M, const Acc& acc) {
     const int v0 = o.m0 + row;
     const float scale = a.state->gradScale;
-    for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
       const int n = o.n0 + col0 + c;
       if (n >= g.N) break;
       float v[32];
@@ -439,12 +450,12 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
 }
 
 // One product: the operands' extents and layouts, the launch.
-template <typename T, bool AMN, bool BMN, class Epi>
+template <typename T, bool AMN, bool BMN, int CHUNK, class Epi>
 vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* b, size_t bLd,
                     size_t M, size_t N, size_t K, const int* dynM, const int* dynK,
                     typename Epi::Args& epi, void* stream) {
   using Shape = GemmShape<kBN, 1>;
-  const void* fn = (const void*)gemm_kernel<T, kBN, 1, AMN, BMN, Epi>;
+  const void* fn = (const void*)gemm_kernel<T, kBN, 1, AMN, BMN, CHUNK, Epi>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   GemmArgs g = {};
   vr_result_t e = gemm_operand(&g.a[0], a, bf16, AMN ? M : K, AMN ? K : M, 1, aLd * 2,
@@ -502,7 +513,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   if (p.T && p.padWeight && (e = pad(&weight, &weightStride, p.V, p.weight)) != VR_SUCCESS) return e;
   if (p.T) {
     StatsEpilogue::Args epi = {target, targetLogit, parts, (int)p.nParts};
-    if ((e = product<T, false, false, StatsEpilogue>(dev, hidden, hiddenStride, weight,
+    if ((e = product<T, false, false, kStatsChunk, StatsEpilogue>(dev, hidden, hiddenStride, weight,
                                                      weightStride, p.T, p.V, p.D, nullptr, nullptr,
                                                      epi, stream)) != VR_SUCCESS)
       return e;
@@ -548,7 +559,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
     typename FactorEpilogue<T>::Args fa = {packedTarget, packedLse2, factors, (long long)p.piece,
                                            (int)v0};
-    if ((e = product<T, false, false, FactorEpilogue<T>>(
+    if ((e = product<T, false, false, 0, FactorEpilogue<T>>(
              dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
              stream)) != VR_SUCCESS)
       return e;
@@ -556,7 +567,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
       typename HiddenEpilogue<T>::Args ha = {
           reinterpret_cast<float*>(w + p.sum), (long long)p.sumLd, static_cast<T*>(dHidden), token,
           state, i == 0, i + 1 == p.nPieces, vecH};
-      if ((e = product<T, false, true, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
+      if ((e = product<T, false, true, 0, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
                                                           weightStride, p.T, p.D, rows,
                                                           &state->valid, nullptr, ha, stream)) !=
           VR_SUCCESS)
@@ -564,7 +575,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     }
     if (dWeight) {
       typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, vecW};
-      if ((e = product<T, true, true, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
+      if ((e = product<T, true, true, 0, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
                                                          p.D, p.T128, nullptr, &state->valid, wa,
                                                          stream)) != VR_SUCCESS)
         return e;

@@ -502,6 +502,33 @@ vr_result_t vr_balance_loss(const void* const* logits, size_t rowStride,
                             int* counts, int* const* chosen, void* const* dlogits,
                             void* workspace, size_t workspaceBytes, void* stream);
 
+/* Matrices of one shape orthogonalised by Newton-Schulz steps, the update an
+ * optimiser makes of summed gradients: with X = src / (|src|_F + eps),
+ * transposed when rows > cols,
+ *   steps times: A = X X^T, X <- a X + (b A + c A A) X
+ * and dst = scale * X (transposed back).  Each matrix by itself.
+ * src, dst: `count` pointers to contiguous rows x cols matrices of dtype;
+ * dst[i] may be src[i].  coefs: NULL (3.4445, -4.775, 2.0315 in every step) or
+ * 3 * steps floats on the host, a, b, c of each step.
+ * The norm is an fp32 sum of squares (entries beyond about 1e18 overflow
+ * it); a zero matrix gives zeros (with eps = 0: NaN), NaN or an infinity a
+ * matrix of NaN.  Products are summed in fp32; X is held to 22 bits between
+ * the steps.  bf16 results take products of operands rounded to 11 bits (an
+ * error below the result's own rounding), fp16 and fp32 results of operands
+ * of 22 bits (about three times the time).
+ * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, rows or cols outside
+ * [1, 2^24], steps outside [1, 32], eps negative, or eps, scale or a
+ * coefficient not finite, a NULL or misaligned buffer, an overlap or a short
+ * workspace; VR_ERR_UNSUPPORTED for coefficients under which singular values
+ * starting in [0, 1] can leave the range the operands hold (|X|, |X X^T| and
+ * |b A + c A A| up to 15). */
+vr_result_t vr_orthogonalize_workspace_bytes(int count, size_t rows, size_t cols,
+                                             vr_dtype_t dtype, size_t* bytes);
+vr_result_t vr_orthogonalize(const void* const* src, void* const* dst, int count, size_t rows,
+                             size_t cols, vr_dtype_t dtype, int steps, const float* coefs,
+                             float eps, float scale, void* workspace, size_t workspaceBytes,
+                             void* stream);
+
 /* ---------------------------------------------------------- cost model
  * The pages' alpha-beta model ([Course13] "理想成本模型"; [Interview]
  * "推导 / 关键公式"), with N ranks, tree depth D (the deeper of the two

@@ -121,3 +121,38 @@ def norm_error(got, want):
     n = float(want.norm())
     d = float((got.double() - want).norm())
     return d / n if n else d
+
+
+COEFS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(m, steps, coefs, eps, scale):
+    x = m.double()
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.t()
+    x = x / (x.norm() + eps)
+    for k in range(steps):
+        # the coefficients reach the operator as fp32
+        a, b, c = (float(torch.tensor(v, dtype=torch.float32)) for v in
+                   (coefs[3 * k:3 * k + 3] if coefs is not None else COEFS))
+        g = x @ x.t()
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return scale * (x.t() if tall else x)
+
+
+def ortho_tolerance(ty, norm, gain):
+    """2-norm of the error over that of the result.  X is held to 22 bits: a
+    rounding of X (norm 1), amplified by at most `gain` (the product of the
+    steps' a) in the directions of the smallest singular values, next to the
+    norm of the result, and the
+    chunks' sums (32 additions truncated to 2^-23 each, both ways).  fp16
+    and bf16: the result's own rounding on top of that; bf16 operands are
+    rounded to 2^-12 on average three times a step and scaled by
+    |b A + c A A| <= 2.8."""
+    exact = 2.0 ** -23 * (gain / norm + 64)
+    if ty == torch.float32:
+        return exact
+    if ty == torch.float16:
+        return exact + 2.0 ** -11
+    return exact + 2.0 ** -9 + 2.0 ** -9

@@ -87,3 +87,41 @@ def test_linear_xent_workspace():
     # the gradient factors are taken in pieces: the workspace does not hold
     # tokens x vocab of them
     assert size(A, 64, A, 64, 1 << 16, 64, 1 << 17, B, 1) < (1 << 33)
+
+
+def ortho_args(**kw):
+    a = dict(src=[A, A + STEP], dst=[A + 2 * STEP, A + 3 * STEP], count=2, rows=40, cols=60,
+             dtype=vr.VR_BFLOAT16, steps=2, coefs=None, eps=1e-7, scale=1.0,
+             workspace=A + 4 * STEP, workspaceBytes=4 << 20)
+    a.update(kw)
+    return list(a.values())
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("bad", [
+    dict(count=0), dict(rows=0), dict(cols=0), dict(rows=1 << 25), dict(cols=1 << 62),
+    dict(dtype=5), dict(steps=0), dict(steps=33), dict(eps=-1.0), dict(eps=NAN), dict(scale=INF),
+    dict(coefs=[1.5, NAN, 0.0] * 2), dict(coefs=[1.0] * 5), dict(src=None), dict(dst=None),
+    dict(src=[A, 0]), dict(dst=[0, A]), dict(src=[A + 1, A + STEP]), dict(workspace=0),
+    dict(workspace=A + 4 * STEP + 8), dict(workspaceBytes=1000),
+    dict(dst=[A + 2 * STEP, A + 2 * STEP + 64]), dict(dst=[A + STEP, A + 3 * STEP]),
+    dict(dst=[A + 16, A + 3 * STEP]), dict(workspace=A + 1024),
+])
+def test_orthogonalize_refusals(bad):
+    assert code(vr.vr_orthogonalize, *ortho_args(**bad)) == INV
+
+
+def test_orthogonalize_refuses_coefficients_that_leave_the_range():
+    assert code(vr.vr_orthogonalize, *ortho_args(coefs=[20.0, 0.0, 0.0] * 2)) == UNS
+    assert code(vr.vr_orthogonalize, *ortho_args(steps=3, coefs=[3.0, 0.0, 0.0] * 3)) == UNS
+    assert code(vr.vr_orthogonalize, *ortho_args(coefs=[1.0, -16.0, 0.0] * 2)) == UNS
+
+
+def test_orthogonalize_workspace():
+    size = vr.vr_orthogonalize_workspace_bytes
+    assert code(size, 0, 8, 8, vr.VR_FLOAT32) == INV
+    assert size(1, 64, 32, vr.VR_FLOAT32) == size(1, 32, 64, vr.VR_FLOAT32)
+    # launches take at most 64 matrices, one after the other
+    assert size(200, 64, 64, vr.VR_BFLOAT16) == size(64, 64, 64, vr.VR_BFLOAT16)
