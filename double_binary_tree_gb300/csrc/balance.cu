@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,7 +45,6 @@ struct BalanceArgs {
   int* chosen[kMaxRanks];
   void* dlogits[kMaxRanks];
   long long tokens;  // per rank
-  unsigned long long divTokens;  // t / tokens = high 64 bits of divTokens * t (0: tokens = 1)
   long long stride;  // elements between rows
   long long total;   // tokens of all ranks
   int E, topK, ctas;
@@ -52,7 +52,10 @@ struct BalanceArgs {
   float* loss;
   int* counts;
   // workspace
-  float* lse;       // [total]; +inf: the token does not count
+  // [total] maximum and reciprocal sum of exponentials (apart: joined as a log
+  // sum, a row at the type's lowest value would lose the sum); (0, 0): the
+  // token does not count
+  float2* softmax;
   float* probPart;  // [ctas][E]
   int* countPart;   // [ctas][E]
   int* validPart;   // [ctas]
@@ -68,16 +71,22 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  if constexpr (G == 32) return __reduce_max_sync(0xffffffffu, v);
+  if constexpr (G == 32) {
+    v = __reduce_max_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = G / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = G / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  }
   return v;
 }
 template <int G>
 __device__ __forceinline__ uint32_t group_min(uint32_t v) {
-  if constexpr (G == 32) return __reduce_min_sync(0xffffffffu, v);
+  if constexpr (G == 32) {
+    v = __reduce_min_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = G / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = G / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+  }
   return v;
 }
 template <int G>
@@ -86,62 +95,98 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = G / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-template <int G>
-__device__ __forceinline__ float group_maxf(float v) {
-#pragma unroll
-  for (int o = G / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 // Logit j of chunk c of lane l: expert (c G + l) VEC + j.
 template <int VEC, int G>
 __device__ __forceinline__ int expert_of(int c, int l, int j) {
   return (c * G + l) * VEC + j;
 }
 
-// A row's logits as loaded; absent experts are -inf when they are widened.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A row's logits as loaded.  Absent experts are -inf: no probability, and
+// never chosen, since equal logits go to the lower index and topK <= E.
 template <typename T, int VEC, int CHUNKS>
 struct RawRow {
-  typename Select<(VEC > 1), uint4, typename Ty<T>::Bits>::type q[CHUNKS];
+  using Load = typename Select<(VEC > 1), uint4, typename Ty<T>::Bits>::type;
+  Load q[CHUNKS];
 };
-struct Place {
-  int rank;
-  long long row;
-};
-__device__ __forceinline__ Place place_of(const BalanceArgs& a, long long t) {
-  Place p;
-  p.rank = a.divTokens ? (int)__umul64hi(a.divTokens, (unsigned long long)t) : (int)t;
-  p.row = t - (long long)p.rank * a.tokens;
-  return p;
+template <typename T>
+__device__ __forceinline__ uint32_t minus_inf() {
+  return sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
 }
+__device__ __forceinline__ void fill(uint4& q, uint32_t v) { q = make_uint4(v, v, v, v); }
+__device__ __forceinline__ void fill(uint32_t& q, uint32_t v) { q = v; }
+__device__ __forceinline__ void fill(uint16_t& q, uint32_t v) { q = (uint16_t)v; }
+
+// A token: its rank and row, walked in steps without a division.
+struct Place {
+  long long t, step;
+  int rank, row, stepRanks, stepRows;
+  __device__ __forceinline__ Place(const BalanceArgs& a, long long first, long long by)
+      : t(first), step(by) {
+    const unsigned n = (unsigned)a.tokens;  // below 2^31, as t and the step
+    rank = (int)((unsigned)first / n);
+    row = (int)((unsigned)first % n);
+    stepRanks = (int)((unsigned)by / n);
+    stepRows = (int)((unsigned)by % n);
+  }
+  __device__ __forceinline__ void advance(const BalanceArgs& a) {
+    t += step;
+    rank += stepRanks;
+    row += stepRows;  // both below tokens <= 2^31 - 1
+    if ((unsigned)row >= (unsigned)a.tokens) row = (int)((unsigned)row - (unsigned)a.tokens), ++rank;
+  }
+  __device__ __forceinline__ bool real(const BalanceArgs& a) const { return t < a.total; }
+};
 template <typename T, int VEC, int CHUNKS, int G>
 __device__ __forceinline__ RawRow<T, VEC, CHUNKS> load_row(const BalanceArgs& a, const Place& at,
                                                            int l) {
-  using Bits = typename Ty<T>::Bits;
-  const Bits* p = static_cast<const Bits*>(a.logits[at.rank]) + at.row * a.stride;
-  RawRow<T, VEC, CHUNKS> r = {};
+  using Row = RawRow<T, VEC, CHUNKS>;
+  Row r;
+  const bool real = at.real(a);
+  const typename Ty<T>::Bits* p =
+      static_cast<const typename Ty<T>::Bits*>(a.logits[real ? at.rank : 0]) + at.row * a.stride;
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     const int e0 = expert_of<VEC, G>(c, l, 0);  // with VEC > 1, E is a multiple of VEC
-    if (e0 < a.E)
-      r.q[c] = *reinterpret_cast<const typename Select<(VEC > 1), uint4, Bits>::type*>(p + e0);
+    fill(r.q[c], minus_inf<T>());
+    if (real && e0 < a.E) r.q[c] = *reinterpret_cast<const typename Row::Load*>(p + e0);
   }
   return r;
 }
-template <typename T, int VEC, int CHUNKS, int G>
-__device__ __forceinline__ typename Ty<T>::Bits raw_bits(const RawRow<T, VEC, CHUNKS>& r, int i) {
-  return reinterpret_cast<const typename Ty<T>::Bits*>(&r.q[i / VEC])[i % VEC];
+template <typename T, int VEC, int CHUNKS>
+__device__ __forceinline__ float raw_value(const RawRow<T, VEC, CHUNKS>& r, int i) {
+  return Ty<T>::widen(reinterpret_cast<const typename Ty<T>::Bits*>(&r.q[i / VEC])[i % VEC]);
 }
-template <typename T, int VEC, int CHUNKS, int G>
-__device__ __forceinline__ float raw_value(const BalanceArgs& a, const RawRow<T, VEC, CHUNKS>& r,
-                                           int l, int i) {
-  return expert_of<VEC, G>(i / VEC, l, i % VEC) < a.E
-             ? Ty<T>::widen(raw_bits<T, VEC, CHUNKS, G>(r, i))
-             : -INFINITY;
+// Two 16-bit logits as order keys.  Adding zero makes -0 +0 and every NaN
+// 0x7fff; then a negative value's bits are inverted, a positive one's sign set.
+template <typename T>
+__device__ __forceinline__ uint32_t order_keys2(uint32_t b) {
+  if (std::is_same<T, __half>::value) {
+    const __half2 v = __hadd2(*reinterpret_cast<__half2*>(&b), __float2half2_rn(0.0f));
+    b = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v =
+        __hadd2(*reinterpret_cast<__nv_bfloat162*>(&b), __float2bfloat162_rn(0.0f));
+    b = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return b ^ (((b >> 15 & 0x00010001u) * 0x7fffu) | 0x80008000u);
+}
+// The logit that a key stands for.
+template <typename T>
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if (sizeof(T) == 4) return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+  const uint32_t h = k >> 16;
+  return Ty<T>::widen((typename Ty<T>::Bits)(h & 0x8000u ? h & 0x7fffu : h ^ 0xffffu));
 }
 
-// The first pass of one CTA: sAcc and sCount get its sums, validOut its
-// tokens that count.
+// The first pass of one CTA: sAcc and sCount get its sums, sValid its tokens
+// that count.
 template <typename T, int VEC, int CHUNKS, int G, int THREADS>
 __device__ __forceinline__ void stats_pass(const BalanceArgs& a, float* sAcc, int* sCount,
                                            int* sValid) {
@@ -154,67 +199,43 @@ __device__ __forceinline__ void stats_pass(const BalanceArgs& a, float* sAcc, in
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   int valid = 0;
   // Whole warps stay in the loop together (the shuffles name all lanes); a
-  // group without a token left repeats the last one and discards it.
+  // group without a token left works on a row of -inf.
   const long long step = (long long)gridDim.x * GROUPS;
-  const int inWarp = group % (32 / G);
-  const long long first = (long long)blockIdx.x * GROUPS + (group - inWarp);
-  auto clamp = [&](long long t) { return t < a.total ? t : a.total - 1; };
-  RawRow<T, VEC, CHUNKS> next = {};
-  if (first < a.total) next = load_row<T, VEC, CHUNKS, G>(a, place_of(a, clamp(first + inWarp)), l);
-  for (long long w = first; w < a.total; w += step) {
-    const bool real = w + inWarp < a.total;
-    const long long t = clamp(w + inWarp);
-    const Place at = place_of(a, t);
+  Place at(a, (long long)blockIdx.x * GROUPS + group, step);
+  long long warpAt = at.t - group % (32 / G);
+  auto kept_of = [&](const Place& p) -> bool {
+    const bool real = p.real(a);
+    const unsigned char* m = real ? a.mask[p.rank] : nullptr;
+    return real && (!m || m[p.row] != 0);
+  };
+  RawRow<T, VEC, CHUNKS> next = load_row<T, VEC, CHUNKS, G>(a, at, l);
+  bool nextKept = kept_of(at);
+  for (; warpAt < a.total; warpAt += step) {
+    const Place here = at;
     const RawRow<T, VEC, CHUNKS> raw = next;
-    if (w + step < a.total)
-      next = load_row<T, VEC, CHUNKS, G>(a, place_of(a, clamp(w + step + inWarp)), l);
-    const bool kept = !a.mask[at.rank] || a.mask[at.rank][at.row] != 0;
+    const bool kept = nextKept;
+    at.advance(a);
+    next = load_row<T, VEC, CHUNKS, G>(a, at, l);
+    nextKept = kept_of(at);
 
-    // softmax statistics in fp32
-    float p[VPL], top = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      p[i] = raw_value<T, VEC, CHUNKS, G>(a, raw, l, i);
-      top = fmaxf(top, p[i]);
-      nan |= p[i] != p[i];
-    }
     uint32_t key[VPL];
+    if (PACKED && VEC > 1) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = expert_of<VEC, G>(i / VEC, l, i % VEC);
-      if (PACKED) {
-        // 16-bit order key above the complement of the index
-        const uint32_t b = raw_bits<T, VEC, CHUNKS, G>(raw, i);
-        uint32_t k = b & 0x8000u ? b ^ 0xffffu : b | 0x8000u;
-        if (b == 0x8000u) k = 0x8000u;  // -0 as +0
-        if (p[i] != p[i]) k = 0xffffu;
-        key[i] = e < a.E ? k << 16 | (0xffffu - (uint32_t)e) : 0u;
-      } else {
-        key[i] = e < a.E ? order_key(p[i]) : 0u;
+      for (int i = 0; i < VPL; i += 2) {
+        const uint32_t k = order_keys2<T>(reinterpret_cast<const uint32_t*>(&raw.q[i / VEC])[i % VEC / 2]);
+        const uint32_t e = 0xffffu - (uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC);
+        key[i] = k << 16 | e;
+        key[i + 1] = (k & 0xffff0000u) | (e - 1);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const uint32_t e = (uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC);
+        key[i] = PACKED ? order_keys2<T>((uint32_t) * reinterpret_cast<const typename Ty<T>::Bits*>(
+                              &raw.q[i])) << 16 | (0xffffu - e)
+                        : order_key(raw_value(raw, i));
       }
     }
-    top = group_maxf<G>(top);
-    nan = __ballot_sync(0xffffffffu, nan) & ((G == 32 ? 0xffffffffu : (1u << (G % 32)) - 1)
-                                             << (G == 32 ? 0 : inWarp * G));
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      p[i] = __expf(p[i] - top);
-      sum += p[i];
-    }
-    sum = group_sum<G>(sum);
-    // a row whose logits are all -inf has no softmax: it does not count
-    const bool live = real && kept && (nan || top != -INFINITY);
-    if (live) {
-      const float inv = __fdividef(1.0f, sum);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
-      valid += l == 0;
-    }
-    if (real && l == 0) a.lse[t] = live ? top + __logf(sum) : INFINITY;
-
-    // topK rounds: the largest key left, the lowest index of equals
     if (SORTED) {
       // the lane's words in descending order (19 comparisons)
       constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6},
@@ -227,44 +248,73 @@ __device__ __forceinline__ void stats_pass(const BalanceArgs& a, float* sAcc, in
         key[net[c][1] % VPL] = min(x, y);
       }
     }
-    int mine = -1;
-    for (int r = 0; r < a.topK; ++r) {
-      uint32_t at32, best = key[0];
+    auto largest = [&]() {
+      uint32_t best = key[0];
       if (!SORTED) {
 #pragma unroll
         for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
       }
-      best = group_max<G>(best);
-      if (SORTED) {
-        const bool won = key[0] == best;
+      return group_max<G>(best);
+    };
+    uint32_t best = largest();
+
+    // softmax statistics in fp32; the largest key is the maximum (or NaN)
+    const float top = key_value<T>(best);
+    float p[VPL], sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i + 1 < VPL; ++i) key[i] = won ? key[i + 1] : key[i];
-        if (won) key[VPL - 1] = 0u;
-      } else if (PACKED) {
+    for (int i = 0; i < VPL; ++i) {
+      p[i] = exp2_fast((raw_value(raw, i) - top) * kLog2e);
+      sum += p[i];
+    }
+    sum = group_sum<G>(sum);
+    // a row whose logits are all -inf has no softmax: it does not count
+    const bool live = kept && top != -INFINITY;
+    const float inv = __fdividef(1.0f, sum);
+    if (live) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (key[i] == best) key[i] = 0u;
-      }
+      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
+      valid += l == 0;
+    }
+    if (here.real(a) && l == 0)
+      a.softmax[here.t] = live ? make_float2(top, inv) : make_float2(0.0f, 0.0f);
+
+    // topK rounds: the largest key left, the lowest index of equals
+    int mine = -1;
+    for (int r = 0;;) {
+      uint32_t chosen;
       if (PACKED) {
-        at32 = 0xffffu - (best & 0xffffu);
+        chosen = 0xffffu - (best & 0xffffu);
+        if (SORTED) {
+          const bool won = key[0] == best;
+#pragma unroll
+          for (int i = 0; i + 1 < VPL; ++i) key[i] = won ? key[i + 1] : key[i];
+          if (won) key[VPL - 1] = 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) key[i] = key[i] == best ? 0u : key[i];
+        }
       } else {
-        at32 = 0xffffffffu;
+        chosen = 0xffffffffu;
 #pragma unroll
         for (int i = VPL - 1; i >= 0; --i)
-          if (key[i] == best) at32 = (uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC);
-        at32 = group_min<G>(at32);
+          if (key[i] == best) chosen = (uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC);
+        chosen = group_min<G>(chosen);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-          if ((uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC) == at32) key[i] = 0u;
+          if ((uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC) == chosen) key[i] = 0u;
       }
-      if (l == r % G) mine = (int)at32;
-      if (r % G == G - 1 || r == a.topK - 1) {
-        if (real && l <= r % G) {
+      if (l == r % G) mine = (int)chosen;
+      ++r;
+      if (r % G == 0 || r == a.topK) {
+        const int from = (r - 1) / G * G;
+        if (here.real(a) && from + l < r) {
           if (live) atomicAdd(&sCount[mine], 1);
-          int* out = a.chosen[at.rank];
-          if (out) out[at.row * a.topK + (r - r % G) + l] = live ? mine : -1;
+          int* out = a.chosen[here.rank];
+          if (out) out[(long long)here.row * a.topK + from + l] = live ? mine : -1;
         }
+        if (r == a.topK) break;
       }
+      best = largest();
     }
   }
   if (valid) atomicAdd(sValid, valid);
@@ -322,60 +372,79 @@ __device__ __forceinline__ float shares(const BalanceArgs& a, int valid, float* 
   return a.coef * (float)a.E * perToken * a.gradScale;
 }
 
-// The second pass of one CTA.
+// Values rounded to T in the layout of a load.
+template <typename T, int VEC>
+__device__ __forceinline__ void store_chunk(typename Ty<T>::Bits* out, const float* v) {
+  if constexpr (VEC == 8) {
+    uint4 q;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(out) = q;
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    out[0] = Ty<T>::narrow(v[0]);
+  }
+}
+
+// The second pass of one CTA: dx = p (F - sum F p), F = factor f.
 template <typename T, int VEC, int CHUNKS, int G, int THREADS>
 __device__ __forceinline__ void grad_pass(const BalanceArgs& a, const float* sShare, float factor) {
-  using Bits = typename Ty<T>::Bits;
   constexpr int VPL = VEC * CHUNKS, GROUPS = THREADS / G;
   constexpr int TOK = VPL > 8 ? 1 : 2;  // tokens of a group in flight
-  const int l = threadIdx.x % G, group = threadIdx.x / G, inWarp = group % (32 / G);
+  const int l = threadIdx.x % G, group = threadIdx.x / G;
   float f[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = expert_of<VEC, G>(i / VEC, l, i % VEC);
-    f[i] = e < a.E ? sShare[e] : 0.0f;
+    f[i] = e < a.E ? factor * sShare[e] : 0.0f;
   }
   const long long step = (long long)gridDim.x * GROUPS;
-  const long long first = (long long)blockIdx.x * GROUPS + (group - inWarp);
-  for (long long w0 = first; w0 < a.total; w0 += TOK * step) {
+  Place at(a, (long long)blockIdx.x * GROUPS + group, step);
+  for (long long warpAt = at.t - group % (32 / G); warpAt < a.total; warpAt += TOK * step) {
     RawRow<T, VEC, CHUNKS> raw[TOK];
-    float lse[TOK];
-    Place at[TOK];
-    bool real[TOK];
+    float2 sm[TOK];
+    typename Ty<T>::Bits* out[TOK];
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
-      const long long want = w0 + k * step + inWarp;
-      real[k] = want < a.total;
-      const long long t = real[k] ? want : a.total - 1;
-      at[k] = place_of(a, t);
-      raw[k] = load_row<T, VEC, CHUNKS, G>(a, at[k], l);
-      lse[k] = a.lse[t];
+      raw[k] = load_row<T, VEC, CHUNKS, G>(a, at, l);
+      out[k] = nullptr;
+      sm[k] = make_float2(0.0f, 0.0f);
+      if (at.real(a)) {
+        sm[k] = a.softmax[at.t];
+        out[k] = static_cast<typename Ty<T>::Bits*>(a.dlogits[at.rank]) + at.row * a.stride;
+      }
+      at.advance(a);
     }
 #pragma unroll
     for (int k = 0; k < TOK; ++k) {
-      const bool live = lse[k] != INFINITY;
+      if (sm[k].y == 0.0f) {  // does not count: whatever it holds, p = 0
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) fill(raw[k].q[c], 0u);
+      }
       float x[VPL], dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const float v = raw_value<T, VEC, CHUNKS, G>(a, raw[k], l, i);
-        x[i] = live ? __expf(v - lse[k]) : 0.0f;
+        x[i] = exp2_fast((raw_value(raw[k], i) - sm[k].x) * kLog2e);
         dot = fmaf(f[i], x[i], dot);
       }
-      dot = group_sum<G>(dot);
-      if (!real[k]) continue;
-      Bits* out = static_cast<Bits*>(a.dlogits[at[k].rank]) + at[k].row * a.stride;
+      const float less = group_sum<G>(dot) * sm[k].y;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) x[i] *= sm[k].y * (f[i] - less);
+      if (!out[k]) continue;
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c) {
         const int e0 = expert_of<VEC, G>(c, l, 0);
-        if (e0 >= a.E) continue;
-        RawRow<T, VEC, 1> r;
-        Bits* b = reinterpret_cast<Bits*>(&r.q[0]);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int i = c * VEC + j;
-          b[j] = Ty<T>::narrow(live ? factor * x[i] * (f[i] - dot) : 0.0f);
-        }
-        *reinterpret_cast<typename Select<(VEC > 1), uint4, Bits>::type*>(out + e0) = r.q[0];
+        if (e0 < a.E) store_chunk<T, VEC>(out[k] + e0, x + c * VEC);
       }
     }
   }
@@ -501,7 +570,7 @@ bool valid_sizes(int R, size_t tokens, int experts) {
 
 size_t workspace(int R, size_t tokens, int experts) {
   const size_t part = op_round((size_t)kMostCtas * experts * 4);
-  return op_round((size_t)R * tokens * 4) + 2 * part + op_round(kMostCtas * 4);
+  return op_round((size_t)R * tokens * sizeof(float2)) + 2 * part + op_round(kMostCtas * 4);
 }
 
 }  // namespace
@@ -572,12 +641,11 @@ vr_result_t vr_balance_loss(const void* const* logits, size_t rowStride,
   a.ctas = stats_ctas(std::min(dev.sms, kMostCtas), a.total, k.groups);
   char* w = static_cast<char*>(workspaceBuf);
   const size_t part = op_round((size_t)kMostCtas * experts * 4);
-  a.lse = reinterpret_cast<float*>(w);
-  w += op_round((size_t)R * tokens * 4);
+  a.softmax = reinterpret_cast<float2*>(w);
+  w += op_round((size_t)R * tokens * sizeof(float2));
   a.probPart = reinterpret_cast<float*>(w);
   a.countPart = reinterpret_cast<int*>(w + part);
   a.validPart = reinterpret_cast<int*>(w + 2 * part);
-  a.divTokens = a.tokens > 1 ? ~0ull / (unsigned long long)a.tokens + 1 : 0ull;
   void* args[] = {&a};
   // Two rounds of one CTA's groups: the second launch and its sums cost more
   // than the idle SMs.
