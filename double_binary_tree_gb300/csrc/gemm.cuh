@@ -3,7 +3,10 @@
 //
 //   D[z][m][n] = sum_k A[z][m][k] B[z][n][k],  16-bit operands, fp32 sums
 //
-// One persistent CTA per SM, 128 x BN tiles.  Warp 0 moves 64-deep slices of
+// Persistent CTAs, one per SM, 128 x BN tiles, or pairs of CTAs (PAIR) that
+// work on one 256 x BN tile: each CTA holds its 128 rows of A and of the
+// accumulator and half of B, so a slice of the tile costs an SM a third less
+// shared memory traffic (what bounds 128-wide tiles) and L2 traffic.  Warp 0 moves 64-deep slices of
 // A and B into a ring of shared-memory stages with tensor copies (TMA), warp
 // 1 issues the products on them, warps 4-11 read finished accumulators from
 // tensor memory and run the epilogue.  Two accumulators take turns, so the
@@ -19,6 +22,11 @@
 // the operand's extents are read as zero by the copy, which makes every
 // ragged edge correct without a second path.
 //
+// SPLIT: too few tiles for the SMs.  A cluster of several CTAs (pairs) takes
+// one tile, each a share of k; the partial sums meet in shared memory and
+// every CTA of the cluster adds up and finishes some of the columns, in the
+// order of the shares.
+//
 // Every wait is bounded.  A CTA that gives up records VR_ERR_TIMEOUT, waits
 // (bounded) for its copies and products in flight, frees its tensor memory
 // and returns.
@@ -26,8 +34,10 @@
 
 #include <cuda.h>
 
+#include <algorithm>
 #include <type_traits>
 
+#include "gemm_host.h"
 #include "staged.cuh"
 
 namespace vr {
@@ -53,13 +63,75 @@ struct Tile {
   int z, m0, n0;
 };
 
+template <bool PAIR>
 __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
+  if constexpr (PAIR) {  // counted on the barrier of the pair's first CTA
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar & 0xfeffffffu)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  }
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of the same place in another CTA of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+// wait_phase (staged.cuh) at cluster scope.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, unsigned parity,
+                                             const volatile int* abort, bool honorAbort,
+                                             unsigned long long limitNs) {
+  auto done = [&]() {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const unsigned long long t0 = global_ns();
+  for (unsigned it = 1;; ++it) {
+    if (done()) return true;
+    if ((it & 15) == 0) {
+      if (honorAbort && *abort) return false;
+      if (global_ns() - t0 > limitNs) return false;
+    }
+  }
 }
 // Shared-memory operand descriptor of a 128-byte swizzled tile.  K-major:
 // rows of 64 elements, eight rows to a 1024-byte group (strideBytes).
@@ -70,19 +142,40 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, unsigned leadByt
   return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(leadBytes >> 4) << 16 |
          (uint64_t)(strideBytes >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_f16(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
-      "l"(a), "l"(b), "r"(idesc), "r"((unsigned)accumulate)
-      : "memory");
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
+        "l"(a), "l"(b), "r"(idesc), "r"((unsigned)accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(acc),
+        "l"(a), "l"(b), "r"(idesc), "r"((unsigned)accumulate)
+        : "memory");
+  }
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
+// Arrives on `bar` (in both CTAs of a pair) when the products issued so far
+// are done.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t pairMask) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(pairMask)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  }
 }
 __device__ __forceinline__ void tmem_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -157,7 +250,7 @@ struct RegAcc {
   int first;
   __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = sum[c - first + i];
+    for (int i = 0; i < 32; ++i) v[i] = sum[c - first + i];  // a constant once unrolled
   }
   template <class F>
   __device__ __forceinline__ void pick(int c, F f) const {
@@ -180,46 +273,52 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool aMn, bool bM
          (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
-template <int BN, int PARTS>
+template <int BN, int PARTS, bool PAIR>
 struct GemmShape {
   static constexpr int kABytes = kTileM * kTileK * 2;
-  static constexpr int kBBytes = BN * kTileK * 2;
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;
+  static constexpr int kBBytes = kBRows * kTileK * 2;
   static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
+  static constexpr int kTileRows = PAIR ? 2 * kTileM : kTileM;
   // columns of an accumulator: with two planes the products of a low plane
   // are summed apart (their size would not survive being added one by one)
   static constexpr int kAcc = PARTS * BN;
   static constexpr int kStages = (kGemmSmem - 2048) / kStageBytes;
   static constexpr int kSmem = 2048 + kStages * kStageBytes;  // header, alignment
   static_assert(kStages >= 2 && 2 * kAcc <= 512, "too large");
+  static_assert(kStages * kStageBytes >= kTileM * BN * 4, "a share's sums do not fit");
 };
 
-// Blocks of 16 tile rows are walked column by column, so that the rows' and
+// Blocks of 2048 rows are walked column by column, so that the rows' and
 // columns' operands of the tiles in flight stay in L2.
-__device__ __forceinline__ Tile tile_of(int t, int tilesM, int tilesN, int BN, bool triangle) {
+// Tiles of a triangle's block row i: those whose first column is not above
+// its last row.
+__host__ __device__ __forceinline__ int triangle_row(int i, int rows, int cols) {
+  return ((i + 1) * rows + cols - 1) / cols;
+}
+template <int ROWS, int BN>
+__device__ __forceinline__ Tile tile_of(int t, int tilesM, int tilesN, bool triangle) {
   Tile o;
-  int per;
   if (triangle) {
-    // row i holds the tiles whose first column is not above its last row
-    const int ratio = BN / kTileM;
-    per = 0;
-    for (int i = 0; i < tilesM; ++i) per += i / ratio + 1;
+    int per = 0;
+    for (int i = 0; i < tilesM; ++i) per += min(triangle_row(i, ROWS, BN), tilesN);
     o.z = t / per;
     t -= o.z * per;
     int i = 0;
-    while (t >= i / ratio + 1) t -= i / ratio + 1, ++i;
-    o.m0 = i * kTileM;
+    for (int n; t >= (n = min(triangle_row(i, ROWS, BN), tilesN)); ++i) t -= n;
+    o.m0 = i * ROWS;
     o.n0 = t * BN;
     return o;
   }
-  per = tilesM * tilesN;
+  const int per = tilesM * tilesN;
   o.z = t / per;
   t -= o.z * per;
-  constexpr int kGroup = 16;
+  constexpr int kGroup = 2048 / ROWS;
   const int group = t / (kGroup * tilesN);
   const int rows = min(kGroup, tilesM - group * kGroup);
   t -= group * kGroup * tilesN;
   o.n0 = t / rows * BN;
-  o.m0 = (group * kGroup + t % rows) * kTileM;
+  o.m0 = (group * kGroup + t % rows) * ROWS;
   return o;
 }
 
@@ -235,33 +334,44 @@ __device__ __forceinline__ Tile tile_of(int t, int tilesM, int tilesN, int BN, b
 // the sum.  Every CHUNK slices of 64 the accumulator is handed to the
 // epilogue warps, which add the partial sums in registers with rounding; the
 // next chunk is summed meanwhile in the other accumulator.
-template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, class Epi>
+template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, bool PAIR, bool SPLIT,
+          class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ typename Epi::Args e) {
-  using Shape = GemmShape<BN, PARTS>;
+  using Shape = GemmShape<BN, PARTS, PAIR>;
   static_assert(PARTS == 1 || CHUNK > 0, "two planes are summed in the epilogue warps");
+  constexpr int kStages = Shape::kStages;
+  constexpr int kCtas = PAIR ? 2 : 1;  // that share a tile's products
   extern __shared__ unsigned char smemRaw[];
-  __shared__ alignas(8) uint64_t bars[2 * Shape::kStages + 5];
+  __shared__ alignas(8) uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmemBase;
   __shared__ volatile int abortFlag;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = PAIR || SPLIT ? cluster_rank() : 0u;
+  const uint32_t inPair = PAIR ? rank & 1u : 0u;
+  const bool leader = inPair == 0;
+  const uint16_t pairMask = (uint16_t)(3u << (rank & ~1u));
   const uint32_t stage0 = (smem_addr(smemRaw) + 1023) & ~1023u;
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (Shape::kStages + s); };
-  auto accFull = [&](int i) { return bar0 + 8u * (2 * Shape::kStages + i); };
-  auto accEmpty = [&](int i) { return bar0 + 8u * (2 * Shape::kStages + 2 + i); };
-  const uint32_t drained = bar0 + 8u * (2 * Shape::kStages + 4);
+  auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto accFull = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
+  auto accEmpty = [&](int i) { return bar0 + 8u * (2 * kStages + 2 + i); };
+  const uint32_t drained = bar0 + 8u * (2 * kStages + 4);
+  auto wait = [&](uint32_t bar, unsigned parity, bool honorAbort = true) {
+    return PAIR ? wait_cluster(bar, parity, &abortFlag, honorAbort, g.timeoutNs)
+                : wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
+  };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < Shape::kStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(accFull(i), 1);
-      mbar_init(accEmpty(i), kEpilogueWarps);
+      mbar_init(accEmpty(i), kEpilogueWarps * kCtas);
     }
     mbar_init(drained, 1);
     abortFlag = 0;
@@ -269,14 +379,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     asm volatile("fence.proxy.async;" ::: "memory");
   }
   if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmemBase)),
-                 "r"(2 * Shape::kAcc)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmemBase)),
+                   "r"(2 * Shape::kAcc)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmemBase)),
+                   "r"(2 * Shape::kAcc)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   tmem_fence_before();
   __syncthreads();
+  if constexpr (PAIR || SPLIT) cluster_sync();  // the peers' barriers are set up
   tmem_fence_after();
   const uint32_t tmem = tmemBase;
   pdl_launch();
@@ -284,27 +403,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   const int M = g.dynM ? min(*g.dynM, g.M) : g.M;
   const int K = g.dynK ? min(*g.dynK, g.K) : g.K;
-  const int tilesM = (M + kTileM - 1) / kTileM, tilesN = (g.N + BN - 1) / BN;
-  const int blocks = (K + kTileK - 1) / kTileK;
-  const int chunk = CHUNK ? CHUNK : max(blocks, 1);
+  const int tilesM = (M + Shape::kTileRows - 1) / Shape::kTileRows, tilesN = (g.N + BN - 1) / BN;
+  const int slices = (K + kTileK - 1) / kTileK;
   constexpr int kHalf = BN / 2;  // columns of an epilogue warp
   int tiles = tilesM * tilesN;
   if (g.triangle) {
     tiles = 0;
-    for (int i = 0; i < tilesM; ++i) tiles += i / (BN / kTileM) + 1;
+    for (int i = 0; i < tilesM; ++i) tiles += min(triangle_row(i, Shape::kTileRows, BN), tilesN);
   }
   tiles *= g.batch;
+  // This CTA's tiles and its share [kb0, kb1) of their slices of k.
+  const int shares = SPLIT ? (int)cluster_size() / kCtas : 1;
+  const int share = SPLIT ? (int)rank / kCtas : 0;
+  const int kb0 = SPLIT ? (int)((long long)slices * share / shares) : 0;
+  const int kb1 = SPLIT ? (int)((long long)slices * (share + 1) / shares) : slices;
+  const int blocks = kb1 - kb0;
+  const int chunk = CHUNK ? CHUNK : max(blocks, 1);
+  const int firstTile = (int)blockIdx.x / (kCtas * shares);
+  const int tileStep = SPLIT ? tiles + 1 : (int)gridDim.x / kCtas;  // SPLIT: one tile
 
   if (warp == 0 && lane == 0) {
     int s = 0, turn = 0;
     bool ok = true;
     long long issued = 0;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile o = tile_of(t, tilesM, tilesN, BN, g.triangle);
-      for (int kb = 0; kb < blocks; ++kb) {
-        ok = wait_phase(empty(s), turn ^ 1, &abortFlag, true, g.timeoutNs);
+    for (int t = firstTile; ok && t < tiles; t += tileStep) {
+      const Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
+      const int m0 = o.m0 + (int)inPair * kTileM, n0 = o.n0 + (int)inPair * Shape::kBRows;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = wait(empty(s), turn ^ 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(full(s), Shape::kStageBytes);
+        if (leader) mbar_arrive_expect_tx(full(s), kCtas * Shape::kStageBytes);
         uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes;
         const int k0 = kb * kTileK;
 #pragma unroll
@@ -312,9 +440,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           if (AMN) {
 #pragma unroll
             for (int i = 0; i < kTileM / 64; ++i)
-              tensor_load(dst + i * (64 * kTileK * 2), &g.a[p], o.m0 + i * 64, k0, o.z, full(s));
+              tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.a[p], m0 + i * 64, k0, o.z, full(s));
           } else {
-            tensor_load(dst, &g.a[p], k0, o.m0, o.z, full(s));
+            tensor_load<PAIR>(dst, &g.a[p], k0, m0, o.z, full(s));
           }
           dst += Shape::kABytes;
         }
@@ -322,41 +450,42 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int p = 0; p < PARTS; ++p) {
           if (BMN) {
 #pragma unroll
-            for (int i = 0; i < BN / 64; ++i)
-              tensor_load(dst + i * (64 * kTileK * 2), &g.b[p], o.n0 + i * 64, k0, o.z, full(s));
+            for (int i = 0; i < Shape::kBRows / 64; ++i)
+              tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.b[p], n0 + i * 64, k0, o.z, full(s));
           } else {
-            tensor_load(dst, &g.b[p], k0, o.n0, o.z, full(s));
+            tensor_load<PAIR>(dst, &g.b[p], k0, n0, o.z, full(s));
           }
           dst += Shape::kBBytes;
         }
         ++issued;
-        if (++s == Shape::kStages) s = 0, turn ^= 1;
+        if (++s == kStages) s = 0, turn ^= 1;
       }
     }
     if (!ok) {
       raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
-      // copies in flight land before the CTA's shared memory is given up
-      for (long long i = issued > Shape::kStages ? issued - Shape::kStages : 0; i < issued; ++i)
-        wait_phase(full((int)(i % Shape::kStages)), (int)(i / Shape::kStages & 1), &abortFlag,
-                   false, g.timeoutNs);
+      // copies in flight land before the CTA's shared memory is given up (in a
+      // pair they are counted on the first CTA's barriers, which waits for both)
+      if (leader)
+        for (long long i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+          wait(full((int)(i % kStages)), (int)(i / kStages & 1), false);
     }
-  } else if (warp == 1 && lane == 0) {
-    constexpr uint32_t idesc = mma_idesc<T>(kTileM, BN, AMN, BMN);
+  } else if (warp == 1 && lane == 0 && leader) {
+    constexpr uint32_t idesc = mma_idesc<T>(Shape::kTileRows, BN, AMN, BMN);
     constexpr unsigned kSlab = 64 * kTileK * 2;  // MN-major: bytes of a 64-wide slab
     // one product takes 16 k: 32 bytes along a K-major row, 16 rows of 128
     // bytes of an MN-major slab
     constexpr unsigned aStep = (AMN ? 16 * 128 : 32) >> 4, bStep = (BMN ? 16 * 128 : 32) >> 4;
     int s = 0, turn = 0, buf = 0, bufTurn = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      for (int kb0 = 0; ok && kb0 < blocks; kb0 += chunk) {
-        ok = wait_phase(accEmpty(buf), bufTurn ^ 1, &abortFlag, true, g.timeoutNs);
+    for (int t = firstTile; ok && t < tiles; t += tileStep) {
+      for (int c0 = 0; ok && c0 < blocks; c0 += chunk) {
+        ok = wait(accEmpty(buf), bufTurn ^ 1);
         if (!ok) break;
         tmem_fence_after();
         const uint32_t acc = tmem + (unsigned)buf * Shape::kAcc;
-        const int kb1 = min(kb0 + chunk, blocks);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = wait_phase(full(s), turn, &abortFlag, true, g.timeoutNs);
+        const int c1 = min(c0 + chunk, blocks);
+        for (int kb = c0; kb < c1; ++kb) {
+          ok = wait(full(s), turn);
           if (!ok) break;
           tmem_fence_after();
           const uint32_t base = stage0 + (unsigned)s * Shape::kStageBytes;
@@ -368,51 +497,66 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint64_t bDesc = operand_desc(bAt, BMN ? kSlab : 16, 1024);
 #pragma unroll
             for (int k = 0; k < kTileK / 16; ++k)
-              mma_f16(p ? acc + BN : acc, aDesc + k * aStep, bDesc + k * bStep, idesc,
-                      (kb - kb0) | (p == 2) | k);
+              mma_f16<PAIR>(p ? acc + BN : acc, aDesc + k * aStep, bDesc + k * bStep, idesc,
+                            (kb - c0) | (p == 2) | k);
           }
-          mma_commit(empty(s));
-          if (++s == Shape::kStages) s = 0, turn ^= 1;
+          mma_commit<PAIR>(empty(s), pairMask);
+          if (++s == kStages) s = 0, turn ^= 1;
         }
         if (!ok) break;
-        mma_commit(accFull(buf));
+        mma_commit<PAIR>(accFull(buf), pairMask);
         if (++buf == 2) buf = 0, bufTurn ^= 1;
       }
     }
     if (!ok) {
       raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
-      mma_commit(drained);
-      wait_phase(drained, 0, &abortFlag, false, g.timeoutNs);
+      mma_commit<PAIR>(drained, pairMask);
+      wait(drained, 0, false);
     }
   } else if (warp >= 4) {
     const int quad = warp % 4, half = (warp - 4) / 4;
+    const int row = quad * 32 + lane;
+    const uint32_t quadBase = tmem + ((uint32_t)(quad * 32) << 16);
     int buf = 0, bufTurn = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const Tile o = tile_of(t, tilesM, tilesN, BN, g.triangle);
-      const uint32_t quadBase = tmem + ((uint32_t)(quad * 32) << 16);
-      const int row = quad * 32 + lane;
-      // the next accumulator, or false when the warp has to leave
-      auto next = [&]() {
-        const bool ready = wait_phase(accFull(buf), bufTurn, &abortFlag, true, g.timeoutNs);
-        if (!__all_sync(0xffffffffu, ready)) {  // as a whole
-          raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
-          return false;
+    // the next accumulator, or false when the warp has to leave, as a whole
+    auto next = [&]() {
+      const bool ready = wait(accFull(buf), bufTurn);
+      if (!__all_sync(0xffffffffu, ready)) {
+        raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
+        return false;
+      }
+      tmem_fence_after();
+      return true;
+    };
+    auto release = [&]() {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) {
+          peer_arrive(peer_addr(accEmpty(buf), rank & ~1u));
+        } else {
+          mbar_arrive(accEmpty(buf));
         }
-        tmem_fence_after();
-        return true;
+      }
+      if (++buf == 2) buf = 0, bufTurn ^= 1;
+    };
+    for (int t = firstTile; t < tiles; t += tileStep) {
+      Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
+      o.m0 += (int)inPair * kTileM;
+      bool left = false;
+      // a share's sums: [column][row] in the stages' memory, free by now
+      auto put = [&](int c, const float(&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage0 + 4u * ((c + i) * kTileM + row)),
+                       "f"(v[i])
+                       : "memory");
       };
-      auto release = [&]() {
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(accEmpty(buf));
-        if (++buf == 2) buf = 0, bufTurn ^= 1;
-      };
-      if (CHUNK) {
+      if constexpr (CHUNK > 0) {
         float sum[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
-        bool left = false;
-        for (int kb0 = 0; kb0 < blocks; kb0 += chunk) {
+        for (int c0 = 0; c0 < blocks; c0 += chunk) {
           left = !next();
           if (left) break;
 #pragma unroll
@@ -431,24 +575,143 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           release();
         }
         if (left) break;
-        Epi::template run<kHalf>(e, g, o, row, half * kHalf, M,
-                                 RegAcc<kHalf>{sum, half * kHalf});
+        const RegAcc<kHalf> acc{sum, half * kHalf};
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            float v[32];
+            acc(half * kHalf + c, v);
+            put(half * kHalf + c, v);
+          }
+        } else {
+          Epi::template run<kHalf>(e, g, o, row, half * kHalf, M, acc);
+        }
       } else {
         if (blocks && !next()) break;
-        Epi::template run<kHalf>(e, g, o, row, half * kHalf, M,
-                                 TmemAcc{quadBase + (unsigned)(buf * Shape::kAcc), blocks != 0});
+        const TmemAcc acc{quadBase + (unsigned)buf * Shape::kAcc, blocks != 0};
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 32) {
+            float v[32];
+            acc(half * kHalf + c, v);
+            put(half * kHalf + c, v);
+          }
+        } else {
+          Epi::template run<kHalf>(e, g, o, row, half * kHalf, M, acc);
+        }
         if (blocks) release();
+      }
+    }
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync();  // all shares' sums are in place
+    constexpr int kGroups = BN / 32;  // of 32 columns; four warps (row quadrants) each
+    if (warp >= 4 && firstTile < tiles) {
+      const int quad = warp % 4, row = quad * 32 + lane;
+      Tile o = tile_of<Shape::kTileRows, BN>(firstTile, tilesM, tilesN, g.triangle);
+      o.m0 += (int)inPair * kTileM;
+      for (int group = share * 2 + (warp - 4) / 4; group < kGroups; group += 2 * shares) {
+        float sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
+        for (int from = 0; from < shares; ++from) {
+          const uint32_t at = peer_addr(stage0, (uint32_t)(from * kCtas) + inPair) +
+                              4u * (unsigned)(group * 32 * kTileM + row);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[i] += peer_load(at + 4u * (unsigned)(i * kTileM));
+        }
+        Epi::template run<32>(e, g, o, row, group * 32, M, RegAcc<32>{sum, group * 32});
       }
     }
   }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  // no CTA leaves while a peer still reads its memory or arrives on its barriers
+  if constexpr (PAIR || SPLIT) cluster_sync();
   if (warp == 2) {
     tmem_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(2 * Shape::kAcc));
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(2 * Shape::kAcc));
+    } else {
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(2 * Shape::kAcc));
+    }
   }
+}
+
+// One product D = A B^T per batch entry: operands as they lie in memory.
+struct Operand {
+  const void *hi, *lo;  // lo: second plane (PARTS = 2)
+  size_t ld;            // elements between rows
+};
+struct GemmSize {
+  size_t M, N, K, batch;
+  bool triangle;
+};
+
+template <int BN, bool PAIR>
+size_t gemm_tiles(const GemmSize& z) {
+  const size_t rows = PAIR ? 2 * kTileM : kTileM;
+  const size_t tm = (z.M + rows - 1) / rows, tn = (z.N + BN - 1) / BN;
+  size_t tiles = tm * tn;
+  if (z.triangle) {
+    tiles = 0;
+    for (size_t i = 0; i < tm; ++i)
+      tiles += std::min<size_t>(triangle_row((int)i, (int)rows, BN), tn);
+  }
+  return tiles * z.batch;
+}
+
+// CTAs (pairs) that share a tile's k: as many as the idle SMs allow, at most
+// a cluster of eight CTAs, and at least four slices of 64 each.
+template <int BN, bool PAIR>
+int gemm_shares(const GemmSize& z, int sms) {
+  const size_t ctas = PAIR ? 2 : 1, tiles = gemm_tiles<BN, PAIR>(z) * ctas;
+  const size_t slices = (z.K + kTileK - 1) / kTileK;
+  int s = 1;
+  while (2 * s * ctas <= 8 && tiles * 2 * s <= (size_t)sms && slices >= (size_t)(8 * s)) s *= 2;
+  return s;
+}
+
+template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, bool PAIR, bool SPLIT,
+          class Epi>
+vr_result_t gemm_launch(const OpDevice& dev, const Operand& a, const Operand& b, const GemmSize& z,
+                        const int* dynM, const int* dynK, typename Epi::Args& epi, int shares,
+                        void* stream) {
+  using Shape = GemmShape<BN, PARTS, PAIR>;
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const void* fn = (const void*)gemm_kernel<T, BN, PARTS, AMN, BMN, CHUNK, PAIR, SPLIT, Epi>;
+  GemmArgs g = {};
+  for (int i = 0; i < PARTS; ++i) {
+    vr_result_t e = gemm_operand(&g.a[i], i ? a.lo : a.hi, bf16, AMN ? z.M : z.K,
+                                 AMN ? z.K : z.M, z.batch, a.ld * 2, a.ld * 2 * (AMN ? z.K : z.M),
+                                 AMN ? kTileK : kTileM);
+    if (e != VR_SUCCESS) return e;
+    e = gemm_operand(&g.b[i], i ? b.lo : b.hi, bf16, BMN ? z.N : z.K, BMN ? z.K : z.N, z.batch,
+                     b.ld * 2, b.ld * 2 * (BMN ? z.K : z.N), BMN ? kTileK : Shape::kBRows);
+    if (e != VR_SUCCESS) return e;
+  }
+  const vr_result_t e = gemm_prepare(fn, dev.device, Shape::kSmem);
+  if (e != VR_SUCCESS) return e;
+  g.M = (int)z.M;
+  g.N = (int)z.N;
+  g.K = (int)z.K;
+  g.batch = (int)z.batch;
+  g.dynM = dynM;
+  g.dynK = dynK;
+  g.triangle = z.triangle;
+  g.status = dev.status;
+  g.timeoutNs = dev.timeoutNs;
+  constexpr size_t kCtas = PAIR ? 2 : 1;
+  const size_t tiles = gemm_tiles<BN, PAIR>(z);
+  const size_t groups = SPLIT ? tiles : std::min<size_t>(tiles, dev.sms / kCtas);
+  const size_t cluster = kCtas * (SPLIT ? (size_t)shares : 1);
+  void* args[] = {&g, &epi};
+  return op_launch(fn, dim3((unsigned)(groups * cluster)), dim3(kGemmThreads), args, Shape::kSmem,
+                   stream, (int)cluster);
 }
 
 }  // namespace vr

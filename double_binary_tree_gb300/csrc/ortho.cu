@@ -26,14 +26,13 @@
 #include <cstdint>
 
 #include "gemm.cuh"
-#include "gemm_host.h"
 
 namespace vr {
 namespace {
 
 constexpr int kMost = 64;          // matrices per launch
 constexpr float kScale = 4096.0f;  // of the planes
-constexpr int kNormCtas = 64;      // partial sums of squares per matrix, at most
+constexpr int kNormCtas = 256;     // partial sums of squares per matrix, at most
 constexpr int kSplitChunk = 2;     // slices of 64 summed before rounding (two planes)
 
 struct Planes {
@@ -248,45 +247,67 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const __grid_constant__
   }
 }
 
-// The normalised matrix into the planes of X, 32 x 32 blocks at a time
-// through shared memory when it is transposed.
+// The normalised matrix into the planes of X: eight elements a thread, or
+// through shared memory, 64 x 32 blocks at a time, when it is transposed.
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_load_kernel(const __grid_constant__ LoadArgs a) {
-  __shared__ float tile[32][33];
+  using Bits = typename Ty<T>::Bits;
+  __shared__ float tile[64][33];
   pdl_launch();
   pdl_wait();
   const int z = blockIdx.y;
   float sum = 0.0f;
   for (int i = 0; i < a.ctas; ++i) sum += a.part[z * kNormCtas + i];
   const float by = kScale / (sqrtf(sum) + a.eps);
-  const typename Ty<T>::Bits* p = static_cast<const typename Ty<T>::Bits*>(a.src[z]);
+  const Bits* p = static_cast<const Bits*>(a.src[z]);
+  __half *hi = a.x.hi + z * a.size, *lo = a.x.lo + z * a.size;
+  if (!a.tall) {
+    const bool vec = a.cols % 8 == 0 && ((uintptr_t)p & 15) == 0;
+    const long long perRow = (a.cols + 7) / 8, units = a.rows * perRow;
+    for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; u < units;
+         u += (long long)gridDim.x * 256) {
+      const long long r = u / perRow, c = u % perRow * 8;
+      alignas(16) Bits in[8];
+      if (vec) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(in) / 16; ++i)
+          reinterpret_cast<uint4*>(in)[i] =
+              reinterpret_cast<const uint4*>(p + r * a.cols + c)[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) in[i] = c + i < a.cols ? p[r * a.cols + c + i] : (Bits)0;
+      }
+      alignas(16) __half h[8], l[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split(Ty<T>::widen(in[i]) * by, h[i], l[i]);
+      // rows are padded to whole groups of 32
+      *reinterpret_cast<uint4*>(hi + r * a.ld + c) = *reinterpret_cast<const uint4*>(h);
+      *reinterpret_cast<uint4*>(lo + r * a.ld + c) = *reinterpret_cast<const uint4*>(l);
+    }
+    return;
+  }
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-  const long long blocksC = (a.cols + 31) / 32, blocks = blocksC * ((a.rows + 31) / 32);
+  const long long blocksC = (a.cols + 31) / 32, blocks = blocksC * ((a.rows + 63) / 64);
   for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const long long r0 = b / blocksC * 32, c0 = b % blocksC * 32;
+    const long long r0 = b / blocksC * 64, c0 = b % blocksC * 32;
+#pragma unroll
+    for (int i = 0; i < 64; i += 8) {
+      const long long r = r0 + ty + i, c = c0 + tx;
+      tile[ty + i][tx] = r < a.rows && c < a.cols ? Ty<T>::widen(p[r * a.cols + c]) * by : 0.0f;
+    }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
-      const long long r = r0 + ty + i, c = c0 + tx;
-      const float v = r < a.rows && c < a.cols ? Ty<T>::widen(p[r * a.cols + c]) * by : 0.0f;
-      if (a.tall) {
-        tile[ty + i][tx] = v;
-      } else if (r < a.rows && c < a.cols) {
-        const long long at = z * a.size + r * a.ld + c;
-        split(v, a.x.hi[at], a.x.lo[at]);
+      const long long r = c0 + ty + i, c = r0 + 2 * tx;  // of X
+      if (r < a.cols && c < a.rows) {
+        __half2 h, l;
+        split(tile[2 * tx][ty + i], h.x, l.x);
+        split(tile[2 * tx + 1][ty + i], h.y, l.y);
+        *reinterpret_cast<__half2*>(hi + r * a.ld + c) = h;
+        *reinterpret_cast<__half2*>(lo + r * a.ld + c) = l;
       }
     }
-    if (a.tall) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        const long long r = c0 + ty + i, c = r0 + tx;  // of X
-        if (r < a.cols && c < a.rows) {
-          const long long at = z * a.size + r * a.ld + c;
-          split(tile[tx][ty + i], a.x.hi[at], a.x.lo[at]);
-        }
-      }
-      __syncthreads();
-    }
+    __syncthreads();
   }
 }
 
@@ -359,42 +380,31 @@ bool in_range(const float* coefs, int steps) {
 
 constexpr float kCoefs[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// The products of one step: `T` only names the result's type.
-template <int BN, int PARTS, bool BMN, class Epi>
+// One product of a step.  Pairs of CTAs where X has more rows than one CTA
+// takes; 256 columns where that leaves no SM idle (one plane: two planes fill
+// tensor memory at 128); k shared out where the tiles leave SMs idle.
+template <int PARTS, bool BMN, class Epi>
 vr_result_t product(const OpDevice& dev, const Planes& a, size_t aLd, const Planes& b, size_t bLd,
-                    size_t M, size_t N, size_t K, size_t batch, bool triangle,
-                    typename Epi::Args& epi, void* stream) {
-  using Shape = GemmShape<BN, PARTS>;
-  const void* fn =
-      (const void*)gemm_kernel<__half, BN, PARTS, false, BMN, PARTS == 2 ? kSplitChunk : 0, Epi>;
-  GemmArgs g = {};
-  for (int i = 0; i < PARTS; ++i) {
-    vr_result_t e = gemm_operand(&g.a[i], i ? a.lo : a.hi, false, K, M, batch, aLd * 2,
-                                 aLd * 2 * M, kTileM);
-    if (e != VR_SUCCESS) return e;
-    e = gemm_operand(&g.b[i], i ? b.lo : b.hi, false, BMN ? N : K, BMN ? K : N, batch, bLd * 2,
-                     bLd * 2 * (BMN ? K : N), BMN ? kTileK : BN);
-    if (e != VR_SUCCESS) return e;
+                    const GemmSize& z, typename Epi::Args& epi, void* stream) {
+  const Operand oa = {a.hi, a.lo, aLd}, ob = {b.hi, b.lo, bLd};
+  constexpr int CHUNK = PARTS == 2 ? kSplitChunk : 0;
+  if (z.M <= kTileM) {
+    const int s = gemm_shares<128, false>(z, dev.sms);
+    return s > 1 ? gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, false, true, Epi>(
+                       dev, oa, ob, z, nullptr, nullptr, epi, s, stream)
+                 : gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, false, false, Epi>(
+                       dev, oa, ob, z, nullptr, nullptr, epi, 1, stream);
   }
-  const vr_result_t e = gemm_prepare(fn, dev.device, Shape::kSmem);
-  if (e != VR_SUCCESS) return e;
-  g.M = (int)M;
-  g.N = (int)N;
-  g.K = (int)K;
-  g.batch = (int)batch;
-  g.triangle = triangle;
-  g.status = dev.status;
-  g.timeoutNs = dev.timeoutNs;
-  const size_t tm = (M + kTileM - 1) / kTileM, tn = (N + BN - 1) / BN;
-  size_t tiles = tm * tn;
-  if (triangle) {
-    tiles = 0;
-    for (size_t i = 0; i < tm; ++i) tiles += i / (BN / kTileM) + 1;
+  if constexpr (PARTS == 1) {
+    if (2 * gemm_tiles<256, true>(z) >= (size_t)dev.sms - 1)
+      return gemm_launch<__half, 256, PARTS, false, BMN, CHUNK, true, false, Epi>(
+          dev, oa, ob, z, nullptr, nullptr, epi, 1, stream);
   }
-  tiles *= batch;
-  void* args[] = {&g, &epi};
-  return op_launch(fn, dim3((unsigned)std::min<size_t>(tiles, dev.sms)), dim3(kGemmThreads), args,
-                   Shape::kSmem, stream);
+  const int s = gemm_shares<128, true>(z, dev.sms);
+  return s > 1 ? gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, true, true, Epi>(
+                     dev, oa, ob, z, nullptr, nullptr, epi, s, stream)
+               : gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, true, false, Epi>(
+                     dev, oa, ob, z, nullptr, nullptr, epi, 1, stream);
 }
 
 template <typename T, int PARTS>
@@ -423,12 +433,15 @@ vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src,
     ap.out[i] = static_cast<T*>(dst[i]);
     if ((uintptr_t)dst[i] & 15) ap.vec = 0;
   }
-  la.ctas = (int)std::max<size_t>(1, std::min<size_t>(kNormCtas, rows * cols / 8192));
+  // about two CTAs per SM over all matrices, 8192 elements each at least
+  la.ctas = (int)std::max<size_t>(
+      1, std::min({(size_t)kNormCtas, rows * cols / 8192, (size_t)(2 * dev.sms / count + 1)}));
   void* args[] = {&la};
   vr_result_t e = op_launch((const void*)ortho_norm_kernel<T>, dim3(la.ctas, count), dim3(256),
                             args, 0, stream);
   if (e != VR_SUCCESS) return e;
-  const size_t blocks = (rows + 31) / 32 * ((cols + 31) / 32);
+  const size_t blocks =
+      tall ? (rows + 63) / 64 * ((cols + 31) / 32) : (rows * ((cols + 7) / 8) + 255) / 256;
   e = op_launch((const void*)ortho_load_kernel<T>,
                 dim3((unsigned)std::min<size_t>(blocks, (size_t)dev.sms * 8), count), dim3(256),
                 args, 0, stream);
@@ -439,14 +452,15 @@ vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src,
     const float shift = shift_of(coefs, steps, k);
     SymmetricEpilogue::Args ga = {{nullptr, nullptr}, A, (long long)p.ldA, sizeA, 0.0f,
                                   1.0f / kScale, 0.0f, PARTS == 2};
-    if ((e = product<128, PARTS, false, SymmetricEpilogue>(dev, from, p.ldX, from, p.ldX, p.m, p.m,
-                                                           p.n, count, true, ga, stream)) !=
+    const size_t n = (size_t)count;
+    if ((e = product<PARTS, false, SymmetricEpilogue>(dev, from, p.ldX, from, p.ldX,
+                                                      {p.m, p.m, p.n, n, true}, ga, stream)) !=
         VR_SUCCESS)
       return e;
     SymmetricEpilogue::Args pa = {A, B, (long long)p.ldA, sizeA, b, c / kScale, shift * kScale,
                                   PARTS == 2};
-    if ((e = product<128, PARTS, false, SymmetricEpilogue>(dev, A, p.ldA, A, p.ldA, p.m, p.m, p.m,
-                                                           count, true, pa, stream)) != VR_SUCCESS)
+    if ((e = product<PARTS, false, SymmetricEpilogue>(
+             dev, A, p.ldA, A, p.ldA, {p.m, p.m, p.m, n, true}, pa, stream)) != VR_SUCCESS)
       return e;
     ap.from = from;
     ap.to = x[1 - k % 2];
@@ -458,8 +472,8 @@ vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src,
     ap.tall = tall;
     ap.byOut = scale / kScale;
     ap.cols = (int)p.n;
-    if ((e = product<128, PARTS, true, ApplyEpilogue<T>>(dev, B, p.ldA, from, p.ldX, p.m, p.n, p.m,
-                                                         count, false, ap, stream)) != VR_SUCCESS)
+    if ((e = product<PARTS, true, ApplyEpilogue<T>>(
+             dev, B, p.ldA, from, p.ldX, {p.m, p.n, p.m, n, false}, ap, stream)) != VR_SUCCESS)
       return e;
   }
   return VR_SUCCESS;

@@ -21,7 +21,6 @@
 #include <cstdint>
 
 #include "gemm.cuh"
-#include "gemm_host.h"
 
 namespace vr {
 namespace {
@@ -449,34 +448,31 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   return true;
 }
 
-// One product: the operands' extents and layouts, the launch.
-template <typename T, bool AMN, bool BMN, int CHUNK, class Epi>
+// One product; pairs of CTAs where the rows fill them.
+template <typename T, bool AMN, bool BMN, int CHUNK, bool SPLIT, class Epi>
 vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* b, size_t bLd,
                     size_t M, size_t N, size_t K, const int* dynM, const int* dynK,
                     typename Epi::Args& epi, void* stream) {
-  using Shape = GemmShape<kBN, 1>;
-  const void* fn = (const void*)gemm_kernel<T, kBN, 1, AMN, BMN, CHUNK, Epi>;
-  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-  GemmArgs g = {};
-  vr_result_t e = gemm_operand(&g.a[0], a, bf16, AMN ? M : K, AMN ? K : M, 1, aLd * 2,
-                               aLd * 2 * (AMN ? K : M), AMN ? kTileK : kTileM);
-  if (e != VR_SUCCESS) return e;
-  e = gemm_operand(&g.b[0], b, bf16, BMN ? N : K, BMN ? K : N, 1, bLd * 2,
-                   bLd * 2 * (BMN ? K : N), BMN ? kTileK : kBN);
-  if (e != VR_SUCCESS) return e;
-  if ((e = gemm_prepare(fn, dev.device, Shape::kSmem)) != VR_SUCCESS) return e;
-  g.M = (int)M;
-  g.N = (int)N;
-  g.K = (int)K;
-  g.batch = 1;
-  g.dynM = dynM;
-  g.dynK = dynK;
-  g.status = dev.status;
-  g.timeoutNs = dev.timeoutNs;
-  const size_t tiles = (M + kTileM - 1) / kTileM * ((N + kBN - 1) / kBN);
-  void* args[] = {&g, &epi};
-  return op_launch(fn, dim3((unsigned)std::min<size_t>(tiles, dev.sms)), dim3(kGemmThreads), args,
-                   Shape::kSmem, stream);
+  const Operand oa = {a, nullptr, aLd}, ob = {b, nullptr, bLd};
+  const GemmSize z = {M, N, K, 1, false};
+  if (M <= kTileM) {
+    if constexpr (SPLIT) {
+      const int s = gemm_shares<kBN, false>(z, dev.sms);
+      if (s > 1)
+        return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, false, true, Epi>(dev, oa, ob, z, dynM, dynK,
+                                                                         epi, s, stream);
+    }
+    return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, false, false, Epi>(dev, oa, ob, z, dynM, dynK,
+                                                                      epi, 1, stream);
+  }
+  if constexpr (SPLIT) {
+    const int s = gemm_shares<kBN, true>(z, dev.sms);
+    if (s > 1)
+      return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, true, true, Epi>(dev, oa, ob, z, dynM, dynK,
+                                                                      epi, s, stream);
+  }
+  return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, true, false, Epi>(dev, oa, ob, z, dynM, dynK, epi,
+                                                                   1, stream);
 }
 
 template <typename T>
@@ -513,7 +509,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   if (p.T && p.padWeight && (e = pad(&weight, &weightStride, p.V, p.weight)) != VR_SUCCESS) return e;
   if (p.T) {
     StatsEpilogue::Args epi = {target, targetLogit, parts, (int)p.nParts};
-    if ((e = product<T, false, false, kStatsChunk, StatsEpilogue>(dev, hidden, hiddenStride, weight,
+    if ((e = product<T, false, false, kStatsChunk, false, StatsEpilogue>(dev, hidden, hiddenStride, weight,
                                                      weightStride, p.T, p.V, p.D, nullptr, nullptr,
                                                      epi, stream)) != VR_SUCCESS)
       return e;
@@ -559,7 +555,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
     typename FactorEpilogue<T>::Args fa = {packedTarget, packedLse2, factors, (long long)p.piece,
                                            (int)v0};
-    if ((e = product<T, false, false, 0, FactorEpilogue<T>>(
+    if ((e = product<T, false, false, 0, false, FactorEpilogue<T>>(
              dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
              stream)) != VR_SUCCESS)
       return e;
@@ -567,7 +563,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
       typename HiddenEpilogue<T>::Args ha = {
           reinterpret_cast<float*>(w + p.sum), (long long)p.sumLd, static_cast<T*>(dHidden), token,
           state, i == 0, i + 1 == p.nPieces, vecH};
-      if ((e = product<T, false, true, 0, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
+      if ((e = product<T, false, true, 0, true, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
                                                           weightStride, p.T, p.D, rows,
                                                           &state->valid, nullptr, ha, stream)) !=
           VR_SUCCESS)
@@ -575,7 +571,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     }
     if (dWeight) {
       typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, vecW};
-      if ((e = product<T, true, true, 0, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
+      if ((e = product<T, true, true, 0, false, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
                                                          p.D, p.T128, nullptr, &state->valid, wa,
                                                          stream)) != VR_SUCCESS)
         return e;
