@@ -80,6 +80,15 @@ __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map
         : "memory");
   }
 }
+// True in one lane of a converged warp (known to be one to the compiler,
+// which keeps what that lane computes in uniform registers).
+__device__ __forceinline__ bool elected() {
+  unsigned is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -183,25 +192,37 @@ __device__ __forceinline__ void tmem_fence_after() {
 __device__ __forceinline__ void tmem_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
-// 32 columns of the warp's 32 accumulator rows: lane = row.
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
+// 32 columns of the warp's 32 accumulator rows: lane = row.  The values are
+// there after tmem_wait, through which they are passed so that nothing uses
+// them earlier.
+__device__ __forceinline__ void tmem_issue32(uint32_t addr, float (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(addr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-
+__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+  tmem_issue32(addr, v);
+  tmem_wait(v);
+}
 __device__ __forceinline__ float tmem_load1(uint32_t addr) {
   uint32_t r;
   asm volatile(
@@ -280,12 +301,16 @@ struct GemmShape {
   static constexpr int kBBytes = kBRows * kTileK * 2;
   static constexpr int kStageBytes = PARTS * (kABytes + kBBytes);
   static constexpr int kTileRows = PAIR ? 2 * kTileM : kTileM;
-  // columns of an accumulator: with two planes the products of a low plane
-  // are summed apart (their size would not survive being added one by one)
-  static constexpr int kAcc = PARTS * BN;
+  // Two accumulators.  With two planes three, since they change hands every
+  // few slices (three cover the way there and back: 0.47 us a slice instead of
+  // 0.57), and one more for the products of a low plane, which are summed
+  // apart over the whole tile (their size would not survive being added one
+  // by one).
+  static constexpr int kAccs = PARTS == 2 ? 3 : 2;
+  static constexpr int kTmem = 2 * PARTS * BN;
   static constexpr int kStages = (kGemmSmem - 2048) / kStageBytes;
   static constexpr int kSmem = 2048 + kStages * kStageBytes;  // header, alignment
-  static_assert(kStages >= 2 && 2 * kAcc <= 512, "too large");
+  static_assert(kStages >= 2 && kTmem <= 512, "too large");
   static_assert(kStages * kStageBytes >= kTileM * BN * 4, "a share's sums do not fit");
 };
 
@@ -343,11 +368,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr int kStages = Shape::kStages;
   constexpr int kCtas = PAIR ? 2 : 1;  // that share a tile's products
   extern __shared__ unsigned char smemRaw[];
-  __shared__ alignas(8) uint64_t bars[2 * kStages + 5];
+  constexpr int kAccs = Shape::kAccs;
+  __shared__ alignas(8) uint64_t bars[2 * kStages + 2 * kAccs + 2];
   __shared__ uint32_t tmemBase;
   __shared__ volatile int abortFlag;
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // (a shuffle, so that the role is known to be the warp's)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = PAIR || SPLIT ? cluster_rank() : 0u;
   const uint32_t inPair = PAIR ? rank & 1u : 0u;
   const bool leader = inPair == 0;
@@ -357,8 +384,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
   auto accFull = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
-  auto accEmpty = [&](int i) { return bar0 + 8u * (2 * kStages + 2 + i); };
-  const uint32_t drained = bar0 + 8u * (2 * kStages + 4);
+  auto accEmpty = [&](int i) { return bar0 + 8u * (2 * kStages + kAccs + i); };
+  const uint32_t drained = bar0 + 8u * (2 * kStages + 2 * kAccs), lowEmpty = drained + 8u;
   auto wait = [&](uint32_t bar, unsigned parity, bool honorAbort = true) {
     return PAIR ? wait_cluster(bar, parity, &abortFlag, honorAbort, g.timeoutNs)
                 : wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
@@ -369,11 +396,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       mbar_init(accFull(i), 1);
       mbar_init(accEmpty(i), kEpilogueWarps * kCtas);
     }
     mbar_init(drained, 1);
+    mbar_init(lowEmpty, kEpilogueWarps * kCtas);
     abortFlag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async;" ::: "memory");
@@ -382,13 +410,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if constexpr (PAIR) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                        smem_addr(&tmemBase)),
-                   "r"(2 * Shape::kAcc)
+                   "r"(Shape::kTmem)
                    : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     } else {
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                        smem_addr(&tmemBase)),
-                   "r"(2 * Shape::kAcc)
+                   "r"(Shape::kTmem)
                    : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int firstTile = (int)blockIdx.x / (kCtas * shares);
   const int tileStep = SPLIT ? tiles + 1 : (int)gridDim.x / kCtas;  // SPLIT: one tile
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     int s = 0, turn = 0;
     bool ok = true;
     long long issued = 0;
@@ -430,37 +458,47 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
       const int m0 = o.m0 + (int)inPair * kTileM, n0 = o.n0 + (int)inPair * Shape::kBRows;
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = wait(empty(s), turn ^ 1);
+        ok = __all_sync(0xffffffffu, wait(empty(s), turn ^ 1)) != 0;
         if (!ok) break;
-        if (leader) mbar_arrive_expect_tx(full(s), kCtas * Shape::kStageBytes);
-        uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes;
-        const int k0 = kb * kTileK;
+        if (elected()) {
+          if (leader) mbar_arrive_expect_tx(full(s), kCtas * Shape::kStageBytes);
+          uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes;
+          const int k0 = kb * kTileK;
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-          if (AMN) {
+          for (int p = 0; p < PARTS; ++p) {
+            if (AMN) {
 #pragma unroll
-            for (int i = 0; i < kTileM / 64; ++i)
-              tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.a[p], m0 + i * 64, k0, o.z, full(s));
-          } else {
-            tensor_load<PAIR>(dst, &g.a[p], k0, m0, o.z, full(s));
+              for (int i = 0; i < kTileM / 64; ++i)
+                tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.a[p], m0 + i * 64, k0, o.z,
+                                  full(s));
+            } else {
+              tensor_load<PAIR>(dst, &g.a[p], k0, m0, o.z, full(s));
+            }
+            dst += Shape::kABytes;
           }
-          dst += Shape::kABytes;
-        }
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-          if (BMN) {
+          for (int p = 0; p < PARTS; ++p) {
+            if (BMN) {
 #pragma unroll
-            for (int i = 0; i < Shape::kBRows / 64; ++i)
-              tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.b[p], n0 + i * 64, k0, o.z, full(s));
-          } else {
-            tensor_load<PAIR>(dst, &g.b[p], k0, n0, o.z, full(s));
+              for (int i = 0; i < Shape::kBRows / 64; ++i)
+                tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.b[p], n0 + i * 64, k0, o.z,
+                                  full(s));
+            } else {
+              tensor_load<PAIR>(dst, &g.b[p], k0, n0, o.z, full(s));
+            }
+            dst += Shape::kBBytes;
           }
-          dst += Shape::kBBytes;
         }
+        __syncwarp();
         ++issued;
         if (++s == kStages) s = 0, turn ^= 1;
       }
     }
+    // The last slices' stages are handed back before the CTA leaves: in a pair
+    // that arrival comes from the other CTA's products and would otherwise
+    // land in whatever runs on this SM next.
+    for (long long i = issued > kStages ? issued - kStages : 0; ok && i < issued; ++i)
+      ok = __all_sync(0xffffffffu, wait(empty((int)(i % kStages)), (int)(i / kStages & 1))) != 0;
     if (!ok) {
       raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
       // copies in flight land before the CTA's shared memory is given up (in a
@@ -469,49 +507,63 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (long long i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
           wait(full((int)(i % kStages)), (int)(i / kStages & 1), false);
     }
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1 && leader) {
+    // the whole warp walks the slices and waits, one lane issues
     constexpr uint32_t idesc = mma_idesc<T>(Shape::kTileRows, BN, AMN, BMN);
     constexpr unsigned kSlab = 64 * kTileK * 2;  // MN-major: bytes of a 64-wide slab
     // one product takes 16 k: 32 bytes along a K-major row, 16 rows of 128
     // bytes of an MN-major slab
     constexpr unsigned aStep = (AMN ? 16 * 128 : 32) >> 4, bStep = (BMN ? 16 * 128 : 32) >> 4;
-    int s = 0, turn = 0, buf = 0, bufTurn = 0;
+    const uint64_t aDesc0 = operand_desc(stage0, AMN ? kSlab : 16, 1024);
+    const uint64_t bDesc0 = operand_desc(stage0 + PARTS * Shape::kABytes, BMN ? kSlab : 16, 1024);
+    int s = 0, turn = 0, buf = 0, bufTurn = 0, lowTurn = 0;
     bool ok = true;
+    auto ready = [&](uint32_t bar, unsigned parity) {
+      const bool mine = wait(bar, parity);
+      return __all_sync(0xffffffffu, mine) != 0;
+    };
     for (int t = firstTile; ok && t < tiles; t += tileStep) {
+      if (PARTS == 2 && blocks) {
+        ok = ready(lowEmpty, lowTurn ^ 1);
+        lowTurn ^= 1;
+      }
       for (int c0 = 0; ok && c0 < blocks; c0 += chunk) {
-        ok = wait(accEmpty(buf), bufTurn ^ 1);
+        ok = ready(accEmpty(buf), bufTurn ^ 1);
         if (!ok) break;
         tmem_fence_after();
-        const uint32_t acc = tmem + (unsigned)buf * Shape::kAcc;
+        const uint32_t acc = tmem + (unsigned)(buf * BN), low = tmem + (unsigned)(kAccs * BN);
         const int c1 = min(c0 + chunk, blocks);
         for (int kb = c0; kb < c1; ++kb) {
-          ok = wait(full(s), turn);
+          ok = ready(full(s), turn);
           if (!ok) break;
           tmem_fence_after();
-          const uint32_t base = stage0 + (unsigned)s * Shape::kStageBytes;
+          if (elected()) {
+            const uint64_t at = (uint64_t)((unsigned)s * (Shape::kStageBytes >> 4));
 #pragma unroll
-          for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
-            const uint32_t aAt = base + (p == 2 ? Shape::kABytes : 0);
-            const uint32_t bAt = base + PARTS * Shape::kABytes + (p == 1 ? Shape::kBBytes : 0);
-            const uint64_t aDesc = operand_desc(aAt, AMN ? kSlab : 16, 1024);
-            const uint64_t bDesc = operand_desc(bAt, BMN ? kSlab : 16, 1024);
+            for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
+              const uint64_t aDesc = aDesc0 + at + (p == 2 ? Shape::kABytes >> 4 : 0);
+              const uint64_t bDesc = bDesc0 + at + (p == 1 ? Shape::kBBytes >> 4 : 0);
 #pragma unroll
-            for (int k = 0; k < kTileK / 16; ++k)
-              mma_f16<PAIR>(p ? acc + BN : acc, aDesc + k * aStep, bDesc + k * bStep, idesc,
-                            (kb - c0) | (p == 2) | k);
+              for (int k = 0; k < kTileK / 16; ++k)
+                mma_f16<PAIR>(p ? low : acc, aDesc + k * aStep, bDesc + k * bStep, idesc,
+                              p ? kb | (p == 2) | k : (kb - c0) | k);
+            }
+            mma_commit<PAIR>(empty(s), pairMask);
+            if (kb + 1 == c1) mma_commit<PAIR>(accFull(buf), pairMask);
           }
-          mma_commit<PAIR>(empty(s), pairMask);
+          __syncwarp();
           if (++s == kStages) s = 0, turn ^= 1;
         }
         if (!ok) break;
-        mma_commit<PAIR>(accFull(buf), pairMask);
-        if (++buf == 2) buf = 0, bufTurn ^= 1;
+        if (++buf == kAccs) buf = 0, bufTurn ^= 1;
       }
     }
     if (!ok) {
       raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
-      mma_commit<PAIR>(drained, pairMask);
-      wait(drained, 0, false);
+      if (elected()) {
+        mma_commit<PAIR>(drained, pairMask);
+        wait(drained, 0, false);
+      }
     }
   } else if (warp >= 4) {
     const int quad = warp % 4, half = (warp - 4) / 4;
@@ -528,17 +580,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tmem_fence_after();
       return true;
     };
-    auto release = [&]() {
+    auto hand_back = [&](uint32_t bar) {
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR) {
-          peer_arrive(peer_addr(accEmpty(buf), rank & ~1u));
+          peer_arrive(peer_addr(bar, rank & ~1u));
         } else {
-          mbar_arrive(accEmpty(buf));
+          mbar_arrive(bar);
         }
       }
-      if (++buf == 2) buf = 0, bufTurn ^= 1;
+    };
+    auto release = [&]() {
+      hand_back(accEmpty(buf));
+      if (++buf == kAccs) buf = 0, bufTurn ^= 1;
     };
     for (int t = firstTile; t < tiles; t += tileStep) {
       Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
@@ -559,20 +614,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int c0 = 0; c0 < blocks; c0 += chunk) {
           left = !next();
           if (left) break;
+          auto add = [&](uint32_t at) {  // two loads in flight
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
-            float v[32];
-            const uint32_t at = quadBase + (unsigned)(buf * Shape::kAcc + half * kHalf + c);
-            tmem_load32(at, v);
+            for (int c = 0; c < kHalf; c += 64) {
+              float v[32], w[32];
+              tmem_issue32(at + (unsigned)c, v);
+              tmem_issue32(at + (unsigned)c + 32, w);
+              tmem_wait(v);
+              tmem_wait(w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[c + i] += v[i];
-            if (PARTS == 2) {
-              tmem_load32(at + BN, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sum[c + i] += v[i];
+              for (int i = 0; i < 32; ++i) sum[c + i] += v[i], sum[c + 32 + i] += w[i];
             }
-          }
+          };
+          add(quadBase + (unsigned)(buf * BN + half * kHalf));
           release();
+          if (PARTS == 2 && c0 + chunk >= blocks) {  // done with the last slice's
+            add(quadBase + (unsigned)(kAccs * BN + half * kHalf));
+            hand_back(lowEmpty);
+          }
         }
         if (left) break;
         const RegAcc<kHalf> acc{sum, half * kHalf};
@@ -588,7 +647,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       } else {
         if (blocks && !next()) break;
-        const TmemAcc acc{quadBase + (unsigned)buf * Shape::kAcc, blocks != 0};
+        const TmemAcc acc{quadBase + (unsigned)(buf * BN), blocks != 0};
         if constexpr (SPLIT) {
 #pragma unroll
           for (int c = 0; c < kHalf; c += 32) {
@@ -634,10 +693,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_fence_after();
     if constexpr (PAIR) {
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                   "r"(2 * Shape::kAcc));
+                   "r"(Shape::kTmem));
     } else {
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                   "r"(2 * Shape::kAcc));
+                   "r"(Shape::kTmem));
     }
   }
 }

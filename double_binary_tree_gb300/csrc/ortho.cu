@@ -380,31 +380,49 @@ bool in_range(const float* coefs, int steps) {
 
 constexpr float kCoefs[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// One product of a step.  Pairs of CTAs where X has more rows than one CTA
-// takes; 256 columns where that leaves no SM idle (one plane: two planes fill
-// tensor memory at 128); k shared out where the tiles leave SMs idle.
+// One product of a step, on the tile shape that a model of the measured
+// times puts first.  A slice of 64 k takes 0.205 us on a 128 x 128 tile of one
+// CTA, 0.167 us on a 256 x 128 tile of a pair (half the operand traffic per
+// SM), 0.31 us on a 256 x 256 one (two planes: 0.56 and 0.47 us, no 256-wide
+// tile, tensor memory holds 128 columns), the epilogue of the last round 3 us
+// per 128 columns, and joining shares of k 2 us.  Wide tiles win when there
+// are many, single CTAs when they fill the SMs once, shares when few tiles
+// leave SMs idle.
 template <int PARTS, bool BMN, class Epi>
 vr_result_t product(const OpDevice& dev, const Planes& a, size_t aLd, const Planes& b, size_t bLd,
                     const GemmSize& z, typename Epi::Args& epi, void* stream) {
   const Operand oa = {a.hi, a.lo, aLd}, ob = {b.hi, b.lo, bLd};
   constexpr int CHUNK = PARTS == 2 ? kSplitChunk : 0;
-  if (z.M <= kTileM) {
-    const int s = gemm_shares<128, false>(z, dev.sms);
-    return s > 1 ? gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, false, true, Epi>(
-                       dev, oa, ob, z, nullptr, nullptr, epi, s, stream)
-                 : gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, false, false, Epi>(
-                       dev, oa, ob, z, nullptr, nullptr, epi, 1, stream);
+  const double slices = (double)((z.K + kTileK - 1) / kTileK);
+  double best = 0;
+  int shape = -1, shares = 1;  // shape: 0 single, 1 pair, 2 wide pair
+  auto offer = [&](int which, size_t tiles, double slice, int s) {
+    const size_t ctas = (which ? 2 : 1) * (size_t)s;
+    // clusters of four and eight leave some SMs of each group of SMs unused
+    const size_t room = std::max<size_t>(1, (ctas > 2 ? dev.sms * 7 / 8 : dev.sms) / ctas);
+    const double rounds = (double)((tiles + room - 1) / room);
+    const double t = rounds * std::ceil(slices / s) * slice + (which == 2 ? 6 : 3) + (s > 1 ? 2 : 0);
+    if (shape < 0 || t < best) best = t, shape = which, shares = s;
+  };
+  const size_t singles = gemm_tiles<128, false>(z), pairs = gemm_tiles<128, true>(z);
+  for (int s = 1; s <= 8 && s <= slices; s *= 2) {
+    offer(0, singles, PARTS == 2 ? 0.56 : 0.205, s);
+    if (s <= 4 && z.M > kTileM) offer(1, pairs, PARTS == 2 ? 0.47 : 0.167, s);
   }
+  if (PARTS == 1 && z.M > kTileM) offer(2, gemm_tiles<256, true>(z), 0.31, 1);
+#define VR_PRODUCT(BN, PAIR, SPLIT)                                                      \
+  return gemm_launch<__half, BN, PARTS, false, BMN, CHUNK, PAIR, SPLIT, Epi>(            \
+      dev, oa, ob, z, nullptr, nullptr, epi, shares, stream)
   if constexpr (PARTS == 1) {
-    if (2 * gemm_tiles<256, true>(z) >= (size_t)dev.sms - 1)
-      return gemm_launch<__half, 256, PARTS, false, BMN, CHUNK, true, false, Epi>(
-          dev, oa, ob, z, nullptr, nullptr, epi, 1, stream);
+    if (shape == 2) VR_PRODUCT(256, true, false);
   }
-  const int s = gemm_shares<128, true>(z, dev.sms);
-  return s > 1 ? gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, true, true, Epi>(
-                     dev, oa, ob, z, nullptr, nullptr, epi, s, stream)
-               : gemm_launch<__half, 128, PARTS, false, BMN, CHUNK, true, false, Epi>(
-                     dev, oa, ob, z, nullptr, nullptr, epi, 1, stream);
+  if (shape == 1) {
+    if (shares > 1) VR_PRODUCT(128, true, true);
+    VR_PRODUCT(128, true, false);
+  }
+  if (shares > 1) VR_PRODUCT(128, false, true);
+  VR_PRODUCT(128, false, false);
+#undef VR_PRODUCT
 }
 
 template <typename T, int PARTS>
