@@ -294,7 +294,7 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool aMn, bool bM
          (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
-template <int BN, int PARTS, bool PAIR>
+template <int BN, int PARTS, bool PAIR, int AUX = 0>
 struct GemmShape {
   static constexpr int kABytes = kTileM * kTileK * 2;
   static constexpr int kBRows = PAIR ? BN / 2 : BN;
@@ -308,10 +308,33 @@ struct GemmShape {
   // by one).
   static constexpr int kAccs = PARTS == 2 ? 3 : 2;
   static constexpr int kTmem = 2 * PARTS * BN;
-  static constexpr int kStages = (kGemmSmem - 2048) / kStageBytes;
-  static constexpr int kSmem = 2048 + kStages * kStageBytes;  // header, alignment
+  static constexpr int kStages = (kGemmSmem - 2048 - AUX) / kStageBytes;
+  // alignment, the stages, the epilogue's tiles
+  static constexpr int kSmem = 2048 + kStages * kStageBytes + AUX;
   static_assert(kStages >= 2 && kTmem <= 512, "too large");
   static_assert(kStages * kStageBytes >= kTileM * BN * 4, "a share's sums do not fit");
+};
+
+// An epilogue that reads and writes 16-bit tiles (Epi::kAux) works on units of
+// 32 columns: one of warps 2 and 3 loads a unit's tiles into shared memory,
+// the four warps of its half of the accumulator change them in place, and the
+// same helper warp stores them.  Two buffers take turns, so a unit's copies
+// overlap the work on the other.  (Read and written by each thread straight
+// from memory, row by row, these tiles took more time than the products: 32
+// rows are 32 lines an access.)
+constexpr int kAuxCols = 32;
+constexpr int kAuxTile = kTileM * kAuxCols * 2;  // 128 rows of 64 bytes, 64-byte swizzled
+constexpr int kAuxHalf = 2 * 2 * kAuxTile;       // two buffers of two planes
+struct AuxArgs {
+  CUtensorMap in[2], out[2];  // the planes as 32 x 128 tiles
+  int nIn, nOut;              // planes loaded and stored
+};
+struct AuxTile {
+  uint32_t smem;
+  // 16 bytes (8 columns) of a row
+  __device__ __forceinline__ uint32_t piece(int plane, int row, int i) const {
+    return smem + (unsigned)(plane * kAuxTile + row * 64 + ((i ^ (row >> 1 & 3)) << 4));
+  }
 };
 
 // Blocks of 2048 rows are walked column by column, so that the rows' and
@@ -352,7 +375,10 @@ __device__ __forceinline__ Tile tile_of(int t, int tilesM, int tilesN, bool tria
 //                              int M, const Acc& acc)
 // (templates: int COLS, class Acc) called by every thread of the epilogue warps for its accumulator row `row`
 // (of the tile) and its columns [col0, col0 + COLS) of the tile; acc(c, v)
-// fetches the 32 accumulator columns from c.
+// fetches the 32 accumulator columns from c.  Epi::kAux (without SPLIT):
+// unit(e, g, o, row, n, c, M, acc, tile) in place of run, for the 32 columns n
+// of the product, c of the tile, unless skip(g, o, n, M), which then holds for
+// the rest of the tile too; e.aux names the planes.
 //
 // CHUNK > 0: the tensor cores truncate where they add a product to the
 // accumulator (one addition per 16 k), an error that grows with the length of
@@ -363,13 +389,14 @@ template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, bool PAI
           class Epi>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ typename Epi::Args e) {
-  using Shape = GemmShape<BN, PARTS, PAIR>;
+  constexpr bool kAux = Epi::kAux && !SPLIT;
+  using Shape = GemmShape<BN, PARTS, PAIR, kAux ? 2 * kAuxHalf : 0>;
   static_assert(PARTS == 1 || CHUNK > 0, "two planes are summed in the epilogue warps");
   constexpr int kStages = Shape::kStages;
   constexpr int kCtas = PAIR ? 2 : 1;  // that share a tile's products
   extern __shared__ unsigned char smemRaw[];
   constexpr int kAccs = Shape::kAccs;
-  __shared__ alignas(8) uint64_t bars[2 * kStages + 2 * kAccs + 2];
+  __shared__ alignas(8) uint64_t bars[2 * kStages + 2 * kAccs + 2 + (kAux ? 8 : 0)];
   __shared__ uint32_t tmemBase;
   __shared__ volatile int abortFlag;
 
@@ -386,6 +413,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto accFull = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
   auto accEmpty = [&](int i) { return bar0 + 8u * (2 * kStages + kAccs + i); };
   const uint32_t drained = bar0 + 8u * (2 * kStages + 2 * kAccs), lowEmpty = drained + 8u;
+  auto auxFull = [&](int half, int i) { return lowEmpty + 8u * (1 + 2 * half + i); };
+  auto auxDone = [&](int half, int i) { return lowEmpty + 8u * (5 + 2 * half + i); };
+  const uint32_t aux0 = stage0 + (unsigned)(kStages * Shape::kStageBytes);
   auto wait = [&](uint32_t bar, unsigned parity, bool honorAbort = true) {
     return PAIR ? wait_cluster(bar, parity, &abortFlag, honorAbort, g.timeoutNs)
                 : wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
@@ -402,6 +432,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     mbar_init(drained, 1);
     mbar_init(lowEmpty, kEpilogueWarps * kCtas);
+    for (int i = 0; kAux && i < 4; ++i) {
+      mbar_init(auxFull(i / 2, i % 2), 1);
+      mbar_init(auxDone(i / 2, i % 2), 4);
+    }
     abortFlag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async;" ::: "memory");
@@ -595,6 +629,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       hand_back(accEmpty(buf));
       if (++buf == kAccs) buf = 0, bufTurn ^= 1;
     };
+    int unit = 0;  // of the Aux tiles
+    auto units = [&](const Tile& o, const auto& acc) {
+      if constexpr (kAux) {
+#pragma unroll
+        for (int c = 0; c < kHalf; c += kAuxCols) {
+          const int n = o.n0 + half * kHalf + c, b = unit & 1;
+          if (Epi::skip(g, o, n, M)) break;
+          const bool there = wait(auxFull(half, b), (unsigned)(unit >> 1 & 1));
+          if (!__all_sync(0xffffffffu, there)) {
+            raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
+            return false;
+          }
+          Epi::unit(e, g, o, row, n, half * kHalf + c, M, acc,
+                    AuxTile{aux0 + (unsigned)(half * kAuxHalf + b * (2 * kAuxTile))});
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(auxDone(half, b));
+          ++unit;
+        }
+      }
+      return true;
+    };
     for (int t = firstTile; t < tiles; t += tileStep) {
       Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
       o.m0 += (int)inPair * kTileM;
@@ -642,6 +698,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             acc(half * kHalf + c, v);
             put(half * kHalf + c, v);
           }
+        } else if constexpr (kAux) {
+          if (!units(o, acc)) break;
         } else {
           Epi::template run<kHalf>(e, g, o, row, half * kHalf, M, acc);
         }
@@ -655,11 +713,70 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             acc(half * kHalf + c, v);
             put(half * kHalf + c, v);
           }
+        } else if constexpr (kAux) {
+          if (!units(o, acc)) break;
         } else {
           Epi::template run<kHalf>(e, g, o, row, half * kHalf, M, acc);
         }
         if (blocks) release();
       }
+    }
+  } else if (kAux && warp >= 2) {
+    if constexpr (kAux) {
+      const int half = warp - 2;
+      int unit = 0, atX[2] = {0, 0}, atY[2] = {0, 0}, atZ[2] = {0, 0};
+      bool ok = true;
+      auto tile_at = [&](int b, int p) {
+        return aux0 + (unsigned)(half * kAuxHalf + b * (2 * kAuxTile) + p * kAuxTile);
+      };
+      // unit v has been worked on: stores its tiles, and waits until they
+      // are read when its buffer is wanted again
+      auto finish = [&](int v) {
+        const int b = v & 1;
+        ok = __all_sync(0xffffffffu, wait(auxDone(half, b), (unsigned)(v >> 1 & 1))) != 0;
+        if (ok && e.aux.nOut && elected()) {
+          for (int p = 0; p < e.aux.nOut; ++p)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], "
+                "[%4];" ::"l"(&e.aux.out[p]),
+                "r"(atX[b]), "r"(atY[b]), "r"(atZ[b]), "r"(tile_at(b, p))
+                : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        __syncwarp();
+      };
+      for (int t = firstTile; ok && t < tiles; t += tileStep) {
+        Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
+        o.m0 += (int)inPair * kTileM;
+        for (int c = 0; ok && c < kHalf; c += kAuxCols) {
+          const int n = o.n0 + half * kHalf + c, b = unit & 1;
+          if (Epi::skip(g, o, n, M)) break;
+          if (unit >= 2) finish(unit - 2);
+          if (!ok) break;
+          if (elected()) {
+            if (e.aux.nIn) {
+              mbar_arrive_expect_tx(auxFull(half, b), (unsigned)(e.aux.nIn * kAuxTile));
+              for (int p = 0; p < e.aux.nIn; ++p)
+                tensor_load<false>(tile_at(b, p), &e.aux.in[p], n, o.m0, o.z, auxFull(half, b));
+            } else {
+              mbar_arrive(auxFull(half, b));
+            }
+          }
+          __syncwarp();
+          atX[b] = n, atY[b] = o.m0, atZ[b] = o.z;
+          ++unit;
+        }
+      }
+      for (int v = max(0, unit - 2); ok && v < unit; ++v) finish(v);
+      if (!ok) {
+        raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
+        // loads in flight land before the CTA's shared memory is given up
+        for (int v = max(0, unit - 2); v < unit; ++v)
+          wait(auxFull(half, v & 1), (unsigned)(v >> 1 & 1), false);
+      }
+      if (elected()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      __syncwarp();
     }
   }
   if constexpr (SPLIT) {
@@ -740,7 +857,7 @@ template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, bool PAI
 vr_result_t gemm_launch(const OpDevice& dev, const Operand& a, const Operand& b, const GemmSize& z,
                         const int* dynM, const int* dynK, typename Epi::Args& epi, int shares,
                         void* stream) {
-  using Shape = GemmShape<BN, PARTS, PAIR>;
+  using Shape = GemmShape<BN, PARTS, PAIR, Epi::kAux && !SPLIT ? 2 * kAuxHalf : 0>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const void* fn = (const void*)gemm_kernel<T, BN, PARTS, AMN, BMN, CHUNK, PAIR, SPLIT, Epi>;
   GemmArgs g = {};

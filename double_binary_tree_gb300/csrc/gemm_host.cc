@@ -39,17 +39,19 @@ std::set<std::pair<const void*, int>> g_prepared;
 }  // namespace
 
 vr_result_t gemm_operand(CUtensorMap* map, const void* p, bool bf16, size_t inner, size_t rows,
-                         size_t batch, size_t rowStride, size_t batchStride, int boxRows) {
+                         size_t batch, size_t rowStride, size_t batchStride, int boxRows,
+                         int boxCols) {
   const EncodeFn encode = encoder();
   if (!encode) return VR_ERR_CUDA;
   const cuuint64_t dims[3] = {inner, rows, batch};
   const cuuint64_t strides[2] = {rowStride, batchStride};
-  const cuuint32_t box[3] = {64, (cuuint32_t)boxRows, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)boxCols, (cuuint32_t)boxRows, 1};
   const cuuint32_t one[3] = {1, 1, 1};
   const CUresult r = encode(
       map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
       const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      boxCols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? VR_SUCCESS : VR_ERR_CUDA;
 }

@@ -75,22 +75,72 @@ __device__ __forceinline__ void residue(float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] -= __half2float(__float2half_rn(v[i]));
 }
 
-// A = X X^T (from = null) or B = b A + c A A, at the planes' scale; the block
-// and, below the diagonal, its mirror image.
+// What an epilogue of a step does with the sum of products v of an element:
+//   v <- byAcc v + byFrom (from_hi + from_lo) [- diagonal]
+// into the planes `to`: on tiles in shared memory (unit; aux.nIn and aux.nOut
+// planes read and written), or row by row where k is shared out over a
+// cluster (run).
+struct PlaneArgs {
+  Planes from, to;
+  long long ld, size;         // elements of a row, of a matrix
+  float byFrom, byAcc, diagonal;
+};
+
+// A thread's row of a tile.
+__device__ __forceinline__ void add_tile(const AuxTile& tile, int plane, int row, float by,
+                                         float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                 : "r"(tile.piece(plane, row, i))
+                 : "memory");
+    const __half2* h = reinterpret_cast<const __half2*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(h[j]);
+      v[8 * i + 2 * j] = fmaf(by, f.x, v[8 * i + 2 * j]);
+      v[8 * i + 2 * j + 1] = fmaf(by, f.y, v[8 * i + 2 * j + 1]);
+    }
+  }
+}
+__device__ __forceinline__ void store_tile(const AuxTile& tile, int plane, int row,
+                                           const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 q;
+    __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile.piece(plane, row, i)),
+                 "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                 : "memory");
+  }
+}
+
+// A = X X^T (no `from`) or B = b A + c A A - d I: the block and, below the
+// diagonal, its mirror image.
+// (Its planes are m x m: not worth the stages that Aux tiles take from the
+// products, 22 against 26 us at 4 x 1024 x 4096.)
 struct SymmetricEpilogue {
+  static constexpr bool kAux = false;
   struct Args {
-    Planes from, to;
-    long long ld, size;  // of a row, of a matrix
-    float byFrom, byAcc;
-    float diagonal;      // subtracted from it
-    int low;             // the result's low plane is wanted
+    PlaneArgs p;
+    int nIn, nOut;  // planes read and written
   };
+  static __device__ __forceinline__ void mirror(const Args& a, const GemmArgs& g, const Tile& o,
+                                                __half* plane, int r, int n, const float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)  // the lanes' rows are consecutive columns here
+      if (n + i < g.N) plane[o.z * a.p.size + (n + i) * a.p.ld + r] = __float2half_rn(v[i]);
+  }
   template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
                                              int row, int col0, int M, const Acc& acc) {
     const int r = o.m0 + row, blockR = o.m0 / kTileM, blockC = (o.n0 + col0) / kTileM;
     const bool live = r < M && blockC <= blockR;
-    const long long base = o.z * a.size;
+    const long long base = o.z * a.p.size;
 #pragma unroll
     for (int c = 0; c < COLS; c += 32) {
       const int n = o.n0 + col0 + c;
@@ -98,30 +148,22 @@ struct SymmetricEpilogue {
       float v[32];
       acc(col0 + c, v);
       if (!live) continue;
-      const long long at = base + r * a.ld + n;
+      const long long at = base + r * a.p.ld + n;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= a.byAcc;
-      if (a.from.hi) {
-        add_plane(a.from.hi + at, a.byFrom, v);
-        if (a.low) add_plane(a.from.lo + at, a.byFrom, v);
-        if (blockC == blockR) {
+      for (int i = 0; i < 32; ++i) v[i] *= a.p.byAcc;
+      if (a.nIn) add_plane(a.p.from.hi + at, a.p.byFrom, v);
+      if (a.nIn > 1) add_plane(a.p.from.lo + at, a.p.byFrom, v);
+      if (blockC == blockR) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n + i == r) v[i] -= a.diagonal;
-        }
+        for (int i = 0; i < 32; ++i)
+          if (n + i == r) v[i] -= a.p.diagonal;
       }
-      auto put = [&](__half* plane) {
-        store_plane(plane + at, v);
-        if (blockC < blockR) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n + i < g.N) plane[base + (n + i) * a.ld + r] = __float2half_rn(v[i]);
-        }
-      };
-      put(a.to.hi);
-      if (a.low) {
+      store_plane(a.p.to.hi + at, v);
+      if (blockC < blockR) mirror(a, g, o, a.p.to.hi, r, n, v);
+      if (a.nOut > 1) {
         residue(v);
-        put(a.to.lo);
+        store_plane(a.p.to.lo + at, v);
+        if (blockC < blockR) mirror(a, g, o, a.p.to.lo, r, n, v);
       }
     }
   }
@@ -131,21 +173,69 @@ struct SymmetricEpilogue {
 // into the result.
 template <typename T>
 struct ApplyEpilogue {
+  static constexpr bool kAux = true;
   struct Args {
-    Planes from, to;
-    long long ld, size;
-    float byFrom, byAcc;
+    AuxArgs aux;
+    PlaneArgs p;
     int last, tall, vec;
     float byOut;
     int cols;         // of X
     T* out[kMost];
   };
+  static __device__ __forceinline__ void finish(const Args& a, const GemmArgs& g, int z, int r,
+                                                int n, int M, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= a.byOut;
+    typename Ty<T>::Bits* out = reinterpret_cast<typename Ty<T>::Bits*>(a.out[z]);
+    if (a.tall) {  // the lanes' rows are consecutive columns of the result
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n + i < g.N) out[(long long)(n + i) * M + r] = Ty<T>::narrow(v[i]);
+    } else if (a.vec && n + 32 <= g.N) {
+      constexpr int U = Ty<T>::U;
+      uint4* p = reinterpret_cast<uint4*>(out + (long long)r * a.cols + n);
+#pragma unroll
+      for (int i = 0; i < 32 / U; ++i) {
+        uint4 q;
+        typename Ty<T>::Bits* b = reinterpret_cast<typename Ty<T>::Bits*>(&q);
+#pragma unroll
+        for (int j = 0; j < U; ++j) b[j] = Ty<T>::narrow(v[i * U + j]);
+        p[i] = q;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n + i < g.N) out[(long long)r * a.cols + n + i] = Ty<T>::narrow(v[i]);
+    }
+  }
+  static __device__ __forceinline__ bool skip(const GemmArgs& g, const Tile& o, int n, int M) {
+    return n >= g.N || o.m0 >= M;
+  }
+  template <class Acc>
+  static __device__ __forceinline__ void unit(const Args& a, const GemmArgs& g, const Tile& o,
+                                              int row, int n, int c, int M, const Acc& acc,
+                                              const AuxTile& tile) {
+    const int r = o.m0 + row;
+    float v[32];
+    acc(c, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= a.p.byAcc;
+    add_tile(tile, 0, row, a.p.byFrom, v);
+    add_tile(tile, 1, row, a.p.byFrom, v);
+    if (a.last) {
+      if (r < M) finish(a, g, o.z, r, n, M, v);
+    } else {
+      store_tile(tile, 0, row, v);
+      residue(v);
+      store_tile(tile, 1, row, v);
+    }
+  }
   template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
                                              int row, int col0, int M, const Acc& acc) {
     const int r = o.m0 + row;
     const bool live = r < M;
-    const long long base = o.z * a.size;
+    const long long base = o.z * a.p.size;
 #pragma unroll
     for (int c = 0; c < COLS; c += 32) {
       const int n = o.n0 + col0 + c;
@@ -153,39 +243,17 @@ struct ApplyEpilogue {
       float v[32];
       acc(col0 + c, v);
       if (!live) continue;
-      const long long at = base + r * a.ld + n;
+      const long long at = base + r * a.p.ld + n;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= a.byAcc;
-      add_plane(a.from.hi + at, a.byFrom, v);
-      add_plane(a.from.lo + at, a.byFrom, v);
-      if (!a.last) {
-        store_plane(a.to.hi + at, v);
-        residue(v);
-        store_plane(a.to.lo + at, v);
-        continue;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= a.byOut;
-      typename Ty<T>::Bits* out = reinterpret_cast<typename Ty<T>::Bits*>(a.out[o.z]);
-      if (a.tall) {  // the lanes' rows are consecutive columns of the result
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (n + i < g.N) out[(long long)(n + i) * M + r] = Ty<T>::narrow(v[i]);
-      } else if (a.vec && n + 32 <= g.N) {
-        constexpr int U = Ty<T>::U;
-        uint4* p = reinterpret_cast<uint4*>(out + (long long)r * a.cols + n);
-#pragma unroll
-        for (int i = 0; i < 32 / U; ++i) {
-          uint4 q;
-          typename Ty<T>::Bits* b = reinterpret_cast<typename Ty<T>::Bits*>(&q);
-#pragma unroll
-          for (int j = 0; j < U; ++j) b[j] = Ty<T>::narrow(v[i * U + j]);
-          p[i] = q;
-        }
+      for (int i = 0; i < 32; ++i) v[i] *= a.p.byAcc;
+      add_plane(a.p.from.hi + at, a.p.byFrom, v);
+      add_plane(a.p.from.lo + at, a.p.byFrom, v);
+      if (a.last) {
+        finish(a, g, o.z, r, n, M, v);
       } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (n + i < g.N) out[(long long)r * a.cols + n + i] = Ty<T>::narrow(v[i]);
+        store_plane(a.p.to.hi + at, v);
+        residue(v);
+        store_plane(a.p.to.lo + at, v);
       }
     }
   }
@@ -338,7 +406,10 @@ bool make_plan(int count, size_t rows, size_t cols, int dtype, OrthoPlan* p) {
   };
   p->part = take(p->group * kNormCtas * 4);
   for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) p->x[i][j] = take(p->group * p->m * p->ldX * 2);
+    for (int j = 0; j < 2; ++j)
+      // one plane: the low plane is no operand, every element of it is read and
+      // written by one thread, so it is updated in place
+      p->x[i][j] = i && j && p->parts == 1 ? p->x[0][1] : take(p->group * p->m * p->ldX * 2);
   for (int j = 0; j < p->parts; ++j) p->a[j] = take(p->group * p->m * p->ldA * 2);
   for (int j = 0; j < p->parts; ++j) p->b[j] = take(p->group * p->m * p->ldA * 2);
   p->bytes = at;
@@ -385,7 +456,7 @@ constexpr float kCoefs[3] = {3.4445f, -4.7750f, 2.0315f};
 // CTA, 0.167 us on a 256 x 128 tile of a pair (half the operand traffic per
 // SM), 0.31 us on a 256 x 256 one (two planes: 0.56 and 0.47 us, no 256-wide
 // tile, tensor memory holds 128 columns), the epilogue of the last round 3 us
-// per 128 columns, and joining shares of k 2 us.  Wide tiles win when there
+// per 128 columns, and joining shares of k 4 us.  Wide tiles win when there
 // are many, single CTAs when they fill the SMs once, shares when few tiles
 // leave SMs idle.
 template <int PARTS, bool BMN, class Epi>
@@ -397,11 +468,13 @@ vr_result_t product(const OpDevice& dev, const Planes& a, size_t aLd, const Plan
   double best = 0;
   int shape = -1, shares = 1;  // shape: 0 single, 1 pair, 2 wide pair
   auto offer = [&](int which, size_t tiles, double slice, int s) {
+    // clusters of four and eight CTAs do not fill the GPU, and are only
+    // worth while in one round
     const size_t ctas = (which ? 2 : 1) * (size_t)s;
-    // clusters of four and eight leave some SMs of each group of SMs unused
-    const size_t room = std::max<size_t>(1, (ctas > 2 ? dev.sms * 7 / 8 : dev.sms) / ctas);
+    const size_t room = ctas > 4 ? 8 : ctas > 2 ? 28 : (size_t)dev.sms / ctas;
     const double rounds = (double)((tiles + room - 1) / room);
-    const double t = rounds * std::ceil(slices / s) * slice + (which == 2 ? 6 : 3) + (s > 1 ? 2 : 0);
+    if (s > 1 && rounds > 1) return;
+    const double t = rounds * std::ceil(slices / s) * slice + (which == 2 ? 6 : 3) + (s > 1 ? 4 : 0);
     if (shape < 0 || t < best) best = t, shape = which, shares = s;
   };
   const size_t singles = gemm_tiles<128, false>(z), pairs = gemm_tiles<128, true>(z);
@@ -464,29 +537,48 @@ vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src,
                 dim3((unsigned)std::min<size_t>(blocks, (size_t)dev.sms * 8), count), dim3(256),
                 args, 0, stream);
   if (e != VR_SUCCESS) return e;
+  const size_t n = (size_t)count;
   for (int k = 0; k < steps; ++k) {
     const float a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
-    const Planes& from = x[k % 2];
+    const Planes &from = x[k % 2], &to = x[1 - k % 2];
     const float shift = shift_of(coefs, steps, k);
-    SymmetricEpilogue::Args ga = {{nullptr, nullptr}, A, (long long)p.ldA, sizeA, 0.0f,
-                                  1.0f / kScale, 0.0f, PARTS == 2};
-    const size_t n = (size_t)count;
+    SymmetricEpilogue::Args sym = {};
+    sym.p.to = A;
+    sym.p.ld = (long long)p.ldA;
+    sym.p.size = sizeA;
+    sym.p.byAcc = 1.0f / kScale;
+    sym.nOut = PARTS;
     if ((e = product<PARTS, false, SymmetricEpilogue>(dev, from, p.ldX, from, p.ldX,
-                                                      {p.m, p.m, p.n, n, true}, ga, stream)) !=
+                                                      {p.m, p.m, p.n, n, true}, sym, stream)) !=
         VR_SUCCESS)
       return e;
-    SymmetricEpilogue::Args pa = {A, B, (long long)p.ldA, sizeA, b, c / kScale, shift * kScale,
-                                  PARTS == 2};
+    sym.p.from = A;
+    sym.p.to = B;
+    sym.p.byFrom = b;
+    sym.p.byAcc = c / kScale;
+    sym.p.diagonal = shift * kScale;
+    sym.nIn = PARTS;
     if ((e = product<PARTS, false, SymmetricEpilogue>(
-             dev, A, p.ldA, A, p.ldA, {p.m, p.m, p.m, n, true}, pa, stream)) != VR_SUCCESS)
+             dev, A, p.ldA, A, p.ldA, {p.m, p.m, p.m, n, true}, sym, stream)) != VR_SUCCESS)
       return e;
-    ap.from = from;
-    ap.to = x[1 - k % 2];
-    ap.ld = (long long)p.ldX;
-    ap.size = sizeX;
-    ap.byFrom = a + shift;
-    ap.byAcc = 1.0f / kScale;
     ap.last = k + 1 == steps;
+    ap.aux.nIn = 2;
+    ap.aux.nOut = ap.last ? 0 : 2;
+    for (int i = 0; i < 2; ++i) {
+      auto tiles = [&](CUtensorMap* map, const __half* plane) {
+        return gemm_operand(map, plane, false, p.n, p.m, n, p.ldX * 2, (size_t)sizeX * 2, kTileM,
+                            kAuxCols);
+      };
+      if ((e = tiles(&ap.aux.in[i], i ? from.lo : from.hi)) != VR_SUCCESS ||
+          (e = tiles(&ap.aux.out[i], i ? to.lo : to.hi)) != VR_SUCCESS)
+        return e;
+    }
+    ap.p.from = from;
+    ap.p.to = to;
+    ap.p.ld = (long long)p.ldX;
+    ap.p.size = sizeX;
+    ap.p.byFrom = a + shift;
+    ap.p.byAcc = 1.0f / kScale;
     ap.tall = tall;
     ap.byOut = scale / kScale;
     ap.cols = (int)p.n;

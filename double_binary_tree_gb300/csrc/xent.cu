@@ -74,6 +74,7 @@ __device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, 
 // Row statistics of a tile of logits: the maximum (in units of log 2) and
 // the sum of exp over each half tile, and the target's logit.
 struct StatsEpilogue {
+  static constexpr bool kAux = false;
   struct Args {
     const int* target;  // [T], -1: none
     float* targetLogit;
@@ -117,6 +118,7 @@ struct StatsEpilogue {
 // Gradient factors of a tile of a piece of the vocabulary.
 template <typename T>
 struct FactorEpilogue {
+  static constexpr bool kAux = false;
   struct Args {
     const int* target;   // packed tokens' targets
     const float* lse2;   // their log sums, in units of log 2
@@ -153,6 +155,7 @@ struct FactorEpilogue {
 // dH: the pieces' products added up in fp32 in piece order, rounded once.
 template <typename T>
 struct HiddenEpilogue {
+  static constexpr bool kAux = false;
   struct Args {
     float* sum;            // [packed tokens][ld]
     long long ld;
@@ -199,6 +202,7 @@ struct HiddenEpilogue {
 // dW: rows of one piece of the vocabulary, whole sums over the tokens.
 template <typename T>
 struct WeightEpilogue {
+  static constexpr bool kAux = false;
   struct Args {
     T* out;  // the piece's first row, [V][N]
     const XentState* state;
