@@ -379,6 +379,384 @@ __global__ void __launch_bounds__(256) ortho_load_kernel(const __grid_constant__
   }
 }
 
+// ------------------------------------------------------- small matrices
+// Up to 128 rows (of X) and 2048 columns: one launch, a cluster of up to eight
+// CTAs per matrix, each holding its 256 columns of X in shared memory for all
+// steps.  (A launch per product costs 5 to 7 us whatever its size, 17 of them
+// 85 us at 8 x 128 x 128.)  A slab of 128 rows of 64 columns, 128 bytes a
+// row, is the K-major operand of X X^T and the MN-major one of B X at once,
+// so nothing is laid out twice.  In a cluster every CTA sums X X^T over its
+// own columns; each adds up a share of A's columns from all of them in rank
+// order and gives the planes of its share to all.
+constexpr int kSmallRows = 128, kSmallCols = 256, kSmallCtas = 8;
+constexpr int kSlab = kSmallRows * 128;                       // bytes of 64 columns
+constexpr int kSmallX = kSmallCols / 64 * kSlab;              // a plane of X
+constexpr int kSmallA = 2 * kSlab;                            // a plane of A or B
+constexpr int kSmallSmem = 1024 + 2 * kSmallX + 2 * kSmallA;
+static_assert(2 * kSmallA == kSmallRows * kSmallRows * 4, "partial sums of A use A's planes");
+
+struct SmallArgs {
+  const void* src[kMost];
+  void* dst[kMost];
+  int m, n, w;      // X: rows, columns, columns of a CTA (whole slabs)
+  int tall, steps;
+  float eps, byOut;
+  float coefs[32][4];  // factor of X, b, c, what is subtracted from B's diagonal
+  unsigned* status;
+  unsigned long long timeoutNs;
+};
+
+__device__ __forceinline__ uint32_t slab_at(uint32_t plane, int r, int c) {
+  return plane + (unsigned)((c >> 6) * kSlab + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) +
+                            (c & 7) * 2);
+}
+__device__ __forceinline__ void shared_store16(uint32_t at, const __half (&h)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(h);
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z),
+               "r"(q.w)
+               : "memory");
+}
+// 32 columns from c of row r of a plane: added to v, or written from it.
+__device__ __forceinline__ void slab_add(uint32_t plane, int r, int c, float by, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                 : "r"(slab_at(plane, r, c + 8 * i))
+                 : "memory");
+    const __half2* h = reinterpret_cast<const __half2*>(&q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(h[j]);
+      v[8 * i + 2 * j] = fmaf(by, f.x, v[8 * i + 2 * j]);
+      v[8 * i + 2 * j + 1] = fmaf(by, f.y, v[8 * i + 2 * j + 1]);
+    }
+  }
+}
+__device__ __forceinline__ void slab_put(uint32_t plane, int r, int c, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    alignas(16) __half h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(v[8 * i + j]);
+    shared_store16(slab_at(plane, r, c + 8 * i), h);
+  }
+}
+
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256, 1) ortho_small_kernel(const __grid_constant__ SmallArgs a) {
+  using Bits = typename Ty<T>::Bits;
+  extern __shared__ unsigned char smemRaw[];
+  __shared__ alignas(8) uint64_t bar;
+  __shared__ uint32_t tmemBase;
+  __shared__ float sSquares[9];  // of the warps, and their sum
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  const int shares = (int)cluster_size(), rank = (int)cluster_rank();
+  const int z = (int)blockIdx.x / shares;
+  const uint32_t base = (smem_addr(smemRaw) + 1023) & ~1023u;
+  const uint32_t xHi = base, xLo = base + kSmallX, aHi = base + 2 * kSmallX, aLo = aHi + kSmallA;
+  const uint32_t done = smem_addr(&bar);
+  if (threadIdx.x == 0) {
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmemBase)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = tmemBase;
+  pdl_launch();
+  pdl_wait();
+
+  // this CTA's columns [c0, c0 + width) of X
+  const int c0 = rank * a.w, width = max(0, min(a.n - c0, a.w));
+  const Bits* src = static_cast<const Bits*>(a.src[z]);
+  // Pieces of eight consecutive elements of src: of a row of X, or, tall (X is
+  // the transpose of src), of a column.
+  const int length = a.tall ? a.m : a.n;  // of a row of src
+  const int perRow = ((a.tall ? a.m : width) + 7) / 8;
+  const int pieces = perRow * (a.tall ? width : a.m);
+  const bool vec = length % 8 == 0 && ((uintptr_t)src & 15) == 0;
+  auto load8 = [&](int i, float(&x)[8], int& line, int& at) {
+    line = i / perRow;  // row of X, or its column from c0
+    at = i % perRow * 8;
+    const Bits* p = src + (a.tall ? (long long)(c0 + line) * length + at
+                                  : (long long)line * length + c0 + at);
+    const int left = (a.tall ? a.m : width) - at;
+    if (vec && left >= 8) {
+      alignas(16) Bits in[8];
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(in) / 16; ++j)
+        reinterpret_cast<uint4*>(in)[j] = reinterpret_cast<const uint4*>(p)[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = Ty<T>::widen(in[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = j < left ? Ty<T>::widen(p[j]) : 0.0f;
+    }
+  };
+
+  // the norm: fp32 squares per thread, then trees, then the ranks in order
+  float squares = 0.0f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < pieces; i += 256) {
+    float x[8], t = 0.0f;
+    int line, at;
+    load8(i, x, line, at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaf(x[j], x[j], t);
+    squares += t;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+  if (lane == 0) sSquares[warp] = squares;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int i = 0; i < 8; ++i) s += sSquares[i];
+    sSquares[8] = s;
+  }
+  __syncthreads();
+  if (shares > 1) cluster_sync();
+  float sum = 0.0f;
+  for (int from = 0; from < shares; ++from)
+    sum += peer_load(peer_addr(smem_addr(&sSquares[8]), (uint32_t)from));
+  const float by = kScale / (sqrtf(sum) + a.eps);
+
+  // X into its planes, zeros around it
+  for (int i = threadIdx.x; i < kSmallRows * (a.w / 8); i += 256) {
+    const int r = i % kSmallRows, c = i / kSmallRows * 8;
+    if (!a.tall && r < a.m && c < width) continue;
+    alignas(16) const __half zero[8] = {};
+    shared_store16(slab_at(xHi, r, c), zero);
+    shared_store16(slab_at(xLo, r, c), zero);
+  }
+  if (a.tall) __syncthreads();
+#pragma unroll 2
+  for (int i = threadIdx.x; i < pieces; i += 256) {
+    float x[8];
+    int line, at;
+    load8(i, x, line, at);
+    alignas(16) __half h[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(x[j] * by, h[j], l[j]);
+    if (a.tall) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + j < a.m) {
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(slab_at(xHi, at + j, line)),
+                       "h"(__half_as_ushort(h[j]))
+                       : "memory");
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(slab_at(xLo, at + j, line)),
+                       "h"(__half_as_ushort(l[j]))
+                       : "memory");
+        }
+    } else {
+      shared_store16(slab_at(xHi, line, at), h);
+      shared_store16(slab_at(xLo, line, at), l);
+    }
+  }
+
+  const int quad = warp % 4, half = warp / 4, row = quad * 32 + lane;
+  const uint32_t rows = tmem + ((uint32_t)(quad * 32) << 16);
+  unsigned turn = 0;
+  bool ok = true;
+  // Everything written to shared memory is there for the products, which
+  // `issue` starts; returns when they are done.  A wait that runs out is
+  // reported, and the kernel goes on without waiting (its peers count on it).
+  auto products = [&](auto issue) {
+    asm volatile("fence.proxy.async;" ::: "memory");
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0 && elected()) {
+      issue();
+      mma_commit<false>(done, 0);
+    }
+    __syncwarp();
+    if (ok) ok = wait_phase(done, turn, nullptr, false, a.timeoutNs);
+    ok = __syncthreads_and(ok) != 0;
+    if (!ok && threadIdx.x == 0) atomicCAS(a.status, 0u, (unsigned)VR_ERR_TIMEOUT);
+    turn ^= 1;
+    tmem_fence_after();
+  };
+  // 32 columns of the sums at `main` (and of the low planes' at 256)
+  auto sums = [&](int column, bool second, float(&v)[32]) {
+    tmem_load32(rows + (unsigned)column, v);
+    float u[32];
+    if (second) {
+      tmem_load32(rows + (unsigned)(128 + column), u);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += u[i];
+    }
+    if (PARTS == 2) {
+      tmem_load32(rows + (unsigned)(256 + column), u);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += u[i];
+    }
+  };
+  auto put_a = [&](int c, float(&v)[32]) {
+    slab_put(aHi, row, c, v);
+    if (PARTS == 2) {
+      residue(v);
+      slab_put(aLo, row, c, v);
+    }
+  };
+  constexpr uint32_t kSquare = mma_idesc<__half>(128, 128, false, false);
+  const uint32_t wide = mma_idesc<__half>(128, a.w, false, true);
+  const int slabs = a.w / 64;
+
+  for (int k = 0; k < a.steps; ++k) {
+    // A = X X^T over this CTA's columns: two sums of two slabs each (they are
+    // truncated where they are added), the low planes' apart
+    products([&]() {
+      for (int s = 0; s < slabs; ++s)
+#pragma unroll
+        for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
+          const uint64_t da = operand_desc((p == 2 ? xLo : xHi) + s * kSlab, 16, 1024);
+          const uint64_t db = operand_desc((p == 1 ? xLo : xHi) + s * kSlab, 16, 1024);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16<false>(tmem + (p ? 256u : s < 2 ? 0u : 128u), da + 2 * j, db + 2 * j, kSquare,
+                           p ? s | (p == 2) | j : (s & 1) | j);
+        }
+    });
+    if (shares == 1) {
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        float v[32];
+        sums(half * 64 + c, slabs > 2, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kScale;
+        put_a(half * 64 + c, v);
+      }
+    } else {
+      // [column][row] in fp32 where A's planes will be
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        float v[32];
+        sums(half * 64 + c, slabs > 2, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(aHi + 4u * ((half * 64 + c + i) * kSmallRows + row)),
+                       "f"(v[i])
+                       : "memory");
+      }
+      cluster_sync();
+      // pieces of eight columns: 16 / shares of them are this CTA's
+      const int own = 16 / shares / 2, r = threadIdx.x % 128;
+      const int piece0 = rank * (16 / shares) + (int)(threadIdx.x / 128) * own;
+      alignas(16) __half h[4][8], l[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q >= own) break;
+        float v[8] = {};
+        for (int from = 0; from < shares; ++from) {
+          const uint32_t at = peer_addr(aHi, (uint32_t)from) +
+                              4u * (unsigned)((piece0 + q) * 8 * kSmallRows + r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += peer_load(at + 4u * (unsigned)(i * kSmallRows));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split(v[i] * (1.0f / kScale), h[q][i], l[q][i]);
+      }
+      cluster_sync();  // every partial sum has been read
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q >= own) break;
+        for (int to = 0; to < shares; ++to)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p ? l[q] : h[q]);
+            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             peer_addr(slab_at(p ? aLo : aHi, r, (piece0 + q) * 8), (uint32_t)to)),
+                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                         : "memory");
+          }
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");
+      cluster_sync();
+    }
+    // B = b A + c A A - d I in A's place
+    products([&]() {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
+          const uint64_t da = operand_desc((p == 2 ? aLo : aHi) + s * kSlab, 16, 1024);
+          const uint64_t db = operand_desc((p == 1 ? aLo : aHi) + s * kSlab, 16, 1024);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16<false>(tmem + (p ? 256u : 0u), da + 2 * j, db + 2 * j, kSquare, s | (p == 2) | j);
+        }
+    });
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      float v[32];
+      const int at = half * 64 + c;
+      sums(at, false, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= a.coefs[k][2] * (1.0f / kScale);
+      slab_add(aHi, row, at, a.coefs[k][1], v);
+      if (PARTS == 2) slab_add(aLo, row, at, a.coefs[k][1], v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (at + i == row) v[i] -= a.coefs[k][3] * kScale;
+      put_a(at, v);
+    }
+    // X <- a X + B X
+    products([&]() {
+#pragma unroll
+      for (int p = 0; p < (PARTS == 2 ? 3 : 1); ++p) {
+        const uint64_t da = operand_desc(p == 2 ? aLo : aHi, 16, 1024);
+        const uint64_t db = operand_desc(p == 1 ? xLo : xHi, kSlab, 1024);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          mma_f16<false>(tmem + (p ? 256u : 0u), da + (j / 4) * (kSlab >> 4) + 2 * (j % 4),
+                         db + j * (2048 >> 4), wide, (p == 2) | j);
+      }
+    });
+    for (int c = 0; c < a.w / 2; c += 32) {
+      float v[32];
+      const int at = half * (a.w / 2) + c;
+      sums(at, false, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= 1.0f / kScale;
+      slab_add(xHi, row, at, a.coefs[k][0], v);
+      slab_add(xLo, row, at, a.coefs[k][0], v);
+      if (k + 1 < a.steps) {
+        slab_put(xHi, row, at, v);
+        residue(v);
+        slab_put(xLo, row, at, v);
+      } else if (row < a.m) {
+        Bits* out = static_cast<Bits*>(a.dst[z]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (at + i >= width) break;
+          const long long to = a.tall ? (long long)(c0 + at + i) * a.m + row
+                                      : (long long)row * a.n + c0 + at + i;
+          out[to] = Ty<T>::narrow(v[i] * a.byOut);
+        }
+      }
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (shares > 1) cluster_sync();  // no peer reads this CTA's memory any more
+  if (warp == 0) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
 struct OrthoPlan {
@@ -503,6 +881,34 @@ vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src,
                 int count, size_t rows, size_t cols, int steps, const float* coefs, float eps,
                 float scale, char* w, void* stream) {
   const bool tall = rows > cols;
+  if (p.m <= kSmallRows && p.n <= (size_t)kSmallCols * kSmallCtas) {
+    SmallArgs a = {};
+    int shares = 1;
+    while ((size_t)shares * kSmallCols < p.n) shares *= 2;
+    a.m = (int)p.m;
+    a.n = (int)p.n;
+    a.w = (int)up((p.n + shares - 1) / shares, 64);
+    a.tall = tall;
+    a.steps = steps;
+    a.eps = eps;
+    a.byOut = scale / kScale;
+    a.status = dev.status;
+    a.timeoutNs = dev.timeoutNs;
+    for (int k = 0; k < steps; ++k) {
+      const float d = shift_of(coefs, steps, k);
+      a.coefs[k][0] = coefs[3 * k] + d;
+      a.coefs[k][1] = coefs[3 * k + 1];
+      a.coefs[k][2] = coefs[3 * k + 2];
+      a.coefs[k][3] = d;
+    }
+    for (int i = 0; i < count; ++i) a.src[i] = src[i], a.dst[i] = dst[i];
+    const void* fn = (const void*)ortho_small_kernel<T, PARTS>;
+    const vr_result_t e = gemm_prepare(fn, dev.device, kSmallSmem);
+    if (e != VR_SUCCESS) return e;
+    void* args[] = {&a};
+    return op_launch(fn, dim3((unsigned)(count * shares)), dim3(256), args, kSmallSmem, stream,
+                     shares);
+  }
   auto plane = [w](size_t at) { return reinterpret_cast<__half*>(w + at); };
   const Planes x[2] = {{plane(p.x[0][0]), plane(p.x[0][1])}, {plane(p.x[1][0]), plane(p.x[1][1])}};
   const Planes A = {plane(p.a[0]), PARTS == 2 ? plane(p.a[1]) : nullptr};

@@ -58,7 +58,10 @@ def compare(got, ms, ty, steps=5, coefs=None, eps=EPS, scale=1.0):
 @pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
 @pytest.mark.parametrize("count,rows,cols", [
     (1, 1, 1), (2, 1, 37), (1, 64, 1), (3, 8, 8), (2, 32, 64), (1, 65, 33), (8, 128, 128),
-    (2, 127, 129), (1, 129, 500), (3, 500, 129), (1, 256, 1000), (1, 777, 333), (2, 384, 640)])
+    (2, 127, 129), (1, 129, 500), (3, 500, 129), (1, 256, 1000), (1, 777, 333), (2, 384, 640),
+    # one launch of a cluster per matrix up to 128 x 2048, and just above
+    (2, 100, 257), (1, 256, 128), (3, 90, 513), (1, 1025, 128), (2, 2048, 77), (1, 128, 2048),
+    (1, 128, 2049), (1, 2100, 64), (2, 5, 1800), (40, 16, 1030)])
 def test_matches_the_definition(count, rows, cols, dtype):
     code, ty = DT[dtype]
     ms = make(count, rows, cols, ty, rows + cols)
