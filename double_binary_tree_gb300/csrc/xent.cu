@@ -6,16 +6,22 @@
 //
 // The logits are never stored.  The first product (gemm.cuh) turns each
 // 128 x 256 tile of them into one maximum and one sum per row in its epilogue;
-// joining the tiles' pairs gives lse.  For the gradients the vocabulary is
-// taken piece by piece: the product runs again, its epilogue now writing
-// exp(l - lse) - [v = y] in 16 bits, and two more products multiply that
-// piece with the weight and with the hidden states while it is in L2 or
-// fresh in memory.  8 T D V operations instead of the 6 T D V of keeping T x V
-// logits.
+// joining the tiles' pairs gives lse.  For the gradients there are two ways:
+//   kept     the same epilogue also writes exp(l - the tile's maximum) in 16
+//            bits; once lse is known a pass over them makes the gradient
+//            factors p - [v = y] of them in place.  6 T D V operations.  Taken
+//            while T x V 16-bit values are no more memory than the weight has
+//            (T <= D), or 256 MB, and the workspace has room for them.
+//   pieces   the vocabulary is taken piece by piece: the product runs again,
+//            its epilogue now writing the factors.  8 T D V operations, a
+//            workspace that does not grow with T x V.
+// Two more products multiply the factors with the weight and with the hidden
+// states.  (4096 tokens x 4096 x 131072, bf16: 8.5 ms kept, 10.4 ms in pieces.)
 //
-// Only tokens that count take part in the gradients: their hidden states are
-// gathered into a packed copy first, which leaves out the products of
-// ignored tokens and whatever such tokens hold (NaN times zero is NaN).
+// Only tokens that count take part in the gradients: the hidden states are
+// packed first, tokens that count before ignored ones, which leaves out the
+// products of ignored tokens and whatever such tokens hold (NaN times zero
+// is NaN).
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -34,6 +40,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Device-side results of the preparation.
 struct XentState {
   int valid;        // tokens that count
+  int rows;         // packed rows: those, zeros up to whole slices, the others
   float lossScale;  // 1 / valid or 1
   float gradScale;  // of the 16-bit gradient factors
 };
@@ -72,14 +79,19 @@ __device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, 
 }
 
 // Row statistics of a tile of logits: the maximum (in units of log 2) and
-// the sum of exp over each half tile, and the target's logit.
+// the sum of exp over each half tile, and the target's logit; KEEP: and each
+// exp(l - maximum) in 16 bits.
+template <typename T, bool KEEP>
 struct StatsEpilogue {
   static constexpr bool kAux = false;
   struct Args {
-    const int* target;  // [T], -1: none
+    const int* target;  // of a row, -1: none
     float* targetLogit;
-    float2* parts;      // [T][nParts]
+    float2* parts;      // [rows][nParts]
     int nParts;
+    T* out;             // KEEP: [rows][ld]
+    long long ld;
+    const XentState* state;
   };
   template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
@@ -87,33 +99,104 @@ struct StatsEpilogue {
     const int t = o.m0 + row;
     const int first = o.n0 + col0;
     const int at = t < M ? a.target[t] - first : -1;
-    float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-      if (first + c >= g.N) break;
-      float v[32];
+    auto fetch = [&](int c, float(&v)[32]) {
       acc(col0 + c, v);
       if (first + c + 32 > g.N) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (first + c + i >= g.N) v[i] = -INFINITY;
       }
-      float m = v[0];
+    };
+    float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
-      m *= kLog2e;
-      const float next = fmaxf(top, m);
-      // nothing but -inf so far: subtract 0, so that exp2 gives 0, not NaN
-      const float base = next == -INFINITY ? 0.0f : next;
-      sum *= exp2_fast(top - base);
+    for (int c = 0; c < COLS; c += 32) {
+      if (first + c >= g.N) break;
+      float v[32];
+      fetch(c, v);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum += exp2_fast(fmaf(v[i], kLog2e, -base));
-      top = next;
+      for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+    }
+    top *= kLog2e;
+    // nothing but -inf: subtract 0, so that exp2 gives 0, not NaN
+    const float base = top == -INFINITY ? 0.0f : top;
+    const bool store = KEEP && t < M && t < a.state->valid;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+      if (first + c >= g.N) break;
+      float v[32];
+      fetch(c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] = exp2_fast(fmaf(v[i], kLog2e, -base));
+        sum += v[i];
+        if (KEEP) v[i] *= (float)(1 << kShift<T>);
+      }
+      if (store) store32(a.out + (long long)t * a.ld + first + c, v, 32, true);
     }
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
     if (t < M) a.parts[(long long)t * a.nParts + first / (kBN / 2)] = make_float2(top, sum);
   }
 };
+
+// The kept exponentials of the packed tokens made into gradient factors, and
+// rows of zeros up to the next whole slice.  The target's factor is made of
+// its fp32 logit: of a sure token it is a small difference.
+template <typename T>
+struct KeptArgs {
+  T* out;
+  long long ld;
+  const float2* parts;
+  int nParts, V;
+  const float* lse2;
+  const int* target;
+  const float* targetLogit;
+  const XentState* state;
+};
+constexpr int kKeptUnits = 4;  // of 8 values a thread
+template <typename T>
+__global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ KeptArgs<T> a) {
+  pdl_launch();
+  pdl_wait();
+  const int valid = a.state->valid, rows = (valid + kTileK - 1) / kTileK * kTileK;
+  const int c0 = (blockIdx.x * kKeptUnits * 256 + threadIdx.x) * 8;
+  for (int t = blockIdx.y; t < rows; t += gridDim.y) {
+    T* out = a.out + t * a.ld;
+    const float lse2 = t < valid ? a.lse2[t] : 0.0f;
+    const int y = t < valid ? a.target[t] : -1;
+    uint4 q[kKeptUnits];
+    float2 part[kKeptUnits];
+#pragma unroll
+    for (int u = 0; u < kKeptUnits; ++u) {
+      const int c = c0 + u * 256 * 8;
+      if (t < valid && c < a.V) {
+        q[u] = *reinterpret_cast<const uint4*>(out + c);
+        part[u] = a.parts[(long long)t * a.nParts + c / (kBN / 2)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kKeptUnits; ++u) {
+      const int c = c0 + u * 256 * 8;
+      if (c >= a.V) break;
+      if (t >= valid) {
+        *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const float by = exp2_fast(part[u].x - lse2);
+      uint32_t* w = reinterpret_cast<uint32_t*>(&q[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = Ty<T>::widen((typename Ty<T>::Bits)(w[i] & 0xffffu)) * by;
+        float z = Ty<T>::widen((typename Ty<T>::Bits)(w[i] >> 16)) * by;
+        if ((y >> 1) == (c >> 1) + i) {
+          const float p = exp2_fast(fmaf(a.targetLogit[t], kLog2e, -lse2)) - 1.0f;
+          (y & 1 ? z : x) = p * (float)(1 << kShift<T>);
+        }
+        w[i] = pack2<T>(x, z);
+      }
+      *reinterpret_cast<uint4*>(out + c) = q[u];
+    }
+  }
+}
 
 // Gradient factors of a tile of a piece of the vocabulary.
 template <typename T>
@@ -237,7 +320,7 @@ struct PrepArgs {
   float gradScale;
   int shift;
   int* target;
-  int* token;
+  int *token, *skipped;  // the tokens that count, and the others, in order
   XentState* state;
   unsigned* status;
 };
@@ -265,23 +348,28 @@ __global__ void __launch_bounds__(1024) xent_prep_kernel(const __grid_constant__
       before += w < warp ? n : 0;
       all += n;
     }
-    if (y >= 0) a.token[base + before + __popc(votes & ((1u << lane) - 1))] = t;
+    const int at = base + before + __popc(votes & ((1u << lane) - 1));
+    if (y >= 0) a.token[at] = t;
+    else if (t < a.T) a.skipped[t - at] = t;
     base += all;
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     const float per = a.mean ? (base ? 1.0f / (float)base : 0.0f) : 1.0f;
     a.state->valid = base;
+    a.state->rows = (base + kTileK - 1) / kTileK * kTileK + a.T - base;
     a.state->lossScale = per;
     a.state->gradScale = per * a.gradScale * exp2f((float)-a.shift);
   }
 }
 
-// A warp per token joins its tiles' (maximum, sum) pairs.
+// A warp per row joins its tiles' (maximum, sum) pairs.
 struct JoinArgs {
   const float2* parts;
   int nParts, T;
-  const int* target;
+  const int* rowToken;  // packed rows' tokens (-1: none), or null: row = token
+  const XentState* state;
+  const int* target;    // of a row
   const float* targetLogit;
   float *lse2, *lse, *losses;
 };
@@ -289,7 +377,10 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x % 32;
-  for (int t = blockIdx.x * 8 + threadIdx.x / 32; t < a.T; t += gridDim.x * 8) {
+  const int rows = a.rowToken ? a.state->rows : a.T;
+  for (int t = blockIdx.x * 8 + threadIdx.x / 32; t < rows; t += gridDim.x * 8) {
+    const int token = a.rowToken ? a.rowToken[t] : t;
+    if (token < 0) continue;
     const float2* p = a.parts + (long long)t * a.nParts;
     float top = -INFINITY;
     for (int i = lane; i < a.nParts; i += 32) top = fmaxf(top, p[i].x);
@@ -304,8 +395,8 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ 
       const float l2 = base + log2f(sum);
       const float l = l2 * kLn2;
       a.lse2[t] = l2;
-      a.lse[t] = l;
-      a.losses[t] = a.target[t] >= 0 ? l - a.targetLogit[t] : 0.0f;
+      a.lse[token] = l;
+      a.losses[token] = a.target[t] >= 0 ? l - a.targetLogit[t] : 0.0f;
     }
   }
 }
@@ -345,46 +436,42 @@ __global__ void __launch_bounds__(256) xent_pad_kernel(const __grid_constant__ P
       a.dst[r * a.ld + c] = c < a.cols ? a.src[r * a.stride + c] : (uint16_t)0;
 }
 
-// The packed hidden states, targets and log sums of the tokens that count,
-// zero rows up to the next whole tile, and zero gradients for the others.
+// The packed hidden states: the tokens that count, zeros up to whole slices
+// of 64 rows, the others; each row's token and target; and zero gradients for
+// the others.
 struct PackArgs {
   const uint16_t* hidden;
   long long stride;
   int T, D, ld, vec;
-  const int *target, *token;
-  const float* lse2;
+  const int *target, *token, *skipped;
   const XentState* state;
   uint16_t* packed;
-  int* packedTarget;
-  float* packedLse2;
+  int *rowToken, *rowTarget;
   uint16_t* dHidden;  // [T][D] or null
 };
 __global__ void __launch_bounds__(256) xent_pack_kernel(const __grid_constant__ PackArgs a) {
   pdl_launch();
   pdl_wait();
-  const int valid = a.state->valid;
-  const int rows = (valid + kTileM - 1) / kTileM * kTileM;
-  const int last = max(rows, a.T);
-  for (int r = blockIdx.x; r < last; r += gridDim.x) {
-    if (r < rows) {
-      const int t = r < valid ? a.token[r] : -1;
-      uint16_t* out = a.packed + (long long)r * a.ld;
-      const uint16_t* in = a.hidden + (t < 0 ? 0 : t * a.stride);
-      if (a.vec) {
-        for (int c = threadIdx.x * 8; c < a.ld; c += 256 * 8)
-          *reinterpret_cast<uint4*>(out + c) =
-              t < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(in + c);
-      } else {
-        for (int c = threadIdx.x; c < a.ld; c += 256)
-          out[c] = t >= 0 && c < a.D ? in[c] : (uint16_t)0;
-      }
-      if (threadIdx.x == 0 && t >= 0) {
-        a.packedTarget[r] = a.target[t];
-        a.packedLse2[r] = a.lse2[t];
-      }
+  const int valid = a.state->valid, rows = a.state->rows;
+  const int whole = (valid + kTileK - 1) / kTileK * kTileK;
+  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int t = r < valid ? a.token[r] : r < whole ? -1 : a.skipped[r - whole];
+    uint16_t* out = a.packed + (long long)r * a.ld;
+    const uint16_t* in = a.hidden + (t < 0 ? 0 : t * a.stride);
+    if (a.vec) {
+      for (int c = threadIdx.x * 8; c < a.ld; c += 256 * 8)
+        *reinterpret_cast<uint4*>(out + c) =
+            t < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(in + c);
+    } else {
+      for (int c = threadIdx.x; c < a.ld; c += 256)
+        out[c] = t >= 0 && c < a.D ? in[c] : (uint16_t)0;
     }
-    if (a.dHidden && r < a.T && a.target[r] < 0)
-      for (int c = threadIdx.x; c < a.D; c += 256) a.dHidden[(long long)r * a.D + c] = 0;
+    if (threadIdx.x == 0) {
+      a.rowToken[r] = t;
+      a.rowTarget[r] = r < valid ? a.target[t] : -1;
+    }
+    if (a.dHidden && r >= whole)
+      for (int c = threadIdx.x; c < a.D; c += 256) a.dHidden[(long long)t * a.D + c] = 0;
   }
 }
 
@@ -395,8 +482,8 @@ size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 // about 256 MB, so that the fp32 sums of dH, read and written once a
 // piece, stay a small part of the traffic.
 constexpr size_t kPieceBytes = (size_t)256 << 20;
-size_t piece_rows(size_t T, size_t V) {
-  const size_t fit = kPieceBytes / (2 * up(T, kTileM)) / kBN * kBN;
+size_t piece_rows(size_t T, size_t V) {  // T: packed rows
+  const size_t fit = kPieceBytes / (2 * T) / kBN * kBN;
   return std::min(up(V, kBN), std::max<size_t>(fit, kBN));
 }
 
@@ -405,26 +492,31 @@ bool packed_rows(const void* p, size_t stride) {
 }
 
 struct XentPlan {
-  bool padHidden, padWeight;
-  size_t T, D, V, Dp, T128, nParts, piece, nPieces, sumLd;
+  bool grads, kept, padHidden, padWeight;
+  size_t T, D, V, Dp, rows, nParts, piece, nPieces, sumLd;
   // offsets into the workspace
-  size_t state, target, token, lse2, targetLogit, parts, hidden, weight, packed, packedTarget,
-      packedLse2, factors, sum, bytes;
+  size_t state, target, token, skipped, rowToken, rowTarget, lse2, targetLogit, parts, hidden,
+      weight, packed, factors, sum, bytes;
 };
 
+// `kept`: the gradients' exponentials are kept (where the rule allows it).
 bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size_t weightStride,
-               size_t T, size_t D, size_t V, int dtype, bool grads, XentPlan* p) {
+               size_t T, size_t D, size_t V, int dtype, bool grads, bool kept, XentPlan* p) {
   if ((dtype != VR_FLOAT16 && dtype != VR_BFLOAT16) || T > (1u << 30) || D < 1 || D > (1u << 24) ||
       V < 1 || V > (1u << 30) || hiddenStride < D || weightStride < D ||
       hiddenStride > (1ull << 32) || weightStride > (1ull << 32))
     return false;
+  *p = XentPlan{};
+  p->grads = grads;
   p->T = T, p->D = D, p->V = V;
-  p->padHidden = !packed_rows(hidden, hiddenStride);
+  // a packed copy of the hidden states serves the gradients
+  p->padHidden = !grads && !packed_rows(hidden, hiddenStride);
   p->padWeight = !packed_rows(weight, weightStride);
   p->Dp = up(D, 8);
-  p->T128 = up(std::max<size_t>(T, 1), kTileM);
+  p->rows = grads ? up(T + kTileK, kTileM) : T;
   p->nParts = 2 * (up(V, kBN) / kBN);
-  p->piece = piece_rows(T, V);
+  p->kept = grads && kept && (T <= D || 2 * p->rows * up(V, kBN) <= kPieceBytes);
+  p->piece = p->kept ? up(V, kBN) : piece_rows(p->rows, V);
   p->nPieces = (V + p->piece - 1) / p->piece;
   p->sumLd = up(D, 32);
   size_t at = 0;
@@ -436,17 +528,18 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   p->state = take(sizeof(XentState));
   p->target = take(T * 4);
   p->token = take(T * 4);
-  p->lse2 = take(T * 4);
-  p->targetLogit = take(T * 4);
-  p->parts = take(T * p->nParts * sizeof(float2));
+  p->skipped = take(T * 4);
+  p->lse2 = take(p->rows * 4);
+  p->targetLogit = take(p->rows * 4);
+  p->parts = take(p->rows * p->nParts * sizeof(float2));
   p->hidden = p->padHidden ? take(T * p->Dp * 2) : 0;
   p->weight = p->padWeight ? take(V * p->Dp * 2) : 0;
   if (grads) {
-    p->packed = take(p->T128 * p->Dp * 2);
-    p->packedTarget = take(p->T128 * 4);
-    p->packedLse2 = take(p->T128 * 4);
-    p->factors = take(p->T128 * p->piece * 2);
-    p->sum = p->nPieces > 1 ? take(p->T128 * p->sumLd * 4) : 0;
+    p->rowToken = take(p->rows * 4);
+    p->rowTarget = take(p->rows * 4);
+    p->packed = take(p->rows * p->Dp * 2);
+    p->factors = take(p->rows * p->piece * 2);
+    p->sum = p->nPieces > 1 ? take(p->rows * p->sumLd * 4) : 0;
   }
   p->bytes = at;
   return true;
@@ -485,15 +578,17 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
                 long long ignoreIndex, int mean, float gradScale, float* losses, float* lse,
                 float* loss, void* dHidden, void* dWeight, char* w, void* stream) {
   XentState* state = reinterpret_cast<XentState*>(w + p.state);
-  int* target = reinterpret_cast<int*>(w + p.target);
-  int* token = reinterpret_cast<int*>(w + p.token);
+  auto ints = [w](size_t at) { return reinterpret_cast<int*>(w + at); };
+  int *target = ints(p.target), *token = ints(p.token), *skipped = ints(p.skipped);
   float* lse2 = reinterpret_cast<float*>(w + p.lse2);
   float* targetLogit = reinterpret_cast<float*>(w + p.targetLogit);
   float2* parts = reinterpret_cast<float2*>(w + p.parts);
+  uint16_t* packed = reinterpret_cast<uint16_t*>(w + p.packed);
+  T* factors = reinterpret_cast<T*>(w + p.factors);
   vr_result_t e;
   {
     PrepArgs a = {targets,   ignoreIndex, (int)p.T, (int)p.V, mean,  gradScale,
-                  kShift<T>, target,      token,    state,    dev.status};
+                  kShift<T>, target,      token,    skipped,  state, dev.status};
     void* args[] = {&a};
     if ((e = op_launch((const void*)xent_prep_kernel, dim3(1), dim3(1024), args, 0, stream)) !=
         VR_SUCCESS)
@@ -511,16 +606,44 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   };
   if (p.T && p.padHidden && (e = pad(&hidden, &hiddenStride, p.T, p.hidden)) != VR_SUCCESS) return e;
   if (p.T && p.padWeight && (e = pad(&weight, &weightStride, p.V, p.weight)) != VR_SUCCESS) return e;
-  if (p.T) {
-    StatsEpilogue::Args epi = {target, targetLogit, parts, (int)p.nParts};
-    if ((e = product<T, false, false, kStatsChunk, false, StatsEpilogue>(dev, hidden, hiddenStride, weight,
-                                                     weightStride, p.T, p.V, p.D, nullptr, nullptr,
-                                                     epi, stream)) != VR_SUCCESS)
+  const int* rowTarget = target;
+  if (p.T && p.grads) {
+    PackArgs a = {static_cast<const uint16_t*>(hidden), (long long)hiddenStride, (int)p.T,
+                  (int)p.D, (int)p.Dp, p.Dp == p.D && packed_rows(hidden, hiddenStride), target,
+                  token, skipped, state, packed, ints(p.rowToken), ints(p.rowTarget),
+                  static_cast<uint16_t*>(dHidden)};
+    void* args[] = {&a};
+    if ((e = op_launch((const void*)xent_pack_kernel,
+                       dim3((unsigned)std::min<size_t>(p.T + kTileK, (size_t)dev.sms * 8)),
+                       dim3(256), args, 0, stream)) != VR_SUCCESS)
       return e;
-    JoinArgs a = {parts, (int)p.nParts, (int)p.T, target, targetLogit, lse2, lse, losses};
+    hidden = packed;
+    hiddenStride = p.Dp;
+    rowTarget = ints(p.rowTarget);
+  }
+  if (p.T) {
+    // rows: an upper bound where they are packed, their number is on the device
+    const size_t rows = p.grads ? p.T + kTileK : p.T;
+    const int* dynRows = p.grads ? &state->rows : nullptr;
+    if (p.kept) {
+      typename StatsEpilogue<T, true>::Args epi = {
+          rowTarget, targetLogit, parts, (int)p.nParts, factors, (long long)p.piece, state};
+      e = product<T, false, false, kStatsChunk, false, StatsEpilogue<T, true>>(
+          dev, hidden, hiddenStride, weight, weightStride, rows, p.V, p.D, dynRows, nullptr, epi,
+          stream);
+    } else {
+      typename StatsEpilogue<T, false>::Args epi = {
+          rowTarget, targetLogit, parts, (int)p.nParts, nullptr, 0, state};
+      e = product<T, false, false, kStatsChunk, false, StatsEpilogue<T, false>>(
+          dev, hidden, hiddenStride, weight, weightStride, rows, p.V, p.D, dynRows, nullptr, epi,
+          stream);
+    }
+    if (e != VR_SUCCESS) return e;
+    JoinArgs a = {parts, (int)p.nParts, (int)p.T, p.grads ? ints(p.rowToken) : nullptr, state,
+                  rowTarget, targetLogit, lse2, lse, losses};
     void* args[] = {&a};
     if ((e = op_launch((const void*)xent_join_kernel,
-                       dim3((unsigned)std::min<size_t>((p.T + 7) / 8, (size_t)dev.sms * 8)),
+                       dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
                        dim3(256), args, 0, stream)) != VR_SUCCESS)
       return e;
   }
@@ -532,24 +655,21 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
         VR_SUCCESS)
       return e;
   }
-  if (!dHidden && !dWeight) return VR_SUCCESS;
+  if (!p.grads) return VR_SUCCESS;
   if (!p.T) {
     if (dWeight && cudaMemsetAsync(dWeight, 0, p.V * p.D * 2, (cudaStream_t)stream) != cudaSuccess)
       return VR_ERR_CUDA;
     return VR_SUCCESS;
   }
-  uint16_t* packed = reinterpret_cast<uint16_t*>(w + p.packed);
-  int* packedTarget = reinterpret_cast<int*>(w + p.packedTarget);
-  float* packedLse2 = reinterpret_cast<float*>(w + p.packedLse2);
-  T* factors = reinterpret_cast<T*>(w + p.factors);
-  {
-    PackArgs a = {static_cast<const uint16_t*>(hidden), (long long)hiddenStride, (int)p.T,
-                  (int)p.D, (int)p.Dp, p.Dp == p.D || p.padHidden, target, token, lse2, state,
-                  packed, packedTarget, packedLse2, static_cast<uint16_t*>(dHidden)};
+  if (p.kept) {
+    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, (int)p.V, lse2, rowTarget,
+                     targetLogit, state};
     void* args[] = {&a};
-    if ((e = op_launch((const void*)xent_pack_kernel,
-                       dim3((unsigned)std::min<size_t>(p.T128, (size_t)dev.sms * 8)), dim3(256),
-                       args, 0, stream)) != VR_SUCCESS)
+    const size_t columns = 256 * kKeptUnits * 8;
+    if ((e = op_launch((const void*)xent_kept_kernel<T>,
+                       dim3((unsigned)((p.V + columns - 1) / columns),
+                            (unsigned)std::min<size_t>(p.T + kTileK, 32768)),
+                       dim3(256), args, 0, stream)) != VR_SUCCESS)
       return e;
   }
   const int vecH = p.D % 8 == 0 && ((uintptr_t)dHidden & 15) == 0;
@@ -557,12 +677,13 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   for (size_t i = 0; i < p.nPieces; ++i) {
     const size_t v0 = i * p.piece, rows = std::min(p.piece, p.V - v0);
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
-    typename FactorEpilogue<T>::Args fa = {packedTarget, packedLse2, factors, (long long)p.piece,
-                                           (int)v0};
-    if ((e = product<T, false, false, 0, false, FactorEpilogue<T>>(
-             dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
-             stream)) != VR_SUCCESS)
-      return e;
+    if (!p.kept) {
+      typename FactorEpilogue<T>::Args fa = {rowTarget, lse2, factors, (long long)p.piece, (int)v0};
+      if ((e = product<T, false, false, 0, false, FactorEpilogue<T>>(
+               dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
+               stream)) != VR_SUCCESS)
+        return e;
+    }
     if (dHidden) {
       typename HiddenEpilogue<T>::Args ha = {
           reinterpret_cast<float*>(w + p.sum), (long long)p.sumLd, static_cast<T*>(dHidden), token,
@@ -576,7 +697,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     if (dWeight) {
       typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, vecW};
       if ((e = product<T, true, true, 0, false, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
-                                                         p.D, p.T128, nullptr, &state->valid, wa,
+                                                         p.D, p.rows, nullptr, &state->valid, wa,
                                                          stream)) != VR_SUCCESS)
         return e;
     }
@@ -596,8 +717,9 @@ vr_result_t vr_linear_xent_workspace_bytes(const void* hidden, size_t hiddenStri
                                            size_t dim, size_t vocab, vr_dtype_t dtype, int grads,
                                            size_t* bytes) {
   XentPlan p = {};
-  if (!bytes || !make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype,
-                           grads != 0, &p))
+  if (!bytes || grads < 0 || grads > 2 ||
+      !make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype, grads != 0,
+                 grads == 1, &p))
     return VR_ERR_INVALID_ARGUMENT;
   *bytes = p.bytes;
   return VR_SUCCESS;
@@ -610,8 +732,12 @@ vr_result_t vr_linear_xent(const void* hidden, size_t hiddenStride, const void* 
                            void* dHidden, void* dWeight, void* workspace, size_t workspaceBytes,
                            void* stream) {
   XentPlan p = {};
-  if (!make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype,
-                 dHidden || dWeight, &p) ||
+  const bool grads = dHidden || dWeight;
+  auto plan = [&](bool kept) {
+    return make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype, grads,
+                     kept, &p);
+  };
+  if (!plan(true) || (workspaceBytes < p.bytes && !plan(false)) ||
       !weight || !loss || !workspace || (tokens && (!hidden || !targets || !losses || !lse)) ||
       workspaceBytes < p.bytes || ((uintptr_t)workspace & 15) || ((uintptr_t)targets & 7) ||
       (((uintptr_t)losses | (uintptr_t)lse | (uintptr_t)loss) & 3) ||

@@ -448,13 +448,19 @@ vr_result_t vr_allreduce_ring_stepwise_noalloc(const void* const* sendbufs, void
  * dHidden (tokens x dim), dWeight (vocab x dim): contiguous, of dtype; each
  * may be NULL, both for the loss alone.
  * Products are exact and summed in fp32, as are the softmax and the losses;
- * in the gradients softmax minus one-hot is rounded to dtype once (fp16:
- * scaled by 2^14 first) and each gradient once (fp16: scale it into range
- * with gradScale).  When no token counts, the loss and the gradients are 0.
+ * in the gradients softmax minus one-hot is rounded to dtype (once, where the
+ * numerators are kept twice; fp16: scaled by 2^14 first) and each gradient
+ * once (fp16: scale it into range with gradScale).  When no token counts, the loss and the gradients are 0.
+ * With gradients, and tokens <= dim (or at most 256 MB of them), the softmax
+ * numerators are kept in 16 bits between the passes, if the workspace has
+ * room: 6 tokens dim vocab operations.  Else the vocabulary is taken in
+ * pieces and the logits are computed twice, 8 tokens dim vocab operations.
+ * vr_linear_xent_workspace_bytes gives the size for the loss alone (grads =
+ * 0), for the gradients (1), and the least for the gradients (2: in pieces).
  * Rows that are not 16-byte units (dim or stride not a multiple of 8, or a
  * misaligned buffer) are copied into the workspace first; its size depends
  * on the buffers' alignment, so vr_linear_xent_workspace_bytes takes the
- * call's own pointers and strides (grads: whether either gradient is wanted).
+ * call's own pointers and strides.
  * Errors: VR_ERR_INVALID_ARGUMENT for fp32 or a bad dtype, dim or vocab < 1,
  * tokens or vocab above 2^30, dim above 2^24, a stride below dim or above
  * 2^32, a NULL or misaligned buffer, an overlap or a short workspace. */

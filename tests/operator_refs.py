@@ -73,7 +73,7 @@ def xent(hidden, weight, targets, ignore, mean, grad_scale):
     """The cross entropy and its gradients in 64 bits, with bounds on what the
     operator's arithmetic may differ by: products exact, fp32 sums that may
     truncate (2^-23 a term), exp and log in fp32, softmax minus one-hot
-    rounded to the type once."""
+    rounded to the type, its softmax part twice at most."""
     ty = hidden.dtype
     h, w = hidden.double(), weight.double()
     T, D = h.shape
@@ -104,7 +104,7 @@ def xent(hidden, weight, targets, ignore, mean, grad_scale):
     one[torch.arange(len(rows), device=h.device), hot[rows]] = 1.0
     g = p - one
     bp = p * (el[rows] + b_lse[rows, None] + big[rows, None] * 2.0 ** -21 + 8 * U32)
-    bg = bp + (g.abs() + bp) * U_T[ty] + (2.0 ** -39 if ty == torch.float16 else 2.0 ** -126)
+    bg = bp + (p + g.abs() + 2 * bp) * U_T[ty] + (2.0 ** -39 if ty == torch.float16 else 2.0 ** -126)
     s = per * grad_scale
     dh = torch.zeros_like(h)
     b_dh = torch.zeros_like(h)

@@ -28,7 +28,8 @@ def make(T, D, V, ty, seed, ignored=0.0, spread=2.0):
     return h, w, y
 
 
-def call(h, w, y, code, mean=True, scale=1.0, dh=True, dw=True, ignore=IGNORE, stream=None):
+def call(h, w, y, code, mean=True, scale=1.0, dh=True, dw=True, ignore=IGNORE, stream=None,
+         least=False):
     T, D = h.shape
     V = w.shape[0]
     losses = torch.full((T,), math.nan, device="cuda")
@@ -37,7 +38,8 @@ def call(h, w, y, code, mean=True, scale=1.0, dh=True, dw=True, ignore=IGNORE, s
     gh = torch.full((T, D), math.nan, device="cuda", dtype=h.dtype) if dh else None
     gw = torch.full((V, D), math.nan, device="cuda", dtype=h.dtype) if dw else None
     hs, ws = max(h.stride(0), D), max(w.stride(0), D)
-    n = vr.vr_linear_xent_workspace_bytes(h, hs, w, ws, T, D, V, code, dh or dw)
+    n = vr.vr_linear_xent_workspace_bytes(h, hs, w, ws, T, D, V, code,
+                                          0 if not (dh or dw) else 2 if least else 1)
     # a workspace that holds NaN at the start
     work = torch.full((n,), 255, device="cuda", dtype=torch.uint8)
     vr.vr_linear_xent(h, hs, w, ws, y, T, D, V, code, ignore, mean, scale, losses, lse, loss, gh,
@@ -55,8 +57,8 @@ def compare(got, want, ty, norm=True):
     refs.assert_close(lse, want["lse"], want["b_lse"], torch.float32, "lse")
     refs.assert_close(losses, want["losses"], want["b_losses"], torch.float32, "losses")
     assert abs(float(loss) - want["loss"]) <= want["b_loss"] + 1e-30
-    # norm: two independent roundings to the type, each u / sqrt(3) at most on
-    # average
+    # norm: three independent roundings to the type at most, each u / sqrt(3)
+    # at most on average
     if gh is not None:
         refs.assert_close(gh, want["dh"], want["b_dh"], ty, "dHidden")
         assert not norm or refs.norm_error(gh, want["dh"]) <= refs.U_T[ty]
@@ -94,6 +96,18 @@ def test_several_pieces_of_the_vocabulary():
     """40 000 x 4096 gradient factors are more than one piece; T is ragged."""
     h, w, y = make(4001, 64, 40000, torch.bfloat16, 3, ignored=0.1)
     check(h, w, y, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,D,V", [(1, 64, 700), (100, 264, 3000), (700, 130, 2500)])
+def test_the_least_workspace(T, D, V, dtype):
+    """Without room for the numerators the vocabulary goes in pieces; the loss
+    is the same to the bit."""
+    h, w, y = make(T, D, V, DT[dtype][1], 21, ignored=0.2)
+    scale = 64.0 * T if dtype == "fp16" else 1.0
+    a, _ = check(h, w, y, dtype, scale=scale, least=True)
+    b = call(h, w, y, DT[dtype][0], scale=scale)
+    assert all(torch.equal(x, z) for x, z in zip(a[:3], b[:3]))
 
 
 @pytest.mark.parametrize("ignored", [0.3, 0.9])

@@ -84,9 +84,12 @@ def test_linear_xent_workspace():
     # rows that are no 16-byte units need a copy
     assert size(A, 65, A, 64, 1000, 64, 5000, B, 0) > loss
     assert size(A + 2, 64, A, 64, 1000, 64, 5000, B, 0) > loss
-    # the gradient factors are taken in pieces: the workspace does not hold
-    # tokens x vocab of them
+    assert code(size, A, 64, A, 64, 10, 64, 100, B, 3) == INV
+    # many tokens, or the least workspace: the gradient factors are taken in
+    # pieces, tokens x vocab of them are not held
     assert size(A, 64, A, 64, 1 << 16, 64, 1 << 17, B, 1) < (1 << 33)
+    kept, least = (size(A, 4096, A, 4096, 4096, 4096, 1 << 17, B, g) for g in (1, 2))
+    assert kept > 2 << 29 and least < 1 << 29
 
 
 def ortho_args(**kw):
