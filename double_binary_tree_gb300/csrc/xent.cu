@@ -34,7 +34,9 @@ namespace {
 constexpr int kBN = 256;
 // The losses are fp32 results: their logits are summed in chunks of 512.
 // (The gradients' roundings to 16 bits are far above the truncation.)
-constexpr int kStatsChunk = 8;
+// Up to 128 rows the weight's traffic bounds the product, whose sums then
+// change hands every 128.
+constexpr int kStatsChunk = 8, kFewRowsChunk = 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Device-side results of the preparation.
@@ -61,16 +63,28 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return (uint32_t)Ty<T>::narrow(a) | (uint32_t)Ty<T>::narrow(b) << 16;
 }
 
-// 32 consecutive 16-bit values of one row; `vec`: 16-byte stores allowed.
+// 32 consecutive 16-bit values of one row.  `align`: bytes that a store may
+// take (2, 16 or 32); a warp's rows are 32 lines apart, so half as many
+// stores are half the time.
 template <typename T>
-__device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, bool vec) {
+__device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, int align) {
   typename Ty<T>::Bits* o = reinterpret_cast<typename Ty<T>::Bits*>(out);
-  if (vec && cols >= 32) {
+  if (align >= 16 && cols >= 32) {
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(o)[i] =
-          make_uint4(pack2<T>(v[8 * i], v[8 * i + 1]), pack2<T>(v[8 * i + 2], v[8 * i + 3]),
-                     pack2<T>(v[8 * i + 4], v[8 * i + 5]), pack2<T>(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    if (align == 32) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 2 * i),
+                     "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                     "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint4*>(o + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
@@ -120,6 +134,7 @@ struct StatsEpilogue {
     // nothing but -inf: subtract 0, so that exp2 gives 0, not NaN
     const float base = top == -INFINITY ? 0.0f : top;
     const bool store = KEEP && t < M && t < a.state->valid;
+    constexpr float up = KEEP ? (float)kShift<T> : 0.0f;  // exact: a power of two
 #pragma unroll
     for (int c = 0; c < COLS; c += 32) {
       if (first + c >= g.N) break;
@@ -127,12 +142,12 @@ struct StatsEpilogue {
       fetch(c, v);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        v[i] = exp2_fast(fmaf(v[i], kLog2e, -base));
+        v[i] = exp2_fast(fmaf(v[i], kLog2e, up - base));
         sum += v[i];
-        if (KEEP) v[i] *= (float)(1 << kShift<T>);
       }
-      if (store) store32(a.out + (long long)t * a.ld + first + c, v, 32, true);
+      if (store) store32(a.out + (long long)t * a.ld + first + c, v, 32, 32);
     }
+    sum *= 1.0f / (float)(1 << (KEEP ? kShift<T> : 0));
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
     if (t < M) a.parts[(long long)t * a.nParts + first / (kBN / 2)] = make_float2(top, sum);
   }
@@ -225,7 +240,7 @@ struct FactorEpilogue {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         v[i] = live ? exp2_fast(fmaf(v[i], kLog2e, sub)) : 0.0f;
-      store32(out + c, v, 32, true);
+      store32(out + c, v, 32, 32);
     }
     // the target's factor over the one just written by the same thread
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) {
@@ -245,7 +260,7 @@ struct HiddenEpilogue {
     T* out;                // [T][N]
     const int* token;      // packed token -> token
     const XentState* state;
-    int first, last, vec;
+    int first, last, align;
   };
   template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
@@ -272,7 +287,7 @@ struct HiddenEpilogue {
       if (a.last) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= scale;
-        store32(out + n, v, g.N - n, a.vec != 0);
+        store32(out + n, v, g.N - n, a.align);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -289,7 +304,7 @@ struct WeightEpilogue {
   struct Args {
     T* out;  // the piece's first row, [V][N]
     const XentState* state;
-    int vec;
+    int align;
   };
   template <int COLS, class Acc>
   static __device__ __forceinline__ void run(const Args& a, const GemmArgs& g, const Tile& o,
@@ -305,7 +320,7 @@ struct WeightEpilogue {
       if (v0 >= M) continue;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= scale;
-      store32(a.out + (long long)v0 * g.N + n, v, g.N - n, a.vec != 0);
+      store32(a.out + (long long)v0 * g.N + n, v, g.N - n, a.align);
     }
   }
 };
@@ -553,13 +568,14 @@ vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* 
   const Operand oa = {a, nullptr, aLd}, ob = {b, nullptr, bLd};
   const GemmSize z = {M, N, K, 1, false};
   if (M <= kTileM) {
+    constexpr int FEW = CHUNK ? kFewRowsChunk : 0;
     if constexpr (SPLIT) {
       const int s = gemm_shares<kBN, false>(z, dev.sms);
       if (s > 1)
-        return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, false, true, Epi>(dev, oa, ob, z, dynM, dynK,
+        return gemm_launch<T, kBN, 1, AMN, BMN, FEW, false, true, Epi>(dev, oa, ob, z, dynM, dynK,
                                                                          epi, s, stream);
     }
-    return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, false, false, Epi>(dev, oa, ob, z, dynM, dynK,
+    return gemm_launch<T, kBN, 1, AMN, BMN, FEW, false, false, Epi>(dev, oa, ob, z, dynM, dynK,
                                                                       epi, 1, stream);
   }
   if constexpr (SPLIT) {
@@ -672,8 +688,11 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
                        dim3(256), args, 0, stream)) != VR_SUCCESS)
       return e;
   }
-  const int vecH = p.D % 8 == 0 && ((uintptr_t)dHidden & 15) == 0;
-  const int vecW = p.D % 8 == 0 && ((uintptr_t)dWeight & 15) == 0;
+  auto aligned = [&](const void* out) {  // of every row of it
+    const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * p.D);
+    return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 2;
+  };
+  const int alignH = aligned(dHidden), alignW = aligned(dWeight);
   for (size_t i = 0; i < p.nPieces; ++i) {
     const size_t v0 = i * p.piece, rows = std::min(p.piece, p.V - v0);
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
@@ -687,7 +706,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     if (dHidden) {
       typename HiddenEpilogue<T>::Args ha = {
           reinterpret_cast<float*>(w + p.sum), (long long)p.sumLd, static_cast<T*>(dHidden), token,
-          state, i == 0, i + 1 == p.nPieces, vecH};
+          state, i == 0, i + 1 == p.nPieces, alignH};
       if ((e = product<T, false, true, 0, true, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
                                                           weightStride, p.T, p.D, rows,
                                                           &state->valid, nullptr, ha, stream)) !=
@@ -695,7 +714,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
         return e;
     }
     if (dWeight) {
-      typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, vecW};
+      typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, alignW};
       if ((e = product<T, true, true, 0, false, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
                                                          p.D, p.rows, nullptr, &state->valid, wa,
                                                          stream)) != VR_SUCCESS)
