@@ -113,34 +113,12 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// Relaxed: what is handed over is tensor memory, ordered by tmem_fence_before.
+// (A release at cluster scope waits for the thread's global stores too: a third
+// of the time of a kernel whose epilogue stores.)
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
-}
-// wait_phase (staged.cuh) at cluster scope.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, unsigned parity,
-                                             const volatile int* abort, bool honorAbort,
-                                             unsigned long long limitNs) {
-  auto done = [&]() {
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  if (done()) return true;
-  const unsigned long long t0 = global_ns();
-  for (unsigned it = 1;; ++it) {
-    if (done()) return true;
-    if ((it & 15) == 0) {
-      if (honorAbort && *abort) return false;
-      if (global_ns() - t0 > limitNs) return false;
-    }
-  }
 }
 // Shared-memory operand descriptor of a 128-byte swizzled tile.  K-major:
 // rows of 64 elements, eight rows to a 1024-byte group (strideBytes).
@@ -417,8 +395,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   auto auxDone = [&](int half, int i) { return lowEmpty + 8u * (5 + 2 * half + i); };
   const uint32_t aux0 = stage0 + (unsigned)(kStages * Shape::kStageBytes);
   auto wait = [&](uint32_t bar, unsigned parity, bool honorAbort = true) {
-    return PAIR ? wait_cluster(bar, parity, &abortFlag, honorAbort, g.timeoutNs)
-                : wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
+    return wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
   };
 
   if (threadIdx.x == 0) {
