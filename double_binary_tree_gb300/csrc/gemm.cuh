@@ -8,8 +8,8 @@
 // accumulator and half of B, so a slice of the tile costs an SM a third less
 // shared memory traffic (what bounds 128-wide tiles) and L2 traffic.  Warp 0 moves 64-deep slices of
 // A and B into a ring of shared-memory stages with tensor copies (TMA), warp
-// 1 issues the products on them, warps 4-11 read finished accumulators from
-// tensor memory and run the epilogue.  Two accumulators take turns, so the
+// 1 issues the products on them, warps 4 on (Epi::kWarps of them, 8 or 16) read
+// finished accumulators from tensor memory and run the epilogue.  Two accumulators take turns, so the
 // epilogue of one tile overlaps the products of the next.
 //
 // PARTS = 2: each operand is the sum of a high and a low 16-bit plane
@@ -44,8 +44,6 @@ namespace vr {
 
 constexpr int kTileM = 128;
 constexpr int kTileK = 64;  // 16-bit elements: one 128-byte swizzled row
-constexpr int kGemmThreads = 384;
-constexpr int kEpilogueWarps = 8;
 constexpr int kGemmSmem = 220 * 1024;  // barriers included
 
 struct GemmArgs {
@@ -197,6 +195,18 @@ __device__ __forceinline__ void tmem_wait(float (&v)[32]) {
                :
                : "memory");
 }
+// The same for 16 columns, in one go.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   tmem_issue32(addr, v);
   tmem_wait(v);
@@ -213,6 +223,7 @@ __device__ __forceinline__ float tmem_load1(uint32_t addr) {
 // A warp's rows of a finished accumulator in tensor memory; called by whole
 // warps.  Without a product (K = 0) the sums are zero and it is not read.
 struct TmemAcc {
+  static constexpr int kStep = 32;  // columns best fetched at a time
   uint32_t addr;
   bool summed;
   __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
@@ -245,11 +256,13 @@ struct TmemAcc {
 // asked for are constants once the epilogue's loops are unrolled.
 template <int N>
 struct RegAcc {
+  static constexpr int kStep = 16;
   const float (&sum)[N];
   int first;
-  __device__ __forceinline__ void operator()(int c, float (&v)[32]) const {
+  template <int K>
+  __device__ __forceinline__ void operator()(int c, float (&v)[K]) const {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = sum[c - first + i];  // a constant once unrolled
+    for (int i = 0; i < K; ++i) v[i] = sum[c - first + i];  // a constant once unrolled
   }
   template <class F>
   __device__ __forceinline__ void pick(int c, F f) const {
@@ -365,7 +378,7 @@ __device__ __forceinline__ Tile tile_of(int t, int tilesM, int tilesN, bool tria
 // next chunk is summed meanwhile in the other accumulator.
 template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, bool PAIR, bool SPLIT,
           class Epi>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(128 + 32 * Epi::kWarps, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ typename Epi::Args e) {
   constexpr bool kAux = Epi::kAux && !SPLIT;
   using Shape = GemmShape<BN, PARTS, PAIR, kAux ? 2 * kAuxHalf : 0>;
@@ -373,7 +386,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   constexpr int kStages = Shape::kStages;
   constexpr int kCtas = PAIR ? 2 : 1;  // that share a tile's products
   extern __shared__ unsigned char smemRaw[];
-  constexpr int kAccs = Shape::kAccs;
+  constexpr int kAccs = Shape::kAccs, kEpilogueWarps = Epi::kWarps;
+  constexpr int kGroups = kEpilogueWarps / 4;  // of four warps: the rows of the accumulator
+  constexpr int kPart = BN / kGroups;          // columns of a group
+  static_assert(!kAux || kGroups == 2, "one helper warp per group");
   __shared__ alignas(8) uint64_t bars[2 * kStages + 2 * kAccs + 2 + (kAux ? 8 : 0)];
   __shared__ uint32_t tmemBase;
   __shared__ volatile int abortFlag;
@@ -444,7 +460,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int K = g.dynK ? min(*g.dynK, g.K) : g.K;
   const int tilesM = (M + Shape::kTileRows - 1) / Shape::kTileRows, tilesN = (g.N + BN - 1) / BN;
   const int slices = (K + kTileK - 1) / kTileK;
-  constexpr int kHalf = BN / 2;  // columns of an epilogue warp
   int tiles = tilesM * tilesN;
   if (g.triangle) {
     tiles = 0;
@@ -610,15 +625,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     auto units = [&](const Tile& o, const auto& acc) {
       if constexpr (kAux) {
 #pragma unroll
-        for (int c = 0; c < kHalf; c += kAuxCols) {
-          const int n = o.n0 + half * kHalf + c, b = unit & 1;
+        for (int c = 0; c < kPart; c += kAuxCols) {
+          const int n = o.n0 + half * kPart + c, b = unit & 1;
           if (Epi::skip(g, o, n, M)) break;
           const bool there = wait(auxFull(half, b), (unsigned)(unit >> 1 & 1));
           if (!__all_sync(0xffffffffu, there)) {
             raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
             return false;
           }
-          Epi::unit(e, g, o, row, n, half * kHalf + c, M, acc,
+          Epi::unit(e, g, o, row, n, half * kPart + c, M, acc,
                     AuxTile{aux0 + (unsigned)(half * kAuxHalf + b * (2 * kAuxTile))});
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -641,59 +656,69 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                        : "memory");
       };
       if constexpr (CHUNK > 0) {
-        float sum[kHalf];
+        float sum[kPart];
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < kPart; ++i) sum[i] = 0.0f;
         for (int c0 = 0; c0 < blocks; c0 += chunk) {
           left = !next();
           if (left) break;
-          auto add = [&](uint32_t at) {  // two loads in flight
+          auto add = [&](uint32_t at) {
+            if constexpr (kEpilogueWarps == 8) {  // two loads in flight
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 64) {
-              float v[32], w[32];
-              tmem_issue32(at + (unsigned)c, v);
-              tmem_issue32(at + (unsigned)c + 32, w);
-              tmem_wait(v);
-              tmem_wait(w);
+              for (int c = 0; c < kPart; c += 64) {
+                float v[32], w[32];
+                tmem_issue32(at + (unsigned)c, v);
+                tmem_issue32(at + (unsigned)c + 32, w);
+                tmem_wait(v);
+                tmem_wait(w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) sum[c + i] += v[i], sum[c + 32 + i] += w[i];
+                for (int i = 0; i < 32; ++i) sum[c + i] += v[i], sum[c + 32 + i] += w[i];
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < kPart; c += 16) {
+                float v[16];
+                tmem_load16(at + (unsigned)c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
+              }
             }
           };
-          add(quadBase + (unsigned)(buf * BN + half * kHalf));
+          add(quadBase + (unsigned)(buf * BN + half * kPart));
           release();
           if (PARTS == 2 && c0 + chunk >= blocks) {  // done with the last slice's
-            add(quadBase + (unsigned)(kAccs * BN + half * kHalf));
+            add(quadBase + (unsigned)(kAccs * BN + half * kPart));
             hand_back(lowEmpty);
           }
         }
         if (left) break;
-        const RegAcc<kHalf> acc{sum, half * kHalf};
+        const RegAcc<kPart> acc{sum, half * kPart};
         if constexpr (SPLIT) {
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
+          for (int c = 0; c < kPart; c += 32) {
             float v[32];
-            acc(half * kHalf + c, v);
-            put(half * kHalf + c, v);
+            acc(half * kPart + c, v);
+            put(half * kPart + c, v);
           }
         } else if constexpr (kAux) {
           if (!units(o, acc)) break;
         } else {
-          Epi::template run<kHalf>(e, g, o, row, half * kHalf, M, acc);
+          Epi::template run<kPart>(e, g, o, row, half * kPart, M, acc);
         }
       } else {
         if (blocks && !next()) break;
         const TmemAcc acc{quadBase + (unsigned)(buf * BN), blocks != 0};
         if constexpr (SPLIT) {
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) {
+          for (int c = 0; c < kPart; c += 32) {
             float v[32];
-            acc(half * kHalf + c, v);
-            put(half * kHalf + c, v);
+            acc(half * kPart + c, v);
+            put(half * kPart + c, v);
           }
         } else if constexpr (kAux) {
           if (!units(o, acc)) break;
         } else {
-          Epi::template run<kHalf>(e, g, o, row, half * kHalf, M, acc);
+          Epi::template run<kPart>(e, g, o, row, half * kPart, M, acc);
         }
         if (blocks) release();
       }
@@ -726,8 +751,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int t = firstTile; ok && t < tiles; t += tileStep) {
         Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
         o.m0 += (int)inPair * kTileM;
-        for (int c = 0; ok && c < kHalf; c += kAuxCols) {
-          const int n = o.n0 + half * kHalf + c, b = unit & 1;
+        for (int c = 0; ok && c < kPart; c += kAuxCols) {
+          const int n = o.n0 + half * kPart + c, b = unit & 1;
           if (Epi::skip(g, o, n, M)) break;
           if (unit >= 2) finish(unit - 2);
           if (!ok) break;
@@ -759,12 +784,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if constexpr (SPLIT) {
     __syncwarp();
     cluster_sync();  // all shares' sums are in place
-    constexpr int kGroups = BN / 32;  // of 32 columns; four warps (row quadrants) each
+    constexpr int kPieces = BN / 32;  // of 32 columns; four warps (row quadrants) each
     if (warp >= 4 && firstTile < tiles) {
       const int quad = warp % 4, row = quad * 32 + lane;
       Tile o = tile_of<Shape::kTileRows, BN>(firstTile, tilesM, tilesN, g.triangle);
       o.m0 += (int)inPair * kTileM;
-      for (int group = share * 2 + (warp - 4) / 4; group < kGroups; group += 2 * shares) {
+      for (int group = share * kGroups + (warp - 4) / 4; group < kPieces;
+           group += kGroups * shares) {
         float sum[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) sum[i] = 0.0f;
@@ -863,7 +889,7 @@ vr_result_t gemm_launch(const OpDevice& dev, const Operand& a, const Operand& b,
   const size_t groups = SPLIT ? tiles : std::min<size_t>(tiles, dev.sms / kCtas);
   const size_t cluster = kCtas * (SPLIT ? (size_t)shares : 1);
   void* args[] = {&g, &epi};
-  return op_launch(fn, dim3((unsigned)(groups * cluster)), dim3(kGemmThreads), args, Shape::kSmem,
+  return op_launch(fn, dim3((unsigned)(groups * cluster)), dim3(128 + 32 * Epi::kWarps), args, Shape::kSmem,
                    stream, (int)cluster);
 }
 

@@ -125,6 +125,7 @@ __device__ __forceinline__ void store_tile(const AuxTile& tile, int plane, int r
 // products, 22 against 26 us at 4 x 1024 x 4096.)
 struct SymmetricEpilogue {
   static constexpr bool kAux = false;
+  static constexpr int kWarps = 8;
   struct Args {
     PlaneArgs p;
     int nIn, nOut;  // planes read and written
@@ -174,6 +175,7 @@ struct SymmetricEpilogue {
 template <typename T>
 struct ApplyEpilogue {
   static constexpr bool kAux = true;
+  static constexpr int kWarps = 8;
   struct Args {
     AuxArgs aux;
     PlaneArgs p;

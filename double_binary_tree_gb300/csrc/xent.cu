@@ -32,6 +32,7 @@ namespace vr {
 namespace {
 
 constexpr int kBN = 256;
+constexpr int kPartCols = kBN / 4;  // columns of one pair of statistics
 // The losses are fp32 results: their logits are summed in chunks of 512.
 // (The gradients' roundings to 16 bits are far above the truncation.)
 // Up to 128 rows the weight's traffic bounds the product, whose sums then
@@ -63,31 +64,31 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return (uint32_t)Ty<T>::narrow(a) | (uint32_t)Ty<T>::narrow(b) << 16;
 }
 
-// 32 consecutive 16-bit values of one row.  `align`: bytes that a store may
+// Consecutive 16-bit values of one row.  `align`: bytes that a store may
 // take (2, 16 or 32); a warp's rows are 32 lines apart, so half as many
 // stores are half the time.
-template <typename T>
-__device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, int align) {
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* out, const float (&v)[N], int cols, int align) {
   typename Ty<T>::Bits* o = reinterpret_cast<typename Ty<T>::Bits*>(out);
-  if (align >= 16 && cols >= 32) {
-    uint32_t w[16];
+  if (align >= 16 && cols >= N) {
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < N / 2; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
     if (align == 32) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 8)
+      for (int i = 0; i < N / 2; i += 8)
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 2 * i),
                      "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
                      "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
                      : "memory");
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
+      for (int i = 0; i < N / 2; i += 4)
         *reinterpret_cast<uint4*>(o + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < N; ++i)
       if (i < cols) o[i] = Ty<T>::narrow(v[i]);
   }
 }
@@ -98,6 +99,7 @@ __device__ __forceinline__ void store32(T* out, const float (&v)[32], int cols, 
 template <typename T, bool KEEP>
 struct StatsEpilogue {
   static constexpr bool kAux = false;
+  static constexpr int kWarps = 16;
   struct Args {
     const int* target;  // of a row, -1: none
     float* targetLogit;
@@ -113,43 +115,46 @@ struct StatsEpilogue {
     const int t = o.m0 + row;
     const int first = o.n0 + col0;
     const int at = t < M ? a.target[t] - first : -1;
-    auto fetch = [&](int c, float(&v)[32]) {
+    constexpr int STEP = Acc::kStep;
+    auto fetch = [&](int c, float(&v)[STEP]) {
       acc(col0 + c, v);
-      if (first + c + 32 > g.N) {
+      if (first + c + STEP > g.N) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < STEP; ++i)
           if (first + c + i >= g.N) v[i] = -INFINITY;
       }
     };
-    float top = -INFINITY, sum = 0.0f;
+    // (four chains each of maxima and sums, one would wait for itself)
+    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sums[4] = {};
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
+    for (int c = 0; c < COLS; c += STEP) {
       if (first + c >= g.N) break;
-      float v[32];
+      float v[STEP];
       fetch(c, v);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+      for (int i = 0; i < STEP; ++i) tops[i % 4] = fmaxf(tops[i % 4], v[i]);
     }
-    top *= kLog2e;
+    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * kLog2e;
     // nothing but -inf: subtract 0, so that exp2 gives 0, not NaN
     const float base = top == -INFINITY ? 0.0f : top;
     const bool store = KEEP && t < M && t < a.state->valid;
     constexpr float up = KEEP ? (float)kShift<T> : 0.0f;  // exact: a power of two
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
+    for (int c = 0; c < COLS; c += STEP) {
       if (first + c >= g.N) break;
-      float v[32];
+      float v[STEP];
       fetch(c, v);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < STEP; ++i) {
         v[i] = exp2_fast(fmaf(v[i], kLog2e, up - base));
-        sum += v[i];
+        sums[i % 4] += v[i];
       }
-      if (store) store32(a.out + (long long)t * a.ld + first + c, v, 32, 32);
+      if (store) store_row(a.out + (long long)t * a.ld + first + c, v, STEP, 32);
     }
-    sum *= 1.0f / (float)(1 << (KEEP ? kShift<T> : 0));
+    const float sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) *
+                      (1.0f / (float)(1 << (KEEP ? kShift<T> : 0)));
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
-    if (t < M) a.parts[(long long)t * a.nParts + first / (kBN / 2)] = make_float2(top, sum);
+    if (t < M) a.parts[(long long)t * a.nParts + first / kPartCols] = make_float2(top, sum);
   }
 };
 
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ 
       const int c = c0 + u * 256 * 8;
       if (t < valid && c < a.V) {
         q[u] = *reinterpret_cast<const uint4*>(out + c);
-        part[u] = a.parts[(long long)t * a.nParts + c / (kBN / 2)];
+        part[u] = a.parts[(long long)t * a.nParts + c / kPartCols];
       }
     }
 #pragma unroll
@@ -217,6 +222,7 @@ __global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ 
 template <typename T>
 struct FactorEpilogue {
   static constexpr bool kAux = false;
+  static constexpr int kWarps = 16;
   struct Args {
     const int* target;   // packed tokens' targets
     const float* lse2;   // their log sums, in units of log 2
@@ -240,7 +246,7 @@ struct FactorEpilogue {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         v[i] = live ? exp2_fast(fmaf(v[i], kLog2e, sub)) : 0.0f;
-      store32(out + c, v, 32, 32);
+      store_row(out + c, v, 32, 32);
     }
     // the target's factor over the one just written by the same thread
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) {
@@ -254,6 +260,7 @@ struct FactorEpilogue {
 template <typename T>
 struct HiddenEpilogue {
   static constexpr bool kAux = false;
+  static constexpr int kWarps = 8;
   struct Args {
     float* sum;            // [packed tokens][ld]
     long long ld;
@@ -287,7 +294,7 @@ struct HiddenEpilogue {
       if (a.last) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= scale;
-        store32(out + n, v, g.N - n, a.align);
+        store_row(out + n, v, g.N - n, a.align);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -301,6 +308,7 @@ struct HiddenEpilogue {
 template <typename T>
 struct WeightEpilogue {
   static constexpr bool kAux = false;
+  static constexpr int kWarps = 8;
   struct Args {
     T* out;  // the piece's first row, [V][N]
     const XentState* state;
@@ -320,7 +328,7 @@ struct WeightEpilogue {
       if (v0 >= M) continue;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= scale;
-      store32(a.out + (long long)v0 * g.N + n, v, g.N - n, a.align);
+      store_row(a.out + (long long)v0 * g.N + n, v, g.N - n, a.align);
     }
   }
 };
@@ -529,7 +537,7 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   p->padWeight = !packed_rows(weight, weightStride);
   p->Dp = up(D, 8);
   p->rows = grads ? up(T + kTileK, kTileM) : T;
-  p->nParts = 2 * (up(V, kBN) / kBN);
+  p->nParts = up(V, kBN) / kPartCols;
   p->kept = grads && kept && (T <= D || 2 * p->rows * up(V, kBN) <= kPieceBytes);
   p->piece = p->kept ? up(V, kBN) : piece_rows(p->rows, V);
   p->nPieces = (V + p->piece - 1) / p->piece;
@@ -560,32 +568,33 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   return true;
 }
 
-// One product; pairs of CTAs where the rows fill them.
+// One product; pairs of CTAs where the rows fill them.  CHUNK > 0: sums in
+// chunks, which one chunk or less does not need.
 template <typename T, bool AMN, bool BMN, int CHUNK, bool SPLIT, class Epi>
 vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* b, size_t bLd,
                     size_t M, size_t N, size_t K, const int* dynM, const int* dynK,
                     typename Epi::Args& epi, void* stream) {
   const Operand oa = {a, nullptr, aLd}, ob = {b, nullptr, bLd};
   const GemmSize z = {M, N, K, 1, false};
-  if (M <= kTileM) {
-    constexpr int FEW = CHUNK ? kFewRowsChunk : 0;
-    if constexpr (SPLIT) {
-      const int s = gemm_shares<kBN, false>(z, dev.sms);
-      if (s > 1)
-        return gemm_launch<T, kBN, 1, AMN, BMN, FEW, false, true, Epi>(dev, oa, ob, z, dynM, dynK,
-                                                                         epi, s, stream);
-    }
-    return gemm_launch<T, kBN, 1, AMN, BMN, FEW, false, false, Epi>(dev, oa, ob, z, dynM, dynK,
-                                                                      epi, 1, stream);
-  }
+  const bool few = M <= kTileM;
+#define VR_PRODUCT(C, PAIR, SHARED, SHARES)                                             \
+  return gemm_launch<T, kBN, 1, AMN, BMN, C, PAIR, SHARED, Epi>(dev, oa, ob, z, dynM, dynK, \
+                                                                epi, SHARES, stream)
   if constexpr (SPLIT) {
-    const int s = gemm_shares<kBN, true>(z, dev.sms);
-    if (s > 1)
-      return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, true, true, Epi>(dev, oa, ob, z, dynM, dynK,
-                                                                      epi, s, stream);
+    static_assert(CHUNK == 0, "shares are summed in one piece");
+    const int shares = few ? gemm_shares<kBN, false>(z, dev.sms) : gemm_shares<kBN, true>(z, dev.sms);
+    if (shares > 1) {
+      if (few) VR_PRODUCT(0, false, true, shares);
+      VR_PRODUCT(0, true, true, shares);
+    }
   }
-  return gemm_launch<T, kBN, 1, AMN, BMN, CHUNK, true, false, Epi>(dev, oa, ob, z, dynM, dynK, epi,
-                                                                   1, stream);
+  if constexpr (CHUNK > 0) {
+    if (few && K > kFewRowsChunk * kTileK) VR_PRODUCT(kFewRowsChunk, false, false, 1);
+    if (!few && K > CHUNK * kTileK) VR_PRODUCT(CHUNK, true, false, 1);
+  }
+  if (few) VR_PRODUCT(0, false, false, 1);
+  VR_PRODUCT(0, true, false, 1);
+#undef VR_PRODUCT
 }
 
 template <typename T>
