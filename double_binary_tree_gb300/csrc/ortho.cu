@@ -45,27 +45,37 @@ __device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
   lo = __float2half_rn(v - __half2float(hi));
 }
 
-// 32 consecutive values of a row of a plane whose rows are whole groups of 32.
+// 32 consecutive values of a row of a plane whose rows are whole groups of
+// 32; 32 bytes an access, since a warp's rows are 32 lines apart.
 __device__ __forceinline__ void store_plane(__half* out, const float (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 q;
-    __half2* h = reinterpret_cast<__half2*>(&q);
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-    reinterpret_cast<uint4*>(out)[i] = q;
+    for (int j = 0; j < 8; ++j) {
+      const __half2 h = __floats2half2_rn(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 16 * i),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                 "r"(w[7])
+                 : "memory");
   }
 }
 __device__ __forceinline__ void add_plane(const __half* in, float by, float (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 q = reinterpret_cast<const uint4*>(in)[i];
-    const __half2* h = reinterpret_cast<const __half2*>(&q);
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[8];
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(in + 16 * i)
+                 : "memory");
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(h[j]);
-      v[8 * i + 2 * j] = fmaf(by, f.x, v[8 * i + 2 * j]);
-      v[8 * i + 2 * j + 1] = fmaf(by, f.y, v[8 * i + 2 * j + 1]);
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      v[16 * i + 2 * j] = fmaf(by, f.x, v[16 * i + 2 * j]);
+      v[16 * i + 2 * j + 1] = fmaf(by, f.y, v[16 * i + 2 * j + 1]);
     }
   }
 }
@@ -125,7 +135,7 @@ __device__ __forceinline__ void store_tile(const AuxTile& tile, int plane, int r
 // products, 22 against 26 us at 4 x 1024 x 4096.)
 struct SymmetricEpilogue {
   static constexpr bool kAux = false;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = 16;
   struct Args {
     PlaneArgs p;
     int nIn, nOut;  // planes read and written

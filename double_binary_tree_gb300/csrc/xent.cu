@@ -260,7 +260,7 @@ struct FactorEpilogue {
 template <typename T>
 struct HiddenEpilogue {
   static constexpr bool kAux = false;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = 16;
   struct Args {
     float* sum;            // [packed tokens][ld]
     long long ld;
@@ -308,7 +308,7 @@ struct HiddenEpilogue {
 template <typename T>
 struct WeightEpilogue {
   static constexpr bool kAux = false;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = 16;
   struct Args {
     T* out;  // the piece's first row, [V][N]
     const XentState* state;
@@ -535,7 +535,7 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   // a packed copy of the hidden states serves the gradients
   p->padHidden = !grads && !packed_rows(hidden, hiddenStride);
   p->padWeight = !packed_rows(weight, weightStride);
-  p->Dp = up(D, 8);
+  p->Dp = up(D, 16);  // whole 32-byte sectors: rows that straddle them cost a product a fifth
   p->rows = grads ? up(T + kTileK, kTileM) : T;
   p->nParts = up(V, kBN) / kPartCols;
   p->kept = grads && kept && (T <= D || 2 * p->rows * up(V, kBN) <= kPieceBytes);
