@@ -146,7 +146,8 @@ def _ptr(x):
 def _ptrs(bufs):
     if bufs is None:
         return None
-    return (ctypes.c_void_p * len(bufs))(*[_ptr(b) for b in bufs])
+    return (VP * len(bufs))(*[b if b is None or isinstance(b, int) else b.data_ptr()
+                              for b in bufs])
 
 
 def _stream(s):

@@ -93,6 +93,23 @@ __device__ __forceinline__ void store_row(T* out, const float (&v)[N], int cols,
   }
 }
 
+// The target of a row, -1 where there is none: prepared with the packed
+// tokens, or, for the loss alone, the caller's own.
+struct Targets {
+  const int* of;
+  const long long* raw;  // used where `of` is null
+  long long ignore;
+  int V;
+  __device__ __forceinline__ bool bad(long long y) const {
+    return y != ignore && (y < 0 || y >= V);
+  }
+  __device__ __forceinline__ int at(int row) const {
+    if (of) return of[row];
+    const long long y = raw[row];
+    return y == ignore || bad(y) ? -1 : (int)y;
+  }
+};
+
 // Row statistics of a tile of logits: the maximum (in units of log 2) and
 // the sum of exp over each half tile, and the target's logit; KEEP: and each
 // exp(l - maximum) in 16 bits.
@@ -101,7 +118,7 @@ struct StatsEpilogue {
   static constexpr bool kAux = false;
   static constexpr int kWarps = 16;
   struct Args {
-    const int* target;  // of a row, -1: none
+    Targets target;
     float* targetLogit;
     float2* parts;      // [rows][nParts]
     int nParts;
@@ -114,7 +131,7 @@ struct StatsEpilogue {
                                              int row, int col0, int M, const Acc& acc) {
     const int t = o.m0 + row;
     const int first = o.n0 + col0;
-    const int at = t < M ? a.target[t] - first : -1;
+    const int at = t < M ? a.target.at(t) - first : -1;
     constexpr int STEP = Acc::kStep;
     auto fetch = [&](int c, float(&v)[STEP]) {
       acc(col0 + c, v);
@@ -386,61 +403,110 @@ __global__ void __launch_bounds__(1024) xent_prep_kernel(const __grid_constant__
   }
 }
 
-// A warp per row joins its tiles' (maximum, sum) pairs.
+// A (maximum, sum) pair over more columns: the other's sum brought to the
+// common maximum.  -inf: nothing so far.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.0f : top;
+  return make_float2(top, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
+}
+
+// Joins the rows' pairs, and, in one CTA (ALL), sums the loss.  A warp takes a
+// row, or, where one CTA has few rows, several warps do.
 struct JoinArgs {
   const float2* parts;
   int nParts, T;
-  const int* rowToken;  // packed rows' tokens (-1: none), or null: row = token
-  const XentState* state;
-  const int* target;    // of a row
+  const int* rowToken;     // packed rows' tokens (-1: none), or null: row = token
+  const XentState* state;  // null with raw targets
+  Targets target;
+  int mean;
   const float* targetLogit;
-  float *lse2, *lse, *losses;
+  float *lse2, *lse, *losses, *loss;
+  unsigned* status;
 };
-__global__ void __launch_bounds__(256) xent_join_kernel(const __grid_constant__ JoinArgs a) {
-  pdl_launch();
-  pdl_wait();
-  const int lane = threadIdx.x % 32;
-  const int rows = a.rowToken ? a.state->rows : a.T;
-  for (int t = blockIdx.x * 8 + threadIdx.x / 32; t < rows; t += gridDim.x * 8) {
-    const int token = a.rowToken ? a.rowToken[t] : t;
-    if (token < 0) continue;
-    const float2* p = a.parts + (long long)t * a.nParts;
-    float top = -INFINITY;
-    for (int i = lane; i < a.nParts; i += 32) top = fmaxf(top, p[i].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    for (int i = lane; i < a.nParts; i += 32) sum += p[i].y * exp2f(p[i].x - base);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      const float l2 = base + log2f(sum);
-      const float l = l2 * kLn2;
-      a.lse2[t] = l2;
-      a.lse[token] = l;
-      a.losses[token] = a.target[t] >= 0 ? l - a.targetLogit[t] : 0.0f;
+// The loss from the tokens' losses, by one CTA of 1024 threads: in 64 bits, in
+// a fixed order.  Raw targets are counted here, and bad ones reported.
+__device__ __forceinline__ void sum_losses(const JoinArgs& a) {
+  __shared__ double sSum[32];
+  __shared__ int sCount[32];
+  double sum = 0.0;
+  int count = 0;
+  for (int t = threadIdx.x; t < a.T; t += 1024) {
+    sum += (double)a.losses[t];
+    if (!a.state) {
+      count += a.target.at(t) >= 0;
+      if (a.target.bad(a.target.raw[t])) atomicCAS(a.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
     }
   }
-}
-
-// One CTA: the loss, summed in a fixed order.
-__global__ void __launch_bounds__(1024)
-    xent_loss_kernel(const float* losses, int T, const XentState* state, float* loss) {
-  __shared__ double s[32];
-  pdl_launch();
-  pdl_wait();
-  double sum = 0.0;
-  for (int t = threadIdx.x; t < T; t += 1024) sum += (double)losses[t];
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = sum;
+  count = __reduce_add_sync(0xffffffffu, count);
+  if (threadIdx.x % 32 == 0) sSum[threadIdx.x / 32] = sum, sCount[threadIdx.x / 32] = count;
   __syncthreads();
   if (threadIdx.x == 0) {
-    sum = 0.0;
-    for (int w = 0; w < 32; ++w) sum += s[w];
-    *loss = (float)(sum * (double)state->lossScale);
+    for (int w = 1; w < 32; ++w) sum += sSum[w], count += sCount[w];
+    const float scale = a.state ? a.state->lossScale : a.mean ? 1.0f / (float)max(count, 1) : 1.0f;
+    *a.loss = (float)(sum * (double)scale);
   }
+}
+template <bool ALL>
+__global__ void __launch_bounds__(ALL ? 1024 : 256)
+    xent_join_kernel(const __grid_constant__ JoinArgs a) {
+  constexpr int WARPS = ALL ? 32 : 8;
+  __shared__ float2 sPair[WARPS];
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int rows = a.rowToken ? a.state->rows : a.T;
+  int each = 1;  // warps of a row
+  while (ALL && 2 * each * max(rows, 1) <= WARPS) each *= 2;
+  const int step = (int)gridDim.x * (WARPS / each);
+  // (all warps of a CTA go the same number of rounds)
+  for (int t0 = (int)blockIdx.x * (WARPS / each); t0 < rows; t0 += step) {
+    const int t = t0 + warp / each;
+    const int token = t >= rows ? -1 : a.rowToken ? a.rowToken[t] : t;
+    float2 pair = make_float2(-INFINITY, 0.0f);
+    if (token >= 0) {
+      const float2* p = a.parts + (long long)t * a.nParts;
+      const int by = 32 * each;
+      int i = lane + 32 * (warp % each);
+      for (; i + 3 * by < a.nParts; i += 4 * by) {
+        float2 q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = p[i + k * by];
+        pair = join(pair, join(join(q[0], q[1]), join(q[2], q[3])));
+      }
+      for (; i < a.nParts; i += by) pair = join(pair, p[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, pair.x, o),
+                                       __shfl_xor_sync(0xffffffffu, pair.y, o));
+      pair = join(pair, other);
+    }
+    if (ALL && each > 1) {
+      if (lane == 0) sPair[warp] = pair;
+      __syncthreads();
+      if (warp % each == 0)
+        for (int w = 1; w < each; ++w) pair = join(pair, sPair[warp + w]);
+      __syncthreads();
+    }
+    if (lane == 0 && warp % each == 0 && token >= 0) {
+      const float base = pair.x == -INFINITY ? 0.0f : pair.x;
+      const float l2 = base + log2f(pair.y), l = l2 * kLn2;
+      a.lse2[t] = l2;
+      a.lse[token] = l;
+      a.losses[token] = a.target.at(t) >= 0 ? l - a.targetLogit[t] : 0.0f;
+    }
+  }
+  if (ALL) {
+    __syncthreads();
+    sum_losses(a);
+  }
+}
+__global__ void __launch_bounds__(1024) xent_loss_kernel(const __grid_constant__ JoinArgs a) {
+  pdl_launch();
+  pdl_wait();
+  sum_losses(a);
 }
 
 // Rows copied into a buffer whose rows are whole 16-byte units, zeros after
@@ -611,7 +677,9 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   uint16_t* packed = reinterpret_cast<uint16_t*>(w + p.packed);
   T* factors = reinterpret_cast<T*>(w + p.factors);
   vr_result_t e;
-  {
+  // The loss alone reads the caller's targets where they are.
+  Targets rowTarget = {nullptr, targets, ignoreIndex, (int)p.V};
+  if (p.grads) {
     PrepArgs a = {targets,   ignoreIndex, (int)p.T, (int)p.V, mean,  gradScale,
                   kShift<T>, target,      token,    skipped,  state, dev.status};
     void* args[] = {&a};
@@ -631,7 +699,6 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   };
   if (p.T && p.padHidden && (e = pad(&hidden, &hiddenStride, p.T, p.hidden)) != VR_SUCCESS) return e;
   if (p.T && p.padWeight && (e = pad(&weight, &weightStride, p.V, p.weight)) != VR_SUCCESS) return e;
-  const int* rowTarget = target;
   if (p.T && p.grads) {
     PackArgs a = {static_cast<const uint16_t*>(hidden), (long long)hiddenStride, (int)p.T,
                   (int)p.D, (int)p.Dp, p.Dp == p.D && packed_rows(hidden, hiddenStride), target,
@@ -644,7 +711,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
       return e;
     hidden = packed;
     hiddenStride = p.Dp;
-    rowTarget = ints(p.rowTarget);
+    rowTarget.of = ints(p.rowTarget);
   }
   if (p.T) {
     // rows: an upper bound where they are packed, their number is on the device
@@ -664,21 +731,34 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
           stream);
     }
     if (e != VR_SUCCESS) return e;
-    JoinArgs a = {parts, (int)p.nParts, (int)p.T, p.grads ? ints(p.rowToken) : nullptr, state,
-                  rowTarget, targetLogit, lse2, lse, losses};
-    void* args[] = {&a};
-    if ((e = op_launch((const void*)xent_join_kernel,
-                       dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
-                       dim3(256), args, 0, stream)) != VR_SUCCESS)
-      return e;
   }
   {
-    int T32 = (int)p.T;
-    const float* in = losses;
-    void* args[] = {&in, &T32, &state, &loss};
-    if ((e = op_launch((const void*)xent_loss_kernel, dim3(1), dim3(1024), args, 0, stream)) !=
-        VR_SUCCESS)
-      return e;
+    const size_t rows = !p.T ? 0 : p.grads ? p.T + kTileK : p.T;
+    JoinArgs a = {parts,
+                  (int)p.nParts,
+                  (int)p.T,
+                  p.T && p.grads ? ints(p.rowToken) : nullptr,
+                  p.grads ? state : nullptr,
+                  rowTarget,
+                  mean,
+                  targetLogit,
+                  lse2,
+                  lse,
+                  losses,
+                  loss,
+                  dev.status};
+    void* args[] = {&a};
+    // Few rows: one CTA joins them and sums the loss, a launch less.
+    if (rows <= 128) {
+      e = op_launch((const void*)xent_join_kernel<true>, dim3(1), dim3(1024), args, 0, stream);
+    } else {
+      e = op_launch((const void*)xent_join_kernel<false>,
+                    dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
+                    dim3(256), args, 0, stream);
+      if (e == VR_SUCCESS)
+        e = op_launch((const void*)xent_loss_kernel, dim3(1), dim3(1024), args, 0, stream);
+    }
+    if (e != VR_SUCCESS) return e;
   }
   if (!p.grads) return VR_SUCCESS;
   if (!p.T) {
@@ -687,8 +767,8 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     return VR_SUCCESS;
   }
   if (p.kept) {
-    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, (int)p.V, lse2, rowTarget,
-                     targetLogit, state};
+    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, (int)p.V, lse2,
+                     rowTarget.of, targetLogit, state};
     void* args[] = {&a};
     const size_t columns = 256 * kKeptUnits * 8;
     if ((e = op_launch((const void*)xent_kept_kernel<T>,
@@ -706,7 +786,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     const size_t v0 = i * p.piece, rows = std::min(p.piece, p.V - v0);
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
     if (!p.kept) {
-      typename FactorEpilogue<T>::Args fa = {rowTarget, lse2, factors, (long long)p.piece, (int)v0};
+      typename FactorEpilogue<T>::Args fa = {rowTarget.of, lse2, factors, (long long)p.piece, (int)v0};
       if ((e = product<T, false, false, 0, false, FactorEpilogue<T>>(
                dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
                stream)) != VR_SUCCESS)
