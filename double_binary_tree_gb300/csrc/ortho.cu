@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(256, 1) ortho_small_kernel(const __grid_consta
         }
     });
     if (shares == 1) {
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 64; c += 32) {
         float v[32];
         sums(half * 64 + c, slabs > 2, v);
@@ -651,34 +651,56 @@ __global__ void __launch_bounds__(256, 1) ortho_small_kernel(const __grid_consta
         put_a(half * 64 + c, v);
       }
     } else {
-      // [column][row] in fp32 where A's planes will be
-#pragma unroll
+      // fp32 where A's planes will be, four columns of a row together
+#pragma unroll 1
       for (int c = 0; c < 64; c += 32) {
         float v[32];
         sums(half * 64 + c, slabs > 2, v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(aHi + 4u * ((half * 64 + c + i) * kSmallRows + row)),
-                       "f"(v[i])
+        for (int i = 0; i < 32; i += 4)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           aHi + 16u * (unsigned)((half * 64 + c + i) / 4 * kSmallRows + row)),
+                       "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3])
                        : "memory");
       }
       cluster_sync();
-      // pieces of eight columns: 16 / shares of them are this CTA's
+      // pieces of eight columns: 16 / shares of them are this CTA's, half of
+      // those this thread's; with the ranks they come from, eight loads
       const int own = 16 / shares / 2, r = threadIdx.x % 128;
       const int piece0 = rank * (16 / shares) + (int)(threadIdx.x / 128) * own;
+      float4 got[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int piece = piece0 + i / shares;
+        const uint32_t at = peer_addr(aHi, (uint32_t)(i % shares)) +
+                            16u * (unsigned)(piece * 2 * kSmallRows + r);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(got[i][j].x), "=f"(got[i][j].y), "=f"(got[i][j].z), "=f"(got[i][j].w)
+                       : "r"(at + 16u * (unsigned)(j * kSmallRows))
+                       : "memory");
+      }
       alignas(16) __half h[4][8], l[4][8];
+      float v[8] = {};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q >= own) break;
-        float v[8] = {};
-        for (int from = 0; from < shares; ++from) {
-          const uint32_t at = peer_addr(aHi, (uint32_t)from) +
-                              4u * (unsigned)((piece0 + q) * 8 * kSmallRows + r);
+      for (int i = 0; i < 8; ++i) {
+        const float* x = reinterpret_cast<const float*>(got[i]);
+        if (i % shares == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += peer_load(at + 4u * (unsigned)(i * kSmallRows));
+          for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) split(v[i] * (1.0f / kScale), h[q][i], l[q][i]);
+        for (int j = 0; j < 8; ++j) v[j] += x[j];
+        if ((i + 1) % shares == 0) {
+          // (i / shares is 0 .. 3 for two shares, 0 .. 1 for four, 0 for eight)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q == i / shares) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) split(v[j] * (1.0f / kScale), h[q][j], l[q][j]);
+            }
+        }
       }
       cluster_sync();  // every partial sum has been read
 #pragma unroll
@@ -710,7 +732,7 @@ __global__ void __launch_bounds__(256, 1) ortho_small_kernel(const __grid_consta
             mma_f16<false>(tmem + (p ? 256u : 0u), da + 2 * j, db + 2 * j, kSquare, s | (p == 2) | j);
         }
     });
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
       float v[32];
       const int at = half * 64 + c;
@@ -736,6 +758,7 @@ __global__ void __launch_bounds__(256, 1) ortho_small_kernel(const __grid_consta
                          db + j * (2048 >> 4), wide, (p == 2) | j);
       }
     });
+#pragma unroll 1
     for (int c = 0; c < a.w / 2; c += 32) {
       float v[32];
       const int at = half * (a.w / 2) + c;
@@ -748,15 +771,35 @@ __global__ void __launch_bounds__(256, 1) ortho_small_kernel(const __grid_consta
         slab_put(xHi, row, at, v);
         residue(v);
         slab_put(xLo, row, at, v);
-      } else if (row < a.m) {
-        Bits* out = static_cast<Bits*>(a.dst[z]);
+      } else if (a.tall) {
+        if (row < a.m) {  // the lanes' rows are consecutive columns of the result
+          Bits* out = static_cast<Bits*>(a.dst[z]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (at + i >= width) break;
-          const long long to = a.tall ? (long long)(c0 + at + i) * a.m + row
-                                      : (long long)row * a.n + c0 + at + i;
-          out[to] = Ty<T>::narrow(v[i] * a.byOut);
+          for (int i = 0; i < 32; ++i)
+            if (at + i < width) out[(long long)(c0 + at + i) * a.m + row] = Ty<T>::narrow(v[i] * a.byOut);
         }
+      } else {
+        // through the warp's corner of A's place, so that a store is a row's
+        // 32 columns, not 32 rows' one
+        const uint32_t corner = aHi + (unsigned)(warp * (32 * 33 * 4));
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(corner + 4u * (unsigned)(lane * 33 + i)),
+                       "f"(v[i] * a.byOut)
+                       : "memory");
+        __syncwarp();
+        Bits* out = static_cast<Bits*>(a.dst[z]) + (long long)(quad * 32) * a.n + c0 + at + lane;
+        const int rowsLeft = min(32, a.m - quad * 32);
+#pragma unroll 8
+        for (int i = 0; i < rowsLeft; ++i) {
+          float x;
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(x)
+                       : "r"(corner + 4u * (unsigned)(i * 33 + lane))
+                       : "memory");
+          if (at + lane < width) out[(long long)i * a.n] = Ty<T>::narrow(x);
+        }
+        __syncwarp();
       }
     }
   }
@@ -896,7 +939,10 @@ vr_result_t run(const OrthoPlan& p, const OpDevice& dev, const void* const* src,
   if (p.m <= kSmallRows && p.n <= (size_t)kSmallCols * kSmallCtas) {
     SmallArgs a = {};
     int shares = 1;
-    while ((size_t)shares * kSmallCols < p.n) shares *= 2;
+    // 128 columns a CTA where the SMs allow, at most 256
+    while ((size_t)shares * kSmallCols < p.n ||
+           (shares < kSmallCtas && (size_t)shares * 128 < p.n && 2 * shares * count <= dev.sms))
+      shares *= 2;
     a.m = (int)p.m;
     a.n = (int)p.n;
     a.w = (int)up((p.n + shares - 1) / shares, 64);
