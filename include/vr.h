@@ -631,7 +631,9 @@ vr_result_t vr_jit_compile_ring(int R, vr_dtype_t dtype, vr_op_t op, int smArch,
  * word: VR_SUCCESS, or the first device-side error any kernel of this library
  * recorded since the last call (VR_ERR_TIMEOUT for a bounded wait that ran
  * out, VR_ERR_INTERNAL for a broken invariant: in the bounds-checked build,
- * an access outside the call's buffers, refused), or VR_ERR_CUDA when the
+ * an access outside the call's buffers, refused; VR_ERR_INVALID_ARGUMENT for
+ * a bad value in device memory, a target of vr_linear_xent), or VR_ERR_CUDA
+ * when the
  * synchronisation itself fails.  The word is per device, not per stream. */
 vr_result_t vr_stream_status(void* stream);
 
@@ -679,7 +681,9 @@ vr_result_t vr_get_option(const char* name, long long* value);
  * bounds-checked build of this library (libvr_debug.so, built by
  * double_binary_tree_gb300.build with debug=True; loaded by the Python
  * binding when VR_BOUNDS_CHECKED=1) compiles every global-memory access of
- * every kernel with a check against the buffers of its call: the send and
+ * every collective's kernel with a check against the buffers of its call (the
+ * operators of a training step run the same there as in the normal build;
+ * their tensor copies are clipped by the hardware): the send and
  * receive buffers (count elements, or the collective's sizes) and the
  * stepwise ring's FIFO.  An access outside them (a store outside the
  * receive buffers and the FIFO) is skipped, VR_ERR_INTERNAL is recorded in

@@ -179,3 +179,25 @@ def test_gradient_against_differences():
         # truncation h^2 |f'''| / 6 <= 1e-8, cancellation 1e-15 / h = 1e-11,
         # fp32 evaluation 1e-6 of values below 1
         assert abs(num - float(out[0][t, e])) <= 2e-6
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+def test_a_row_at_the_lowest_value_is_uniform(dtype):
+    """A router that masks with the type's lowest value, all experts of a
+    token: equal probabilities, the first topK experts."""
+    code, ty = DT[dtype]
+    E, T = 32, 6
+    logits = draw(1, T, E, ty, 14)
+    logits[0][2] = torch.finfo(ty).min
+    logits[0][4, 1:] = torch.finfo(ty).min
+    scale = float(64 * T) if dtype == "fp16" else 1.0
+    loss, counts, picks, out = call(logits, None, 2, code, 1.0, scale)
+    f = counts.cpu().double() / (2 * T)
+    factor = scale * E / T
+    uniform = factor / E * (f - f.mean())
+    # exp and the sum of 32 terms in fp32, one rounding to the type
+    tol = uniform.abs().max() * (2.0 ** -18 + refs.U_T[ty]) + refs.MIN_T[ty]
+    assert float((out[0][2].cpu().double() - uniform).abs().max()) <= float(tol)
+    assert picks[0][2].tolist() == [0, 1]
+    # the other's only open expert has probability one: no gradient
+    assert float(out[0][4].cpu().double().abs().max()) <= factor * 2.0 ** -20
