@@ -163,6 +163,21 @@ template <typename T, int VEC, int CHUNKS>
 __device__ __forceinline__ float raw_value(const RawRow<T, VEC, CHUNKS>& r, int i) {
   return Ty<T>::widen(reinterpret_cast<const typename Ty<T>::Bits*>(&r.q[i / VEC])[i % VEC]);
 }
+// exp(x - top) of a row's logits: one multiply-add and exp2 each, unless the
+// product with log2 e could overflow (rows at the type's lowest value).
+template <typename T, int VEC, int CHUNKS>
+__device__ __forceinline__ void exponentials(const RawRow<T, VEC, CHUNKS>& r, float top,
+                                             float (&p)[VEC * CHUNKS]) {
+  if (std::is_same<T, __half>::value || fabsf(top) < 1e38f) {
+    const float top2 = top * kLog2e;
+#pragma unroll
+    for (int i = 0; i < VEC * CHUNKS; ++i)
+      p[i] = exp2_fast(fmaf(raw_value(r, i), kLog2e, -top2));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC * CHUNKS; ++i) p[i] = exp2_fast((raw_value(r, i) - top) * kLog2e);
+  }
+}
 // Two 16-bit logits as order keys.  Adding zero makes -0 +0 and every NaN
 // 0x7fff; then a negative value's bits are inverted, a positive one's sign set.
 template <typename T>
@@ -261,11 +276,9 @@ __device__ __forceinline__ void stats_pass(const BalanceArgs& a, float* sAcc, in
     // softmax statistics in fp32; the largest key is the maximum (or NaN)
     const float top = key_value<T>(best);
     float p[VPL], sum = 0.0f;
+    exponentials(raw, top, p);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      p[i] = exp2_fast((raw_value(raw, i) - top) * kLog2e);
-      sum += p[i];
-    }
+    for (int i = 0; i < VPL; ++i) sum += p[i];
     sum = group_sum<G>(sum);
     // a row whose logits are all -inf has no softmax: it does not count
     const bool live = kept && top != -INFINITY;
@@ -278,23 +291,23 @@ __device__ __forceinline__ void stats_pass(const BalanceArgs& a, float* sAcc, in
     if (here.real(a) && l == 0)
       a.softmax[here.t] = live ? make_float2(top, inv) : make_float2(0.0f, 0.0f);
 
-    // topK rounds: the largest key left, the lowest index of equals
-    int mine = -1;
-    for (int r = 0;;) {
-      uint32_t chosen;
+    // topK rounds: the largest key left, the lowest index of equals.  Lane r of
+    // the group keeps round r's.
+    auto take = [&](uint32_t& word) {  // what `best` stands for leaves its lane's keys
       if (PACKED) {
-        chosen = 0xffffu - (best & 0xffffu);
+        word = best;
         if (SORTED) {
-          const bool won = key[0] == best;
+          if (key[0] == best) {
 #pragma unroll
-          for (int i = 0; i + 1 < VPL; ++i) key[i] = won ? key[i + 1] : key[i];
-          if (won) key[VPL - 1] = 0u;
+            for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+            key[VPL - 1] = 0u;
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < VPL; ++i) key[i] = key[i] == best ? 0u : key[i];
         }
       } else {
-        chosen = 0xffffffffu;
+        uint32_t chosen = 0xffffffffu;
 #pragma unroll
         for (int i = VPL - 1; i >= 0; --i)
           if (key[i] == best) chosen = (uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC);
@@ -302,18 +315,26 @@ __device__ __forceinline__ void stats_pass(const BalanceArgs& a, float* sAcc, in
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
           if ((uint32_t)expert_of<VEC, G>(i / VEC, l, i % VEC) == chosen) key[i] = 0u;
+        word = 0xffffu - chosen;
       }
-      if (l == r % G) mine = (int)chosen;
-      ++r;
-      if (r % G == 0 || r == a.topK) {
-        const int from = (r - 1) / G * G;
-        if (here.real(a) && from + l < r) {
-          if (live) atomicAdd(&sCount[mine], 1);
-          int* out = a.chosen[here.rank];
-          if (out) out[(long long)here.row * a.topK + from + l] = live ? mine : -1;
-        }
-        if (r == a.topK) break;
+    };
+    for (int from = 0;; from += G) {
+      const int n = min(a.topK - from, G);
+      uint32_t mine = 0;
+      for (int r = 0;;) {
+        uint32_t word;
+        take(word);
+        if (l == r) mine = word;
+        if (++r == n) break;
+        best = largest();
       }
+      if (here.real(a) && l < n) {
+        const int e = 0xffff - (int)(mine & 0xffffu);
+        if (live) atomicAdd(&sCount[e], 1);
+        int* out = a.chosen[here.rank];
+        if (out) out[(long long)here.row * a.topK + from + l] = live ? e : -1;
+      }
+      if (from + n == a.topK) break;
       best = largest();
     }
   }
@@ -432,14 +453,14 @@ __device__ __forceinline__ void grad_pass(const BalanceArgs& a, const float* sSh
         for (int c = 0; c < CHUNKS; ++c) fill(raw[k].q[c], 0u);
       }
       float x[VPL], dot = 0.0f;
+      exponentials(raw[k], sm[k].x, x);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        x[i] = exp2_fast((raw_value(raw[k], i) - sm[k].x) * kLog2e);
         dot = fmaf(f[i], x[i], dot);
       }
-      const float less = group_sum<G>(dot) * sm[k].y;
+      const float inv = sm[k].y, less = group_sum<G>(dot) * inv * inv;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) x[i] *= sm[k].y * (f[i] - less);
+      for (int i = 0; i < VPL; ++i) x[i] *= fmaf(f[i], inv, -less);
       if (!out[k]) continue;
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c) {
