@@ -87,6 +87,9 @@ __device__ __forceinline__ bool elected() {
       : "=r"(is));
   return is != 0;
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -432,6 +435,17 @@ __global__ void __launch_bounds__(128 + 32 * Epi::kWarps, 1)
     abortFlag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async;" ::: "memory");
+  }
+  if (warp == 1 && elected()) {  // the copies' descriptors, before the data is there
+    for (int p = 0; p < PARTS; ++p) {
+      prefetch_map(&g.a[p]);
+      prefetch_map(&g.b[p]);
+    }
+    if constexpr (kAux)
+      for (int p = 0; p < 2; ++p) {
+        prefetch_map(&e.aux.in[p]);
+        if (p < e.aux.nOut) prefetch_map(&e.aux.out[p]);
+      }
   }
   if (warp == 2) {
     if constexpr (PAIR) {

@@ -889,7 +889,7 @@ constexpr float kCoefs[3] = {3.4445f, -4.7750f, 2.0315f};
 // CTA, 0.167 us on a 256 x 128 tile of a pair (half the operand traffic per
 // SM), 0.31 us on a 256 x 256 one (two planes: 0.56 and 0.47 us, no 256-wide
 // tile, tensor memory holds 128 columns), the epilogue of the last round 3 us
-// per 128 columns, and joining shares of k 4 us.  Wide tiles win when there
+// per 128 columns, and joining s shares of k s + 2 us.  Wide tiles win when there
 // are many, single CTAs when they fill the SMs once, shares when few tiles
 // leave SMs idle.
 template <int PARTS, bool BMN, class Epi>
@@ -901,13 +901,13 @@ vr_result_t product(const OpDevice& dev, const Planes& a, size_t aLd, const Plan
   double best = 0;
   int shape = -1, shares = 1;  // shape: 0 single, 1 pair, 2 wide pair
   auto offer = [&](int which, size_t tiles, double slice, int s) {
-    // clusters of four and eight CTAs do not fill the GPU, and are only
-    // worth while in one round
+    // clusters of four and eight CTAs do not fill the GPU (36 and 15 of them are
+    // resident at a time), and are only worth while in one round
     const size_t ctas = (which ? 2 : 1) * (size_t)s;
-    const size_t room = ctas > 4 ? 8 : ctas > 2 ? 28 : (size_t)dev.sms / ctas;
+    const size_t room = ctas > 4 ? 15 : ctas > 2 ? 36 : (size_t)dev.sms / ctas;
     const double rounds = (double)((tiles + room - 1) / room);
     if (s > 1 && rounds > 1) return;
-    const double t = rounds * std::ceil(slices / s) * slice + (which == 2 ? 6 : 3) + (s > 1 ? 4 : 0);
+    const double t = rounds * std::ceil(slices / s) * slice + (which == 2 ? 6 : 3) + (s > 1 ? s + 2 : 0);
     if (shape < 0 || t < best) best = t, shape = which, shares = s;
   };
   const size_t singles = gemm_tiles<128, false>(z), pairs = gemm_tiles<128, true>(z);

@@ -327,7 +327,8 @@ struct WeightEpilogue {
   static constexpr bool kAux = false;
   static constexpr int kWarps = 16;
   struct Args {
-    T* out;  // the piece's first row, [V][N]
+    T* out;  // the piece's first row
+    long long ld;
     const XentState* state;
     int align;
   };
@@ -345,7 +346,7 @@ struct WeightEpilogue {
       if (v0 >= M) continue;
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= scale;
-      store_row(a.out + (long long)v0 * g.N + n, v, g.N - n, a.align);
+      store_row(a.out + v0 * a.ld + n, v, g.N - n, a.align);
     }
   }
 };
@@ -509,8 +510,9 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const __grid_constant__
   sum_losses(a);
 }
 
-// Rows copied into a buffer whose rows are whole 16-byte units, zeros after
-// the last column.
+// Rows of `cols` elements between a dense buffer of any alignment and one
+// whose rows are whole sectors (ld): in, with zeros after the last column, or
+// out.  A warp takes a row, so that its accesses are one run of bytes.
 struct PadArgs {
   const uint16_t* src;
   long long stride, rows;
@@ -520,9 +522,38 @@ struct PadArgs {
 __global__ void __launch_bounds__(256) xent_pad_kernel(const __grid_constant__ PadArgs a) {
   pdl_launch();
   pdl_wait();
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < a.ld; c += 256)
-      a.dst[r * a.ld + c] = c < a.cols ? a.src[r * a.stride + c] : (uint16_t)0;
+  const int lane = threadIdx.x % 32;
+  for (long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows;
+       r += (long long)gridDim.x * 8) {
+    const uint16_t* in = a.src + r * a.stride;
+    uint4* out = reinterpret_cast<uint4*>(a.dst + r * a.ld);
+#pragma unroll 2
+    for (int u = lane; u < a.ld / 8; u += 32) {
+      alignas(16) uint16_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = u * 8 + i < a.cols ? in[u * 8 + i] : (uint16_t)0;
+      out[u] = *reinterpret_cast<const uint4*>(v);
+    }
+  }
+}
+__global__ void __launch_bounds__(256) xent_unpad_kernel(const __grid_constant__ PadArgs a) {
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32;
+  for (long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows;
+       r += (long long)gridDim.x * 8) {
+    const uint16_t* in = a.src + r * a.ld;
+    uint16_t* out = a.dst + r * a.cols;
+    const int odd = (int)((uintptr_t)out >> 1 & 1);  // 32-bit stores begin after it
+    const int words = (a.cols - odd) / 2;
+    if (lane == 0 && odd) out[0] = in[0];
+    if (lane == 1 && odd + 2 * words < a.cols) out[a.cols - 1] = in[a.cols - 1];
+#pragma unroll 4
+    for (int w = lane; w < words; w += 32) {
+      const int c = odd + 2 * w;
+      *reinterpret_cast<uint32_t*>(out + c) = (uint32_t)in[c] | (uint32_t)in[c + 1] << 16;
+    }
+  }
 }
 
 // The packed hidden states: the tokens that count, zeros up to whole slices
@@ -694,8 +725,8 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     *src = w + at;
     *stride = p.Dp;
     return op_launch((const void*)xent_pad_kernel,
-                     dim3((unsigned)std::min<size_t>(rows, (size_t)dev.sms * 8)), dim3(256), args,
-                     0, stream);
+                     dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
+                     dim3(256), args, 0, stream);
   };
   if (p.T && p.padHidden && (e = pad(&hidden, &hiddenStride, p.T, p.hidden)) != VR_SUCCESS) return e;
   if (p.T && p.padWeight && (e = pad(&weight, &weightStride, p.V, p.weight)) != VR_SUCCESS) return e;
@@ -782,6 +813,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 2;
   };
   const int alignH = aligned(dHidden), alignW = aligned(dWeight);
+  const bool viaPad = dWeight && p.padWeight && alignW == 2;
   for (size_t i = 0; i < p.nPieces; ++i) {
     const size_t v0 = i * p.piece, rows = std::min(p.piece, p.V - v0);
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
@@ -803,12 +835,27 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
         return e;
     }
     if (dWeight) {
-      typename WeightEpilogue<T>::Args wa = {static_cast<T*>(dWeight) + v0 * p.D, state, alignW};
+      // Rows that are no 16-byte units: into the padded weight's rows, which
+      // this piece's products have read, and from there in a pass of its own
+      // (stored element by element, 32 rows at a time, they took three times
+      // as long as everything else).
+      T* out = viaPad ? static_cast<T*>(const_cast<void*>(weight)) + v0 * p.Dp
+                      : static_cast<T*>(dWeight) + v0 * p.D;
+      typename WeightEpilogue<T>::Args wa = {out, (long long)(viaPad ? p.Dp : p.D), state,
+                                             viaPad ? 32 : alignW};
       if ((e = product<T, true, true, 0, false, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
                                                          p.D, p.rows, nullptr, &state->valid, wa,
                                                          stream)) != VR_SUCCESS)
         return e;
     }
+  }
+  if (viaPad) {
+    PadArgs a = {static_cast<const uint16_t*>(weight), 0, (long long)p.V, (int)p.D, (int)p.Dp,
+                 static_cast<uint16_t*>(dWeight)};
+    void* args[] = {&a};
+    return op_launch((const void*)xent_unpad_kernel,
+                     dim3((unsigned)std::min<size_t>((p.V + 7) / 8, (size_t)dev.sms * 8)),
+                     dim3(256), args, 0, stream);
   }
   return VR_SUCCESS;
 }
