@@ -682,6 +682,19 @@ vr_result_t op_device(OpDevice* out) {
   }
 }
 
+vr_result_t op_reachable(const void* const* p, int n, int device) {
+  return check_reachable(p, n, device);
+}
+
+vr_result_t op_reachable(const OpBuffer* b, int n, int device) {
+  for (int i = 0; i < n; ++i) {
+    const vr_result_t e =
+        b[i].rows && b[i].rowBytes ? check_reachable(&b[i].p, 1, device) : VR_SUCCESS;
+    if (e != VR_SUCCESS) return e;
+  }
+  return VR_SUCCESS;
+}
+
 vr_result_t op_launch(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
                       void* stream, int cluster) {
   cudaLaunchConfig_t cfg = {};

@@ -10,7 +10,7 @@
 // the probabilities and counts of each CTA; every CTA of balance_grad_kernel
 // first adds up the CTAs' sums in CTA order (the same bits everywhere and on
 // every run; less than the launch of a kernel of its own), then recomputes p
-// from the stored log sum and writes its gradients.  A call whose tokens fit
+// from the stored maximum and sum and writes its gradients.  A call whose tokens fit
 // one CTA twice over runs all of it in one launch (balance_small_kernel).
 //
 // A token is held by a group of G lanes, VPL logits per lane in registers
@@ -21,6 +21,11 @@
 // warp-wide maximum.  16-bit logits carry their index in the low half of the
 // compared word, so a round is one reduction, and with 8 logits a lane they
 // are sorted once per lane, so a round looks at one word per lane.
+//
+// Measured on GB300, 8 ranks x 16384 tokens x 256 experts, topK 8, bf16 (138 MB,
+// 21 us at the copy bandwidth): 63 us for the first pass, bound by the integer
+// instructions of the choice (about 400 instructions a token, issued in 75 %
+// of the cycles), 29 us for the second, near its traffic.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -645,7 +650,7 @@ vr_result_t vr_balance_loss(const void* const* logits, size_t rowStride,
 
   OpDevice dev;
   vr_result_t e = op_device(&dev);
-  if (e != VR_SUCCESS) return e;
+  if (e != VR_SUCCESS || (e = op_reachable(buf, n, dev.device)) != VR_SUCCESS) return e;
   const bool vec = (align & 15) == 0;
   const BalanceKernels k = dtype == VR_FLOAT32   ? pick<float, 4>(experts, vec)
                            : dtype == VR_FLOAT16 ? pick<__half, 8>(experts, vec)

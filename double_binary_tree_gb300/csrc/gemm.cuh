@@ -27,6 +27,15 @@
 // every CTA of the cluster adds up and finishes some of the columns, in the
 // order of the shares.
 //
+// Measured on GB300, 4864 x 4864 x 4096 fp16 with an epilogue that stores
+// nothing: pairs 256 x 256 1950 TFLOP/s (1.02 of a cuBLAS bf16 product of
+// 8192^3; either operand K- or MN-major), summed in chunks of 512 1910,
+// 256 x 128 1800, single CTAs 128 x 256 1850, 128 x 128 1490 (shared memory
+// bandwidth); two planes, sums handed over every 128, 1660 over their three
+// products.  One tile of 64 k takes 2.7 us, 4.2 us on a pair.  What bounds a
+// call is the products, where k is long; the epilogue, where it is short
+// (a 256 x 256 tile's products take 0.31 us per 64 k).
+//
 // Every wait is bounded.  A CTA that gives up records VR_ERR_TIMEOUT, waits
 // (bounded) for its copies and products in flight, frees its tensor memory
 // and returns.

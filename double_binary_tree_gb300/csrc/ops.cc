@@ -28,15 +28,31 @@ bool touch(const OpBuffer& a, const OpBuffer& b) {
 }  // namespace
 
 bool op_buffers_ok(const OpBuffer* b, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (!b[i].write) continue;
-    for (int j = 0; j < n; ++j) {
-      if (j == i || (b[j].write && j < i) || !touch(b[i], b[j])) continue;
-      const bool inPlace = j == i - 1 && !b[j].write && b[j].p == b[i].p &&
-                           b[j].rowBytes == b[i].rowBytes && b[j].strideBytes == b[i].strideBytes;
+  // By address, only buffers whose extents overlap are compared: few or none.
+  struct Span {
+    uintptr_t lo, hi;
+    int i;
+  };
+  constexpr int kMost = 4 * VR_MAX_RANKS + 3;
+  Span v[kMost];
+  if (n > kMost) return false;
+  int m = 0;
+  for (int i = 0; i < n; ++i)
+    if (b[i].rows && b[i].rowBytes) {
+      const uintptr_t lo = (uintptr_t)b[i].p;
+      v[m++] = {lo, lo + (b[i].rows - 1) * b[i].strideBytes + b[i].rowBytes, i};
+    }
+  std::sort(v, v + m, [](const Span& x, const Span& y) { return x.lo < y.lo; });
+  for (int x = 0; x < m; ++x)
+    for (int y = x + 1; y < m && v[y].lo < v[x].hi; ++y) {
+      const OpBuffer &p = b[v[x].i], &q = b[v[y].i];
+      if ((!p.write && !q.write) || !touch(p, q)) continue;
+      const int first = std::min(v[x].i, v[y].i), second = std::max(v[x].i, v[y].i);
+      const bool inPlace = second == first + 1 && !b[first].write && b[second].write &&
+                           p.p == q.p && p.rowBytes == q.rowBytes &&
+                           p.strideBytes == q.strideBytes;
       if (!inPlace) return false;
     }
-  }
   return true;
 }
 

@@ -42,6 +42,11 @@ bool op_buffers_ok(const OpBuffer* b, int n);
 bool op_lists_ok(const void* const* src, void* const* dst, int count, size_t bytes,
                  const void* workspace, size_t workspaceBytes);
 
+// The option VR_VALIDATE_POINTERS (api.cc): whether every buffer can be
+// reached from the current device.
+vr_result_t op_reachable(const OpBuffer* b, int n, int device);
+vr_result_t op_reachable(const void* const* p, int n, int device);
+
 // Bytes rounded up to the alignment of a workspace's parts.
 inline size_t op_round(size_t n) { return (n + 255) & ~(size_t)255; }
 

@@ -1091,6 +1091,11 @@ vr_result_t vr_orthogonalize(const void* const* src, void* const* dst, int count
   if (!in_range(use, steps)) return VR_ERR_UNSUPPORTED;
   OpDevice dev;
   vr_result_t e = op_device(&dev);
+  const void* const work = workspace;
+  if (e != VR_SUCCESS || (e = op_reachable(src, count, dev.device)) != VR_SUCCESS ||
+      (e = op_reachable(dst, count, dev.device)) != VR_SUCCESS ||
+      (e = op_reachable(&work, 1, dev.device)) != VR_SUCCESS)
+    return e;
   char* w = static_cast<char*>(workspace);
   for (int at = 0; at < count && e == VR_SUCCESS; at += kMost) {
     const int n = std::min(kMost, count - at);

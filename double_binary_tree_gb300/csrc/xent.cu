@@ -16,7 +16,7 @@
 //            its epilogue now writing the factors.  8 T D V operations, a
 //            workspace that does not grow with T x V.
 // Two more products multiply the factors with the weight and with the hidden
-// states.  (4096 tokens x 4096 x 131072, bf16: 8.5 ms kept, 10.4 ms in pieces.)
+// states.  (4096 tokens x 4096 x 131072, bf16: 8.4 ms kept, 10.4 ms in pieces.)
 //
 // Only tokens that count take part in the gradients: the hidden states are
 // packed first, tokens that count before ignored ones, which leaves out the
@@ -177,7 +177,8 @@ struct StatsEpilogue {
 
 // The kept exponentials of the packed tokens made into gradient factors, and
 // rows of zeros up to the next whole slice.  The target's factor is made of
-// its fp32 logit: of a sure token it is a small difference.
+// its fp32 logit: of a sure token it is a small difference.  One read and one
+// write: 2048 x 32768 in 39 us, 6.9 TB/s.
 template <typename T>
 struct KeptArgs {
   T* out;
@@ -912,8 +913,8 @@ vr_result_t vr_linear_xent(const void* hidden, size_t hiddenStride, const void* 
   if (dWeight) buf[n++] = {dWeight, 1, vocab * dim * 2, vocab * dim * 2, true};
   if (!op_buffers_ok(buf, n)) return VR_ERR_INVALID_ARGUMENT;
   OpDevice dev;
-  const vr_result_t e = op_device(&dev);
-  if (e != VR_SUCCESS) return e;
+  vr_result_t e = op_device(&dev);
+  if (e != VR_SUCCESS || (e = op_reachable(buf, n, dev.device)) != VR_SUCCESS) return e;
   char* w = static_cast<char*>(workspace);
   return dtype == VR_BFLOAT16
              ? run<__nv_bfloat16>(p, dev, hidden, hiddenStride, weight, weightStride, targets,
