@@ -32,7 +32,9 @@ namespace vr {
 namespace {
 
 constexpr int kBN = 256;
-constexpr int kPartCols = kBN / 4;  // columns of one pair of statistics
+// Columns of one pair of statistics: a quarter of a tile of 256, or of 128
+// where few rows and few tiles would leave SMs idle.
+constexpr int kPartCols = kBN / 4;
 // The losses are fp32 results: their logits are summed in chunks of 512.
 // (The gradients' roundings to 16 bits are far above the truncation.)
 // Up to 128 rows the weight's traffic bounds the product, whose sums then
@@ -171,7 +173,7 @@ struct StatsEpilogue {
     const float sum = ((sums[0] + sums[1]) + (sums[2] + sums[3])) *
                       (1.0f / (float)(1 << (KEEP ? kShift<T> : 0)));
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) { a.targetLogit[t] = x; });
-    if (t < M) a.parts[(long long)t * a.nParts + first / kPartCols] = make_float2(top, sum);
+    if (t < M) a.parts[(long long)t * a.nParts + first / COLS] = make_float2(top, sum);
   }
 };
 
@@ -184,7 +186,7 @@ struct KeptArgs {
   T* out;
   long long ld;
   const float2* parts;
-  int nParts, V;
+  int nParts, partCols, V;
   const float* lse2;
   const int* target;
   const float* targetLogit;
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ 
       const int c = c0 + u * 256 * 8;
       if (t < valid && c < a.V) {
         q[u] = *reinterpret_cast<const uint4*>(out + c);
-        part[u] = a.parts[(long long)t * a.nParts + c / kPartCols];
+        part[u] = a.parts[(long long)t * a.nParts + c / a.partCols];
       }
     }
 #pragma unroll
@@ -351,6 +353,42 @@ struct WeightEpilogue {
     }
   }
 };
+
+// The same through shared memory and tensor copies, for rows of whole 16-byte
+// units.  With few tokens the stores are what takes the time: 777 x 1000 x
+// 50001 65 us row by row, 46 us this way; with many the products want the
+// shared memory for their stages.
+template <typename T>
+struct WeightTilesEpilogue {
+  static constexpr bool kAux = true;
+  static constexpr int kWarps = 8;
+  struct Args {
+    AuxArgs aux;
+    const XentState* state;
+  };
+  static __device__ __forceinline__ bool skip(const GemmArgs& g, const Tile& o, int n, int M) {
+    return n >= g.N || o.m0 >= M;
+  }
+  template <class Acc>
+  static __device__ __forceinline__ void unit(const Args& a, const GemmArgs& g, const Tile& o,
+                                              int row, int n, int c, int M, const Acc& acc,
+                                              const AuxTile& tile) {
+    const float scale = a.state->gradScale;
+    float v[32];
+    acc(c, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack2<T>(v[8 * i + 2 * j] * scale, v[8 * i + 2 * j + 1] * scale);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile.piece(0, row, i)),
+                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                   : "memory");
+    }
+  }
+};
+constexpr size_t kTilesMostTokens = 1024;
 
 // One CTA: the targets narrowed (-1: ignored), the tokens that count packed
 // in order, their number and the scales.  A target outside the vocabulary is
@@ -614,6 +652,7 @@ bool packed_rows(const void* p, size_t stride) {
 
 struct XentPlan {
   bool grads, kept, padHidden, padWeight;
+  int partCols;
   size_t T, D, V, Dp, rows, nParts, piece, nPieces, sumLd;
   // offsets into the workspace
   size_t state, target, token, skipped, rowToken, rowTarget, lse2, targetLogit, parts, hidden,
@@ -623,6 +662,7 @@ struct XentPlan {
 // `kept`: the gradients' exponentials are kept (where the rule allows it).
 bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size_t weightStride,
                size_t T, size_t D, size_t V, int dtype, bool grads, bool kept, XentPlan* p) {
+  constexpr int sms = 152;  // (the workspace's size is asked for without a device, too)
   if ((dtype != VR_FLOAT16 && dtype != VR_BFLOAT16) || T > (1u << 30) || D < 1 || D > (1u << 24) ||
       V < 1 || V > (1u << 30) || hiddenStride < D || weightStride < D ||
       hiddenStride > (1ull << 32) || weightStride > (1ull << 32))
@@ -635,7 +675,11 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   p->padWeight = !packed_rows(weight, weightStride);
   p->Dp = up(D, 16);  // whole 32-byte sectors: rows that straddle them cost a product a fifth
   p->rows = grads ? up(T + kTileK, kTileM) : T;
-  p->nParts = up(V, kBN) / kPartCols;
+  // (the rows of the launch: T, or the packed rows' upper bound)
+  p->partCols = (grads ? T + kTileK : T) <= kTileM && up(V, kBN) / kBN <= (size_t)sms / 2
+                    ? kPartCols / 2
+                    : kPartCols;
+  p->nParts = up(V, 4 * (size_t)p->partCols) / p->partCols;
   p->kept = grads && kept && (T <= D || 2 * p->rows * up(V, kBN) <= kPieceBytes);
   p->piece = p->kept ? up(V, kBN) : piece_rows(p->rows, V);
   p->nPieces = (V + p->piece - 1) / p->piece;
@@ -671,13 +715,21 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
 template <typename T, bool AMN, bool BMN, int CHUNK, bool SPLIT, class Epi>
 vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* b, size_t bLd,
                     size_t M, size_t N, size_t K, const int* dynM, const int* dynK,
-                    typename Epi::Args& epi, void* stream) {
+                    typename Epi::Args& epi, void* stream, bool narrow = false) {
   const Operand oa = {a, nullptr, aLd}, ob = {b, nullptr, bLd};
   const GemmSize z = {M, N, K, 1, false};
   const bool few = M <= kTileM;
 #define VR_PRODUCT(C, PAIR, SHARED, SHARES)                                             \
   return gemm_launch<T, kBN, 1, AMN, BMN, C, PAIR, SHARED, Epi>(dev, oa, ob, z, dynM, dynK, \
                                                                 epi, SHARES, stream)
+  if constexpr (CHUNK > 0) {
+    if (narrow && K > kFewRowsChunk * kTileK)
+      return gemm_launch<T, 128, 1, AMN, BMN, kFewRowsChunk, false, false, Epi>(
+          dev, oa, ob, z, dynM, dynK, epi, 1, stream);
+    if (narrow)
+      return gemm_launch<T, 128, 1, AMN, BMN, 0, false, false, Epi>(dev, oa, ob, z, dynM, dynK,
+                                                                    epi, 1, stream);
+  }
   if constexpr (SPLIT) {
     static_assert(CHUNK == 0, "shares are summed in one piece");
     const int shares = few ? gemm_shares<kBN, false>(z, dev.sms) : gemm_shares<kBN, true>(z, dev.sms);
@@ -754,13 +806,13 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
           rowTarget, targetLogit, parts, (int)p.nParts, factors, (long long)p.piece, state};
       e = product<T, false, false, kStatsChunk, false, StatsEpilogue<T, true>>(
           dev, hidden, hiddenStride, weight, weightStride, rows, p.V, p.D, dynRows, nullptr, epi,
-          stream);
+          stream, p.partCols != kPartCols);
     } else {
       typename StatsEpilogue<T, false>::Args epi = {
           rowTarget, targetLogit, parts, (int)p.nParts, nullptr, 0, state};
       e = product<T, false, false, kStatsChunk, false, StatsEpilogue<T, false>>(
           dev, hidden, hiddenStride, weight, weightStride, rows, p.V, p.D, dynRows, nullptr, epi,
-          stream);
+          stream, p.partCols != kPartCols);
     }
     if (e != VR_SUCCESS) return e;
   }
@@ -799,7 +851,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     return VR_SUCCESS;
   }
   if (p.kept) {
-    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, (int)p.V, lse2,
+    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, p.partCols, (int)p.V, lse2,
                      rowTarget.of, targetLogit, state};
     void* args[] = {&a};
     const size_t columns = 256 * kKeptUnits * 8;
@@ -842,12 +894,24 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
       // as long as everything else).
       T* out = viaPad ? static_cast<T*>(const_cast<void*>(weight)) + v0 * p.Dp
                       : static_cast<T*>(dWeight) + v0 * p.D;
-      typename WeightEpilogue<T>::Args wa = {out, (long long)(viaPad ? p.Dp : p.D), state,
-                                             viaPad ? 32 : alignW};
-      if ((e = product<T, true, true, 0, false, WeightEpilogue<T>>(dev, factors, p.piece, packed, p.Dp, rows,
-                                                         p.D, p.rows, nullptr, &state->valid, wa,
-                                                         stream)) != VR_SUCCESS)
-        return e;
+      const size_t ld = viaPad ? p.Dp : p.D;
+      if (p.T <= kTilesMostTokens && (viaPad || alignW >= 16)) {
+        typename WeightTilesEpilogue<T>::Args wa = {};
+        wa.aux.nOut = 1;
+        wa.state = state;
+        if ((e = gemm_operand(&wa.aux.out[0], out, std::is_same<T, __nv_bfloat16>::value, p.D, rows,
+                              1, ld * 2, ld * 2 * rows, kTileM, kAuxCols)) != VR_SUCCESS)
+          return e;
+        e = product<T, true, true, 0, false, WeightTilesEpilogue<T>>(
+            dev, factors, p.piece, packed, p.Dp, rows, p.D, p.rows, nullptr, &state->valid, wa,
+            stream);
+      } else {
+        typename WeightEpilogue<T>::Args wa = {out, (long long)ld, state, viaPad ? 32 : alignW};
+        e = product<T, true, true, 0, false, WeightEpilogue<T>>(
+            dev, factors, p.piece, packed, p.Dp, rows, p.D, p.rows, nullptr, &state->valid, wa,
+            stream);
+      }
+      if (e != VR_SUCCESS) return e;
     }
   }
   if (viaPad) {
