@@ -867,17 +867,6 @@ size_t gemm_tiles(const GemmSize& z) {
   return tiles * z.batch;
 }
 
-// CTAs (pairs) that share a tile's k: as many as the idle SMs allow, at most
-// a cluster of eight CTAs, and at least four slices of 64 each.
-template <int BN, bool PAIR>
-int gemm_shares(const GemmSize& z, int sms) {
-  const size_t ctas = PAIR ? 2 : 1, tiles = gemm_tiles<BN, PAIR>(z) * ctas;
-  const size_t slices = (z.K + kTileK - 1) / kTileK;
-  int s = 1;
-  while (2 * s * ctas <= 8 && tiles * 2 * s <= (size_t)sms && slices >= (size_t)(8 * s)) s *= 2;
-  return s;
-}
-
 template <typename T, int BN, int PARTS, bool AMN, bool BMN, int CHUNK, bool PAIR, bool SPLIT,
           class Epi>
 vr_result_t gemm_launch(const OpDevice& dev, const Operand& a, const Operand& b, const GemmSize& z,

@@ -24,6 +24,7 @@
 // is NaN).
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include "gemm.cuh"
@@ -732,11 +733,46 @@ vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* 
   }
   if constexpr (SPLIT) {
     static_assert(CHUNK == 0, "shares are summed in one piece");
-    const int shares = few ? gemm_shares<kBN, false>(z, dev.sms) : gemm_shares<kBN, true>(z, dev.sms);
-    if (shares > 1) {
-      if (few) VR_PRODUCT(0, false, true, shares);
-      VR_PRODUCT(0, true, true, shares);
+    // By the measured times: a slice of 64 k takes 0.31 us on a 256-wide tile
+    // of a pair (single CTA 0.33), 0.167 (0.205) on a 128-wide one, a third
+    // more where the weight's rows straddle sectors; 36 clusters of four CTAs
+    // and 15 of eight are resident at a time (16 are let in: some are empty
+    // where tokens are ignored), and a second round of clusters starts slowly;
+    // joining s shares takes about s + 2 us.
+    const double slices = (double)((K + kTileK - 1) / kTileK);
+    const bool odd = bLd % 16 != 0;
+    double best = 0;
+    int shares = 1;
+    bool wide = true;
+    auto offer = [&](bool w, int s, size_t tiles, double slice) {
+      const int ctas = (few ? 1 : 2) * s;
+      const size_t room = ctas > 4 ? 16 : ctas > 2 ? 36 : (size_t)(dev.sms / ctas);
+      if (s > 1 && tiles > room) return;
+      const double t = (double)((tiles + room - 1) / room) * std::ceil(slices / s) * slice +
+                       (s > 1 ? s + 2 : 0);
+      if (s == 1 || t < best) best = t, shares = s, wide = w;
+    };
+    if (few) offer(true, 1, gemm_tiles<kBN, false>(z), 0.33);
+    else offer(true, 1, gemm_tiles<kBN, true>(z), 0.31);
+    for (int s = 2; s <= (few ? 8 : 4) && s <= slices; s *= 2) {
+      if (few) {
+        offer(true, s, gemm_tiles<kBN, false>(z), 0.33);
+        offer(false, s, gemm_tiles<128, false>(z), 0.205);
+      } else {
+        offer(true, s, gemm_tiles<kBN, true>(z), odd ? 0.38 : 0.31);
+        offer(false, s, gemm_tiles<128, true>(z), odd ? 0.23 : 0.167);
+      }
     }
+#define VR_SHARED(BN, PAIR)                                                                   \
+  return gemm_launch<T, BN, 1, AMN, BMN, 0, PAIR, true, Epi>(dev, oa, ob, z, dynM, dynK, epi, \
+                                                             shares, stream)
+    if (shares > 1) {
+      if (few && wide) VR_SHARED(kBN, false);
+      if (few) VR_SHARED(128, false);
+      if (wide) VR_SHARED(kBN, true);
+      VR_SHARED(128, true);
+    }
+#undef VR_SHARED
   }
   if constexpr (CHUNK > 0) {
     if (few && K > kFewRowsChunk * kTileK) VR_PRODUCT(kFewRowsChunk, false, false, 1);
