@@ -256,6 +256,9 @@ struct FactorEpilogue {
                                              int row, int col0, int M, const Acc& acc) {
     const int t = o.m0 + row;
     const bool live = t < M;
+    // dW reads whole slices of tokens: zeros up to there.  A tile's rows go on
+    // past the buffer's.
+    const bool stored = t < (M + kTileK - 1) / kTileK * kTileK;
     const float sub = live ? (float)kShift<T> - a.lse2[t] : 0.0f;
     const int at = live ? a.target[t] - a.v0 - o.n0 - col0 : -1;
     T* out = a.out + (long long)t * a.ld + o.n0 + col0;
@@ -267,7 +270,7 @@ struct FactorEpilogue {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         v[i] = live ? exp2_fast(fmaf(v[i], kLog2e, sub)) : 0.0f;
-      store_row(out + c, v, 32, 32);
+      if (stored) store_row(out + c, v, 32, 32);
     }
     // the target's factor over the one just written by the same thread
     acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) {
@@ -654,6 +657,8 @@ bool packed_rows(const void* p, size_t stride) {
 struct XentPlan {
   bool grads, kept, padHidden, padWeight;
   int partCols;
+  // rows: of every buffer of packed tokens; at least T up to whole slices of
+  // kTileK, the last row that a kernel stores to
   size_t T, D, V, Dp, rows, nParts, piece, nPieces, sumLd;
   // offsets into the workspace
   size_t state, target, token, skipped, rowToken, rowTarget, lse2, targetLogit, parts, hidden,
