@@ -48,6 +48,14 @@ vr_result_t op_reachable(const OpBuffer* b, int n, int device);
 vr_result_t op_reachable(const void* const* p, int n, int device);
 
 // Bytes rounded up to the alignment of a workspace's parts.
-inline size_t op_round(size_t n) { return (n + 255) & ~(size_t)255; }
+constexpr size_t kOpAlign = 256;
+inline size_t op_round(size_t n) { return (n + kOpAlign - 1) & ~(kOpAlign - 1); }
+// Callers align a workspace to 16 bytes; kernels that access its parts 32
+// bytes at a time take them from the first multiple of kOpAlign in it, for
+// which the size that the caller was told has kOpSlack bytes.
+constexpr size_t kOpSlack = kOpAlign - 16;
+inline char* op_workspace(void* p) {
+  return reinterpret_cast<char*>(op_round(reinterpret_cast<size_t>(p)));
+}
 
 }  // namespace vr

@@ -845,7 +845,7 @@ bool make_plan(int count, size_t rows, size_t cols, int dtype, OrthoPlan* p) {
       p->x[i][j] = i && j && p->parts == 1 ? p->x[0][1] : take(p->group * p->m * p->ldX * 2);
   for (int j = 0; j < p->parts; ++j) p->a[j] = take(p->group * p->m * p->ldA * 2);
   for (int j = 0; j < p->parts; ++j) p->b[j] = take(p->group * p->m * p->ldA * 2);
-  p->bytes = at;
+  p->bytes = at + kOpSlack;
   return true;
 }
 
@@ -1096,7 +1096,7 @@ vr_result_t vr_orthogonalize(const void* const* src, void* const* dst, int count
       (e = op_reachable(dst, count, dev.device)) != VR_SUCCESS ||
       (e = op_reachable(&work, 1, dev.device)) != VR_SUCCESS)
     return e;
-  char* w = static_cast<char*>(workspace);
+  char* w = op_workspace(workspace);
   for (int at = 0; at < count && e == VR_SUCCESS; at += kMost) {
     const int n = std::min(kMost, count - at);
     e = dtype == VR_FLOAT32 ? run<float, 2>(p, dev, src + at, dst + at, n, rows, cols, steps, use,

@@ -712,7 +712,7 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
     p->factors = take(p->rows * p->piece * 2);
     p->sum = p->nPieces > 1 ? take(p->rows * p->sumLd * 4) : 0;
   }
-  p->bytes = at;
+  p->bytes = at + kOpSlack;
   return true;
 }
 
@@ -1020,7 +1020,7 @@ vr_result_t vr_linear_xent(const void* hidden, size_t hiddenStride, const void* 
   OpDevice dev;
   vr_result_t e = op_device(&dev);
   if (e != VR_SUCCESS || (e = op_reachable(buf, n, dev.device)) != VR_SUCCESS) return e;
-  char* w = static_cast<char*>(workspace);
+  char* w = op_workspace(workspace);
   return dtype == VR_BFLOAT16
              ? run<__nv_bfloat16>(p, dev, hidden, hiddenStride, weight, weightStride, targets,
                                   ignoreIndex, mean, gradScale, losses, lse, loss, dHidden, dWeight,

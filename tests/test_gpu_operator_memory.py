@@ -71,3 +71,78 @@ def test_pieces_of_the_vocabulary_with_ragged_tokens(T, D, V, dtype):
     assert vr.vr_stream_status() == 0
     assert arena.intact()
     compare(got, refs.xent(h, w, y, IGNORE, True, scale), ty)
+
+
+# A workspace needs 16-byte alignment, whatever the width of the accesses that
+# the kernels make into it: the same bits from every such place.
+OFFSETS = [16, 32, 112, 240]
+
+
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,D,V,least", [
+    (70, 64, 300, False), (300, 136, 1000, False), (130, 65, 1000, False),  # padded weight
+    (300, 64, 380000, False),                                                # in pieces
+    (600, 640, 240000, True)])                                               # by the workspace
+def test_xent_workspace_alignment(T, D, V, least, dtype, offset):
+    code, ty = DT[dtype]
+    scale = 64.0 * T if dtype == "fp16" else 1.0
+    h, w, y = make(T, D, V, ty, 5, ignored=0.1)
+    want = xent(Arena(), h, w, y, code, scale, 2 if least else 1)
+    arena = Arena()
+    got = xent(arena, h, w, y, code, scale, 2 if least else 1, offset)
+    assert vr.vr_stream_status() == 0
+    assert arena.intact()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def ortho(arena, ms, code, offset=0):
+    rows, cols = ms[0].shape
+    n = vr.vr_orthogonalize_workspace_bytes(len(ms), rows, cols, code)
+    work = arena.cut(n, offset)
+    out = [arena.like((rows, cols), ms[0].dtype) for _ in ms]
+    vr.vr_orthogonalize(ms, out, len(ms), rows, cols, code, 5, None, 1e-7, 1.0, work, n,
+                        torch.cuda.current_stream())
+    return out
+
+
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("count,rows,cols", [(2, 100, 60), (3, 200, 333), (1, 333, 200),
+                                             (1, 1500, 1030)])
+def test_orthogonalize_workspace_alignment(count, rows, cols, dtype, offset):
+    code, ty = dict(DT, fp32=(vr.VR_FLOAT32, torch.float32))[dtype]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    ms = [torch.randn(rows, cols, generator=g, device="cuda").to(ty) for _ in range(count)]
+    want = ortho(Arena(), ms, code)
+    arena = Arena()
+    got = ortho(arena, ms, code, offset)
+    assert vr.vr_stream_status() == 0
+    assert arena.intact()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("R,T,E", [(2, 7, 30), (4, 500, 64), (2, 3000, 257)])
+def test_balance_workspace_alignment(R, T, E, offset):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    logits = [torch.randn(T, E, generator=g, device="cuda") for _ in range(R)]
+
+    def run(arena, at):
+        n = vr.vr_balance_loss_workspace_bytes(R, T, E)
+        work = arena.cut(n, at)
+        loss, counts = arena.like((1,), torch.float32), arena.like((E,), torch.int32)
+        picks = [arena.like((T, 3), torch.int32) for _ in range(R)]
+        out = [arena.like((T, E), torch.float32) for _ in range(R)]
+        vr.vr_balance_loss(logits, E, None, R, T, E, 3, vr.VR_FLOAT32, 0.01, 1.0, loss, counts,
+                           picks, out, work, n, torch.cuda.current_stream())
+        return [loss, counts] + picks + out
+
+    want = run(Arena(), 0)
+    arena = Arena()
+    got = run(arena, offset)
+    assert vr.vr_stream_status() == 0
+    assert arena.intact()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
