@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(128 + 32 * Epi::kWarps, 1)
     }
     if constexpr (kAux)
       for (int p = 0; p < 2; ++p) {
-        prefetch_map(&e.aux.in[p]);
+        if (p < e.aux.nIn) prefetch_map(&e.aux.in[p]);
         if (p < e.aux.nOut) prefetch_map(&e.aux.out[p]);
       }
   }
