@@ -70,14 +70,15 @@ struct Tile {
   int z, m0, n0;
 };
 
+// PAIR: `bar` may be in the other CTA of the pair (peer_addr).
 template <bool PAIR>
 __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint32_t bar) {
-  if constexpr (PAIR) {  // counted on the barrier of the pair's first CTA
+  if constexpr (PAIR) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar & 0xfeffffffu)
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
   } else {
     asm volatile(
@@ -503,6 +504,8 @@ __global__ void __launch_bounds__(128 + 32 * Epi::kWarps, 1)
     int s = 0, turn = 0;
     bool ok = true;
     long long issued = 0;
+    // a pair's copies are counted on the barriers of its first CTA
+    const uint32_t landed0 = PAIR ? peer_addr(full(0), rank & ~1u) : full(0);
     for (int t = firstTile; ok && t < tiles; t += tileStep) {
       const Tile o = tile_of<Shape::kTileRows, BN>(t, tilesM, tilesN, g.triangle);
       const int m0 = o.m0 + (int)inPair * kTileM, n0 = o.n0 + (int)inPair * Shape::kBRows;
@@ -513,15 +516,16 @@ __global__ void __launch_bounds__(128 + 32 * Epi::kWarps, 1)
           if (leader) mbar_arrive_expect_tx(full(s), kCtas * Shape::kStageBytes);
           uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes;
           const int k0 = kb * kTileK;
+          const uint32_t landed = landed0 + 8u * s;
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
             if (AMN) {
 #pragma unroll
               for (int i = 0; i < kTileM / 64; ++i)
                 tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.a[p], m0 + i * 64, k0, o.z,
-                                  full(s));
+                                  landed);
             } else {
-              tensor_load<PAIR>(dst, &g.a[p], k0, m0, o.z, full(s));
+              tensor_load<PAIR>(dst, &g.a[p], k0, m0, o.z, landed);
             }
             dst += Shape::kABytes;
           }
@@ -531,9 +535,9 @@ __global__ void __launch_bounds__(128 + 32 * Epi::kWarps, 1)
 #pragma unroll
               for (int i = 0; i < Shape::kBRows / 64; ++i)
                 tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.b[p], n0 + i * 64, k0, o.z,
-                                  full(s));
+                                  landed);
             } else {
-              tensor_load<PAIR>(dst, &g.b[p], k0, n0, o.z, full(s));
+              tensor_load<PAIR>(dst, &g.b[p], k0, n0, o.z, landed);
             }
             dst += Shape::kBBytes;
           }
