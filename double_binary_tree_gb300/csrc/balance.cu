@@ -168,12 +168,15 @@ template <typename T, int VEC, int CHUNKS>
 __device__ __forceinline__ float raw_value(const RawRow<T, VEC, CHUNKS>& r, int i) {
   return Ty<T>::widen(reinterpret_cast<const typename Ty<T>::Bits*>(&r.q[i / VEC])[i % VEC]);
 }
-// exp(x - top) of a row's logits: one multiply-add and exp2 each, unless the
-// product with log2 e could overflow (rows at the type's lowest value).
+// exp(x - top) of a row's logits: one multiply-add and exp2 each while the
+// rounding of top log2 e, which stays in every exponent and cancels in the
+// softmax, is small (at most 2^-4 below 2^20; beyond, it would come to
+// exponentials of 0 or infinity: 440 at 1e10).  Larger logits, by which a
+// router masks, are subtracted first.
 template <typename T, int VEC, int CHUNKS>
 __device__ __forceinline__ void exponentials(const RawRow<T, VEC, CHUNKS>& r, float top,
                                              float (&p)[VEC * CHUNKS]) {
-  if (std::is_same<T, __half>::value || fabsf(top) < 1e38f) {
+  if (std::is_same<T, __half>::value || fabsf(top) < 0x1p20f) {
     const float top2 = top * kLog2e;
 #pragma unroll
     for (int i = 0; i < VEC * CHUNKS; ++i)
