@@ -113,9 +113,11 @@ struct Targets {
   }
 };
 
-// Row statistics of a tile of logits: the maximum (in units of log 2) and
-// the sum of exp over each half tile, and the target's logit; KEEP: and each
-// exp(l - maximum) in 16 bits.
+// Row statistics of a tile of logits: the maximum and the sum of exp(l -
+// maximum) over each part of it, and the target's logit; KEEP: and each
+// exp(l - maximum) in 16 bits.  The difference is taken first, not in one
+// multiply-add with a rounded maximum log2 e: that rounding (2^-18 at 60) would
+// be all that is left of a confident token's 1 - p, and of its loss.
 template <typename T, bool KEEP>
 struct StatsEpilogue {
   static constexpr bool kAux = false;
@@ -154,7 +156,7 @@ struct StatsEpilogue {
 #pragma unroll
       for (int i = 0; i < STEP; ++i) tops[i % 4] = fmaxf(tops[i % 4], v[i]);
     }
-    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * kLog2e;
+    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     // nothing but -inf: subtract 0, so that exp2 gives 0, not NaN
     const float base = top == -INFINITY ? 0.0f : top;
     const bool store = KEEP && t < M && t < a.state->valid;
@@ -166,7 +168,7 @@ struct StatsEpilogue {
       fetch(c, v);
 #pragma unroll
       for (int i = 0; i < STEP; ++i) {
-        v[i] = exp2_fast(fmaf(v[i], kLog2e, up - base));
+        v[i] = exp2_fast(fmaf(v[i] - base, kLog2e, up));
         sums[i % 4] += v[i];
       }
       if (store) store_row(a.out + (long long)t * a.ld + first + c, v, STEP, 32);
@@ -180,7 +182,7 @@ struct StatsEpilogue {
 
 // The kept exponentials of the packed tokens made into gradient factors, and
 // rows of zeros up to the next whole slice.  The target's factor is made of
-// its fp32 logit: of a sure token it is a small difference.  One read and one
+// its fp32 logit (target_factor).  One read and one
 // write: 2048 x 32768 in 39 us, 6.9 TB/s.
 template <typename T>
 struct KeptArgs {
@@ -188,11 +190,16 @@ struct KeptArgs {
   long long ld;
   const float2* parts;
   int nParts, partCols, V;
-  const float* lse2;
+  const float2* softmax;
   const int* target;
   const float* targetLogit;
   const XentState* state;
 };
+// p - 1 of the target, of a confident token a small difference: (e - sum) / sum
+// with the same e that the sum holds is what the others' sum is.
+__device__ __forceinline__ float target_factor(float logit, float2 softmax, float by) {
+  return (exp2_fast((logit - softmax.x) * kLog2e) - softmax.y) * by;
+}
 constexpr int kKeptUnits = 4;  // of 8 values a thread
 template <typename T>
 __global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ KeptArgs<T> a) {
@@ -202,7 +209,8 @@ __global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ 
   const int c0 = (blockIdx.x * kKeptUnits * 256 + threadIdx.x) * 8;
   for (int t = blockIdx.y; t < rows; t += gridDim.y) {
     T* out = a.out + t * a.ld;
-    const float lse2 = t < valid ? a.lse2[t] : 0.0f;
+    const float2 row = t < valid ? a.softmax[t] : make_float2(0.0f, 1.0f);
+    const float inv = __fdividef(1.0f, row.y);
     const int y = t < valid ? a.target[t] : -1;
     uint4 q[kKeptUnits];
     float2 part[kKeptUnits];
@@ -222,16 +230,14 @@ __global__ void __launch_bounds__(256) xent_kept_kernel(const __grid_constant__ 
         *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
         continue;
       }
-      const float by = exp2_fast(part[u].x - lse2);
+      const float by = exp2_fast((part[u].x - row.x) * kLog2e) * inv;
       uint32_t* w = reinterpret_cast<uint32_t*>(&q[u]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float x = Ty<T>::widen((typename Ty<T>::Bits)(w[i] & 0xffffu)) * by;
         float z = Ty<T>::widen((typename Ty<T>::Bits)(w[i] >> 16)) * by;
-        if ((y >> 1) == (c >> 1) + i) {
-          const float p = exp2_fast(fmaf(a.targetLogit[t], kLog2e, -lse2)) - 1.0f;
-          (y & 1 ? z : x) = p * (float)(1 << kShift<T>);
-        }
+        if ((y >> 1) == (c >> 1) + i)
+          (y & 1 ? z : x) = target_factor(a.targetLogit[t], row, inv * (float)(1 << kShift<T>));
         w[i] = pack2<T>(x, z);
       }
       *reinterpret_cast<uint4*>(out + c) = q[u];
@@ -245,9 +251,10 @@ struct FactorEpilogue {
   static constexpr bool kAux = false;
   static constexpr int kWarps = 16;
   struct Args {
-    const int* target;   // packed tokens' targets
-    const float* lse2;   // their log sums, in units of log 2
-    T* out;              // [tokens][ld]
+    const int* target;         // packed tokens' targets
+    const float* targetLogit;  // and their logits, as the sums hold them
+    const float2* softmax;     // maximum and sum of each
+    T* out;                    // [tokens][ld]
     long long ld;
     int v0;              // the piece's first row of the vocabulary
   };
@@ -259,7 +266,8 @@ struct FactorEpilogue {
     // dW reads whole slices of tokens: zeros up to there.  A tile's rows go on
     // past the buffer's.
     const bool stored = t < (M + kTileK - 1) / kTileK * kTileK;
-    const float sub = live ? (float)kShift<T> - a.lse2[t] : 0.0f;
+    const float2 sum = live ? a.softmax[t] : make_float2(0.0f, 1.0f);
+    const float by = __fdividef((float)(1 << kShift<T>), sum.y);
     const int at = live ? a.target[t] - a.v0 - o.n0 - col0 : -1;
     T* out = a.out + (long long)t * a.ld + o.n0 + col0;
 #pragma unroll
@@ -269,14 +277,13 @@ struct FactorEpilogue {
       acc(col0 + c, v);
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        v[i] = live ? exp2_fast(fmaf(v[i], kLog2e, sub)) : 0.0f;
+        v[i] = live ? exp2_fast((v[i] - sum.x) * kLog2e) * by : 0.0f;
       if (stored) store_row(out + c, v, 32, 32);
     }
     // the target's factor over the one just written by the same thread
-    acc.pick(at >= 0 && at < COLS ? col0 + at : -1, [&](float x) {
-      const float p = exp2_fast(fmaf(x, kLog2e, sub)) - (float)(1 << kShift<T>);
-      reinterpret_cast<typename Ty<T>::Bits*>(out)[at] = Ty<T>::narrow(p);
-    });
+    if (at >= 0 && at < COLS && o.n0 + col0 + at < g.N)
+      reinterpret_cast<typename Ty<T>::Bits*>(out)[at] =
+          Ty<T>::narrow(target_factor(a.targetLogit[t], sum, by));
   }
 };
 
@@ -447,11 +454,11 @@ __global__ void __launch_bounds__(1024) xent_prep_kernel(const __grid_constant__
   }
 }
 
-// A (maximum, sum) pair over more columns: the other's sum brought to the
-// common maximum.  -inf: nothing so far.
+// A (maximum, sum of exp(l - maximum)) pair over more columns: the other's sum
+// brought to the common maximum.  -inf: nothing so far.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
   const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.0f : top;
-  return make_float2(top, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
+  return make_float2(top, a.y * exp2f((a.x - base) * kLog2e) + b.y * exp2f((b.x - base) * kLog2e));
 }
 
 // Joins the rows' pairs, and, in one CTA (ALL), sums the loss.  A warp takes a
@@ -464,7 +471,8 @@ struct JoinArgs {
   Targets target;
   int mean;
   const float* targetLogit;
-  float *lse2, *lse, *losses, *loss;
+  float2* softmax;         // the rows' joined pairs
+  float *lse, *losses, *loss;
   unsigned* status;
 };
 // The loss from the tokens' losses, by one CTA of 1024 threads: in 64 bits, in
@@ -536,10 +544,11 @@ __global__ void __launch_bounds__(ALL ? 1024 : 256)
     }
     if (lane == 0 && warp % each == 0 && token >= 0) {
       const float base = pair.x == -INFINITY ? 0.0f : pair.x;
-      const float l2 = base + log2f(pair.y), l = l2 * kLn2;
-      a.lse2[t] = l2;
-      a.lse[token] = l;
-      a.losses[token] = a.target.at(t) >= 0 ? l - a.targetLogit[t] : 0.0f;
+      const float rest = log2f(pair.y) * kLn2;
+      a.softmax[t] = pair;
+      a.lse[token] = base + rest;
+      // (not lse - l, which keeps only what lse has digits for)
+      a.losses[token] = a.target.at(t) >= 0 ? (base - a.targetLogit[t]) + rest : 0.0f;
     }
   }
   if (ALL) {
@@ -661,7 +670,7 @@ struct XentPlan {
   // kTileK, the last row that a kernel stores to
   size_t T, D, V, Dp, rows, nParts, piece, nPieces, sumLd;
   // offsets into the workspace
-  size_t state, target, token, skipped, rowToken, rowTarget, lse2, targetLogit, parts, hidden,
+  size_t state, target, token, skipped, rowToken, rowTarget, softmax, targetLogit, parts, hidden,
       weight, packed, factors, sum, bytes;
 };
 
@@ -700,7 +709,7 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
   p->target = take(T * 4);
   p->token = take(T * 4);
   p->skipped = take(T * 4);
-  p->lse2 = take(p->rows * 4);
+  p->softmax = take(p->rows * sizeof(float2));
   p->targetLogit = take(p->rows * 4);
   p->parts = take(p->rows * p->nParts * sizeof(float2));
   p->hidden = p->padHidden ? take(T * p->Dp * 2) : 0;
@@ -796,7 +805,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
   XentState* state = reinterpret_cast<XentState*>(w + p.state);
   auto ints = [w](size_t at) { return reinterpret_cast<int*>(w + at); };
   int *target = ints(p.target), *token = ints(p.token), *skipped = ints(p.skipped);
-  float* lse2 = reinterpret_cast<float*>(w + p.lse2);
+  float2* softmax = reinterpret_cast<float2*>(w + p.softmax);
   float* targetLogit = reinterpret_cast<float*>(w + p.targetLogit);
   float2* parts = reinterpret_cast<float2*>(w + p.parts);
   uint16_t* packed = reinterpret_cast<uint16_t*>(w + p.packed);
@@ -867,7 +876,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
                   rowTarget,
                   mean,
                   targetLogit,
-                  lse2,
+                  softmax,
                   lse,
                   losses,
                   loss,
@@ -892,7 +901,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     return VR_SUCCESS;
   }
   if (p.kept) {
-    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, p.partCols, (int)p.V, lse2,
+    KeptArgs<T> a = {factors, (long long)p.piece, parts, (int)p.nParts, p.partCols, (int)p.V, softmax,
                      rowTarget.of, targetLogit, state};
     void* args[] = {&a};
     const size_t columns = 256 * kKeptUnits * 8;
@@ -912,7 +921,8 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     const size_t v0 = i * p.piece, rows = std::min(p.piece, p.V - v0);
     const T* wPiece = static_cast<const T*>(weight) + v0 * weightStride;
     if (!p.kept) {
-      typename FactorEpilogue<T>::Args fa = {rowTarget.of, lse2, factors, (long long)p.piece, (int)v0};
+      typename FactorEpilogue<T>::Args fa = {rowTarget.of, targetLogit, softmax, factors,
+                                             (long long)p.piece, (int)v0};
       if ((e = product<T, false, false, 0, false, FactorEpilogue<T>>(
                dev, packed, p.Dp, wPiece, weightStride, p.T, rows, p.D, &state->valid, nullptr, fa,
                stream)) != VR_SUCCESS)
