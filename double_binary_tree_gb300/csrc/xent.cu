@@ -987,12 +987,15 @@ vr_result_t vr_linear_xent_workspace_bytes(const void* hidden, size_t hiddenStri
                                            const void* weight, size_t weightStride, size_t tokens,
                                            size_t dim, size_t vocab, vr_dtype_t dtype, int grads,
                                            size_t* bytes) {
-  XentPlan p = {};
-  if (!bytes || grads < 0 || grads > 2 ||
-      !make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype, grads != 0,
-                 grads == 1, &p))
+  XentPlan p = {}, q = {};
+  auto plan = [&](bool kept, XentPlan* to) {
+    return make_plan(hidden, hiddenStride, weight, weightStride, tokens, dim, vocab, dtype,
+                     grads != 0, kept, to);
+  };
+  if (!bytes || grads < 0 || grads > 2 || !plan(true, &p) || !plan(false, &q))
     return VR_ERR_INVALID_ARGUMENT;
-  *bytes = p.bytes;
+  // a little over one piece, the sums of the pieces take more than keeping all
+  *bytes = grads == 2 ? std::min(p.bytes, q.bytes) : p.bytes;
   return VR_SUCCESS;
 }
 

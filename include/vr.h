@@ -456,7 +456,8 @@ vr_result_t vr_allreduce_ring_stepwise_noalloc(const void* const* sendbufs, void
  * room: 6 tokens dim vocab operations.  Else the vocabulary is taken in
  * pieces and the logits are computed twice, 8 tokens dim vocab operations.
  * vr_linear_xent_workspace_bytes gives the size for the loss alone (grads =
- * 0), for the gradients (1), and the least for the gradients (2: in pieces).
+ * 0), for the gradients (1), and the least for the gradients (2: in pieces,
+ * where that takes less).
  * Rows that are not 16-byte units (dim or stride not a multiple of 8, or a
  * misaligned buffer) are copied into the workspace first; its size depends
  * on the buffers' alignment, so vr_linear_xent_workspace_bytes takes the
