@@ -37,10 +37,16 @@ constexpr int kBN = 256;
 // where few rows and few tiles would leave SMs idle.
 constexpr int kPartCols = kBN / 4;
 // The losses are fp32 results: their logits are summed in chunks of 512.
-// (The gradients' roundings to 16 bits are far above the truncation.)
+// The gradients are rounded to 16 bits; the truncation takes 1.6e-8 off them
+// per 16 k (1.3e-4 of a dH summed over 131072 in one go: with fp16's rounding of
+// 2.08e-4 on average 2.58e-4 in all, 2.09e-4 in chunks; with bf16's 1.663e-3
+// 1.671e-3).  Sums that it would cost more than a sixth of the rounding go in
+// chunks of 2048, which takes no longer.
 // Up to 128 rows the weight's traffic bounds the product, whose sums then
 // change hands every 128.
-constexpr int kStatsChunk = 8, kFewRowsChunk = 2;
+constexpr int kStatsChunk = 8, kFewRowsChunk = 2, kLongChunk = 32;
+template <typename T>
+constexpr size_t kLongSum = std::is_same<T, __half>::value ? 32768 : 262144;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Device-side results of the preparation.
@@ -726,14 +732,16 @@ bool make_plan(const void* hidden, size_t hiddenStride, const void* weight, size
 }
 
 // One product; pairs of CTAs where the rows fill them.  CHUNK > 0: sums in
-// chunks, which one chunk or less does not need.
-template <typename T, bool AMN, bool BMN, int CHUNK, bool SPLIT, class Epi>
+// chunks, which one chunk or less does not need; LONG: in long chunks, sums of
+// more than kLongSum.
+template <typename T, bool AMN, bool BMN, int CHUNK, bool SPLIT, class Epi, bool LONG = false>
 vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* b, size_t bLd,
                     size_t M, size_t N, size_t K, const int* dynM, const int* dynK,
                     typename Epi::Args& epi, void* stream, bool narrow = false) {
   const Operand oa = {a, nullptr, aLd}, ob = {b, nullptr, bLd};
   const GemmSize z = {M, N, K, 1, false};
   const bool few = M <= kTileM;
+  constexpr int kLong = LONG ? kLongChunk : 0;
 #define VR_PRODUCT(C, PAIR, SHARED, SHARES)                                             \
   return gemm_launch<T, kBN, 1, AMN, BMN, C, PAIR, SHARED, Epi>(dev, oa, ob, z, dynM, dynK, \
                                                                 epi, SHARES, stream)
@@ -777,20 +785,32 @@ vr_result_t product(const OpDevice& dev, const void* a, size_t aLd, const void* 
         offer(false, s, gemm_tiles<128, true>(z), odd ? 0.23 : 0.167);
       }
     }
-#define VR_SHARED(BN, PAIR)                                                                   \
-  return gemm_launch<T, BN, 1, AMN, BMN, 0, PAIR, true, Epi>(dev, oa, ob, z, dynM, dynK, epi, \
+#define VR_SHARED(C, BN, PAIR)                                                                \
+  return gemm_launch<T, BN, 1, AMN, BMN, C, PAIR, true, Epi>(dev, oa, ob, z, dynM, dynK, epi, \
                                                              shares, stream)
+    if constexpr (kLong > 0) {
+      if (shares > 1 && K > kLongSum<T> * shares) {
+        if (few && wide) VR_SHARED(kLong, kBN, false);
+        if (few) VR_SHARED(kLong, 128, false);
+        if (wide) VR_SHARED(kLong, kBN, true);
+        VR_SHARED(kLong, 128, true);
+      }
+    }
     if (shares > 1) {
-      if (few && wide) VR_SHARED(kBN, false);
-      if (few) VR_SHARED(128, false);
-      if (wide) VR_SHARED(kBN, true);
-      VR_SHARED(128, true);
+      if (few && wide) VR_SHARED(0, kBN, false);
+      if (few) VR_SHARED(0, 128, false);
+      if (wide) VR_SHARED(0, kBN, true);
+      VR_SHARED(0, 128, true);
     }
 #undef VR_SHARED
   }
   if constexpr (CHUNK > 0) {
     if (few && K > kFewRowsChunk * kTileK) VR_PRODUCT(kFewRowsChunk, false, false, 1);
     if (!few && K > CHUNK * kTileK) VR_PRODUCT(CHUNK, true, false, 1);
+  }
+  if constexpr (kLong > 0) {
+    if (few && K > kLongSum<T>) VR_PRODUCT(kLong, false, false, 1);
+    if (K > kLongSum<T>) VR_PRODUCT(kLong, true, false, 1);
   }
   if (few) VR_PRODUCT(0, false, false, 1);
   VR_PRODUCT(0, true, false, 1);
@@ -932,10 +952,9 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
       typename HiddenEpilogue<T>::Args ha = {
           reinterpret_cast<float*>(w + p.sum), (long long)p.sumLd, static_cast<T*>(dHidden), token,
           state, i == 0, i + 1 == p.nPieces, alignH};
-      if ((e = product<T, false, true, 0, true, HiddenEpilogue<T>>(dev, factors, p.piece, wPiece,
-                                                          weightStride, p.T, p.D, rows,
-                                                          &state->valid, nullptr, ha, stream)) !=
-          VR_SUCCESS)
+      if ((e = product<T, false, true, 0, true, HiddenEpilogue<T>, true>(
+               dev, factors, p.piece, wPiece, weightStride, p.T, p.D, rows, &state->valid, nullptr,
+               ha, stream)) != VR_SUCCESS)
         return e;
     }
     if (dWeight) {
@@ -958,7 +977,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
             stream);
       } else {
         typename WeightEpilogue<T>::Args wa = {out, (long long)ld, state, viaPad ? 32 : alignW};
-        e = product<T, true, true, 0, false, WeightEpilogue<T>>(
+        e = product<T, true, true, 0, false, WeightEpilogue<T>, true>(
             dev, factors, p.piece, packed, p.Dp, rows, p.D, p.rows, nullptr, &state->valid, wa,
             stream);
       }
