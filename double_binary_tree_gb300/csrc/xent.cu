@@ -372,9 +372,17 @@ struct WeightEpilogue {
 };
 
 // The same through shared memory and tensor copies, for rows of whole 16-byte
-// units.  With few tokens the stores are what takes the time: 777 x 1000 x
-// 50001 65 us row by row, 46 us this way; with many the products want the
-// shared memory for their stages.
+// units that are no 32-byte ones.  With few tokens their stores, twice as many
+// and across sectors, are what takes the time; with many the products want the
+// shared memory for their stages.  Loss and dWeight, bf16, us row by row and
+// this way:
+//   tokens              64        256        768       1024       1280       2048
+//   dim 1032 x 131072   260 204   287 232    478 431   571 533    773 781  1228 1256
+//   dim 1000 x 50001    111 104   122 112    192 175   233 220    269 260   387 386
+//   dim 2056 x 32768    139 133   152 143    221 197   254 239    300 292   441 436
+// Rows of 32-byte units are stored row by row:
+//   dim 2048 x 32768     99 112   111 123    176 180   195 214    239 260   375 376
+//   dim 1024 x 131072   191 212   215 241    346 357   441 452    623 612  1036 1060
 template <typename T>
 struct WeightTilesEpilogue {
   static constexpr bool kAux = true;
@@ -965,7 +973,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
       T* out = viaPad ? static_cast<T*>(const_cast<void*>(weight)) + v0 * p.Dp
                       : static_cast<T*>(dWeight) + v0 * p.D;
       const size_t ld = viaPad ? p.Dp : p.D;
-      if (p.T <= kTilesMostTokens && (viaPad || alignW >= 16)) {
+      if (p.T <= kTilesMostTokens && !viaPad && alignW == 16) {
         typename WeightTilesEpilogue<T>::Args wa = {};
         wa.aux.nOut = 1;
         wa.state = state;
