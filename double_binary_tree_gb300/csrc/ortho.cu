@@ -15,8 +15,12 @@
 // every later step in the directions of small singular values, where a
 // rounding of an operand of B X is not (it enters between a small and a large
 // direction, which the next steps damp).  So bf16 results take one product of
-// high planes (operand roundings 2^-12, together below the result's own 2^-9),
-// fp16 and fp32 results three products of both planes, summed in chunks.
+// high planes, fp16 and fp32 results three products of both planes, summed in
+// chunks.  The operands' roundings of 2^-12, a few per step, average out over
+// many directions: 1.2e-3 before the result's own rounding (1.7e-3) at 128 x
+// 1024, 3.4e-3 at most over 200 matrices of 32 x 500, but up to 1.6e-2 at 2 x 3.
+// Up to 16 rows (of X) bf16 results take both planes, too (8 matrices of 16 x
+// 128: 25 -> 38 us; as exact as fp32's).
 // (Holding X in fp32 beside the planes measured 4 % slower at 4096 x 1024
 // and no more exact, but where all but a few singular values are below 1e-3:
 // 1.2e-5 against 1.5e-5, fp32 arithmetic throughout 2.2e-5.)
@@ -34,6 +38,7 @@ constexpr int kMost = 64;          // matrices per launch
 constexpr float kScale = 4096.0f;  // of the planes
 constexpr int kNormCtas = 256;     // partial sums of squares per matrix, at most
 constexpr int kSplitChunk = 2;     // slices of 64 summed before rounding (two planes)
+constexpr size_t kFewRows = 16;    // of X: bf16 results take both planes, too
 
 struct Planes {
   __half *hi, *lo;
@@ -825,8 +830,8 @@ bool make_plan(int count, size_t rows, size_t cols, int dtype, OrthoPlan* p) {
   if (!op_elem_size(dtype) || count < 1 || rows < 1 || cols < 1 || rows > (1u << 24) ||
       cols > (1u << 24))
     return false;
-  p->parts = dtype == VR_BFLOAT16 ? 1 : 2;
   p->m = std::min(rows, cols);
+  p->parts = dtype == VR_BFLOAT16 && p->m > kFewRows ? 1 : 2;
   p->n = std::max(rows, cols);
   p->ldX = up(p->n, 32);
   p->ldA = up(p->m, 32);
@@ -1104,6 +1109,9 @@ vr_result_t vr_orthogonalize(const void* const* src, void* const* dst, int count
         : dtype == VR_FLOAT16
             ? run<__half, 2>(p, dev, src + at, dst + at, n, rows, cols, steps, use, eps, scale, w,
                              stream)
+        : p.parts == 2
+            ? run<__nv_bfloat16, 2>(p, dev, src + at, dst + at, n, rows, cols, steps, use, eps,
+                                    scale, w, stream)
             : run<__nv_bfloat16, 1>(p, dev, src + at, dst + at, n, rows, cols, steps, use, eps,
                                     scale, w, stream);
   }

@@ -518,11 +518,14 @@ vr_result_t vr_balance_loss(const void* const* logits, size_t rowStride,
  * dst[i] may be src[i].  coefs: NULL (3.4445, -4.775, 2.0315 in every step) or
  * 3 * steps floats on the host, a, b, c of each step.
  * The norm is an fp32 sum of squares (entries beyond about 1e18 overflow
- * it); a zero matrix gives zeros (with eps = 0: NaN), NaN or an infinity a
- * matrix of NaN.  Products are summed in fp32; X is held to 22 bits between
- * the steps.  bf16 results take products of operands rounded to 11 bits (an
- * error below the result's own rounding), fp16 and fp32 results of operands
- * of 22 bits (about three times the time).
+ * it, those below about 1e-19 are lost in it); a zero matrix gives zeros (with
+ * eps = 0: NaN), NaN or an infinity a matrix of NaN.  Products are summed in
+ * fp32; X is held to 22 bits between the steps, and to 2^-37 where |src|_F far
+ * below eps leaves it small.  fp16 and fp32 results, and bf16 results of up to
+ * 16 rows or columns, take products of operands of 22 bits (up to three times
+ * the time), other bf16 results of operands rounded to 11 bits: an error of
+ * the size of the result's own rounding (1e-3 to 3e-3, 2-norm), more where all
+ * but a few singular values are zero (1.6e-2 at most for two).
  * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, rows or cols outside
  * [1, 2^24], steps outside [1, 32], eps negative, or eps, scale or a
  * coefficient not finite, a NULL or misaligned buffer, an overlap or a short
