@@ -28,7 +28,7 @@
 // order of the shares.
 //
 // Measured on GB300, 4864 x 4864 x 4096 fp16 with an epilogue that stores
-// nothing: pairs 256 x 256 1950 TFLOP/s (1.02 of a cuBLAS bf16 product of
+// nothing: pairs 256 x 256 1950 TFLOP/s (1.01 of a cuBLAS bf16 product of
 // 8192^3; either operand K- or MN-major), summed in chunks of 512 1910,
 // 256 x 128 1800, single CTAs 128 x 256 1850, 128 x 128 1490 (shared memory
 // bandwidth); two planes, sums handed over every 128, 1660 over their three

@@ -4,19 +4,20 @@
 //   l_tv = h_t . w_v;  lse_t = log sum_v exp l_tv;  loss_t = lse_t - l_t,y(t)
 //   g_tv = s (exp(l_tv - lse_t) - [v = y(t)]);  dH = G W;  dW = G^T H
 //
-// The logits are never stored.  The first product (gemm.cuh) turns each
-// 128 x 256 tile of them into one maximum and one sum per row in its epilogue;
-// joining the tiles' pairs gives lse.  For the gradients there are two ways:
+// The logits are never stored.  The first product (gemm.cuh) turns every 64
+// (few rows: 32) columns of a row of them into one maximum and one sum of
+// exp(l - maximum) in its epilogue; joining these pairs gives the row's, and
+// lse.  For the gradients there are two ways:
 //   kept     the same epilogue also writes exp(l - the tile's maximum) in 16
 //            bits; once lse is known a pass over them makes the gradient
 //            factors p - [v = y] of them in place.  6 T D V operations.  Taken
 //            while T x V 16-bit values are no more memory than the weight has
 //            (T <= D), or 256 MB, and the workspace has room for them.
 //   pieces   the vocabulary is taken piece by piece: the product runs again,
-//            its epilogue now writing the factors.  8 T D V operations, a
-//            workspace that does not grow with T x V.
+//            its epilogue now writing the factors.  8 T D V operations; of the
+//            workspace only the pairs grow with T x V, an eighth of a byte each.
 // Two more products multiply the factors with the weight and with the hidden
-// states.  (4096 tokens x 4096 x 131072, bf16: 8.4 ms kept, 10.4 ms in pieces.)
+// states.  (4096 tokens x 4096 x 131072, bf16: 8.4-8.6 ms kept, 10.4 ms in pieces.)
 //
 // Only tokens that count take part in the gradients: the hidden states are
 // packed first, tokens that count before ignored ones, which leaves out the
@@ -188,8 +189,8 @@ struct StatsEpilogue {
 
 // The kept exponentials of the packed tokens made into gradient factors, and
 // rows of zeros up to the next whole slice.  The target's factor is made of
-// its fp32 logit (target_factor).  One read and one
-// write: 2048 x 32768 in 39 us, 6.9 TB/s.
+// its fp32 logit (target_factor).  One read and one write: 2048 x 32768 in 48 us
+// from cold caches (ncu), 5.6 TB/s.
 template <typename T>
 struct KeptArgs {
   T* out;

@@ -448,9 +448,11 @@ vr_result_t vr_allreduce_ring_stepwise_noalloc(const void* const* sendbufs, void
  * dHidden (tokens x dim), dWeight (vocab x dim): contiguous, of dtype; each
  * may be NULL, both for the loss alone.
  * Products are exact and summed in fp32, as are the softmax and the losses;
- * in the gradients softmax minus one-hot is rounded to dtype (once, where the
- * numerators are kept twice; fp16: scaled by 2^14 first) and each gradient
- * once (fp16: scale it into range with gradScale).  When no token counts, the loss and the gradients are 0.
+ * (a confident token's loss is as exact as its logits); in the gradients
+ * softmax minus one-hot is rounded to dtype (once, where the numerators are
+ * kept twice; fp16: scaled by 2^14 first) and each gradient once (fp16: scale
+ * it into range with gradScale).  When no token counts, the loss and the
+ * gradients are 0.
  * With gradients, and tokens <= dim (or at most 256 MB of them), the softmax
  * numerators are kept in 16 bits between the passes, if the workspace has
  * room: 6 tokens dim vocab operations.  Else the vocabulary is taken in
@@ -525,7 +527,7 @@ vr_result_t vr_balance_loss(const void* const* logits, size_t rowStride,
  * 16 rows or columns, take products of operands of 22 bits (up to three times
  * the time), other bf16 results of operands rounded to 11 bits: an error of
  * the size of the result's own rounding (1e-3 to 3e-3, 2-norm), more where all
- * but a few singular values are zero (1.6e-2 at most for two).
+ * but a few singular values are zero (up to 1.6e-2 measured with two left).
  * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, rows or cols outside
  * [1, 2^24], steps outside [1, 32], eps negative, or eps, scale or a
  * coefficient not finite, a NULL or misaligned buffer, an overlap or a short
