@@ -56,30 +56,29 @@ bool op_buffers_ok(const OpBuffer* b, int n) {
   return true;
 }
 
+bool op_spans_ok(OpSpan* v, size_t n) {
+  std::sort(v, v + n, [](const OpSpan& a, const OpSpan& b) { return a.lo < b.lo; });
+  // the furthest end so far of any span, and of a written one
+  size_t any = 0, written = 0;
+  for (const OpSpan* s = v; s < v + n; ++s) {
+    if (s->lo < written || (s->write && s->lo < any)) return false;
+    any = std::max(any, s->hi);
+    if (s->write) written = std::max(written, s->hi);
+  }
+  return true;
+}
+
 bool op_lists_ok(const void* const* src, void* const* dst, int count, size_t bytes,
                  const void* workspace, size_t workspaceBytes) {
   try {
-    struct Span {
-      uintptr_t lo, hi;
-      int i;  // list index; -1: the workspace
-      bool write;
-    };
-    std::vector<Span> v;
+    std::vector<OpSpan> v;
     v.reserve(2 * (size_t)count + 1);
     for (int i = 0; i < count; ++i) {
-      v.push_back({(uintptr_t)dst[i], (uintptr_t)dst[i] + bytes, i, true});
-      if (src[i] != dst[i]) v.push_back({(uintptr_t)src[i], (uintptr_t)src[i] + bytes, i, false});
+      v.push_back({(uintptr_t)dst[i], (uintptr_t)dst[i] + bytes, true});
+      if (src[i] != dst[i]) v.push_back({(uintptr_t)src[i], (uintptr_t)src[i] + bytes, false});
     }
-    v.push_back({(uintptr_t)workspace, (uintptr_t)workspace + workspaceBytes, -1, true});
-    std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-    // the furthest end so far of any span, and of a written one
-    uintptr_t any = 0, written = 0;
-    for (const Span& s : v) {
-      if (s.lo < written || (s.write && s.lo < any)) return false;
-      any = std::max(any, s.hi);
-      if (s.write) written = std::max(written, s.hi);
-    }
-    return true;
+    v.push_back({(uintptr_t)workspace, (uintptr_t)workspace + workspaceBytes, true});
+    return op_spans_ok(v.data(), v.size());
   } catch (...) {  // no host memory for the list
     return false;
   }

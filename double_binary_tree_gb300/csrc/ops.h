@@ -42,6 +42,14 @@ bool op_buffers_ok(const OpBuffer* b, int n);
 bool op_lists_ok(const void* const* src, void* const* dst, int count, size_t bytes,
                  const void* workspace, size_t workspaceBytes);
 
+// Any number of extents, in any order (sorted here): no written one may touch
+// another one.
+struct OpSpan {
+  size_t lo, hi;
+  bool write;
+};
+bool op_spans_ok(OpSpan* v, size_t n);
+
 // The option VR_VALIDATE_POINTERS (api.cc): whether every buffer can be
 // reached from the current device.
 vr_result_t op_reachable(const OpBuffer* b, int n, int device);

@@ -28,7 +28,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "gemm.cuh"
+#include "rows.cuh"
 
 namespace vr {
 namespace {
@@ -67,40 +67,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)Ty<T>::narrow(a) | (uint32_t)Ty<T>::narrow(b) << 16;
-}
-
-// Consecutive 16-bit values of one row.  `align`: bytes that a store may
-// take (2, 16 or 32); a warp's rows are 32 lines apart, so half as many
-// stores are half the time.
-template <typename T, int N>
-__device__ __forceinline__ void store_row(T* out, const float (&v)[N], int cols, int align) {
-  typename Ty<T>::Bits* o = reinterpret_cast<typename Ty<T>::Bits*>(out);
-  if (align >= 16 && cols >= N) {
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-    if (align == 32) {
-#pragma unroll
-      for (int i = 0; i < N / 2; i += 8)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 2 * i),
-                     "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
-                     "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
-                     : "memory");
-    } else {
-#pragma unroll
-      for (int i = 0; i < N / 2; i += 4)
-        *reinterpret_cast<uint4*>(o + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < cols) o[i] = Ty<T>::narrow(v[i]);
-  }
 }
 
 // The target of a row, -1 where there is none: prepared with the packed
@@ -577,52 +543,6 @@ __global__ void __launch_bounds__(1024) xent_loss_kernel(const __grid_constant__
   sum_losses(a);
 }
 
-// Rows of `cols` elements between a dense buffer of any alignment and one
-// whose rows are whole sectors (ld): in, with zeros after the last column, or
-// out.  A warp takes a row, so that its accesses are one run of bytes.
-struct PadArgs {
-  const uint16_t* src;
-  long long stride, rows;
-  int cols, ld;
-  uint16_t* dst;
-};
-__global__ void __launch_bounds__(256) xent_pad_kernel(const __grid_constant__ PadArgs a) {
-  pdl_launch();
-  pdl_wait();
-  const int lane = threadIdx.x % 32;
-  for (long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows;
-       r += (long long)gridDim.x * 8) {
-    const uint16_t* in = a.src + r * a.stride;
-    uint4* out = reinterpret_cast<uint4*>(a.dst + r * a.ld);
-#pragma unroll 2
-    for (int u = lane; u < a.ld / 8; u += 32) {
-      alignas(16) uint16_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = u * 8 + i < a.cols ? in[u * 8 + i] : (uint16_t)0;
-      out[u] = *reinterpret_cast<const uint4*>(v);
-    }
-  }
-}
-__global__ void __launch_bounds__(256) xent_unpad_kernel(const __grid_constant__ PadArgs a) {
-  pdl_launch();
-  pdl_wait();
-  const int lane = threadIdx.x % 32;
-  for (long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows;
-       r += (long long)gridDim.x * 8) {
-    const uint16_t* in = a.src + r * a.ld;
-    uint16_t* out = a.dst + r * a.cols;
-    const int odd = (int)((uintptr_t)out >> 1 & 1);  // 32-bit stores begin after it
-    const int words = (a.cols - odd) / 2;
-    if (lane == 0 && odd) out[0] = in[0];
-    if (lane == 1 && odd + 2 * words < a.cols) out[a.cols - 1] = in[a.cols - 1];
-#pragma unroll 4
-    for (int w = lane; w < words; w += 32) {
-      const int c = odd + 2 * w;
-      *reinterpret_cast<uint32_t*>(out + c) = (uint32_t)in[c] | (uint32_t)in[c + 1] << 16;
-    }
-  }
-}
-
 // The packed hidden states: the tokens that count, zeros up to whole slices
 // of 64 rows, the others; each row's token and target; and zero gradients for
 // the others.
@@ -663,8 +583,6 @@ __global__ void __launch_bounds__(256) xent_pack_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------- host side
-size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
-
 // Rows of the vocabulary taken at a time: a piece of the gradient factors of
 // about 256 MB, so that the fp32 sums of dH, read and written once a
 // piece, stay a small part of the traffic.
@@ -672,10 +590,6 @@ constexpr size_t kPieceBytes = (size_t)256 << 20;
 size_t piece_rows(size_t T, size_t V) {  // T: packed rows
   const size_t fit = kPieceBytes / (2 * T) / kBN * kBN;
   return std::min(up(V, kBN), std::max<size_t>(fit, kBN));
-}
-
-bool packed_rows(const void* p, size_t stride) {
-  return ((uintptr_t)p & 15) == 0 && stride % 8 == 0;
 }
 
 struct XentPlan {
@@ -856,7 +770,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     void* args[] = {&a};
     *src = w + at;
     *stride = p.Dp;
-    return op_launch((const void*)xent_pad_kernel,
+    return op_launch((const void*)pad_kernel,
                      dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
                      dim3(256), args, 0, stream);
   };
@@ -997,7 +911,7 @@ vr_result_t run(const XentPlan& p, const OpDevice& dev, const void* hidden, size
     PadArgs a = {static_cast<const uint16_t*>(weight), 0, (long long)p.V, (int)p.D, (int)p.Dp,
                  static_cast<uint16_t*>(dWeight)};
     void* args[] = {&a};
-    return op_launch((const void*)xent_unpad_kernel,
+    return op_launch((const void*)unpad_kernel,
                      dim3((unsigned)std::min<size_t>((p.V + 7) / 8, (size_t)dev.sms * 8)),
                      dim3(256), args, 0, stream);
   }
