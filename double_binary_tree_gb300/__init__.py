@@ -72,6 +72,16 @@ _SIGNATURES = {
     "vr_orthogonalize": (I, [PP, PP, I, S, S, I, I, P(F), F, F, VP, S, VP]),
     "vr_balance_loss_workspace_bytes": (I, [I, S, I, P(S)]),
     "vr_balance_loss": (I, [PP, S, PP, I, S, I, I, I, F, F, VP, VP, PP, PP, VP, S, VP]),
+    "vr_embedding": (I, [VP, S, VP, S, S, S, I, LL, F, VP, S, VP]),
+    "vr_embedding_grad_workspace_bytes": (I, [S, S, S, I, P(S)]),
+    "vr_embedding_grad": (I, [VP, S, VP, S, S, S, I, LL, F, I, VP, VP, S, VP]),
+    "vr_grouped_linear_workspace_bytes": (I, [VP, S, VP, S, S, S, I, I, P(S)]),
+    "vr_grouped_linear": (I, [VP, S, VP, VP, S, S, S, I, I, VP, S, VP, S, VP]),
+    "vr_grouped_linear_grad_workspace_bytes": (I, [VP, S, VP, S, VP, S, S, S, I, I, P(S)]),
+    "vr_grouped_linear_grad": (I, [VP, S, VP, S, VP, VP, S, S, S, I, I, VP, VP, VP, S, VP]),
+    "vr_adamw": (I, [PP, PP, PP, PP, PP, PP, PP, P(S), I, I, I, I, F, F, F, F, F, LL, F,
+                     ctypes.c_ulonglong, VP, VP]),
+    "vr_adamw_values": (I, [PP, PP, PP, PP, P(S), I, PP, PP, VP]),
     "vr_predict_us": (I, [I, I, I, S, P(vr_cost_model_t), P(ctypes.c_double)]),
     "vr_select_algo": (I, [I, I, S, P(vr_cost_model_t), P(I)]),
     "vr_set_cost_model": (I, [P(vr_cost_model_t)]),
@@ -144,10 +154,21 @@ def _ptr(x):
 
 
 def _ptrs(bufs):
-    if bufs is None:
-        return None
+    if bufs is None or isinstance(bufs, ctypes.Array):
+        return bufs
     return (VP * len(bufs))(*[b if b is None or isinstance(b, int) else b.data_ptr()
                               for b in bufs])
+
+
+def pointer_array(bufs):
+    """The pointers of a list of buffers, to pass instead of the list in calls
+    that repeat: the buffers must stay where they are.  None gives None."""
+    return _ptrs(bufs)
+
+
+def size_array(sizes):
+    """A list of sizes in the same way."""
+    return sizes if isinstance(sizes, ctypes.Array) else (S * len(sizes))(*sizes)
 
 
 def _stream(s):
@@ -335,6 +356,73 @@ def vr_orthogonalize(src, dst, count, rows, cols, dtype, steps, coefs, eps, scal
     _check(_L().vr_orthogonalize(_ptrs(src), _ptrs(dst), count, rows, cols, dtype, steps, coefs,
                                  eps, scale, _ptr(workspace), workspaceBytes, _stream(stream)),
            "vr_orthogonalize")
+
+
+def vr_embedding(weight, weightStride, ids, tokens, dim, vocab, dtype, ignoreIndex, scale, out,
+                 outStride, stream=None):
+    _check(_L().vr_embedding(_ptr(weight), weightStride, _ptr(ids), tokens, dim, vocab, dtype,
+                             ignoreIndex, scale, _ptr(out), outStride, _stream(stream)),
+           "vr_embedding")
+
+
+def vr_embedding_grad_workspace_bytes(tokens, dim, vocab, dtype):
+    return _size(_L().vr_embedding_grad_workspace_bytes, "vr_embedding_grad_workspace_bytes",
+                 tokens, dim, vocab, dtype)
+
+
+def vr_embedding_grad(dOut, dOutStride, ids, tokens, dim, vocab, dtype, ignoreIndex, scale,
+                      accumulate, dWeight, workspace, workspaceBytes, stream=None):
+    _check(_L().vr_embedding_grad(_ptr(dOut), dOutStride, _ptr(ids), tokens, dim, vocab, dtype,
+                                  ignoreIndex, scale, int(accumulate), _ptr(dWeight),
+                                  _ptr(workspace), workspaceBytes, _stream(stream)),
+           "vr_embedding_grad")
+
+
+def vr_grouped_linear_workspace_bytes(x, xStride, weight, rows, dim, outDim, groups, dtype):
+    return _size(_L().vr_grouped_linear_workspace_bytes, "vr_grouped_linear_workspace_bytes",
+                 _ptr(x), xStride, _ptr(weight), rows, dim, outDim, groups, dtype)
+
+
+def vr_grouped_linear(x, xStride, weight, counts, rows, dim, outDim, groups, dtype, out, outStride,
+                      workspace, workspaceBytes, stream=None):
+    _check(_L().vr_grouped_linear(_ptr(x), xStride, _ptr(weight), _ptr(counts), rows, dim, outDim,
+                                  groups, dtype, _ptr(out), outStride, _ptr(workspace),
+                                  workspaceBytes, _stream(stream)), "vr_grouped_linear")
+
+
+def vr_grouped_linear_grad_workspace_bytes(dOut, dOutStride, x, xStride, weight, rows, dim, outDim,
+                                           groups, dtype):
+    return _size(_L().vr_grouped_linear_grad_workspace_bytes,
+                 "vr_grouped_linear_grad_workspace_bytes", _ptr(dOut), dOutStride, _ptr(x), xStride,
+                 _ptr(weight), rows, dim, outDim, groups, dtype)
+
+
+def vr_grouped_linear_grad(dOut, dOutStride, x, xStride, weight, counts, rows, dim, outDim, groups,
+                           dtype, dX, dWeight, workspace, workspaceBytes, stream=None):
+    """dX / dWeight may be None (that gradient is not computed)."""
+    _check(_L().vr_grouped_linear_grad(_ptr(dOut), dOutStride, _ptr(x), xStride, _ptr(weight),
+                                       _ptr(counts), rows, dim, outDim, groups, dtype, _ptr(dX),
+                                       _ptr(dWeight), _ptr(workspace), workspaceBytes,
+                                       _stream(stream)), "vr_grouped_linear_grad")
+
+
+def vr_adamw(params, grads, m, v, mScales, vScales, masters, sizes, count, dtype, gradDtype,
+             stateBits, lr, beta1, beta2, eps, weightDecay, step, gradScale, seed, control,
+             stream=None):
+    """Sequences of `count` buffers (mScales / vScales None with 32-bit
+    states, masters None without master copies) and of their sizes, or what
+    pointer_array and size_array made of them; control may be None."""
+    _check(_L().vr_adamw(_ptrs(params), _ptrs(grads), _ptrs(m), _ptrs(v), _ptrs(mScales),
+                         _ptrs(vScales), _ptrs(masters), size_array(sizes), count, dtype, gradDtype,
+                         stateBits, lr, beta1, beta2, eps, weightDecay, step, gradScale, seed,
+                         _ptr(control), _stream(stream)), "vr_adamw")
+
+
+def vr_adamw_values(m, v, mScales, vScales, sizes, count, mValues, vValues, stream=None):
+    """m, mScales, mValues or v, vScales, vValues may be None."""
+    _check(_L().vr_adamw_values(_ptrs(m), _ptrs(v), _ptrs(mScales), _ptrs(vScales),
+                                size_array(sizes), count, _ptrs(mValues), _ptrs(vValues),
+                                _stream(stream)), "vr_adamw_values")
 
 
 # ------------------------------------------------------------- cost model

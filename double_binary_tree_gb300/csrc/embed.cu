@@ -1,0 +1,701 @@
+// Embedding lookup with scaling (vr_embedding) and the gradient of the table
+// (vr_embedding_grad).
+//
+//   out_t = scale w[id_t];  dw_v (+)= scale sum_{t: id_t = v} dout_t
+//
+// The lookup is a gather: a warp takes a piece of a token's row.
+//
+// The gradient sorts the tokens by word, stably, by the words' digits from the
+// lowest up (each pass counts the digits of every warp's run of tokens, adds
+// the counts up and moves the tokens), so that a word's rows are summed in
+// token order: the same bits on every run, without atomic additions.  Up to
+// kSmallSort tokens are sorted by one CTA in shared memory; more take two
+// launches a pass.  The sorted tokens are cut into chunks; a warp sums a slice
+// of the columns of a chunk in fp32 and writes each word's row that lies in the
+// chunk as a whole; a word that goes on over the chunk's end leaves a partial
+// sum, and a last launch adds the partial sums up in chunk order.  Rows of
+// words that do not occur are zeroed by the same launch as the sums: a lane
+// looks up its word among the sorted ones.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "common.h"
+#include "fold.cuh"
+#include "gemm_host.h"
+
+namespace vr {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// `N` consecutive elements of a row as one access, or one element.
+template <typename T, int N>
+struct Pack {
+  using Bits = typename Ty<T>::Bits;
+  using Raw = typename Select<
+      N * sizeof(Bits) == 16, uint4,
+      typename Select<N * sizeof(Bits) == 4, uint32_t, Bits>::type>::type;
+  static __device__ __forceinline__ void widen(const Raw& r, float (&x)[N]) {
+    const Bits* b = reinterpret_cast<const Bits*>(&r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = Ty<T>::widen(b[i]);
+  }
+  static __device__ __forceinline__ Raw narrow(const float (&x)[N]) {
+    Raw r;
+    Bits* b = reinterpret_cast<Bits*>(&r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = Ty<T>::narrow(x[i]);
+    return r;
+  }
+};
+
+// ---------------------------------------------------------------- lookup
+struct LookupArgs {
+  const void* weight;
+  const long long* ids;
+  void* out;
+  long long weightStride, outStride, units, ignore;
+  int dim, vocab, slices;  // slices of kLookupLoads accesses a lane
+  float scale;
+  unsigned* status;
+};
+constexpr int kLookupLoads = 4;
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) embed_lookup_kernel(
+    const __grid_constant__ LookupArgs a) {
+  using Raw = typename Pack<T, N>::Raw;
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32;
+  const long long step = (long long)gridDim.x * kWarps;
+  for (long long u = (long long)blockIdx.x * kWarps + threadIdx.x / 32; u < a.units; u += step) {
+    const long long t = u / a.slices;
+    const int slice = (int)(u - t * a.slices);
+    const long long id = a.ids[t];
+    const bool there = id >= 0 && id < a.vocab && id != a.ignore;
+    if (!there && id != a.ignore && lane == 0 && slice == 0)
+      atomicCAS(a.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
+    const T* in = static_cast<const T*>(a.weight) + (there ? id : 0) * a.weightStride;
+    T* out = static_cast<T*>(a.out) + t * a.outStride;
+    const int c0 = (slice * kLookupLoads * 32 + lane) * N;
+    Raw r[kLookupLoads];
+#pragma unroll
+    for (int i = 0; i < kLookupLoads; ++i) {
+      const int c = c0 + i * 32 * N;
+      if (there && c < a.dim) r[i] = *reinterpret_cast<const Raw*>(in + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kLookupLoads; ++i) {
+      const int c = c0 + i * 32 * N;
+      if (c >= a.dim) break;
+      float x[N];
+      if (there) Pack<T, N>::widen(r[i], x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = there ? x[j] * a.scale : 0.0f;
+      *reinterpret_cast<Raw*>(out + c) = Pack<T, N>::narrow(x);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sorting
+// An item is a word and the token that has it; a token that does not count has
+// the word `vocab`, behind all others.
+using Item = unsigned long long;
+__device__ __forceinline__ unsigned word_of(Item x) { return (unsigned)(x >> 32); }
+__device__ __forceinline__ unsigned token_of(Item x) { return (unsigned)x; }
+
+constexpr int kMaxBits = 9, kDigits = 1 << kMaxBits;  // of one pass
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSmallSort = 8192;
+
+struct SortArgs {
+  const long long* ids;
+  long long ignore;
+  int tokens, vocab;
+  int passes, bits;   // of each pass
+  int shift;          // this pass's lowest bit (large)
+  int ctas, run;      // large: CTAs, and tokens of each
+  const Item* in;     // large: null in the first pass
+  Item* out;
+  int* counts;        // large: [ctas][kDigits]
+  unsigned* status;
+};
+
+__device__ __forceinline__ Item item_of(const SortArgs& a, int t) {
+  const long long id = a.ids[t];
+  const bool there = id >= 0 && id < a.vocab && id != a.ignore;
+  if (!there && id != a.ignore) atomicCAS(a.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
+  return (Item)(unsigned)(there ? (int)id : a.vocab) << 32 | (unsigned)t;
+}
+
+// Counts the digits of a warp's run [lo, hi) of items into its row of counters,
+// or (MOVE) sends each to the place that its digit's counter gives.  Equal
+// digits of 32 items take consecutive places, so the order is kept.
+template <bool MOVE, class Get, class Put>
+__device__ __forceinline__ void digits_of_run(unsigned* row, int lo, int hi, int shift,
+                                              unsigned mask, Get get, Put put) {
+  const int lane = threadIdx.x % 32;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const bool live = i0 + lane < hi;
+    const Item x = live ? get(i0 + lane) : 0;
+    const unsigned d = live ? word_of(x) >> shift & mask : kDigits;
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int first = __ffs(same) - 1;
+    unsigned base = 0;
+    if (live && lane == first) {
+      base = row[d];
+      row[d] = base + __popc(same);
+    }
+    if (MOVE) {
+      base = __shfl_sync(0xffffffffu, base, first);
+      if (live) put(base + __popc(same & ((1u << lane) - 1)), x);
+    }
+    __syncwarp();
+  }
+}
+
+// The counters of the warps made into places: of each digit, the items of lower
+// digits and of its earlier warps before it.  `base(d, n)` adds what lies
+// before this CTA's n items of the digit, as a whole sum over lower digits
+// (the CTAs' totals) and earlier CTAs.
+template <class Base>
+__device__ __forceinline__ void places(unsigned (*rows)[kDigits], unsigned* sScan, Base base) {
+  const int d = threadIdx.x;
+  unsigned total = 0;
+  if (d < kDigits) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const unsigned n = rows[w][d];
+      rows[w][d] = total;
+      total += n;
+    }
+  }
+  // exclusive sum over the digits of all items that have them
+  unsigned all = total, before = 0;
+  if (d < kDigits) base(d, &all, &before);
+  unsigned sum = all;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const unsigned up = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += up;
+  }
+  if (lane == 31) sScan[warp] = d < kDigits ? sum : 0;
+  __syncthreads();
+  if (d < kDigits) {
+    unsigned start = sum - all + before;
+    for (int w = 0; w < warp; ++w) start += sScan[w];
+    for (int w = 0; w < kSortWarps; ++w) rows[w][d] += start;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void clear(unsigned (*rows)[kDigits]) {
+  unsigned* p = &rows[0][0];
+  for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) p[i] = 0;
+  __syncthreads();
+}
+
+// Up to kSmallSort tokens by one CTA: all passes in shared memory.
+constexpr size_t kSmallSmem = 2 * kSmallSort * sizeof(Item) + kSortWarps * kDigits * 4;
+__global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(
+    const __grid_constant__ SortArgs a) {
+  extern __shared__ Item smem[];
+  __shared__ unsigned sScan[kSortWarps];
+  Item *from = smem, *to = smem + kSmallSort;
+  unsigned(*rows)[kDigits] = reinterpret_cast<unsigned(*)[kDigits]>(smem + 2 * kSmallSort);
+  pdl_launch();
+  pdl_wait();
+  for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) from[t] = item_of(a, t);
+  const int warp = threadIdx.x / 32;
+  const int run = (a.tokens + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
+  const int lo = min(warp * run, a.tokens), hi = min(lo + run, a.tokens);
+  for (int p = 0; p < a.passes; ++p) {
+    clear(rows);
+    const int shift = p * a.bits;
+    const unsigned mask = (1u << a.bits) - 1;
+    auto get = [&](int i) { return from[i]; };
+    digits_of_run<false>(rows[warp], lo, hi, shift, mask, get, [](unsigned, Item) {});
+    __syncthreads();
+    places(rows, sScan, [](int, unsigned*, unsigned*) {});
+    if (p + 1 == a.passes) {
+      digits_of_run<true>(rows[warp], lo, hi, shift, mask, get,
+                          [&](unsigned at, Item x) { a.out[at] = x; });
+    } else {
+      digits_of_run<true>(rows[warp], lo, hi, shift, mask, get,
+                          [&](unsigned at, Item x) { to[at] = x; });
+    }
+    __syncthreads();
+    Item* t = from;
+    from = to;
+    to = t;
+  }
+}
+
+// One pass over many tokens: a launch that counts every CTA's digits, one that
+// moves the items.
+template <bool MOVE>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
+    const __grid_constant__ SortArgs a) {
+  extern __shared__ Item smem[];
+  __shared__ unsigned sScan[kSortWarps];
+  unsigned(*rows)[kDigits] = reinterpret_cast<unsigned(*)[kDigits]>(smem);
+  pdl_launch();
+  clear(rows);
+  pdl_wait();
+  const int warp = threadIdx.x / 32;
+  const int begin = (int)min((long long)blockIdx.x * a.run, (long long)a.tokens);
+  const int n = min(a.run, a.tokens - begin);
+  const int run = (n + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
+  const int lo = begin + min(warp * run, n), hi = min(lo + run, begin + n);
+  const unsigned mask = (1u << a.bits) - 1;
+  auto get = [&](int i) { return a.in ? a.in[i] : item_of(a, i); };
+  digits_of_run<false>(rows[warp], lo, hi, a.shift, mask, get, [](unsigned, Item) {});
+  __syncthreads();
+  if (!MOVE) {
+    if (threadIdx.x < kDigits) {
+      unsigned total = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) total += rows[w][threadIdx.x];
+      a.counts[blockIdx.x * kDigits + threadIdx.x] = (int)total;
+    }
+    return;
+  }
+  places(rows, sScan, [&](int d, unsigned* all, unsigned* before) {
+    unsigned sum = 0, mine = 0;
+#pragma unroll 16
+    for (int c = 0; c < a.ctas; ++c) {
+      const unsigned k = (unsigned)a.counts[c * kDigits + d];
+      sum += k;
+      mine += c < (int)blockIdx.x ? k : 0;
+    }
+    *all = sum;
+    *before = mine;
+  });
+  digits_of_run<true>(rows[warp], lo, hi, a.shift, mask, get,
+                      [&](unsigned at, Item x) { a.out[at] = x; });
+}
+
+// --------------------------------------------------------------------- sums
+struct SumArgs {
+  const void* dout;
+  void* dweight;
+  const Item* items;
+  float* parts;      // [chunks][2][dim]: of the word that a chunk begins and ends with
+  long long stride;  // of dout
+  long long fillUnits, units;
+  int tokens, dim, vocab, add;
+  int chunk, chunks, slices;
+  float scale;
+};
+constexpr int kFillRows = 8;  // rows of the table that a warp zeroes at a time
+
+// A slice of a row: REP accesses of N elements a lane.
+template <typename T, int N, int REP>
+struct Slice {
+  using Raw = typename Pack<T, N>::Raw;
+  static constexpr int kCols = 32 * N * REP;
+  static __device__ __forceinline__ int col(int slice, int i) {
+    return slice * kCols + (i * 32 + (int)threadIdx.x % 32) * N;
+  }
+  // the final row of a word: scaled, added to what is there, rounded once
+  static __device__ __forceinline__ void write(const SumArgs& a, unsigned word, int slice,
+                                               const float (&sum)[REP][N]) {
+    T* out = static_cast<T*>(a.dweight) + (long long)word * a.dim;
+    Raw old[REP];
+    if (a.add) {
+#pragma unroll
+      for (int i = 0; i < REP; ++i)
+        if (col(slice, i) < a.dim) old[i] = *reinterpret_cast<const Raw*>(out + col(slice, i));
+    }
+#pragma unroll
+    for (int i = 0; i < REP; ++i) {
+      if (col(slice, i) >= a.dim) break;
+      float x[N];
+      if (a.add) Pack<T, N>::widen(old[i], x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = fmaf(sum[i][j], a.scale, a.add ? x[j] : 0.0f);
+      *reinterpret_cast<Raw*>(out + col(slice, i)) = Pack<T, N>::narrow(x);
+    }
+  }
+  static __device__ __forceinline__ float* part(const SumArgs& a, int chunk, int end) {
+    return a.parts + ((long long)chunk * 2 + end) * a.dim;
+  }
+  static __device__ __forceinline__ void store_part(const SumArgs& a, int chunk, int end,
+                                                    int slice, const float (&sum)[REP][N]) {
+    float* p = part(a, chunk, end);
+#pragma unroll
+    for (int i = 0; i < REP; ++i) {
+      if (col(slice, i) >= a.dim) break;
+#pragma unroll
+      for (int j = 0; j < N; ++j) p[col(slice, i) + j] = sum[i][j];
+    }
+  }
+};
+
+// Whether `word` occurs among the sorted items.
+__device__ __forceinline__ bool occurs(const SumArgs& a, unsigned word) {
+  int lo = 0, hi = a.tokens;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (word_of(a.items[mid]) < word) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo < a.tokens && word_of(a.items[lo]) == word;
+}
+
+template <typename T, int N, int REP>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ SumArgs a) {
+  using S = Slice<T, N, REP>;
+  using Raw = typename S::Raw;
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x % 32;
+  const long long step = (long long)gridDim.x * kWarps;
+  for (long long u = (long long)blockIdx.x * kWarps + threadIdx.x / 32; u < a.units; u += step) {
+    if (u < a.fillUnits) {  // rows of words that do not occur
+      const long long v = u * kFillRows + lane;
+      const bool zero = lane < kFillRows && v < a.vocab && !occurs(a, (unsigned)v);
+      unsigned rows = __ballot_sync(0xffffffffu, zero);
+      Raw none = {};
+      while (rows) {
+        T* out = static_cast<T*>(a.dweight) + (u * kFillRows + __ffs(rows) - 1) * a.dim;
+        rows &= rows - 1;
+#pragma unroll 4
+        for (int c = lane * N; c < a.dim; c += 32 * N) *reinterpret_cast<Raw*>(out + c) = none;
+      }
+      continue;
+    }
+    const long long at = u - a.fillUnits;
+    const int chunk = (int)(at / a.slices), slice = (int)(at - (long long)chunk * a.slices);
+    const int lo = chunk * a.chunk, hi = min(lo + a.chunk, a.tokens);
+    unsigned word = word_of(a.items[lo]);
+    if (word >= (unsigned)a.vocab) continue;  // tokens that do not count are last
+    bool head = lo > 0 && word_of(a.items[lo - 1]) == word;  // goes on from the last chunk
+    float sum[REP][N] = {};
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const Item mine = i0 + lane < hi ? a.items[i0 + lane] : (Item)~0u << 32;
+      const int n = min(32, hi - i0);
+      constexpr int kAhead = 8 / REP;
+      for (int j0 = 0; j0 < n; j0 += kAhead) {
+        Raw r[kAhead][REP];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const Item x = __shfl_sync(0xffffffffu, mine, (j0 + k) & 31);
+          if (j0 + k >= n || word_of(x) >= (unsigned)a.vocab) continue;
+          const T* in = static_cast<const T*>(a.dout) + (long long)token_of(x) * a.stride;
+#pragma unroll
+          for (int i = 0; i < REP; ++i)
+            if (S::col(slice, i) < a.dim)
+              r[k][i] = *reinterpret_cast<const Raw*>(in + S::col(slice, i));
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const unsigned w = word_of(__shfl_sync(0xffffffffu, mine, (j0 + k) & 31));
+          if (j0 + k >= n) continue;
+          if (w != word) {
+            if (word < (unsigned)a.vocab) {
+              if (head) S::store_part(a, chunk, 0, slice, sum);
+              else S::write(a, word, slice, sum);
+            }
+            head = false;
+            word = w;
+#pragma unroll
+            for (int i = 0; i < REP; ++i)
+#pragma unroll
+              for (int j = 0; j < N; ++j) sum[i][j] = 0.0f;
+          }
+          if (w >= (unsigned)a.vocab) continue;
+#pragma unroll
+          for (int i = 0; i < REP; ++i) {
+            float x[N];
+            Pack<T, N>::widen(r[k][i], x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum[i][j] += x[j];
+          }
+        }
+      }
+    }
+    if (word >= (unsigned)a.vocab) continue;
+    const bool tail = hi < a.tokens && word_of(a.items[hi]) == word;
+    if (head) S::store_part(a, chunk, 0, slice, sum);
+    else if (tail) S::store_part(a, chunk, 1, slice, sum);
+    else S::write(a, word, slice, sum);
+  }
+}
+
+// The words that go on over a chunk's end: a warp adds the partial sums of a
+// slice of one up, in chunk order.
+template <typename T, int N, int REP>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ SumArgs a) {
+  using S = Slice<T, N, REP>;
+  pdl_launch();
+  pdl_wait();
+  const long long step = (long long)gridDim.x * kWarps;
+  const long long units = (long long)(a.chunks - 1) * a.slices;
+  for (long long u = (long long)blockIdx.x * kWarps + threadIdx.x / 32; u < units; u += step) {
+    const int chunk = (int)(u / a.slices), slice = (int)(u - (long long)chunk * a.slices);
+    const int lo = chunk * a.chunk, hi = lo + a.chunk;  // not the last chunk
+    const unsigned word = word_of(a.items[hi - 1]);
+    if (word >= (unsigned)a.vocab || word_of(a.items[hi]) != word) continue;
+    // it begins in this chunk
+    if (lo > 0 && word_of(a.items[lo]) == word && word_of(a.items[lo - 1]) == word) continue;
+    int from = hi + 1, to = a.tokens;  // the first item behind it
+    while (from < to) {
+      const int mid = (from + to) / 2;
+      if (word_of(a.items[mid]) == word) from = mid + 1;
+      else to = mid;
+    }
+    const int last = (from - 1) / a.chunk;
+    float sum[REP][N] = {};
+    auto add = [&](const float* p) {
+#pragma unroll
+      for (int i = 0; i < REP; ++i)
+        if (S::col(slice, i) < a.dim) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) sum[i][j] += p[S::col(slice, i) + j];
+        }
+    };
+    add(S::part(a, chunk, 1));
+#pragma unroll 4
+    for (int k = chunk + 1; k <= last; ++k) add(S::part(a, k, 0));
+    S::write(a, word, slice, sum);
+  }
+}
+
+// ------------------------------------------------------------- host side
+constexpr size_t kMostTokens = (size_t)1 << 30, kMostVocab = (size_t)1 << 30,
+                 kMostDim = (size_t)1 << 24, kMostStride = (size_t)1 << 31;
+constexpr int kMostCtas = 152;
+constexpr size_t kSortRun = 2048;  // the fewest tokens that a CTA of a large sort takes
+
+// The sorted tokens are cut into chunks of 32 or more, fewer than 4096.
+size_t chunk_of(size_t tokens) {
+  size_t c = 32;
+  while (tokens / c > 4096) c *= 2;
+  return c;
+}
+
+struct EmbedPlan {
+  bool small;
+  size_t run, ctas, chunk, chunks;
+  size_t items, other, counts, parts, bytes;  // offsets into the workspace
+};
+bool make_plan(size_t tokens, size_t dim, size_t vocab, int dtype, EmbedPlan* p) {
+  if (!op_elem_size(dtype) || tokens > kMostTokens || dim < 1 || dim > kMostDim || vocab < 1 ||
+      vocab > kMostVocab)
+    return false;
+  *p = EmbedPlan{};
+  p->small = tokens <= (size_t)kSmallSort;
+  p->run = std::max(kSortRun, (tokens + kMostCtas - 1) / kMostCtas);
+  p->ctas = (tokens + p->run - 1) / p->run;
+  p->chunk = chunk_of(tokens);
+  p->chunks = (tokens + p->chunk - 1) / p->chunk;
+  size_t at = 0;
+  auto take = [&at](size_t n) {
+    const size_t here = at;
+    at += op_round(n);
+    return here;
+  };
+  p->items = take(tokens * sizeof(Item));
+  p->other = p->small ? 0 : take(tokens * sizeof(Item));
+  p->counts = p->small ? 0 : take(p->ctas * kDigits * 4);
+  p->parts = take(p->chunks * 2 * dim * 4);
+  p->bytes = at + kOpSlack;
+  return true;
+}
+
+// The widest access that all rows allow: 16 bytes, 4 or one element.
+int access_bytes(uintptr_t bits, size_t elem) {
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : (int)elem;
+}
+
+template <typename T, int N, int REP>
+vr_result_t launch_sums(const EmbedPlan& p, const OpDevice& dev, SumArgs& a, void* stream) {
+  a.slices = (a.dim + Slice<T, N, REP>::kCols - 1) / Slice<T, N, REP>::kCols;
+  a.fillUnits = a.add ? 0 : ((long long)a.vocab + kFillRows - 1) / kFillRows;
+  a.units = a.fillUnits + (long long)p.chunks * a.slices;
+  void* args[] = {&a};
+  auto grid = [&](long long units) {
+    return dim3((unsigned)std::min<long long>((units + kWarps - 1) / kWarps, dev.sms * 8LL));
+  };
+  vr_result_t e = op_launch((const void*)embed_sum_kernel<T, N, REP>, grid(a.units),
+                            dim3(kThreads), args, 0, stream);
+  if (e != VR_SUCCESS || p.chunks < 2) return e;
+  return op_launch((const void*)embed_join_kernel<T, N, REP>,
+                   grid((long long)(p.chunks - 1) * a.slices), dim3(kThreads), args, 0, stream);
+}
+
+template <typename T>
+vr_result_t sums(const EmbedPlan& p, const OpDevice& dev, SumArgs& a, int access, void* stream) {
+  constexpr int kElem = (int)sizeof(T), kWide = 16 / kElem;
+  if (access == 16) return launch_sums<T, kWide, 8 / kWide>(p, dev, a, stream);
+  if constexpr (kElem == 2)
+    if (access == 4) return launch_sums<T, 2, 4>(p, dev, a, stream);
+  return launch_sums<T, 1, 4>(p, dev, a, stream);
+}
+
+template <typename T>
+const void* lookup(int access, int* n) {
+  constexpr int kElem = (int)sizeof(T);
+  *n = access / kElem;
+  if (access == 16) return (const void*)embed_lookup_kernel<T, 16 / kElem>;
+  if constexpr (kElem == 2)
+    if (access == 4) return (const void*)embed_lookup_kernel<T, 2>;
+  return (const void*)embed_lookup_kernel<T, 1>;
+}
+
+}  // namespace
+}  // namespace vr
+
+using namespace vr;
+
+extern "C" {
+
+vr_result_t vr_embedding(const void* weight, size_t weightStride, const long long* ids,
+                         size_t tokens, size_t dim, size_t vocab, vr_dtype_t dtype,
+                         long long ignoreIndex, float scale, void* out, size_t outStride,
+                         void* stream) {
+  const size_t E = op_elem_size(dtype);
+  EmbedPlan p;
+  if (!make_plan(tokens, dim, vocab, dtype, &p) || weightStride < dim || outStride < dim ||
+      weightStride > kMostStride || outStride > kMostStride || !weight ||
+      (tokens && (!ids || !out)) || ((uintptr_t)ids & 7) ||
+      ((uintptr_t)weight | (uintptr_t)out) % E)
+    return VR_ERR_INVALID_ARGUMENT;
+  // (an output listed before the inputs may be none of them)
+  const OpBuffer buf[3] = {{out, tokens, dim * E, outStride * E, true},
+                           {weight, vocab, dim * E, weightStride * E, false},
+                           {ids, 1, tokens * 8, tokens * 8, false}};
+  if (!op_buffers_ok(buf, 3)) return VR_ERR_INVALID_ARGUMENT;
+  if (!tokens) return VR_SUCCESS;
+  OpDevice dev;
+  vr_result_t e = op_device(&dev);
+  if (e != VR_SUCCESS || (e = op_reachable(buf, 3, dev.device)) != VR_SUCCESS) return e;
+  const int access = access_bytes((uintptr_t)weight | (uintptr_t)out | (uintptr_t)(dim * E) |
+                                      (uintptr_t)(weightStride * E) | (uintptr_t)(outStride * E),
+                                  E);
+  int n = 0;
+  const void* fn = dtype == VR_FLOAT32   ? lookup<float>(access, &n)
+                   : dtype == VR_FLOAT16 ? lookup<__half>(access, &n)
+                                         : lookup<__nv_bfloat16>(access, &n);
+  LookupArgs a = {};
+  a.weight = weight;
+  a.ids = ids;
+  a.out = out;
+  a.weightStride = (long long)weightStride;
+  a.outStride = (long long)outStride;
+  a.ignore = ignoreIndex;
+  a.dim = (int)dim;
+  a.vocab = (int)vocab;
+  a.slices = (int)((dim + kLookupLoads * 32 * n - 1) / (kLookupLoads * 32 * n));
+  a.units = (long long)tokens * a.slices;
+  a.scale = scale;
+  a.status = dev.status;
+  void* args[] = {&a};
+  return op_launch(fn,
+                   dim3((unsigned)std::min<long long>((a.units + kWarps - 1) / kWarps,
+                                                      dev.sms * 8LL)),
+                   dim3(kThreads), args, 0, stream);
+}
+
+vr_result_t vr_embedding_grad_workspace_bytes(size_t tokens, size_t dim, size_t vocab,
+                                              vr_dtype_t dtype, size_t* bytes) {
+  EmbedPlan p;
+  if (!bytes || !make_plan(tokens, dim, vocab, dtype, &p)) return VR_ERR_INVALID_ARGUMENT;
+  *bytes = p.bytes;
+  return VR_SUCCESS;
+}
+
+vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long long* ids,
+                              size_t tokens, size_t dim, size_t vocab, vr_dtype_t dtype,
+                              long long ignoreIndex, float scale, int accumulate, void* dWeight,
+                              void* workspace, size_t workspaceBytes, void* stream) {
+  const size_t E = op_elem_size(dtype);
+  EmbedPlan p;
+  if (!make_plan(tokens, dim, vocab, dtype, &p) || dOutStride < dim || dOutStride > kMostStride ||
+      !dWeight || !workspace || (tokens && (!ids || !dOut)) || ((uintptr_t)ids & 7) ||
+      ((uintptr_t)dOut | (uintptr_t)dWeight) % E || ((uintptr_t)workspace & 15) ||
+      workspaceBytes < p.bytes)
+    return VR_ERR_INVALID_ARGUMENT;
+  const OpBuffer buf[4] = {{workspace, 1, workspaceBytes, workspaceBytes, true},
+                           {dWeight, 1, vocab * dim * E, vocab * dim * E, true},
+                           {dOut, tokens, dim * E, dOutStride * E, false},
+                           {ids, 1, tokens * 8, tokens * 8, false}};
+  if (!op_buffers_ok(buf, 4)) return VR_ERR_INVALID_ARGUMENT;
+  OpDevice dev;
+  vr_result_t e = op_device(&dev);
+  if (e != VR_SUCCESS || (e = op_reachable(buf, 4, dev.device)) != VR_SUCCESS) return e;
+  if (!tokens) {
+    if (accumulate) return VR_SUCCESS;
+    return cudaMemsetAsync(dWeight, 0, vocab * dim * E, (cudaStream_t)stream) == cudaSuccess
+               ? VR_SUCCESS
+               : VR_ERR_CUDA;
+  }
+  char* w = op_workspace(workspace);
+  SortArgs s = {};
+  s.ids = ids;
+  s.ignore = ignoreIndex;
+  s.tokens = (int)tokens;
+  s.vocab = (int)vocab;
+  s.status = dev.status;
+  int bits = 1;  // of the words 0 .. vocab
+  while (vocab >> bits) ++bits;
+  s.passes = (bits + kMaxBits - 1) / kMaxBits;
+  s.bits = (bits + s.passes - 1) / s.passes;
+  Item* items = reinterpret_cast<Item*>(w + p.items);
+  if (p.small) {
+    s.out = items;
+    void* args[] = {&s};
+    const void* fn = (const void*)embed_sort_small_kernel;
+    if ((e = gemm_prepare(fn, dev.device, kSmallSmem)) != VR_SUCCESS ||
+        (e = op_launch(fn, dim3(1), dim3(kSortThreads), args, kSmallSmem, stream)) != VR_SUCCESS)
+      return e;
+  } else {
+    Item* other = reinterpret_cast<Item*>(w + p.other);
+    constexpr size_t kSmem = (size_t)kSortWarps * kDigits * 4;
+    const void *count = (const void*)embed_sort_kernel<false>,
+               *move = (const void*)embed_sort_kernel<true>;
+    if ((e = gemm_prepare(count, dev.device, kSmem)) != VR_SUCCESS ||
+        (e = gemm_prepare(move, dev.device, kSmem)) != VR_SUCCESS)
+      return e;
+    s.counts = reinterpret_cast<int*>(w + p.counts);
+    s.ctas = (int)p.ctas;
+    s.run = (int)p.run;
+    for (int i = 0; i < s.passes; ++i) {
+      s.shift = i * s.bits;
+      // the last pass ends in `items`
+      s.out = (s.passes - 1 - i) % 2 ? other : items;
+      void* args[] = {&s};
+      if ((e = op_launch(count, dim3((unsigned)p.ctas), dim3(kSortThreads), args, kSmem,
+                         stream)) != VR_SUCCESS ||
+          (e = op_launch(move, dim3((unsigned)p.ctas), dim3(kSortThreads), args, kSmem,
+                         stream)) != VR_SUCCESS)
+        return e;
+      s.in = s.out;
+    }
+  }
+  SumArgs a = {};
+  a.dout = dOut;
+  a.dweight = dWeight;
+  a.items = items;
+  a.parts = reinterpret_cast<float*>(w + p.parts);
+  a.stride = (long long)dOutStride;
+  a.tokens = (int)tokens;
+  a.dim = (int)dim;
+  a.vocab = (int)vocab;
+  a.add = accumulate != 0;
+  a.chunk = (int)p.chunk;
+  a.chunks = (int)p.chunks;
+  a.scale = scale;
+  const int access = access_bytes((uintptr_t)dOut | (uintptr_t)dWeight | (uintptr_t)(dim * E) |
+                                      (uintptr_t)(dOutStride * E),
+                                  E);
+  return dtype == VR_FLOAT32   ? sums<float>(p, dev, a, access, stream)
+         : dtype == VR_FLOAT16 ? sums<__half>(p, dev, a, access, stream)
+                               : sums<__nv_bfloat16>(p, dev, a, access, stream);
+}
+
+}  // extern "C"

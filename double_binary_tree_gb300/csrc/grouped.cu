@@ -1,0 +1,701 @@
+// Matrix products grouped by expert (vr_grouped_linear) and their gradients
+// (vr_grouped_linear_grad).
+//
+//   y_r = W_e(r) x_r;   dx_r = W_e(r)^T dy_r;   dW_e = sum_{r: e(r) = e} dy_r x_r^T
+//
+// Rows are sorted by group; how many each group has is known on the device
+// only.  One launch takes the tiles of all groups: every CTA adds the counts up
+// for itself (a few microseconds less than a launch that writes a table) and
+// walks the tiles with the grid's stride, the roles of its warps those of the
+// products of gemm.cuh: tensor copies, tcgen05 products, epilogue.
+//
+//   rows    tiles of a group's rows by 256 output columns.  A tile reads on
+//           into the next group's rows, whose results are not stored.
+//   few     few rows a group: the weights take the place of the rows, 128 of
+//           their rows to a tile, and up to 32 rows of the group that of the
+//           columns, so that a tile is what has to be read of the weights.
+//   weight  dW: a sum over the group's rows.  The last slice of 64 reads on
+//           into the next group; the rows behind the end, up to the next
+//           multiple of the 16 that a product takes, are zeroed in shared memory
+//           (in both operands: they may hold NaN).
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "rows.cuh"
+
+namespace vr {
+namespace {
+
+constexpr int kMostGroups = 1024;
+constexpr int kGroupedSmem = 212 * 1024;  // the stages; the tables of the groups are beside them
+
+enum Kind : int { kLinear, kGradRows, kGradWeight, kFewLinear, kFewGradRows };
+template <int KIND>
+struct KindOf {
+  static constexpr bool kFew = KIND == kFewLinear || KIND == kFewGradRows;
+  static constexpr bool kWeight = KIND == kGradWeight;
+  static constexpr bool kRows = !kFew && !kWeight;
+  // operands whose rows are the summed dimension
+  static constexpr bool kAMn = kWeight || KIND == kFewGradRows;
+  static constexpr bool kBMn = kWeight || KIND == kGradRows;
+};
+
+struct GroupedArgs {
+  CUtensorMap a, b;
+  const int* counts;
+  int groups, rows;  // rows: that the buffers have
+  int M, N, K;       // of the product; the one that is counted on the device is not used
+  void* out;
+  long long ld;      // elements between its rows
+  int align;
+  unsigned* status;
+  unsigned long long timeoutNs;
+};
+
+template <int BN, bool PAIR>
+struct GroupedShape {
+  static constexpr int kABytes = kTileM * kTileK * 2;
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;
+  static constexpr int kBBytes = kBRows * kTileK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kTileRows = PAIR ? 2 * kTileM : kTileM;
+  static constexpr int kStages = kGroupedSmem / kStageBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes;
+  static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kWarps = BN >= 128 ? 16 : 4;  // of the epilogue
+};
+
+// A tile: its group, its place in the product, the group's rows [lo, hi).
+struct GroupTile {
+  int g, m0, n0, lo, hi;
+};
+
+template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
+__global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
+    grouped_kernel(const __grid_constant__ GroupedArgs g) {
+  using Shape = GroupedShape<BN, PAIR>;
+  using Is = KindOf<KIND>;
+  constexpr bool AMN = Is::kAMn, BMN = Is::kBMn;
+  constexpr int kStages = Shape::kStages, kCtas = PAIR ? 2 : 1, kRows = Shape::kTileRows;
+  constexpr int kEpilogueWarps = Shape::kWarps, kGroups = kEpilogueWarps / 4, kPart = BN / kGroups;
+  static_assert(!(PAIR && Is::kWeight), "the end of a group is zeroed by one CTA for itself");
+  extern __shared__ unsigned char smemRaw[];
+  __shared__ alignas(8) uint64_t bars[2 * kStages + 2 * 2 + 1];
+  __shared__ uint32_t tmemBase;
+  __shared__ volatile int abortFlag;
+  __shared__ int rowStart[kMostGroups + 1], tileStart[kMostGroups + 1];
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const bool leader = rank == 0;
+  const uint16_t pairMask = 3;
+  const uint32_t stage0 = (smem_addr(smemRaw) + 1023) & ~1023u;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+  auto accFull = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
+  auto accEmpty = [&](int i) { return bar0 + 8u * (2 * kStages + 2 + i); };
+  const uint32_t drained = bar0 + 8u * (2 * kStages + 4);
+  auto wait = [&](uint32_t bar, unsigned parity, bool honorAbort = true) {
+    return wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
+  };
+  auto all_wait = [&](uint32_t bar, unsigned parity) {
+    const bool mine = wait(bar, parity);
+    return __all_sync(0xffffffffu, mine) != 0;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(accFull(i), 1);
+      mbar_init(accEmpty(i), kEpilogueWarps * kCtas);
+    }
+    mbar_init(drained, 1);
+    abortFlag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async;" ::: "memory");
+  }
+  if (warp == 1 && elected()) {
+    prefetch_map(&g.a);
+    prefetch_map(&g.b);
+  }
+  if (warp == 2) {
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmemBase)),
+                   "r"(Shape::kTmem)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmemBase)),
+                   "r"(Shape::kTmem)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+  }
+  pdl_launch();
+  pdl_wait();
+  const int tilesN = (g.N + BN - 1) / BN, tilesM = (g.M + kRows - 1) / kRows;
+  if (warp == 3) {  // the groups' rows and tiles
+    int rows = 0, tiles = 0;
+#pragma unroll 4
+    for (int e0 = 0; e0 < g.groups; e0 += 32) {
+      const int e = e0 + lane;
+      const int given = e < g.groups ? g.counts[e] : 0;
+      // sums of what is given, held to the buffers' rows: what a bad count
+      // reaches is reported, not read or written
+      long long end = max(given, 0);
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const long long up = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += up;
+      }
+      end += rows;
+      if (given < 0 || end > g.rows) atomicCAS(g.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
+      const int hi = (int)min(end, (long long)g.rows);
+      const int lo = max(__shfl_up_sync(0xffffffffu, hi, 1), lane ? 0 : rows);
+      const int from = lane ? lo : rows, n = hi - from;
+      int mine = 0;
+      if (e < g.groups)
+        mine = Is::kWeight ? tilesM * tilesN
+                           : Is::kRows ? (n + kRows - 1) / kRows * tilesN
+                                       : (n + BN - 1) / BN * tilesM;
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (e < g.groups) {
+        rowStart[e + 1] = hi;
+        tileStart[e + 1] = tiles + sum;
+      }
+      rows = __shfl_sync(0xffffffffu, hi, 31);
+      tiles += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) rowStart[0] = tileStart[0] = 0;
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers are set up
+  tmem_fence_after();
+  const uint32_t tmem = tmemBase;
+  const int tiles = tileStart[g.groups];
+  const int firstTile = (int)blockIdx.x / kCtas, tileStep = (int)gridDim.x / kCtas;
+  // Tiles are walked upwards: `e` is the group of the last one.
+  auto tile_at = [&](int t, int& e) {
+    while (t >= tileStart[e + 1]) ++e;
+    GroupTile o = {e, 0, 0, rowStart[e], rowStart[e + 1]};
+    t -= tileStart[e];
+    if constexpr (Is::kFew) {  // a group's rows first: its weights are in L2 by then
+      const int across = (o.hi - o.lo + BN - 1) / BN;
+      o.m0 = t / across * kRows;
+      o.n0 = o.lo + t % across * BN;
+    } else {  // 2048 rows at a time, column by column
+      const int high = Is::kWeight ? tilesM : (o.hi - o.lo + kRows - 1) / kRows;
+      constexpr int kHigh = 2048 / kRows;
+      const int block = t / (kHigh * tilesN), rows = min(kHigh, high - block * kHigh);
+      t -= block * kHigh * tilesN;
+      o.n0 = t / rows * BN;
+      o.m0 = (Is::kRows ? o.lo : 0) + (block * kHigh + t % rows) * kRows;
+    }
+    return o;
+  };
+  auto slices_of = [&](const GroupTile& o) {
+    return ((Is::kWeight ? o.hi - o.lo : g.K) + kTileK - 1) / kTileK;
+  };
+
+  if (warp == 0) {
+    int s = 0, turn = 0, e = 0;
+    bool ok = true;
+    long long issued = 0;
+    const uint32_t landed0 = PAIR ? peer_addr(full(0), 0) : full(0);
+    for (int t = firstTile; ok && t < tiles; t += tileStep) {
+      const GroupTile o = tile_at(t, e);
+      const int slices = slices_of(o);
+      const int m0 = o.m0 + (int)rank * kTileM, n0 = o.n0 + (int)rank * Shape::kBRows;
+      const int first = Is::kWeight ? o.lo : 0;
+      const int za = Is::kFew ? o.g : 0, zb = Is::kRows ? o.g : 0;
+      for (int kb = 0; kb < slices; ++kb) {
+        ok = all_wait(empty(s), turn ^ 1);
+        if (!ok) break;
+        if (elected()) {
+          if (leader) mbar_arrive_expect_tx(full(s), kCtas * Shape::kStageBytes);
+          const uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes, landed = landed0 + 8u * s;
+          const int k0 = first + kb * kTileK;
+          if constexpr (AMN) {
+#pragma unroll
+            for (int i = 0; i < kTileM / 64; ++i)
+              tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.a, m0 + i * 64, k0, za, landed);
+          } else {
+            tensor_load<PAIR>(dst, &g.a, k0, m0, za, landed);
+          }
+          if constexpr (BMN) {
+#pragma unroll
+            for (int i = 0; i < Shape::kBRows / 64; ++i)
+              tensor_load<PAIR>(dst + Shape::kABytes + i * (64 * kTileK * 2), &g.b, n0 + i * 64, k0,
+                                zb, landed);
+          } else {
+            tensor_load<PAIR>(dst + Shape::kABytes, &g.b, k0, n0, zb, landed);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == kStages) s = 0, turn ^= 1;
+      }
+    }
+    // as in gemm_kernel: no arrival of the other CTA's products after this one
+    // has left, no copy into memory that is no longer its own
+    for (long long i = issued > kStages ? issued - kStages : 0; ok && i < issued; ++i)
+      ok = all_wait(empty((int)(i % kStages)), (unsigned)(i / kStages & 1));
+    if (!ok) {
+      raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
+      if (leader)
+        for (long long i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+          wait(full((int)(i % kStages)), (unsigned)(i / kStages & 1), false);
+    }
+  } else if (warp == 1 && leader) {
+    constexpr uint32_t idesc = mma_idesc<T>(kRows, BN, AMN, BMN);
+    constexpr unsigned kSlab = 64 * kTileK * 2;
+    constexpr unsigned aStep = (AMN ? 16 * 128 : 32) >> 4, bStep = (BMN ? 16 * 128 : 32) >> 4;
+    const uint64_t aDesc0 = operand_desc(stage0, AMN ? kSlab : 16, 1024);
+    const uint64_t bDesc0 = operand_desc(stage0 + Shape::kABytes, BMN ? kSlab : 16, 1024);
+    int s = 0, turn = 0, buf = 0, bufTurn = 0, e = 0;
+    bool ok = true;
+    for (int t = firstTile; ok && t < tiles; t += tileStep) {
+      const GroupTile o = tile_at(t, e);
+      const int slices = slices_of(o), chunk = CHUNK ? CHUNK : max(slices, 1);
+      for (int c0 = 0; ok && c0 < slices; c0 += chunk) {
+        ok = all_wait(accEmpty(buf), bufTurn ^ 1);
+        if (!ok) break;
+        tmem_fence_after();
+        const uint32_t acc = tmem + (unsigned)(buf * BN);
+        const int c1 = min(c0 + chunk, slices);
+        for (int kb = c0; kb < c1; ++kb) {
+          ok = all_wait(full(s), turn);
+          if (!ok) break;
+          int steps = kTileK / 16;
+          if constexpr (Is::kWeight) {
+            const int left = o.hi - o.lo - kb * kTileK;  // rows of the group in this slice
+            if (left < kTileK) {
+              steps = (left + 15) / 16;
+              const uint32_t from = stage0 + (unsigned)s * Shape::kStageBytes;
+              const int none = (steps * 16 - left) * 8;  // 16-byte pieces of a slab
+              for (int slab = 0; slab < Shape::kStageBytes / (int)kSlab; ++slab)
+                for (int i = lane; i < none; i += 32)
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                   from + slab * kSlab + (unsigned)(left * 128 + i * 16)),
+                               "r"(0)
+                               : "memory");
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
+          }
+          tmem_fence_after();
+          if (elected()) {
+            const uint64_t at = (uint64_t)((unsigned)s * (Shape::kStageBytes >> 4));
+#pragma unroll
+            for (int k = 0; k < kTileK / 16; ++k)
+              if (!Is::kWeight || k < steps)
+                mma_f16<PAIR>(acc, aDesc0 + at + k * aStep, bDesc0 + at + k * bStep, idesc,
+                              (kb - c0) | k);
+            mma_commit<PAIR>(empty(s), pairMask);
+            if (kb + 1 == c1) mma_commit<PAIR>(accFull(buf), pairMask);
+          }
+          __syncwarp();
+          if (++s == kStages) s = 0, turn ^= 1;
+        }
+        if (!ok) break;
+        if (++buf == 2) buf = 0, bufTurn ^= 1;
+      }
+    }
+    if (!ok) {
+      raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
+      if (elected()) {
+        mma_commit<PAIR>(drained, pairMask);
+        wait(drained, 0, false);
+      }
+    }
+  } else if (warp >= 4) {
+    const int quad = warp % 4, part = (warp - 4) / 4;
+    const int row = quad * 32 + lane;
+    const uint32_t quadBase = tmem + ((uint32_t)(quad * 32) << 16);
+    int buf = 0, bufTurn = 0, e = 0;
+    auto next = [&]() {
+      if (!all_wait(accFull(buf), bufTurn)) {
+        raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
+        return false;
+      }
+      tmem_fence_after();
+      return true;
+    };
+    auto release = [&]() {
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) peer_arrive(peer_addr(accEmpty(buf), 0));
+        else mbar_arrive(accEmpty(buf));
+      }
+      if (++buf == 2) buf = 0, bufTurn ^= 1;
+    };
+    T* out = static_cast<T*>(g.out);
+    // 32 columns from c of the tile
+    auto store = [&](const GroupTile& o, int c, const float(&v)[32]) {
+      if constexpr (Is::kFew) {
+        const int m = o.m0 + (int)rank * kTileM + row;
+        if (m >= g.M) return;
+        typename Ty<T>::Bits* p =
+            reinterpret_cast<typename Ty<T>::Bits*>(out) + (long long)(o.n0 + c) * g.ld + m;
+        const int n = o.hi - o.n0 - c;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < n) p[i * g.ld] = Ty<T>::narrow(v[i]);
+      } else {
+        const int r = o.m0 + (int)rank * kTileM + row;
+        if (r >= (Is::kWeight ? g.M : o.hi)) return;
+        const long long at = Is::kWeight ? (long long)o.g * g.M + r : (long long)r;
+        store_row(out + at * g.ld + o.n0 + c, v, g.N - o.n0 - c, g.align);
+      }
+    };
+    // whether the columns from c on are in the product
+    auto there = [&](const GroupTile& o, int c) {
+      return o.n0 + c < (Is::kFew ? o.hi : g.N);
+    };
+    for (int t = firstTile; t < tiles; t += tileStep) {
+      const GroupTile o = tile_at(t, e);
+      const int slices = slices_of(o);
+      if constexpr (CHUNK > 0) {
+        float sum[kPart];
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) sum[i] = 0.0f;
+        bool left = false;
+        for (int c0 = 0; c0 < slices; c0 += CHUNK) {
+          left = !next();
+          if (left) break;
+#pragma unroll
+          for (int c = 0; c < kPart; c += 16) {
+            float v[16];
+            tmem_load16(quadBase + (unsigned)(buf * BN + part * kPart + c), v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
+          }
+          release();
+        }
+        if (left) break;
+#pragma unroll
+        for (int c = 0; c < kPart; c += 32) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = sum[c + i];
+          if (there(o, part * kPart + c)) store(o, part * kPart + c, v);
+        }
+      } else {
+        if (slices && !next()) break;
+#pragma unroll
+        for (int c = 0; c < kPart; c += 32) {
+          if (!there(o, part * kPart + c)) break;
+          float v[32];
+          __syncwarp();
+          if (slices) {
+            tmem_load32(quadBase + (unsigned)(buf * BN + part * kPart + c), v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          }
+          store(o, part * kPart + c, v);
+        }
+        if (slices) release();
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  if (warp == 2) {
+    tmem_fence_after();
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(Shape::kTmem));
+    } else {
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(Shape::kTmem));
+    }
+  }
+}
+
+// ------------------------------------------------------------- host side
+constexpr size_t kMostRows = (size_t)1 << 30, kMostDim = (size_t)1 << 24,
+                 kMostStride = (size_t)1 << 31;
+
+// A matrix of 16-bit elements as it is given, or its copy in whole sectors.
+struct Matrix {
+  const void* p;
+  size_t rows, cols, stride;  // batch * rows of them
+  size_t batch;
+  size_t copy;                // place of the copy in the workspace, where it needs one
+  bool pad;
+};
+struct GroupedPlan {
+  Matrix x, w, dy;
+  size_t bytes;
+};
+
+bool plan_matrix(const void* p, size_t rows, size_t cols, size_t stride, size_t batch, Matrix* m,
+                 size_t* at) {
+  *m = {p, rows, cols, stride, batch, 0, !packed_rows(p, stride)};
+  if (m->pad) {
+    m->copy = *at;
+    *at += op_round(batch * rows * up(cols, 16) * 2);
+  }
+  return true;
+}
+
+bool sizes_ok(size_t rows, size_t dim, size_t outDim, int groups, int dtype) {
+  return (dtype == VR_FLOAT16 || dtype == VR_BFLOAT16) && rows <= kMostRows && dim >= 1 &&
+         dim <= kMostDim && outDim >= 1 && outDim <= kMostDim && groups >= 1 &&
+         groups <= kMostGroups;
+}
+bool stride_ok(size_t stride, size_t cols) { return stride >= cols && stride <= kMostStride; }
+
+bool plan_linear(const void* x, size_t xStride, const void* w, size_t rows, size_t dim,
+                 size_t outDim, int groups, int dtype, GroupedPlan* p) {
+  if (!sizes_ok(rows, dim, outDim, groups, dtype) || !stride_ok(xStride, dim)) return false;
+  size_t at = 0;
+  *p = GroupedPlan{};
+  plan_matrix(x, rows, dim, xStride, 1, &p->x, &at);
+  plan_matrix(w, outDim, dim, dim, (size_t)groups, &p->w, &at);
+  p->bytes = at + kOpSlack;
+  return true;
+}
+bool plan_grad(const void* dy, size_t dyStride, const void* x, size_t xStride, const void* w,
+               size_t rows, size_t dim, size_t outDim, int groups, int dtype, GroupedPlan* p) {
+  if (!sizes_ok(rows, dim, outDim, groups, dtype) || !stride_ok(xStride, dim) ||
+      !stride_ok(dyStride, outDim))
+    return false;
+  size_t at = 0;
+  *p = GroupedPlan{};
+  plan_matrix(dy, rows, outDim, dyStride, 1, &p->dy, &at);
+  plan_matrix(x, rows, dim, xStride, 1, &p->x, &at);
+  plan_matrix(w, outDim, dim, dim, (size_t)groups, &p->w, &at);
+  p->bytes = at + kOpSlack;
+  return true;
+}
+
+vr_result_t pad_matrix(Matrix* m, char* w, const OpDevice& dev, void* stream) {
+  if (!m->pad || !m->rows) return VR_SUCCESS;
+  const size_t ld = up(m->cols, 16), rows = m->batch * m->rows;
+  PadArgs a = {static_cast<const uint16_t*>(m->p), (long long)m->stride, (long long)rows,
+               (int)m->cols, (int)ld, reinterpret_cast<uint16_t*>(w + m->copy)};
+  void* args[] = {&a};
+  m->p = w + m->copy;
+  m->stride = ld;
+  return op_launch((const void*)pad_kernel,
+                   dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
+                   dim3(256), args, 0, stream);
+}
+
+template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
+vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, size_t M, size_t N,
+                   size_t K, size_t rows, int groups, const int* counts, void* out, size_t ld,
+                   void* stream) {
+  using Shape = GroupedShape<BN, PAIR>;
+  using Is = KindOf<KIND>;
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const void* fn = (const void*)grouped_kernel<T, BN, KIND, PAIR, CHUNK>;
+  GroupedArgs g = {};
+  auto map = [&](CUtensorMap* to, const Matrix& m, int boxRows) {
+    return gemm_operand(to, m.p, bf16, m.cols, m.rows, m.batch, m.stride * 2,
+                        m.stride * 2 * m.rows, boxRows);
+  };
+  vr_result_t e = map(&g.a, a, Is::kAMn ? kTileK : kTileM);
+  if (e != VR_SUCCESS || (e = map(&g.b, b, Is::kBMn ? kTileK : Shape::kBRows)) != VR_SUCCESS ||
+      (e = gemm_prepare(fn, dev.device, Shape::kSmem)) != VR_SUCCESS)
+    return e;
+  g.counts = counts;
+  g.groups = groups;
+  g.rows = (int)rows;
+  g.M = (int)M;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.out = out;
+  g.ld = (long long)ld;
+  const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * ld);
+  g.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 2;
+  g.status = dev.status;
+  g.timeoutNs = dev.timeoutNs;
+  // at most so many tiles: every group's last one may be cut
+  const size_t tm = (M + Shape::kTileRows - 1) / Shape::kTileRows, tn = (N + BN - 1) / BN;
+  const size_t some = std::min<size_t>((size_t)groups, rows);
+  const size_t tiles = Is::kWeight ? (size_t)groups * tm * tn
+                       : Is::kRows ? (rows / Shape::kTileRows + some) * tn
+                                   : (rows / BN + some) * tm;
+  constexpr size_t kCtas = PAIR ? 2 : 1;
+  const size_t grid = std::min<size_t>(tiles, dev.sms / kCtas) * kCtas;
+  void* args[] = {&g};
+  return op_launch(fn, dim3((unsigned)grid), dim3(128 + 32 * Shape::kWarps), args, Shape::kSmem,
+                   stream, (int)kCtas);
+}
+
+// Sums longer than these are taken in chunks of 2048: the tensor cores truncate
+// where a product is added, 1.6e-8 of the sum per 16 k (xent.cu).
+constexpr int kLongChunk = 32;
+template <typename T>
+constexpr size_t kLongSum = std::is_same<T, __half>::value ? 32768 : 262144;
+
+constexpr size_t kFewRows = 32, kPairRows = 512;  // a group on average
+
+template <typename T>
+vr_result_t linear(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
+                   size_t outDim, int groups, const int* counts, void* out, size_t ld,
+                   void* stream) {
+  const bool lng = dim > kLongSum<T>;
+#define VR_GO(BN, KIND, PAIR, A, B, M, N)                                                       \
+  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, A, B, M, N, dim, rows, groups, counts, out, \
+                                               ld, stream)                                      \
+       : launch<T, BN, KIND, PAIR, 0>(dev, A, B, M, N, dim, rows, groups, counts, out, ld, stream))
+  if (rows <= kFewRows * (size_t)groups) return VR_GO(32, kFewLinear, false, p.w, p.x, outDim, rows);
+  if (rows < kPairRows * (size_t)groups) return VR_GO(256, kLinear, false, p.x, p.w, rows, outDim);
+  return VR_GO(256, kLinear, true, p.x, p.w, rows, outDim);
+#undef VR_GO
+}
+template <typename T>
+vr_result_t grad_rows(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
+                      size_t outDim, int groups, const int* counts, void* out, void* stream) {
+  const bool lng = outDim > kLongSum<T>;
+#define VR_GO(BN, KIND, PAIR, A, B, M, N)                                                          \
+  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, A, B, M, N, outDim, rows, groups, counts, out, \
+                                               dim, stream)                                        \
+       : launch<T, BN, KIND, PAIR, 0>(dev, A, B, M, N, outDim, rows, groups, counts, out, dim,     \
+                                      stream))
+  if (rows <= kFewRows * (size_t)groups) return VR_GO(32, kFewGradRows, false, p.w, p.dy, dim, rows);
+  if (rows < kPairRows * (size_t)groups) return VR_GO(256, kGradRows, false, p.dy, p.w, rows, dim);
+  return VR_GO(256, kGradRows, true, p.dy, p.w, rows, dim);
+#undef VR_GO
+}
+template <typename T>
+vr_result_t grad_weight(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
+                        size_t outDim, int groups, const int* counts, void* out, void* stream) {
+  if (rows > kLongSum<T>)
+    return launch<T, 256, kGradWeight, false, kLongChunk>(dev, p.dy, p.x, outDim, dim, rows, rows,
+                                                          groups, counts, out, dim, stream);
+  return launch<T, 256, kGradWeight, false, 0>(dev, p.dy, p.x, outDim, dim, rows, rows, groups,
+                                               counts, out, dim, stream);
+}
+
+}  // namespace
+}  // namespace vr
+
+using namespace vr;
+
+extern "C" {
+
+vr_result_t vr_grouped_linear_workspace_bytes(const void* x, size_t xStride, const void* weight,
+                                              size_t rows, size_t dim, size_t outDim, int groups,
+                                              vr_dtype_t dtype, size_t* bytes) {
+  GroupedPlan p;
+  if (!bytes || !plan_linear(x, xStride, weight, rows, dim, outDim, groups, dtype, &p))
+    return VR_ERR_INVALID_ARGUMENT;
+  *bytes = p.bytes;
+  return VR_SUCCESS;
+}
+
+vr_result_t vr_grouped_linear(const void* x, size_t xStride, const void* weight, const int* counts,
+                              size_t rows, size_t dim, size_t outDim, int groups, vr_dtype_t dtype,
+                              void* out, size_t outStride, void* workspace, size_t workspaceBytes,
+                              void* stream) {
+  GroupedPlan p;
+  if (!plan_linear(x, xStride, weight, rows, dim, outDim, groups, dtype, &p) ||
+      !stride_ok(outStride, outDim) || !weight || !counts || !workspace ||
+      (rows && (!x || !out)) || ((uintptr_t)workspace & 15) || workspaceBytes < p.bytes ||
+      ((uintptr_t)counts & 3) || (((uintptr_t)x | (uintptr_t)weight | (uintptr_t)out) & 1))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t nw = (size_t)groups * outDim * dim * 2;
+  // (an output listed before the inputs may be none of them)
+  const OpBuffer buf[5] = {{workspace, 1, workspaceBytes, workspaceBytes, true},
+                           {out, rows, outDim * 2, outStride * 2, true},
+                           {x, rows, dim * 2, xStride * 2, false},
+                           {weight, 1, nw, nw, false},
+                           {counts, 1, (size_t)groups * 4, (size_t)groups * 4, false}};
+  if (!op_buffers_ok(buf, 5)) return VR_ERR_INVALID_ARGUMENT;
+  OpDevice dev;
+  vr_result_t e = op_device(&dev);
+  if (e != VR_SUCCESS || (e = op_reachable(buf, 5, dev.device)) != VR_SUCCESS) return e;
+  if (!rows) return VR_SUCCESS;
+  char* w = op_workspace(workspace);
+  if ((e = pad_matrix(&p.x, w, dev, stream)) != VR_SUCCESS ||
+      (e = pad_matrix(&p.w, w, dev, stream)) != VR_SUCCESS)
+    return e;
+  return dtype == VR_BFLOAT16 ? linear<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts,
+                                                      out, outStride, stream)
+                              : linear<__half>(p, dev, rows, dim, outDim, groups, counts, out,
+                                               outStride, stream);
+}
+
+vr_result_t vr_grouped_linear_grad_workspace_bytes(const void* dOut, size_t dOutStride,
+                                                   const void* x, size_t xStride,
+                                                   const void* weight, size_t rows, size_t dim,
+                                                   size_t outDim, int groups, vr_dtype_t dtype,
+                                                   size_t* bytes) {
+  GroupedPlan p;
+  if (!bytes ||
+      !plan_grad(dOut, dOutStride, x, xStride, weight, rows, dim, outDim, groups, dtype, &p))
+    return VR_ERR_INVALID_ARGUMENT;
+  *bytes = p.bytes;
+  return VR_SUCCESS;
+}
+
+vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const void* x,
+                                   size_t xStride, const void* weight, const int* counts,
+                                   size_t rows, size_t dim, size_t outDim, int groups,
+                                   vr_dtype_t dtype, void* dX, void* dWeight, void* workspace,
+                                   size_t workspaceBytes, void* stream) {
+  GroupedPlan p;
+  if (!plan_grad(dOut, dOutStride, x, xStride, weight, rows, dim, outDim, groups, dtype, &p) ||
+      !counts || !workspace || (!dX && !dWeight) || (dX && !weight) ||
+      (rows && (!dOut || (dWeight && !x))) || ((uintptr_t)workspace & 15) ||
+      workspaceBytes < p.bytes || ((uintptr_t)counts & 3) ||
+      (((uintptr_t)dOut | (uintptr_t)x | (uintptr_t)weight | (uintptr_t)dX | (uintptr_t)dWeight) &
+       1))
+    return VR_ERR_INVALID_ARGUMENT;
+  const size_t nw = (size_t)groups * outDim * dim * 2, nx = rows * dim * 2;
+  OpBuffer buf[7] = {{workspace, 1, workspaceBytes, workspaceBytes, true}};
+  int n = 1;
+  if (dX) buf[n++] = {dX, 1, nx, nx, true};
+  if (dWeight) buf[n++] = {dWeight, 1, nw, nw, true};
+  buf[n++] = {dOut, rows, outDim * 2, dOutStride * 2, false};
+  if (dWeight) buf[n++] = {x, rows, dim * 2, xStride * 2, false};
+  if (dX) buf[n++] = {weight, 1, nw, nw, false};
+  buf[n++] = {counts, 1, (size_t)groups * 4, (size_t)groups * 4, false};
+  if (!op_buffers_ok(buf, n)) return VR_ERR_INVALID_ARGUMENT;
+  OpDevice dev;
+  vr_result_t e = op_device(&dev);
+  if (e != VR_SUCCESS || (e = op_reachable(buf, n, dev.device)) != VR_SUCCESS) return e;
+  if (!rows) {
+    if (dWeight && cudaMemsetAsync(dWeight, 0, nw, (cudaStream_t)stream) != cudaSuccess)
+      return VR_ERR_CUDA;
+    return VR_SUCCESS;
+  }
+  char* w = op_workspace(workspace);
+  if ((e = pad_matrix(&p.dy, w, dev, stream)) != VR_SUCCESS ||
+      (dWeight && (e = pad_matrix(&p.x, w, dev, stream)) != VR_SUCCESS) ||
+      (dX && (e = pad_matrix(&p.w, w, dev, stream)) != VR_SUCCESS))
+    return e;
+  const bool bf16 = dtype == VR_BFLOAT16;
+  if (dX && (e = bf16 ? grad_rows<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts, dX,
+                                                 stream)
+                      : grad_rows<__half>(p, dev, rows, dim, outDim, groups, counts, dX,
+                                          stream)) != VR_SUCCESS)
+    return e;
+  if (!dWeight) return VR_SUCCESS;
+  return bf16 ? grad_weight<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts, dWeight,
+                                           stream)
+              : grad_weight<__half>(p, dev, rows, dim, outDim, groups, counts, dWeight, stream);
+}
+
+}  // extern "C"

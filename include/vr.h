@@ -541,6 +541,137 @@ vr_result_t vr_orthogonalize(const void* const* src, void* const* dst, int count
                              float eps, float scale, void* workspace, size_t workspaceBytes,
                              void* stream);
 
+/* Rows of an embedding table by token, scaled:
+ *   out_t = scale * weight_ids[t]
+ * rounded once to dtype (fp32, fp16 or bf16).  weight: `vocab` rows of dim
+ * elements, weightStride apart; out: `tokens` rows, outStride apart.  ids:
+ * 64-bit indices below vocab; a token with ignoreIndex gets a row of zeros, as
+ * does one with any other index outside the vocabulary, which vr_stream_status
+ * reports as VR_ERR_INVALID_ARGUMENT.  tokens == 0 enqueues nothing.
+ * Errors: VR_ERR_INVALID_ARGUMENT for a bad dtype, dim or vocab < 1, tokens or
+ * vocab above 2^30, dim above 2^24, a stride below dim or above 2^31, a NULL
+ * or misaligned buffer or an overlap. */
+vr_result_t vr_embedding(const void* weight, size_t weightStride, const long long* ids,
+                         size_t tokens, size_t dim, size_t vocab, vr_dtype_t dtype,
+                         long long ignoreIndex, float scale, void* out, size_t outStride,
+                         void* stream);
+
+/* The gradient of the table:
+ *   dWeight_v = scale * sum_{t: ids[t] = v} dOut_t          (accumulate = 0)
+ *   dWeight_v = dWeight_v + scale * sum ...                  (accumulate = 1)
+ * dOut: `tokens` rows of dim elements, dOutStride apart; dWeight (vocab x
+ * dim): contiguous; both of dtype.  Without accumulate every row is written,
+ * zeros for words that do not occur; with it their rows are neither read nor
+ * written (the gradient of an output layer that shares the table goes first).
+ * Sums are fp32 in token order (more than 32 equal tokens: of 32 or more at a
+ * time), rounded once to dtype.  Ignored tokens and indices outside the
+ * vocabulary as above; what their rows of dOut hold is not read.
+ * Errors: those of vr_embedding, or a short workspace. */
+vr_result_t vr_embedding_grad_workspace_bytes(size_t tokens, size_t dim, size_t vocab,
+                                              vr_dtype_t dtype, size_t* bytes);
+vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long long* ids,
+                              size_t tokens, size_t dim, size_t vocab, vr_dtype_t dtype,
+                              long long ignoreIndex, float scale, int accumulate, void* dWeight,
+                              void* workspace, size_t workspaceBytes, void* stream);
+
+/* Matrix products grouped by expert: rows sorted by group, each times its
+ * group's weight.
+ *   out_r = weight_e x_r    for the rows r of group e
+ * x: `rows` rows of dim elements, xStride apart; weight: `groups` contiguous
+ * matrices of outDim rows of dim; out: rows of outDim, outStride apart; all
+ * fp16 or all bf16.  counts: `groups` ints on the device, the rows of each
+ * group, which follow one another (the counts that vr_balance_loss gives).
+ * Any group may have none.  Rows behind the last group's are not read into any
+ * result, and their results are left as they were.  Counts that are negative
+ * or add up to more than `rows` are cut off there and reported by
+ * vr_stream_status as VR_ERR_INVALID_ARGUMENT.
+ * Products are exact and summed in fp32, results rounded once.  The kernels
+ * are chosen by rows / groups: up to 32 rows a group on average are fastest
+ * where few have many more.
+ * Rows that are not 16-byte units (dim or stride not a multiple of 8, or a
+ * misaligned buffer) are copied into the workspace first, so that its size
+ * depends on the call's own pointers and strides.
+ * Errors: VR_ERR_INVALID_ARGUMENT for fp32 or a bad dtype, dim or outDim
+ * outside [1, 2^24], rows above 2^30, groups outside [1, 1024], a stride below
+ * its row or above 2^31, a NULL or misaligned buffer, an overlap or a short
+ * workspace. */
+vr_result_t vr_grouped_linear_workspace_bytes(const void* x, size_t xStride, const void* weight,
+                                              size_t rows, size_t dim, size_t outDim, int groups,
+                                              vr_dtype_t dtype, size_t* bytes);
+vr_result_t vr_grouped_linear(const void* x, size_t xStride, const void* weight, const int* counts,
+                              size_t rows, size_t dim, size_t outDim, int groups, vr_dtype_t dtype,
+                              void* out, size_t outStride, void* workspace, size_t workspaceBytes,
+                              void* stream);
+
+/* The gradients of such a product:
+ *   dX_r = weight_e^T dOut_r,   dWeight_e = sum_{r of group e} dOut_r x_r^T
+ * dOut: `rows` rows of outDim elements, dOutStride apart; dX (rows x dim) and
+ * dWeight (groups x outDim x dim): contiguous, of dtype; either may be NULL
+ * (dX NULL: weight is not used; dWeight NULL: x is not used).  Every
+ * group's dWeight is written, zeros for one without rows; rows of dX behind the
+ * last group's are left as they were.  Each gradient is rounded once (fp16:
+ * scale dOut so that it stays in range).  Otherwise as vr_grouped_linear. */
+vr_result_t vr_grouped_linear_grad_workspace_bytes(const void* dOut, size_t dOutStride,
+                                                   const void* x, size_t xStride,
+                                                   const void* weight, size_t rows, size_t dim,
+                                                   size_t outDim, int groups, vr_dtype_t dtype,
+                                                   size_t* bytes);
+vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const void* x,
+                                   size_t xStride, const void* weight, const int* counts,
+                                   size_t rows, size_t dim, size_t outDim, int groups,
+                                   vr_dtype_t dtype, void* dX, void* dWeight, void* workspace,
+                                   size_t workspaceBytes, void* stream);
+
+/* One AdamW step over many tensors at once, in place: with t = step and
+ * g = gradScale * grads[i],
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = (1 - lr weightDecay) p
+ *       - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * params[i], grads[i], m[i], v[i]: sizes[i] elements (0: skipped), of dtype and
+ * gradDtype; any alignment (fastest where each begins at a multiple of 8
+ * elements).
+ *   masters: NULL, or fp32 copies of 16-bit parameters: p is read from and
+ *     written to them, and params[i] receives it rounded, unread.
+ *   stateBits 32: m, v are fp32 (mScales, vScales NULL).  stateBits 8: m, v are
+ *     bytes, and mScales[i], vScales[i] ceil(sizes[i] / 256) floats, one for 256
+ *     consecutive elements.  Zeroed bytes and scales are states of zero.  A
+ *     byte of m is a sign, four bits of exponent and three of mantissa (the
+ *     e4m3 format), one of v five and three, with exponents offset by 15; the
+ *     value is that times the block's scale, a power of two by which the block's
+ *     largest value begins at 2^7 (m) or 2^15 (v).  New states are rounded at
+ *     random, so that they are right on average (a mean over thousands of steps
+ *     would stand still otherwise): up or down in proportion to the rest, by 16
+ *     random bits that are a function of seed, step and the element's place
+ *     among the call's tensors.  A positive v keeps a code above 0.  p is made of the
+ *     states before that rounding.  A NaN or an infinity in a block makes its
+ *     scale NaN.
+ *   control: NULL, or three floats in device memory, read when the kernel runs:
+ *     lr, step and gradScale in place of the arguments, which a captured step
+ *     needs.  A gradScale there that is not finite leaves everything as it was.
+ * States are fp32 operations each rounded by itself, in the order written, with
+ * 1 - beta in fp32: the same bits wherever they are computed.
+ * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, a bad dtype, gradDtype or
+ * stateBits, masters with fp32 parameters, scales that do not go with
+ * stateBits, a size above 2^40, beta1 or beta2 outside [0, 1), eps negative or
+ * not finite, weightDecay or (without control) lr or gradScale not finite or
+ * step < 1, a NULL or misaligned buffer, or any overlap. */
+vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const* m,
+                     void* const* v, float* const* mScales, float* const* vScales,
+                     float* const* masters, const size_t* sizes, int count, vr_dtype_t dtype,
+                     vr_dtype_t gradDtype, int stateBits, float lr, float beta1, float beta2,
+                     float eps, float weightDecay, long long step, float gradScale,
+                     unsigned long long seed, const float* control, void* stream);
+
+/* The values of 8-bit states of vr_adamw in fp32, exactly (to look at, or to
+ * store in a checkpoint): mValues[i], vValues[i] receive sizes[i] floats;
+ * mValues (with m, mScales) or vValues (with v, vScales) may be NULL.
+ * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, both NULL, a size above 2^40,
+ * a NULL or misaligned buffer, or an overlap. */
+vr_result_t vr_adamw_values(const void* const* m, const void* const* v,
+                            const float* const* mScales, const float* const* vScales,
+                            const size_t* sizes, int count, float* const* mValues,
+                            float* const* vValues, void* stream);
+
 /* ---------------------------------------------------------- cost model
  * The pages' alpha-beta model ([Course13] "理想成本模型"; [Interview]
  * "推导 / 关键公式"), with N ranks, tree depth D (the deeper of the two
