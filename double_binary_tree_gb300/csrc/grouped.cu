@@ -5,16 +5,21 @@
 //
 // Rows are sorted by group; how many each group has is known on the device
 // only.  One launch takes the tiles of all groups: every CTA adds the counts up
-// for itself (a few microseconds less than a launch that writes a table) and
+// for itself (a microsecond or two, less than a launch that writes a table) and
 // walks the tiles with the grid's stride, the roles of its warps those of the
 // products of gemm.cuh: tensor copies, tcgen05 products, epilogue.
 //
-//   rows    tiles of a group's rows by 256 output columns.  A tile reads on
-//           into the next group's rows, whose results are not stored.
-//   few     few rows a group: the weights take the place of the rows, 128 of
-//           their rows to a tile, and up to 32 rows of the group that of the
-//           columns, so that a tile is what has to be read of the weights.
-//   weight  dW: a sum over the group's rows.  The last slice of 64 reads on
+//   rows    (out, dX)  The weight's rows fill the 128 or 256 rows of a tile and a
+//           group's rows are its columns, since an instruction takes any
+//           multiple of 16 (pairs of CTAs: 32) of those: a group's last tile costs what it
+//           holds.  (The other way round 64 groups of 512 rows on average pay
+//           for 640: 2048 x 4096 in 400 us instead of the 286 of the peak.)  A group's
+//           rows are cut into tiles of about the same size.  A thread then has
+//           one output column of many rows; pairs of lanes exchange values, so
+//           that a store is two columns of one row.
+//   few     The same for few rows a group: up to 32 columns, so that nearly all
+//           of shared memory holds weights on their way.
+//   weight  (dW)  A sum over the group's rows.  The last slice of 64 reads on
 //           into the next group; the rows behind the end, up to the next
 //           multiple of the 16 that a product takes, are zeroed in shared memory
 //           (in both operands: they may hold NaN).
@@ -30,22 +35,21 @@ namespace {
 constexpr int kMostGroups = 1024;
 constexpr int kGroupedSmem = 212 * 1024;  // the stages; the tables of the groups are beside them
 
-enum Kind : int { kLinear, kGradRows, kGradWeight, kFewLinear, kFewGradRows };
+enum Kind : int { kLinear, kGradRows, kGradWeight };
 template <int KIND>
 struct KindOf {
-  static constexpr bool kFew = KIND == kFewLinear || KIND == kFewGradRows;
   static constexpr bool kWeight = KIND == kGradWeight;
-  static constexpr bool kRows = !kFew && !kWeight;
   // operands whose rows are the summed dimension
-  static constexpr bool kAMn = kWeight || KIND == kFewGradRows;
-  static constexpr bool kBMn = kWeight || KIND == kGradRows;
+  static constexpr bool kAMn = KIND != kLinear, kBMn = kWeight;
 };
+constexpr int kBox = 32;  // rows that a tensor copy of a group's rows fetches
 
 struct GroupedArgs {
   CUtensorMap a, b;
   const int* counts;
   int groups, rows;  // rows: that the buffers have
-  int M, N, K;       // of the product; the one that is counted on the device is not used
+  int M, N, K;       // of the product; N (rows) or K (weight) is counted on the device
+  int cap;           // most columns of a tile of rows, a multiple of 32
   void* out;
   long long ld;      // elements between its rows
   int align;
@@ -62,26 +66,78 @@ struct GroupedShape {
   static constexpr int kTileRows = PAIR ? 2 * kTileM : kTileM;
   static constexpr int kStages = kGroupedSmem / kStageBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes;
-  static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kTmem = 2 * BN;
   static constexpr int kWarps = BN >= 128 ? 16 : 4;  // of the epilogue
+  static constexpr int kGrain = PAIR ? 32 : 16;      // columns of an instruction
 };
 
-// A tile: its group, its place in the product, the group's rows [lo, hi).
+// A tile: its group, its place in the product and its columns, a multiple of
+// what an instruction takes; the group's rows [lo, hi).
 struct GroupTile {
-  int g, m0, n0, lo, hi;
+  int g, m0, n0, width, lo, hi;
 };
+
+// The same arrive and wait as mbar_arrive and mbar_test for what another CTA of
+// the cluster wrote.
+__device__ __forceinline__ void peer_arrive_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// Rows [from, to) of the MN-major slabs of a stage made zero by a warp, for
+// products that are issued after this.  (A row is 128 bytes; the swizzle moves
+// 16-byte pieces within it.)
+template <int SLABS>
+__device__ __forceinline__ void zero_rows(uint32_t stage, int from, int to, int lane) {
+  constexpr unsigned kSlab = 64 * kTileK * 2;
+#pragma unroll
+  for (int slab = 0; slab < SLABS; ++slab)
+    for (int i = from * 8 + lane; i < to * 8; i += 32)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(stage + slab * kSlab +
+                                                                    (unsigned)(i * 16)),
+                   "r"(0)
+                   : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
+// A warp's 32 columns m of `rows` (at most 32) rows, 32 values a lane, one of
+// each row.  align >= 4: two columns of a row in one store, which a pair of
+// lanes make of each two rows.
+template <typename T>
+__device__ __forceinline__ void store_columns(T* out, long long ld, const float (&v)[32], int rows,
+                                              int m, int M, int align) {
+  if (align >= 4 && M % 2 == 0) {
+    const bool odd = m & 1;
+    uint32_t* p = reinterpret_cast<uint32_t*>(out + (odd ? ld : 0) + (m & ~1));
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const uint32_t mine = pack2<T>(v[i], v[i + 1]);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+      const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+      if (m < M && i + (int)odd < rows) p[i * (ld / 2)] = both;
+    }
+  } else {
+    typename Ty<T>::Bits* p = reinterpret_cast<typename Ty<T>::Bits*>(out) + m;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (m < M && i < rows) p[i * ld] = Ty<T>::narrow(v[i]);
+  }
+}
 
 template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
 __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
     grouped_kernel(const __grid_constant__ GroupedArgs g) {
   using Shape = GroupedShape<BN, PAIR>;
   using Is = KindOf<KIND>;
-  constexpr bool AMN = Is::kAMn, BMN = Is::kBMn;
+  constexpr bool AMN = Is::kAMn, BMN = Is::kBMn, kWeight = Is::kWeight;
   constexpr int kStages = Shape::kStages, kCtas = PAIR ? 2 : 1, kRows = Shape::kTileRows;
-  constexpr int kEpilogueWarps = Shape::kWarps, kGroups = kEpilogueWarps / 4, kPart = BN / kGroups;
-  static_assert(!(PAIR && Is::kWeight), "the end of a group is zeroed by one CTA for itself");
+  constexpr int kEpilogueWarps = Shape::kWarps, kGroups = kEpilogueWarps / 4;
+  constexpr int kUnits = BN / 32 / kGroups;  // of 32 columns, for each group of four warps
+  constexpr bool kTails = PAIR && kWeight;
+  constexpr unsigned kSlab = 64 * kTileK * 2;  // MN-major: bytes of a 64-wide slab
   extern __shared__ unsigned char smemRaw[];
-  __shared__ alignas(8) uint64_t bars[2 * kStages + 2 * 2 + 1];
+  __shared__ alignas(8) uint64_t bars[2 * kStages + 5 + (kTails ? 2 * kStages : 0)];
   __shared__ uint32_t tmemBase;
   __shared__ volatile int abortFlag;
   __shared__ int rowStart[kMostGroups + 1], tileStart[kMostGroups + 1];
@@ -97,6 +153,10 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
   auto accFull = [&](int i) { return bar0 + 8u * (2 * kStages + i); };
   auto accEmpty = [&](int i) { return bar0 + 8u * (2 * kStages + 2 + i); };
   const uint32_t drained = bar0 + 8u * (2 * kStages + 4);
+  // the end of a group on a pair: the CTA's own copies have landed in stage s; the
+  // other CTA has zeroed its rows of it
+  auto tailFull = [&](int s) { return bar0 + 8u * (2 * kStages + 5 + s); };
+  auto tailPeer = [&](int s) { return bar0 + 8u * (3 * kStages + 5 + s); };
   auto wait = [&](uint32_t bar, unsigned parity, bool honorAbort = true) {
     return wait_phase(bar, parity, &abortFlag, honorAbort, g.timeoutNs);
   };
@@ -109,6 +169,10 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
+      if (kTails) {
+        mbar_init(tailFull(s), 1);
+        mbar_init(tailPeer(s), 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(accFull(i), 1);
@@ -140,7 +204,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
   }
   pdl_launch();
   pdl_wait();
-  const int tilesN = (g.N + BN - 1) / BN, tilesM = (g.M + kRows - 1) / kRows;
+  const int tilesM = (g.M + kRows - 1) / kRows, tilesN = (g.N + BN - 1) / BN;
   if (warp == 3) {  // the groups' rows and tiles
     int rows = 0, tiles = 0;
 #pragma unroll 4
@@ -158,18 +222,13 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
       end += rows;
       if (given < 0 || end > g.rows) atomicCAS(g.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
       const int hi = (int)min(end, (long long)g.rows);
-      const int lo = max(__shfl_up_sync(0xffffffffu, hi, 1), lane ? 0 : rows);
-      const int from = lane ? lo : rows, n = hi - from;
-      int mine = 0;
-      if (e < g.groups)
-        mine = Is::kWeight ? tilesM * tilesN
-                           : Is::kRows ? (n + kRows - 1) / kRows * tilesN
-                                       : (n + BN - 1) / BN * tilesM;
-      int sum = mine;
+      const int up = __shfl_up_sync(0xffffffffu, hi, 1), lo = lane ? up : rows;
+      int sum = 0;
+      if (e < g.groups) sum = kWeight ? tilesM * tilesN : (hi - lo + g.cap - 1) / g.cap * tilesM;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
-        const int up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
+        const int more = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += more;
       }
       if (e < g.groups) {
         rowStart[e + 1] = hi;
@@ -190,61 +249,76 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
   // Tiles are walked upwards: `e` is the group of the last one.
   auto tile_at = [&](int t, int& e) {
     while (t >= tileStart[e + 1]) ++e;
-    GroupTile o = {e, 0, 0, rowStart[e], rowStart[e + 1]};
+    GroupTile o = {e, 0, 0, BN, rowStart[e], rowStart[e + 1]};
     t -= tileStart[e];
-    if constexpr (Is::kFew) {  // a group's rows first: its weights are in L2 by then
-      const int across = (o.hi - o.lo + BN - 1) / BN;
-      o.m0 = t / across * kRows;
-      o.n0 = o.lo + t % across * BN;
-    } else {  // 2048 rows at a time, column by column
-      const int high = Is::kWeight ? tilesM : (o.hi - o.lo + kRows - 1) / kRows;
-      constexpr int kHigh = 2048 / kRows;
-      const int block = t / (kHigh * tilesN), rows = min(kHigh, high - block * kHigh);
-      t -= block * kHigh * tilesN;
-      o.n0 = t / rows * BN;
-      o.m0 = (Is::kRows ? o.lo : 0) + (block * kHigh + t % rows) * kRows;
+    // the tiles of a block of 2048 rows of the product column by column, so that
+    // the operands of the tiles in flight stay in L2
+    constexpr int kHigh = 2048 / kRows;
+    constexpr int G = Shape::kGrain;
+    const int n = o.hi - o.lo, across = kWeight ? tilesN : (n + g.cap - 1) / g.cap;
+    const int block = t / (kHigh * across), high = min(kHigh, tilesM - block * kHigh);
+    t -= block * kHigh * across;
+    o.m0 = (block * kHigh + t % high) * kRows;
+    if constexpr (kWeight) {
+      o.n0 = t / high * BN;
+    } else {  // columns in shares of about one size, none of them empty
+      const int share = ((n + G - 1) / G + across - 1) / across * G, from = t / high * share;
+      o.n0 = o.lo + from;
+      o.width = min(share, (n - from + G - 1) / G * G);
     }
     return o;
   };
   auto slices_of = [&](const GroupTile& o) {
-    return ((Is::kWeight ? o.hi - o.lo : g.K) + kTileK - 1) / kTileK;
+    return ((kWeight ? o.hi - o.lo : g.K) + kTileK - 1) / kTileK;
   };
 
   if (warp == 0) {
     int s = 0, turn = 0, e = 0;
+    unsigned tailTurn = 0, tailed = 0;  // a bit for each stage
     bool ok = true;
     long long issued = 0;
     const uint32_t landed0 = PAIR ? peer_addr(full(0), 0) : full(0);
     for (int t = firstTile; ok && t < tiles; t += tileStep) {
       const GroupTile o = tile_at(t, e);
       const int slices = slices_of(o);
-      const int m0 = o.m0 + (int)rank * kTileM, n0 = o.n0 + (int)rank * Shape::kBRows;
-      const int first = Is::kWeight ? o.lo : 0;
-      const int za = Is::kFew ? o.g : 0, zb = Is::kRows ? o.g : 0;
+      const int mine = PAIR ? o.width / 2 : o.width;  // columns that this CTA holds
+      const int m0 = o.m0 + (int)rank * kTileM, n0 = o.n0 + (int)rank * mine;
+      const int first = kWeight ? o.lo : 0, boxes = (mine + kBox - 1) / kBox;
+      const unsigned bytes = Shape::kABytes + (kWeight ? Shape::kBBytes : boxes * (kBox * 128));
       for (int kb = 0; kb < slices; ++kb) {
         ok = all_wait(empty(s), turn ^ 1);
         if (!ok) break;
+        const bool tail = kTails && o.hi - o.lo < (kb + 1) * kTileK;
         if (elected()) {
-          if (leader) mbar_arrive_expect_tx(full(s), kCtas * Shape::kStageBytes);
-          const uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes, landed = landed0 + 8u * s;
-          const int k0 = first + kb * kTileK;
+          uint32_t landed = landed0 + 8u * s;
+          if (tail) {
+            mbar_arrive_expect_tx(tailFull(s), bytes);
+            landed = peer_addr(tailFull(s), rank);
+          } else if (leader) {
+            mbar_arrive_expect_tx(full(s), kCtas * bytes);
+          }
+          const uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes;
+          const int k0 = first + kb * kTileK, z = kWeight ? 0 : o.g;
           if constexpr (AMN) {
 #pragma unroll
             for (int i = 0; i < kTileM / 64; ++i)
-              tensor_load<PAIR>(dst + i * (64 * kTileK * 2), &g.a, m0 + i * 64, k0, za, landed);
+              tensor_load<PAIR>(dst + i * kSlab, &g.a, m0 + i * 64, k0, z, landed);
           } else {
-            tensor_load<PAIR>(dst, &g.a, k0, m0, za, landed);
+            tensor_load<PAIR>(dst, &g.a, k0, m0, z, landed);
           }
           if constexpr (BMN) {
 #pragma unroll
             for (int i = 0; i < Shape::kBRows / 64; ++i)
-              tensor_load<PAIR>(dst + Shape::kABytes + i * (64 * kTileK * 2), &g.b, n0 + i * 64, k0,
-                                zb, landed);
+              tensor_load<PAIR>(dst + Shape::kABytes + i * kSlab, &g.b, n0 + i * 64, k0, 0, landed);
           } else {
-            tensor_load<PAIR>(dst + Shape::kABytes, &g.b, k0, n0, zb, landed);
+            for (int i = 0; i < boxes; ++i)
+              tensor_load<PAIR>(dst + Shape::kABytes + i * (kBox * 128), &g.b, k0, n0 + i * kBox, 0,
+                                landed);
           }
         }
         __syncwarp();
+        if (tail) tailTurn ^= 1u << s, tailed |= 1u << s;
+        else tailed &= ~(1u << s);
         ++issued;
         if (++s == kStages) s = 0, turn ^= 1;
       }
@@ -255,13 +329,15 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
       ok = all_wait(empty((int)(i % kStages)), (unsigned)(i / kStages & 1));
     if (!ok) {
       raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
-      if (leader)
-        for (long long i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          wait(full((int)(i % kStages)), (unsigned)(i / kStages & 1), false);
+      for (long long i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
+        const int at = (int)(i % kStages);
+        if (tailed >> at & 1) wait(tailFull(at), (tailTurn >> at & 1) ^ 1, false);
+        else if (leader) wait(full(at), (unsigned)(i / kStages & 1), false);
+      }
     }
   } else if (warp == 1 && leader) {
-    constexpr uint32_t idesc = mma_idesc<T>(kRows, BN, AMN, BMN);
-    constexpr unsigned kSlab = 64 * kTileK * 2;
+    // (the number of columns is the tile's)
+    constexpr uint32_t idesc0 = mma_idesc<T>(kRows, 0, AMN, BMN);
     constexpr unsigned aStep = (AMN ? 16 * 128 : 32) >> 4, bStep = (BMN ? 16 * 128 : 32) >> 4;
     const uint64_t aDesc0 = operand_desc(stage0, AMN ? kSlab : 16, 1024);
     const uint64_t bDesc0 = operand_desc(stage0 + Shape::kABytes, BMN ? kSlab : 16, 1024);
@@ -270,6 +346,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
     for (int t = firstTile; ok && t < tiles; t += tileStep) {
       const GroupTile o = tile_at(t, e);
       const int slices = slices_of(o), chunk = CHUNK ? CHUNK : max(slices, 1);
+      const uint32_t idesc = idesc0 | (uint32_t)(o.width >> 3) << 17;
       for (int c0 = 0; ok && c0 < slices; c0 += chunk) {
         ok = all_wait(accEmpty(buf), bufTurn ^ 1);
         if (!ok) break;
@@ -280,20 +357,12 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
           ok = all_wait(full(s), turn);
           if (!ok) break;
           int steps = kTileK / 16;
-          if constexpr (Is::kWeight) {
+          if constexpr (kWeight) {
             const int left = o.hi - o.lo - kb * kTileK;  // rows of the group in this slice
             if (left < kTileK) {
               steps = (left + 15) / 16;
-              const uint32_t from = stage0 + (unsigned)s * Shape::kStageBytes;
-              const int none = (steps * 16 - left) * 8;  // 16-byte pieces of a slab
-              for (int slab = 0; slab < Shape::kStageBytes / (int)kSlab; ++slab)
-                for (int i = lane; i < none; i += 32)
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                   from + slab * kSlab + (unsigned)(left * 128 + i * 16)),
-                               "r"(0)
-                               : "memory");
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
+              if (!kTails) zero_rows<Shape::kStageBytes / (int)kSlab>(
+                  stage0 + (unsigned)s * Shape::kStageBytes, left, steps * 16, lane);
             }
           }
           tmem_fence_after();
@@ -301,7 +370,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
             const uint64_t at = (uint64_t)((unsigned)s * (Shape::kStageBytes >> 4));
 #pragma unroll
             for (int k = 0; k < kTileK / 16; ++k)
-              if (!Is::kWeight || k < steps)
+              if (!kWeight || k < steps)
                 mma_f16<PAIR>(acc, aDesc0 + at + k * aStep, bDesc0 + at + k * bStep, idesc,
                               (kb - c0) | k);
             mma_commit<PAIR>(empty(s), pairMask);
@@ -321,6 +390,36 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
         wait(drained, 0, false);
       }
     }
+  } else if (kTails && warp == 3) {
+    // The ends of the groups on a pair: each CTA zeroes its rows behind the end
+    // once its copies have landed, the first one hands the stage on when both
+    // have.
+    int e = 0;
+    long long done = 0;  // slices before the tile
+    unsigned tailTurn = 0;
+    bool ok = true;
+    for (int t = firstTile; ok && t < tiles; t += tileStep) {
+      const GroupTile o = tile_at(t, e);
+      const int slices = slices_of(o), left = (o.hi - o.lo) % kTileK;
+      done += slices;
+      if (!left) continue;
+      const int s = (int)((done - 1) % kStages);
+      const unsigned parity = tailTurn >> s & 1;
+      tailTurn ^= 1u << s;
+      ok = all_wait(tailFull(s), parity);
+      if (!ok) break;
+      zero_rows<Shape::kStageBytes / (int)kSlab>(stage0 + (unsigned)s * Shape::kStageBytes, left,
+                                                 (left + 15) / 16 * 16, lane);
+      if (leader) {
+        ok = all_wait(tailPeer(s), parity);
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        if (ok && lane == 0) mbar_arrive(full(s));
+      } else if (lane == 0) {
+        peer_arrive_release(peer_addr(tailPeer(s), 0));
+      }
+      __syncwarp();
+    }
+    if (!ok) raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
   } else if (warp >= 4) {
     const int quad = warp % 4, part = (warp - 4) / 4;
     const int row = quad * 32 + lane;
@@ -346,68 +445,68 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
     T* out = static_cast<T*>(g.out);
     // 32 columns from c of the tile
     auto store = [&](const GroupTile& o, int c, const float(&v)[32]) {
-      if constexpr (Is::kFew) {
-        const int m = o.m0 + (int)rank * kTileM + row;
-        if (m >= g.M) return;
-        typename Ty<T>::Bits* p =
-            reinterpret_cast<typename Ty<T>::Bits*>(out) + (long long)(o.n0 + c) * g.ld + m;
-        const int n = o.hi - o.n0 - c;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < n) p[i * g.ld] = Ty<T>::narrow(v[i]);
+      const int m = o.m0 + (int)rank * kTileM + row;
+      if constexpr (kWeight) {
+        if (m < g.M)
+          store_row(out + ((long long)o.g * g.M + m) * g.ld + o.n0 + c, v, g.N - o.n0 - c, g.align);
       } else {
-        const int r = o.m0 + (int)rank * kTileM + row;
-        if (r >= (Is::kWeight ? g.M : o.hi)) return;
-        const long long at = Is::kWeight ? (long long)o.g * g.M + r : (long long)r;
-        store_row(out + at * g.ld + o.n0 + c, v, g.N - o.n0 - c, g.align);
+        store_columns(out + (o.n0 + c) * g.ld, g.ld, v, min(o.hi - o.n0, o.width) - c, m, g.M,
+                      g.align);
       }
     };
-    // whether the columns from c on are in the product
+    // whether the 32 columns from c are in the product
     auto there = [&](const GroupTile& o, int c) {
-      return o.n0 + c < (Is::kFew ? o.hi : g.N);
+      return kWeight ? o.n0 + c < g.N : c < o.width && o.n0 + c < o.hi;
     };
     for (int t = firstTile; t < tiles; t += tileStep) {
       const GroupTile o = tile_at(t, e);
       const int slices = slices_of(o);
       if constexpr (CHUNK > 0) {
-        float sum[kPart];
+        float sum[kUnits * 32];
 #pragma unroll
-        for (int i = 0; i < kPart; ++i) sum[i] = 0.0f;
+        for (int i = 0; i < kUnits * 32; ++i) sum[i] = 0.0f;
         bool left = false;
         for (int c0 = 0; c0 < slices; c0 += CHUNK) {
           left = !next();
           if (left) break;
 #pragma unroll
-          for (int c = 0; c < kPart; c += 16) {
-            float v[16];
-            tmem_load16(quadBase + (unsigned)(buf * BN + part * kPart + c), v);
+          for (int i = 0; i < kUnits; ++i) {
+            const int c = (part + i * kGroups) * 32;
+            if (!there(o, c)) break;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[c + i] += v[i];
+            for (int h = 0; h < 32; h += 16) {
+              float v[16];
+              tmem_load16(quadBase + (unsigned)(buf * BN + c + h), v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[i * 32 + h + j] += v[j];
+            }
           }
           release();
         }
         if (left) break;
 #pragma unroll
-        for (int c = 0; c < kPart; c += 32) {
+        for (int i = 0; i < kUnits; ++i) {
+          const int c = (part + i * kGroups) * 32;
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = sum[c + i];
-          if (there(o, part * kPart + c)) store(o, part * kPart + c, v);
+          for (int j = 0; j < 32; ++j) v[j] = sum[i * 32 + j];
+          if (there(o, c)) store(o, c, v);
         }
       } else {
         if (slices && !next()) break;
 #pragma unroll
-        for (int c = 0; c < kPart; c += 32) {
-          if (!there(o, part * kPart + c)) break;
+        for (int i = 0; i < kUnits; ++i) {
+          const int c = (part + i * kGroups) * 32;
+          if (!there(o, c)) break;
           float v[32];
           __syncwarp();
           if (slices) {
-            tmem_load32(quadBase + (unsigned)(buf * BN + part * kPart + c), v);
+            tmem_load32(quadBase + (unsigned)(buf * BN + c), v);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
           }
-          store(o, part * kPart + c, v);
+          store(o, c, v);
         }
         if (slices) release();
       }
@@ -500,10 +599,15 @@ vr_result_t pad_matrix(Matrix* m, char* w, const OpDevice& dev, void* stream) {
                    dim3(256), args, 0, stream);
 }
 
+// What a call multiplies: K summed; rows and dW's sums are counted on the device.
+struct GroupedSize {
+  size_t M, N, K, rows;
+  int groups;
+};
+
 template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
-vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, size_t M, size_t N,
-                   size_t K, size_t rows, int groups, const int* counts, void* out, size_t ld,
-                   void* stream) {
+vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, const GroupedSize& z,
+                   int cap, const int* counts, void* out, size_t ld, void* stream) {
   using Shape = GroupedShape<BN, PAIR>;
   using Is = KindOf<KIND>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -514,27 +618,27 @@ vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, size_t
                         m.stride * 2 * m.rows, boxRows);
   };
   vr_result_t e = map(&g.a, a, Is::kAMn ? kTileK : kTileM);
-  if (e != VR_SUCCESS || (e = map(&g.b, b, Is::kBMn ? kTileK : Shape::kBRows)) != VR_SUCCESS ||
+  if (e != VR_SUCCESS || (e = map(&g.b, b, Is::kBMn ? kTileK : kBox)) != VR_SUCCESS ||
       (e = gemm_prepare(fn, dev.device, Shape::kSmem)) != VR_SUCCESS)
     return e;
   g.counts = counts;
-  g.groups = groups;
-  g.rows = (int)rows;
-  g.M = (int)M;
-  g.N = (int)N;
-  g.K = (int)K;
+  g.groups = z.groups;
+  g.rows = (int)z.rows;
+  g.M = (int)z.M;
+  g.N = (int)z.N;
+  g.K = (int)z.K;
+  g.cap = cap;
   g.out = out;
   g.ld = (long long)ld;
   const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * ld);
-  g.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 2;
+  g.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
   g.status = dev.status;
   g.timeoutNs = dev.timeoutNs;
   // at most so many tiles: every group's last one may be cut
-  const size_t tm = (M + Shape::kTileRows - 1) / Shape::kTileRows, tn = (N + BN - 1) / BN;
-  const size_t some = std::min<size_t>((size_t)groups, rows);
-  const size_t tiles = Is::kWeight ? (size_t)groups * tm * tn
-                       : Is::kRows ? (rows / Shape::kTileRows + some) * tn
-                                   : (rows / BN + some) * tm;
+  const size_t tm = (z.M + Shape::kTileRows - 1) / Shape::kTileRows;
+  const size_t tiles =
+      Is::kWeight ? (size_t)z.groups * tm * ((z.N + BN - 1) / BN)
+                  : (z.rows / cap + std::min<size_t>((size_t)z.groups, z.rows)) * tm;
   constexpr size_t kCtas = PAIR ? 2 : 1;
   const size_t grid = std::min<size_t>(tiles, dev.sms / kCtas) * kCtas;
   void* args[] = {&g};
@@ -548,44 +652,46 @@ constexpr int kLongChunk = 32;
 template <typename T>
 constexpr size_t kLongSum = std::is_same<T, __half>::value ? 32768 : 262144;
 
-constexpr size_t kFewRows = 32, kPairRows = 512;  // a group on average
+constexpr size_t kFewRows = 32;  // a group on average
 
+// out or dX: w's rows by a group's rows.
+template <typename T, int KIND>
+vr_result_t rows_product(const OpDevice& dev, const Matrix& w, const Matrix& x,
+                         const GroupedSize& z, const int* counts, void* out, size_t ld,
+                         void* stream) {
+  const bool lng = z.K > kLongSum<T>;
+#define VR_GO(BN, PAIR, CAP)                                                                   \
+  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, w, x, z, CAP, counts, out, ld, stream)     \
+       : launch<T, BN, KIND, PAIR, 0>(dev, w, x, z, CAP, counts, out, ld, stream))
+  if (z.rows <= kFewRows * (size_t)z.groups) return VR_GO(32, false, 32);
+  if (z.M <= kTileM) return VR_GO(256, false, 256);
+  return VR_GO(256, true, 256);
+#undef VR_GO
+}
 template <typename T>
 vr_result_t linear(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
                    size_t outDim, int groups, const int* counts, void* out, size_t ld,
                    void* stream) {
-  const bool lng = dim > kLongSum<T>;
-#define VR_GO(BN, KIND, PAIR, A, B, M, N)                                                       \
-  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, A, B, M, N, dim, rows, groups, counts, out, \
-                                               ld, stream)                                      \
-       : launch<T, BN, KIND, PAIR, 0>(dev, A, B, M, N, dim, rows, groups, counts, out, ld, stream))
-  if (rows <= kFewRows * (size_t)groups) return VR_GO(32, kFewLinear, false, p.w, p.x, outDim, rows);
-  if (rows < kPairRows * (size_t)groups) return VR_GO(256, kLinear, false, p.x, p.w, rows, outDim);
-  return VR_GO(256, kLinear, true, p.x, p.w, rows, outDim);
-#undef VR_GO
+  return rows_product<T, kLinear>(dev, p.w, p.x, {outDim, rows, dim, rows, groups}, counts, out,
+                                  ld, stream);
 }
 template <typename T>
 vr_result_t grad_rows(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
                       size_t outDim, int groups, const int* counts, void* out, void* stream) {
-  const bool lng = outDim > kLongSum<T>;
-#define VR_GO(BN, KIND, PAIR, A, B, M, N)                                                          \
-  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, A, B, M, N, outDim, rows, groups, counts, out, \
-                                               dim, stream)                                        \
-       : launch<T, BN, KIND, PAIR, 0>(dev, A, B, M, N, outDim, rows, groups, counts, out, dim,     \
-                                      stream))
-  if (rows <= kFewRows * (size_t)groups) return VR_GO(32, kFewGradRows, false, p.w, p.dy, dim, rows);
-  if (rows < kPairRows * (size_t)groups) return VR_GO(256, kGradRows, false, p.dy, p.w, rows, dim);
-  return VR_GO(256, kGradRows, true, p.dy, p.w, rows, dim);
-#undef VR_GO
+  return rows_product<T, kGradRows>(dev, p.w, p.dy, {dim, rows, outDim, rows, groups}, counts, out,
+                                    dim, stream);
 }
 template <typename T>
 vr_result_t grad_weight(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
                         size_t outDim, int groups, const int* counts, void* out, void* stream) {
-  if (rows > kLongSum<T>)
-    return launch<T, 256, kGradWeight, false, kLongChunk>(dev, p.dy, p.x, outDim, dim, rows, rows,
-                                                          groups, counts, out, dim, stream);
-  return launch<T, 256, kGradWeight, false, 0>(dev, p.dy, p.x, outDim, dim, rows, rows, groups,
-                                               counts, out, dim, stream);
+  const GroupedSize z = {outDim, dim, rows, rows, groups};
+#define VR_GO(PAIR)                                                                               \
+  (rows > kLongSum<T>                                                                             \
+       ? launch<T, 256, kGradWeight, PAIR, kLongChunk>(dev, p.dy, p.x, z, 256, counts, out, dim,  \
+                                                       stream)                                    \
+       : launch<T, 256, kGradWeight, PAIR, 0>(dev, p.dy, p.x, z, 256, counts, out, dim, stream))
+  return outDim <= kTileM ? VR_GO(false) : VR_GO(true);
+#undef VR_GO
 }
 
 }  // namespace
