@@ -6,7 +6,12 @@
 //
 // All tensors of a launch are cut into chunks, which the CTAs take in turn; a
 // warp updates blocks of 256 elements, eight consecutive ones a lane, in one
-// pass over every array.
+// pass over every array.  With states of 32 bits that is bound by memory: 147 M
+// parameters in bf16 with masters, 28 bytes each, take 620 to 638 us (6.4 to 6.6
+// TB/s).  With states of 8 bits it is 16 bytes and 65 instructions an element: 122
+// M take 365 to 380 us (5.2 to 5.4 TB/s), the issue slots 57 to 60 % busy (82
+// instructions and 430 us before codes were packed four at a time and decoded by
+// conversions).
 //
 // States of 8 bits.  256 elements share a power of two as scale, by the
 // largest of them.  m keeps a sign, four bits of exponent and three of
@@ -23,15 +28,18 @@
 // The states are computed with each operation rounded by itself, so that the
 // codes are the same wherever the formulas are evaluated in 32 bits.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
 #include <vector>
 
+#include <cuda_fp16.h>
+
 #include "common.h"
 #include "fold.cuh"
-#include "ops.h"
+#include "gemm_host.h"
 
 namespace vr {
 namespace {
@@ -64,12 +72,14 @@ struct AdamArgs {
 };
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments exceed 4 KB");
 
-// A bijection of 32-bit numbers in which every bit depends on all bits.
+// A bijection of 32-bit numbers in which every bit depends on all bits.  (A
+// changed bit of x changes each bit of the result with a probability within
+// 0.004 of a half, what 200000 samples resolve; the factors are digits of the
+// roots of 2 and 3.)
+constexpr unsigned kMix1 = 0x6a09e667u, kMix2 = 0xbb67ae85u;
 __host__ __device__ __forceinline__ unsigned mix(unsigned x) {
-  x ^= x >> 16;
-  x *= 0x6a09e667u;
-  x ^= x >> 15;
-  x *= 0xbb67ae85u;
+  x = (x ^ x >> 16) * kMix1;
+  x = (x ^ x >> 15) * kMix2;
   return x ^ x >> 16;
 }
 
@@ -83,13 +93,16 @@ struct Eight {
     if (vec && n >= kLane) {
       uint32_t w[kWords];
       load_words(p, w);
-      const Bits* r = reinterpret_cast<const Bits*>(w);
-#pragma unroll
-      for (int i = 0; i < kLane; ++i) x[i] = Ty<T>::widen(r[i]);
+      widen(w, x);
     } else {
 #pragma unroll
       for (int i = 0; i < kLane; ++i) x[i] = i < n ? Ty<T>::widen(b[i]) : 0.0f;
     }
+  }
+  static __device__ __forceinline__ void widen(const uint32_t (&w)[kWords], float (&x)[kLane]) {
+    const Bits* r = reinterpret_cast<const Bits*>(w);
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) x[i] = Ty<T>::widen(r[i]);
   }
   static __device__ __forceinline__ void store(void* p, int n, bool vec,
                                                const float (&x)[kLane]) {
@@ -127,8 +140,7 @@ struct Eight {
   }
 };
 
-// Codes of eight elements, and what they stand for: the code's digits as those
-// of a 32-bit number, times 2^LIFT and the block's scale.
+// Codes of eight elements.
 __device__ __forceinline__ uint2 load_codes(const void* p, int n, bool vec) {
   if (vec && n >= kLane) return *static_cast<const uint2*>(p);
   const uint8_t* b = static_cast<const uint8_t*>(p);
@@ -148,52 +160,117 @@ __device__ __forceinline__ void store_codes(void* p, int n, bool vec, uint2 q) {
   for (int i = 0; i < kLane; ++i)
     if (i < n) b[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
 }
-__device__ __forceinline__ unsigned code_at(uint2 q, int i) {
-  return (i < 4 ? q.x : q.y) >> (8 * (i % 4)) & 255u;
-}
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float power(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
+// The top bytes of four words.
+__device__ __forceinline__ unsigned top_bytes(const unsigned (&x)[kLane], int first) {
+  const unsigned lo = __byte_perm(x[first], x[first + 1], 0x0073);
+  return __byte_perm(lo, __byte_perm(x[first + 2], x[first + 3], 0x0073), 0x5410);
+}
 
-template <bool SECOND>
-struct State8 {
-  static constexpr int kTop = SECOND ? 15 : 7;       // exponent of a block's largest value
-  static constexpr int kLift = SECOND ? 112 : 120;   // of a code's value above the 32-bit number's
-  static __device__ __forceinline__ void decode(uint2 q, float scale, float (&x)[kLane]) {
+// Exponents: of a block's largest value, and of a code's value above that of
+// the 32-bit number with its digits.
+constexpr int kTopM = 7, kLiftM = 120, kTopV = 15, kLiftV = 112;
+
+__device__ __forceinline__ void decode_m(uint2 q, float scale, float (&x)[kLane]) {
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) {
-      const unsigned c = code_at(q, i);
-      const float y =
-          __fmul_rn(__fmul_rn(__uint_as_float((SECOND ? c : c & 127u) << 20), power(kLift)), scale);
-      x[i] = __uint_as_float(__float_as_uint(y) | (SECOND ? 0u : (c & 128u) << 24));
-    }
+  for (int i = 0; i < 2; ++i) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(i ? q.y : q.x));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    x[4 * i] = a.x * scale, x[4 * i + 1] = a.y * scale;
+    x[4 * i + 2] = b.x * scale, x[4 * i + 3] = b.y * scale;
   }
-  // The codes of a warp's block and its scale; `cut`: 20 random bits each.
-  // A NaN or an infinity makes the scale NaN.
-  static __device__ __forceinline__ uint2 encode(const float (&x)[kLane],
-                                                 const unsigned (&cut)[kLane], float* scale) {
-    unsigned top = 0;  // of the absolute values; NaN is above infinity
+}
+__device__ __forceinline__ void decode_v(uint2 q, float scale, float (&x)[kLane]) {
+  // (2^lift scale in one factor where that is a 32-bit number)
+  const bool large = scale >= power(127 - kLiftV);
+  const float by = large ? power(kLiftV) : scale * power(kLiftV);
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-    uint2 q = make_uint2(0, 0);
-    if (top >= 0x7f800000u) {
-      *scale = __uint_as_float(0x7fffffffu);
-      return q;
-    }
-    const int e = max((int)(top >> 23) - 127, -110);
-    *scale = power(e - kTop);
-    const float up = power(kTop - e);
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) {
-      const float y = __fmul_rn(__fmul_rn(fabsf(x[i]), up), power(-kLift));
-      unsigned c = (__float_as_uint(y) + cut[i]) >> 20;
-      if (SECOND) c = x[i] > 0.0f ? max(c, 1u) : c;
-      else c |= x[i] < 0.0f && c ? 128u : 0u;
-      (i < 4 ? q.x : q.y) |= c << (8 * (i % 4));
-    }
-    return q;
+  for (int i = 0; i < 4; ++i) {  // two codes: 20 bits up each
+    const unsigned two = __byte_perm(i < 2 ? q.x : q.y, 0, i % 2 ? 0x4342 : 0x4140) * 16u;
+    x[2 * i] = __fmul_rn(__uint_as_float(two << 16), by);
+    x[2 * i + 1] = __fmul_rn(__uint_as_float(two & 0xffff0000u), by);
   }
-};
+  if (large) {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) x[i] = __fmul_rn(x[i], scale);
+  }
+}
+// max of |a| and b that keeps NaN
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmax.NaN.f32 %0, t, %2;\n\t}"
+      : "=f"(r)
+      : "f"(a), "f"(b));
+  return r;
+}
+// A warp's block by its largest absolute value: its scale, 2^(exponent - top),
+// and x multiplied so that the codes' digits are those of 32-bit numbers from
+// bit 20 on.  (One factor, which may be a denormal; where it would be less, x
+// goes down by 2^64 first.)  An infinity or a NaN makes the scale NaN.
+template <int TOP, int LIFT>
+__device__ __forceinline__ float block_scale(const float (&x)[kLane], float (&y)[kLane]) {
+  float largest = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) largest = max_abs(x[i], largest);
+  const unsigned all = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
+  int e = max((int)(all >> 23) - 127, -110);
+  const float scale = all >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : power(e - TOP);
+  if (e > 149 + TOP - LIFT) {
+    e -= 64;
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) y[i] = __fmul_rn(x[i], power(-64));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) y[i] = x[i];
+  }
+  const int k = TOP - LIFT - e;
+  const float by = __uint_as_float(k >= -126 ? (unsigned)(k + 127) << 23 : 1u << (k + 149));
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) y[i] = __fmul_rn(y[i], by);
+  return scale;
+}
+// New codes; `cut`: 16 random bits each, from bit 8.  (Shifted up by 4, a code
+// is a word's top byte.)
+__device__ __forceinline__ uint2 encode_m(const float (&x)[kLane], const unsigned (&cut)[kLane],
+                                          float* scale) {
+  float y[kLane];
+  *scale = block_scale<kTopM, kLiftM>(x, y);
+  unsigned t[kLane], u[kLane];
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) {
+    t[i] = __float_as_uint(y[i]);
+    u[i] = t[i] * 16u + cut[i];
+  }
+  if (*scale != *scale) return make_uint2(0, 0);
+  return make_uint2((top_bytes(t, 0) & 0x80808080u) | top_bytes(u, 0),
+                    (top_bytes(t, 4) & 0x80808080u) | top_bytes(u, 4));
+}
+__device__ __forceinline__ uint2 encode_v(const float (&x)[kLane], const unsigned (&cut)[kLane],
+                                          float* scale) {
+  float y[kLane];
+  *scale = block_scale<kTopV, kLiftV>(x, y);
+  unsigned t[kLane], u[kLane], least = ~0u;
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) {
+    t[i] = __float_as_uint(y[i]);
+    least = min(least, t[i]);
+  }
+  if (least < 1u << 20) {  // a positive one does not become zero
+#pragma unroll
+    for (int i = 0; i < kLane; ++i)
+      if (x[i] > 0.0f) t[i] = max(t[i], 1u << 20);
+  }
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) u[i] = t[i] * 16u + cut[i];
+  if (*scale != *scale) return make_uint2(0, 0);
+  return make_uint2(top_bytes(u, 0), top_bytes(u, 4));
+}
 
 __device__ __forceinline__ bool bit_of(const unsigned (&w)[2], int i) {
   return (w[i / 32] >> (i % 32) & 1) != 0;
@@ -210,91 +287,285 @@ __device__ __forceinline__ int tensor_of(const AdamArgs& a, int c) {
   return lo;
 }
 
+// The chunks that a CTA takes one after the other, and a warp's place in each:
+// kParts blocks kStride elements apart.  States of 32 bits: those of the warps
+// interleaved (620 to 638 us for 147 M parameters; 645 where a warp's follow one
+// another), states of 8 bits: a warp's side by side (365 to 380 us for 122 M;
+// 390 interleaved).
+constexpr int kParts = kChunk / (kWarps * kBlock);
+template <int BITS>
+constexpr int kStride = BITS == 8 ? kBlock : kWarps * kBlock;
+struct Cursor {
+  int chunk, tensor;
+  __device__ __forceinline__ Cursor(const AdamArgs& a)
+      : chunk((int)blockIdx.x), tensor(tensor_of(a, min(chunk, a.first[a.count] - 1))) {}
+  __device__ __forceinline__ bool more(const AdamArgs& a) const { return chunk < a.first[a.count]; }
+  __device__ __forceinline__ void advance(const AdamArgs& a) {
+    chunk += gridDim.x;
+    while (more(a) && chunk >= a.first[tensor + 1]) ++tensor;
+  }
+  // the first element of the warp's first block
+  template <int BITS>
+  __device__ __forceinline__ long long at(const AdamArgs& a) const {
+    constexpr int kWarp = BITS == 8 ? kParts * kBlock : kBlock;
+    return (long long)(chunk - a.first[tensor]) * kChunk + (int)(threadIdx.x / 32) * kWarp;
+  }
+};
+// Whole blocks with vector accesses.
+template <int BITS>
+__device__ __forceinline__ bool whole(const AdamArgs& a, int tensor, const Tensor& t, long long at) {
+  return bit_of(a.vec, tensor) && t.size - at >= (kParts - 1) * kStride<BITS> + kBlock;
+}
+
+// Blocks on their way.  With states of 8 bits a block is 2 KB, too little to
+// keep the memory busy while it is computed on: each lane copies its share of
+// the next chunk's blocks into shared memory (cp.async, no registers).
+constexpr int kAhead = 2;
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+// A block of a warp's slot: planes of 16 bytes a lane, the codes, the scales.
+template <typename P, typename G>
+struct Slot {
+  static constexpr int kG = Eight<G>::kWords / 4, kP = Eight<P>::kWords / 4;  // planes
+  static constexpr int kCodes = (kG + kP) * 512, kScales = kCodes + 512, kBytes = kScales + 16;
+  // (blocks that are not whole: the scales of those that are there)
+  static __device__ __forceinline__ void fill(uint32_t slot, const Tensor& t, const void* param,
+                                              long long at, bool whole) {
+    const int lane = threadIdx.x % 32;
+    if (whole) {
+      const long long i0 = at + lane * kLane;
+      const char* g = reinterpret_cast<const char*>(static_cast<const G*>(t.grad) + i0);
+      const char* p = reinterpret_cast<const char*>(static_cast<const P*>(param) + i0);
+      const char *m = static_cast<const char*>(t.m) + i0, *v = static_cast<const char*>(t.v) + i0;
+      const uint32_t to = slot + lane * 16, codes = slot + kCodes + lane * 8;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+          copy_async(to + k * kBytes + i * 512, g + k * (kStride<8> * (int)sizeof(G)) + i * 16, 16);
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+          copy_async(to + k * kBytes + (kG + i) * 512, p + k * (kStride<8> * (int)sizeof(P)) + i * 16,
+                     16);
+        copy_async(codes + k * kBytes, m + k * kStride<8>, 8);
+        copy_async(codes + k * kBytes + 256, v + k * kStride<8>, 8);
+      }
+    }
+    const int k = lane / 2;
+    if (k < kParts && at + k * kStride<8> < t.size)
+      copy_async(slot + k * kBytes + kScales + lane % 2 * 4,
+                 (lane % 2 ? t.vScale : t.mScale) + (at / kBlock + k * (kStride<8> / kBlock)), 4);
+  }
+  template <int PLANES>
+  static __device__ __forceinline__ void read(uint32_t plane, uint32_t (&w)[4 * PLANES]) {
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(plane + i * 512 + threadIdx.x % 32 * 16)
+                   : "memory");
+  }
+  static __device__ __forceinline__ void gradient(uint32_t slot, float (&x)[kLane]) {
+    uint32_t w[4 * kG];
+    read<kG>(slot, w);
+    Eight<G>::widen(w, x);
+  }
+  static __device__ __forceinline__ void parameter(uint32_t slot, float (&x)[kLane]) {
+    uint32_t w[4 * kP];
+    read<kP>(slot + kG * 512, w);
+    Eight<P>::widen(w, x);
+  }
+  static __device__ __forceinline__ uint2 codes(uint32_t slot, int which) {
+    uint2 q;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(q.x), "=r"(q.y)
+                 : "r"(slot + kCodes + which * 256 + threadIdx.x % 32 * 8)
+                 : "memory");
+    return q;
+  }
+  static __device__ __forceinline__ float scale(uint32_t slot, int which) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(slot + kScales + which * 4) : "memory");
+    return x;
+  }
+};
+
+// What a step multiplies by.
+struct Step {
+  float gradScale, up, down, keep;
+  unsigned key;
+};
+
+// Where a lane's elements of a warp's first block are.
+template <typename P, typename G, bool MASTER>
+struct Lane {
+  using Read = typename Select<MASTER, float, P>::type;  // the parameters that are read
+  const G* grad;
+  P* param;
+  Read* read;
+  char *m, *v;
+  float *mScale, *vScale;
+  unsigned long long place;  // among the call's tensors
+  __device__ __forceinline__ Lane(const Tensor& t, long long at, int bytes) {
+    const long long i0 = at + (int)(threadIdx.x % 32) * kLane;
+    grad = static_cast<const G*>(t.grad) + i0;
+    param = static_cast<P*>(t.param) + i0;
+    if constexpr (MASTER) read = t.master + i0;
+    else read = param;
+    m = static_cast<char*>(t.m) + i0 * bytes;
+    v = static_cast<char*>(t.v) + i0 * bytes;
+    if (bytes == 1) {
+      const long long block = (long long)((unsigned long long)at / kBlock);
+      mScale = t.mScale + block;
+      vScale = t.vScale + block;
+      place = (unsigned long long)(t.block + block) * kBlock + threadIdx.x % 32 * kLane;
+    }
+  }
+};
+
+// Block `part` of a warp's, its inputs in `slot` of shared memory (states of 8
+// bits, WHOLE blocks) or where they are.  n: elements of the lane that are there.
+template <typename P, typename G, int BITS, bool MASTER, bool WHOLE>
+__device__ __forceinline__ void update_block(const AdamArgs& a, const Step& s,
+                                             const Lane<P, G, MASTER>& l, int part, int n,
+                                             uint32_t slot) {
+  using Read = typename Select<MASTER, float, P>::type;
+  using S = Slot<Read, G>;
+  const int off = part * kStride<BITS>;
+  float g[kLane], p[kLane], m[kLane], v[kLane];
+  char *codesM = l.m + off, *codesV = l.v + off;
+  float *wordsM = reinterpret_cast<float*>(l.m) + off, *wordsV = reinterpret_cast<float*>(l.v) + off;
+  if (BITS == 8) {
+    uint2 qm, qv;
+    if (WHOLE) {
+      S::gradient(slot, g);
+      S::parameter(slot, p);
+      qm = S::codes(slot, 0);
+      qv = S::codes(slot, 1);
+    } else {
+      qm = load_codes(codesM, n, false);
+      qv = load_codes(codesV, n, false);
+    }
+    decode_m(qm, S::scale(slot, 0), m);
+    decode_v(qv, S::scale(slot, 1), v);
+  } else {
+    Eight<float>::load(wordsM, n, WHOLE, m);
+    Eight<float>::load(wordsV, n, WHOLE, v);
+  }
+  if (BITS != 8 || !WHOLE) {
+    Eight<G>::load(l.grad + off, n, WHOLE, g);
+    Eight<Read>::load(l.read + off, n, WHOLE, p);
+  }
+  const float rest1 = 1.0f - a.beta1, rest2 = 1.0f - a.beta2;
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) {
+    const float x = __fmul_rn(g[i], s.gradScale);
+    m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, rest1));
+    v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), rest2));
+    // (root + eps is 0 or above 2^-75: no denormal to be flushed)
+    float root, inv;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i] * s.down));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(root + a.eps));
+    p[i] = p[i] * s.keep - s.up * m[i] * inv;
+  }
+  if (MASTER) Eight<Read>::store(l.read + off, n, WHOLE, p);
+  Eight<P>::store(l.param + off, n, WHOLE, p);
+  if (BITS == 8) {
+    // mix(x ^ i) of the lane's eight places (i < 8 leaves x >> 16 as it is): the
+    // upper half of r for v, its lower half after r ^= r >> 16 for m
+    const unsigned long long place = l.place + (unsigned)off;
+    const unsigned x = mix(s.key ^ (unsigned)(place >> 32)) ^ (unsigned)place;
+    unsigned cutM[kLane], cutV[kLane];
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) {
+      unsigned r = ((x ^ x >> 16) ^ (unsigned)i) * kMix1;
+      r = (r ^ r >> 15) * kMix2;
+      cutV[i] = __byte_perm(r, 0, 0x4324);
+      cutM[i] = __byte_perm(r, 0, 0x4104) ^ cutV[i];
+    }
+    float scaleM, scaleV;
+    const uint2 qm = encode_m(m, cutM, &scaleM), qv = encode_v(v, cutV, &scaleV);
+    store_codes(codesM, n, WHOLE, qm);
+    store_codes(codesV, n, WHOLE, qv);
+    if (threadIdx.x % 32 == 0) l.mScale[off / kBlock] = scaleM, l.vScale[off / kBlock] = scaleV;
+  } else {
+    Eight<float>::store(wordsM, n, WHOLE, m);
+    Eight<float>::store(wordsV, n, WHOLE, v);
+  }
+}
+// The blocks of a warp that are not whole.
+template <typename P, typename G, int BITS, bool MASTER>
+__device__ __noinline__ void update_rest(const AdamArgs& a, const Step& s, const Tensor& t,
+                                         long long at, uint32_t slot) {
+  const Lane<P, G, MASTER> l(t, at, BITS / 8);
+#pragma unroll 1
+  for (int k = 0; k < kParts && at + k * kStride<BITS> < t.size; ++k) {
+    const long long left = t.size - at - k * kStride<BITS> - (int)(threadIdx.x % 32) * kLane;
+    update_block<P, G, BITS, MASTER, false>(
+        a, s, l, k, (int)max(min(left, (long long)kLane), 0LL),
+        slot + (unsigned)(k * Slot<typename Lane<P, G, MASTER>::Read, G>::kBytes));
+  }
+}
+
 // P: of the parameters, G: of the gradients; BITS of the states; MASTER: 32-bit
 // parameters beside P's, which are written only.
 template <typename P, typename G, int BITS, bool MASTER>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 2 : 4) adamw_kernel(const __grid_constant__ AdamArgs a) {
+  using S = Slot<typename Lane<P, G, MASTER>::Read, G>;
+  extern __shared__ uint4 smem[];
   pdl_launch();
   pdl_wait();
-  float gradScale = a.gradScale, up = a.up, down = a.down, keep = a.keep;
+  Step s = {a.gradScale, a.up, a.down, a.keep, 0};
   long long step = a.step;
   if (a.control) {
     const float lr = a.control[0], t = a.control[1];
-    gradScale = a.control[2];
-    if (!(fabsf(gradScale) < INFINITY)) return;  // no step
+    s.gradScale = a.control[2];
+    if (!(fabsf(s.gradScale) < INFINITY)) return;  // no step
     step = (long long)t;
-    up = lr / -expm1f(t * a.logBeta1);
-    down = 1.0f / -expm1f(t * a.logBeta2);
-    keep = 1.0f - lr * a.weightDecay;
+    s.up = lr / -expm1f(t * a.logBeta1);
+    s.down = 1.0f / -expm1f(t * a.logBeta2);
+    s.keep = 1.0f - lr * a.weightDecay;
   }
-  unsigned key = 0;
-  if (BITS == 8) key = mix(mix(a.seedKey ^ (unsigned)step) ^ (unsigned)(step >> 32));
-  const float rest1 = 1.0f - a.beta1, rest2 = 1.0f - a.beta2;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int chunks = a.first[a.count];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int lo = tensor_of(a, c);
-    const Tensor& t = a.tensor[lo];
-    const bool vec = bit_of(a.vec, lo);
-    const long long from = (long long)(c - a.first[lo]) * kChunk;
-#pragma unroll 1
-    for (int part = 0; part < kChunk / (kWarps * kBlock); ++part) {
-      const long long at = from + (part * kWarps + warp) * kBlock;  // of the warp's block
-      if (at >= t.size) break;
-      const long long i0 = at + lane * kLane;
-      const int n = (int)max(min(t.size - i0, (long long)kLane), 0LL);
-      float g[kLane], p[kLane], m[kLane], v[kLane];
-      uint2 qm, qv;
-      float scaleM, scaleV;
-      char *codesM = static_cast<char*>(t.m) + i0, *codesV = static_cast<char*>(t.v) + i0;
-      float *wordsM = static_cast<float*>(t.m) + i0, *wordsV = static_cast<float*>(t.v) + i0;
-      if (BITS == 8) {
-        qm = load_codes(codesM, n, vec);
-        qv = load_codes(codesV, n, vec);
-        scaleM = t.mScale[at / kBlock];
-        scaleV = t.vScale[at / kBlock];
-      } else {
-        Eight<float>::load(wordsM, n, vec, m);
-        Eight<float>::load(wordsV, n, vec, v);
+  if (BITS == 8) s.key = mix(mix(a.seedKey ^ (unsigned)step) ^ (unsigned)(step >> 32));
+  constexpr unsigned kSlot = kParts * S::kBytes;
+  const uint32_t slot0 = BITS == 8 ? smem_addr(smem) + threadIdx.x / 32 * (kAhead * kSlot) : 0u;
+  Cursor now(a), ahead(a);
+  auto fill = [&](int slot) {
+    if (BITS == 8) {
+      if (ahead.more(a)) {
+        const Tensor& t = a.tensor[ahead.tensor];
+        const long long at = ahead.at<BITS>(a);
+        S::fill(slot0 + (unsigned)slot * kSlot, t, MASTER ? (void*)t.master : t.param, at,
+                whole<BITS>(a, ahead.tensor, t, at));
+        ahead.advance(a);
       }
-      Eight<G>::load(static_cast<const G*>(t.grad) + i0, n, vec, g);
-      if (MASTER) Eight<float>::load(t.master + i0, n, vec, p);
-      else Eight<P>::load(static_cast<const P*>(t.param) + i0, n, vec, p);
-      if (BITS == 8) {
-        State8<false>::decode(qm, scaleM, m);
-        State8<true>::decode(qv, scaleV, v);
-      }
-#pragma unroll
-      for (int i = 0; i < kLane; ++i) {
-        const float x = __fmul_rn(g[i], gradScale);
-        m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, rest1));
-        v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), rest2));
-        float root;
-        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i] * down));
-        p[i] = p[i] * keep - __fdividef(up * m[i], root + a.eps);
-      }
-      if (MASTER) Eight<float>::store(t.master + i0, n, vec, p);
-      Eight<P>::store(static_cast<P*>(t.param) + i0, n, vec, p);
-      if (BITS == 8) {
-        const unsigned long long place =
-            (unsigned long long)(t.block + at / kBlock) * kBlock + lane * kLane;
-        const unsigned by = mix(key ^ (unsigned)(place >> 32));
-        unsigned cutM[kLane], cutV[kLane];
-#pragma unroll
-        for (int i = 0; i < kLane; ++i) {
-          const unsigned r = mix(by ^ ((unsigned)place + i));
-          cutM[i] = (r & 0xffffu) << 4;
-          cutV[i] = r >> 16 << 4;
-        }
-        qm = State8<false>::encode(m, cutM, &scaleM);
-        qv = State8<true>::encode(v, cutV, &scaleV);
-        store_codes(codesM, n, vec, qm);
-        store_codes(codesV, n, vec, qv);
-        if (lane == 0) t.mScale[at / kBlock] = scaleM, t.vScale[at / kBlock] = scaleV;
-      } else {
-        Eight<float>::store(wordsM, n, vec, m);
-        Eight<float>::store(wordsV, n, vec, v);
-      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  fill(0);
+  for (int slot = 0; now.more(a); now.advance(a), slot ^= 1) {
+    __syncwarp();  // (the scales of the slot that is filled next have been read)
+    fill(slot ^ 1);
+    const Tensor& t = a.tensor[now.tensor];
+    const long long at = now.at<BITS>(a);
+    const uint32_t from = slot0 + (unsigned)slot * kSlot;
+    if (BITS == 8) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+    }
+    if (whole<BITS>(a, now.tensor, t, at)) {
+      const Lane<P, G, MASTER> l(t, at, BITS / 8);
+#pragma unroll(BITS == 8 ? kParts : 1)
+      for (int k = 0; k < kParts; ++k)
+        update_block<P, G, BITS, MASTER, true>(a, s, l, k, kLane, from + k * S::kBytes);
+    } else {
+      update_rest<P, G, BITS, MASTER>(a, s, t, at, from);
     }
   }
 }
@@ -320,13 +591,11 @@ __global__ void __launch_bounds__(kThreads) adamw_values_kernel(
       const int n = (int)max(min(t.size - i0, (long long)kLane), 0LL);
       float x[kLane];
       if (t.param) {
-        State8<false>::decode(load_codes(static_cast<const char*>(t.m) + i0, n, vec),
-                              t.mScale[at / kBlock], x);
+        decode_m(load_codes(static_cast<const char*>(t.m) + i0, n, vec), t.mScale[at / kBlock], x);
         Eight<float>::store(static_cast<float*>(t.param) + i0, n, vec, x);
       }
       if (t.master) {
-        State8<true>::decode(load_codes(static_cast<const char*>(t.v) + i0, n, vec),
-                             t.vScale[at / kBlock], x);
+        decode_v(load_codes(static_cast<const char*>(t.v) + i0, n, vec), t.vScale[at / kBlock], x);
         Eight<float>::store(t.master + i0, n, vec, x);
       }
     }
@@ -334,21 +603,25 @@ __global__ void __launch_bounds__(kThreads) adamw_values_kernel(
 }
 
 // ------------------------------------------------------------- host side
+struct AdamKernel {
+  const void* fn;
+  size_t smem;
+};
+template <typename P, typename G, bool MASTER>
+AdamKernel kernel_of(int bits) {
+  using Read = typename Select<MASTER, float, P>::type;
+  if (bits == 32) return {(const void*)adamw_kernel<P, G, 32, MASTER>, 0};
+  return {(const void*)adamw_kernel<P, G, 8, MASTER>,
+          (size_t)kWarps * kAhead * kParts * Slot<Read, G>::kBytes};
+}
 template <typename P, typename G>
-const void* kernel_of(int bits, bool master) {
-  if constexpr (std::is_same<P, float>::value) {
-    return bits == 8 ? (const void*)adamw_kernel<P, G, 8, false>
-                     : (const void*)adamw_kernel<P, G, 32, false>;
-  } else {
-    if (master)
-      return bits == 8 ? (const void*)adamw_kernel<P, G, 8, true>
-                       : (const void*)adamw_kernel<P, G, 32, true>;
-    return bits == 8 ? (const void*)adamw_kernel<P, G, 8, false>
-                     : (const void*)adamw_kernel<P, G, 32, false>;
-  }
+AdamKernel kernel_of(int bits, bool master) {
+  if constexpr (!std::is_same<P, float>::value)
+    if (master) return kernel_of<P, G, true>(bits);
+  return kernel_of<P, G, false>(bits);
 }
 template <typename P>
-const void* kernel_of(int gradDtype, int bits, bool master) {
+AdamKernel kernel_of(int gradDtype, int bits, bool master) {
   return gradDtype == VR_FLOAT32   ? kernel_of<P, float>(bits, master)
          : gradDtype == VR_FLOAT16 ? kernel_of<P, __half>(bits, master)
                                    : kernel_of<P, __nv_bfloat16>(bits, master);
@@ -367,7 +640,7 @@ struct Spans {
 // Launches `fn` over the tensors, kTensors at a time.  `fill` writes tensor i
 // and returns the address bits of its rows.
 template <class Fill>
-vr_result_t over_tensors(const void* fn, AdamArgs& a, const size_t* sizes, int count,
+vr_result_t over_tensors(const AdamKernel& k, AdamArgs& a, const size_t* sizes, int count,
                          const OpDevice& dev, void* stream, Fill fill) {
   long long block = 0;
   int i = 0;
@@ -392,8 +665,8 @@ vr_result_t over_tensors(const void* fn, AdamArgs& a, const size_t* sizes, int c
     a.first[a.count] = (int)chunks;
     void* args[] = {&a};
     const vr_result_t e =
-        op_launch(fn, dim3((unsigned)std::min<long long>(chunks, dev.sms * 8LL)), dim3(kThreads),
-                  args, 0, stream);
+        op_launch(k.fn, dim3((unsigned)std::min<long long>(chunks, dev.sms * 8LL)), dim3(kThreads),
+                  args, k.smem, stream);
     if (e != VR_SUCCESS) return e;
   }
   return VR_SUCCESS;
@@ -418,7 +691,7 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
   if (!E || !GE || (stateBits != 8 && stateBits != 32) || count < 1 || !params || !grads || !m ||
       !v || !sizes || few != (mScales != nullptr) || few != (vScales != nullptr) ||
       (masters && dtype == VR_FLOAT32) || !beta_ok(beta1) || !beta_ok(beta2) || !(eps >= 0.0f) ||
-      !std::isfinite(eps) || ((uintptr_t)control & 3) ||
+      !std::isfinite(eps) || (eps > 0.0f && eps < FLT_MIN) || ((uintptr_t)control & 3) ||
       (!control && (!std::isfinite(lr) || !std::isfinite(gradScale) || step < 1)) ||
       !std::isfinite(weightDecay))
     return VR_ERR_INVALID_ARGUMENT;
@@ -471,10 +744,12 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
     a.control = control;
     a.seedKey = mix(mix((unsigned)seed) ^ (unsigned)(seed >> 32));
     a.step = step;
-    const void* fn = dtype == VR_FLOAT32   ? kernel_of<float>(gradDtype, stateBits, false)
-                     : dtype == VR_FLOAT16 ? kernel_of<__half>(gradDtype, stateBits, masters)
-                                           : kernel_of<__nv_bfloat16>(gradDtype, stateBits, masters);
-    return over_tensors(fn, a, sizes, count, dev, stream, [&](int i, Tensor* t) {
+    const AdamKernel k = dtype == VR_FLOAT32   ? kernel_of<float>(gradDtype, stateBits, false)
+                         : dtype == VR_FLOAT16 ? kernel_of<__half>(gradDtype, stateBits, masters)
+                                               : kernel_of<__nv_bfloat16>(gradDtype, stateBits,
+                                                                          masters);
+    if (k.smem && (e = gemm_prepare(k.fn, dev.device, k.smem)) != VR_SUCCESS) return e;
+    return over_tensors(k, a, sizes, count, dev, stream, [&](int i, Tensor* t) {
       *t = {params[i],
             grads[i],
             m[i],
@@ -526,7 +801,7 @@ vr_result_t vr_adamw_values(const void* const* m, const void* const* v,
       if ((e = op_reachable(&p, 1, dev.device)) != VR_SUCCESS) return e;
     }
     AdamArgs a;
-    return over_tensors((const void*)adamw_values_kernel, a, sizes, count, dev, stream,
+    return over_tensors({(const void*)adamw_values_kernel, 0}, a, sizes, count, dev, stream,
                         [&](int i, Tensor* t) {
                           *t = {mValues ? mValues[i] : nullptr,
                                 nullptr,

@@ -8,14 +8,18 @@
 // The gradient sorts the tokens by word, stably, by the words' digits from the
 // lowest up (each pass counts the digits of every warp's run of tokens, adds
 // the counts up and moves the tokens), so that a word's rows are summed in
-// token order: the same bits on every run, without atomic additions.  Up to
-// kSmallSort tokens are sorted by one CTA in shared memory; more take two
-// launches a pass.  The sorted tokens are cut into chunks; a warp sums a slice
-// of the columns of a chunk in fp32 and writes each word's row that lies in the
-// chunk as a whole; a word that goes on over the chunk's end leaves a partial
-// sum, and a last launch adds the partial sums up in chunk order.  Rows of
-// words that do not occur are zeroed by the same launch as the sums: a lane
-// looks up its word among the sorted ones.
+// token order: the same bits on every run, without atomic additions.  Up to 8192
+// tokens (16384 where word and token fit 32 bits) are sorted by one CTA in
+// shared memory; more take two launches a pass.  The sorted tokens are cut into
+// chunks; a warp sums a slice of the columns of a chunk in fp32 and writes each
+// word's row that lies in the chunk as a whole; a word that goes on over the
+// chunk's end leaves a partial sum, and a last launch adds the partial sums up in
+// chunk order.
+//
+// Rows of words that do not occur are most of what is written.  They are zeroed
+// by the CTAs beside the one that sorts, each of which marks the words of its
+// part of the table for itself; after a sort over all SMs, by the launch that
+// sums, where a lane looks its word up among the sorted ones.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -100,47 +104,58 @@ __global__ void __launch_bounds__(kThreads) embed_lookup_kernel(
 }
 
 // ------------------------------------------------------------------ sorting
-// An item is a word and the token that has it; a token that does not count has
-// the word `vocab`, behind all others.
+// An item is a word and, in the lowest tokenBits bits, the token that has it; a
+// token that does not count has the word `vocab`, behind all others.
 using Item = unsigned long long;
-__device__ __forceinline__ unsigned word_of(Item x) { return (unsigned)(x >> 32); }
+constexpr int kItemBits = 32;  // tokenBits of the sorted items
+__device__ __forceinline__ unsigned word_of(Item x) { return (unsigned)(x >> kItemBits); }
 __device__ __forceinline__ unsigned token_of(Item x) { return (unsigned)x; }
 
 constexpr int kMaxBits = 9, kDigits = 1 << kMaxBits;  // of one pass
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kSmallSort = 8192;
+constexpr size_t kSmallBytes = 64 << 10;  // of items that one CTA sorts
 
 struct SortArgs {
   const long long* ids;
   long long ignore;
   int tokens, vocab;
   int passes, bits;   // of each pass
+  int tokenBits;
   int shift;          // this pass's lowest bit (large)
   int ctas, run;      // large: CTAs, and tokens of each
   const Item* in;     // large: null in the first pass
   Item* out;
   int* counts;        // large: [ctas][kDigits]
   unsigned* status;
+  // small: the table, whose rows of words that do not occur are zeroed (null: not)
+  char* table;
+  long long rowBytes;
+  int access;
 };
 
-__device__ __forceinline__ Item item_of(const SortArgs& a, int t) {
+__device__ __forceinline__ bool counts_as_word(const SortArgs& a, long long id) {
+  return id >= 0 && id < a.vocab && id != a.ignore;
+}
+template <typename K>
+__device__ __forceinline__ K item_of(const SortArgs& a, int t) {
   const long long id = a.ids[t];
-  const bool there = id >= 0 && id < a.vocab && id != a.ignore;
+  const bool there = counts_as_word(a, id);
   if (!there && id != a.ignore) atomicCAS(a.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
-  return (Item)(unsigned)(there ? (int)id : a.vocab) << 32 | (unsigned)t;
+  return (K)(unsigned)(there ? (int)id : a.vocab) << a.tokenBits | (unsigned)t;
 }
 
-// Counts the digits of a warp's run [lo, hi) of items into its row of counters,
-// or (MOVE) sends each to the place that its digit's counter gives.  Equal
-// digits of 32 items take consecutive places, so the order is kept.
-template <bool MOVE, class Get, class Put>
+// Counts the digits (from bit `shift` of an item) of a warp's run [lo, hi) of
+// items into its row of counters, or (MOVE) sends each to the place that its
+// digit's counter gives.  Equal digits of 32 items take consecutive places, so
+// the order is kept.
+template <typename K, bool MOVE, class Get, class Put>
 __device__ __forceinline__ void digits_of_run(unsigned* row, int lo, int hi, int shift,
                                               unsigned mask, Get get, Put put) {
   const int lane = threadIdx.x % 32;
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const bool live = i0 + lane < hi;
-    const Item x = live ? get(i0 + lane) : 0;
-    const unsigned d = live ? word_of(x) >> shift & mask : kDigits;
+    const K x = live ? get(i0 + lane) : 0;
+    const unsigned d = live ? (unsigned)(x >> shift) & mask : kDigits;
     const unsigned same = __match_any_sync(0xffffffffu, d);
     const int first = __ffs(same) - 1;
     unsigned base = 0;
@@ -198,37 +213,82 @@ __device__ __forceinline__ void clear(unsigned (*rows)[kDigits]) {
   __syncthreads();
 }
 
-// Up to kSmallSort tokens by one CTA: all passes in shared memory.
-constexpr size_t kSmallSmem = 2 * kSmallSort * sizeof(Item) + kSortWarps * kDigits * 4;
+// The rows of a part of the table whose words do not occur, zeroed by one CTA.
+constexpr int kMarked = 8192;  // words that are marked at a time
+__device__ __forceinline__ void zero_row(char* row, long long bytes, int access) {
+  const int lane = threadIdx.x % 32;
+  if (access == 16) {
+#pragma unroll 4
+    for (long long i = lane * 16; i < bytes; i += 32 * 16)
+      *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
+  } else if (access == 4) {
+#pragma unroll 4
+    for (long long i = lane * 4; i < bytes; i += 32 * 4) *reinterpret_cast<unsigned*>(row + i) = 0;
+  } else {
+#pragma unroll 4
+    for (long long i = lane * 2; i < bytes; i += 32 * 2)
+      *reinterpret_cast<unsigned short*>(row + i) = 0;
+  }
+}
+__device__ __forceinline__ void zero_rows(const SortArgs& a, unsigned* marks, int part, int parts) {
+  const int lo = (int)((long long)a.vocab * part / parts);
+  const int hi = (int)((long long)a.vocab * (part + 1) / parts);
+  for (int v0 = lo; v0 < hi; v0 += kMarked) {
+    const int n = min(kMarked, hi - v0);
+    for (int i = threadIdx.x; i < kMarked / 32; i += kSortThreads) marks[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) {
+      const long long id = a.ids[t];
+      if (id >= v0 && id < v0 + n && id != a.ignore)
+        atomicOr(&marks[(id - v0) / 32], 1u << ((id - v0) % 32));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x / 32; i < n; i += kSortWarps)
+      if (!(marks[i / 32] >> (i % 32) & 1))
+        zero_row(a.table + (long long)(v0 + i) * a.rowBytes, a.rowBytes, a.access);
+    __syncthreads();
+  }
+}
+
+// Few tokens: CTA 0 sorts them in shared memory, the others zero rows.
+constexpr size_t kSmallSmem = 2 * kSmallBytes + kSortWarps * kDigits * 4;
+template <typename K>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(
     const __grid_constant__ SortArgs a) {
   extern __shared__ Item smem[];
   __shared__ unsigned sScan[kSortWarps];
-  Item *from = smem, *to = smem + kSmallSort;
-  unsigned(*rows)[kDigits] = reinterpret_cast<unsigned(*)[kDigits]>(smem + 2 * kSmallSort);
+  K *from = reinterpret_cast<K*>(smem), *to = from + kSmallBytes / sizeof(K);
+  unsigned(*rows)[kDigits] =
+      reinterpret_cast<unsigned(*)[kDigits]>(reinterpret_cast<char*>(smem) + 2 * kSmallBytes);
   pdl_launch();
   pdl_wait();
-  for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) from[t] = item_of(a, t);
+  if (blockIdx.x > 0) {
+    zero_rows(a, &rows[0][0], (int)blockIdx.x - 1, (int)gridDim.x - 1);
+    return;
+  }
+  for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) from[t] = item_of<K>(a, t);
   const int warp = threadIdx.x / 32;
   const int run = (a.tokens + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
   const int lo = min(warp * run, a.tokens), hi = min(lo + run, a.tokens);
+  const unsigned mask = (1u << a.bits) - 1;
   for (int p = 0; p < a.passes; ++p) {
     clear(rows);
-    const int shift = p * a.bits;
-    const unsigned mask = (1u << a.bits) - 1;
+    const int shift = a.tokenBits + p * a.bits;
     auto get = [&](int i) { return from[i]; };
-    digits_of_run<false>(rows[warp], lo, hi, shift, mask, get, [](unsigned, Item) {});
+    digits_of_run<K, false>(rows[warp], lo, hi, shift, mask, get, [](unsigned, K) {});
     __syncthreads();
     places(rows, sScan, [](int, unsigned*, unsigned*) {});
     if (p + 1 == a.passes) {
-      digits_of_run<true>(rows[warp], lo, hi, shift, mask, get,
-                          [&](unsigned at, Item x) { a.out[at] = x; });
+      digits_of_run<K, true>(rows[warp], lo, hi, shift, mask, get, [&](unsigned at, K x) {
+        a.out[at] = (Item)(x >> a.tokenBits) << kItemBits | (unsigned)(x & ((K)1 << a.tokenBits) - 1);
+      });
     } else {
-      digits_of_run<true>(rows[warp], lo, hi, shift, mask, get,
-                          [&](unsigned at, Item x) { to[at] = x; });
+      digits_of_run<K, true>(rows[warp], lo, hi, shift, mask, get,
+                             [&](unsigned at, K x) { to[at] = x; });
     }
     __syncthreads();
-    Item* t = from;
+    K* t = from;
     from = to;
     to = t;
   }
@@ -251,8 +311,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
   const int run = (n + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
   const int lo = begin + min(warp * run, n), hi = min(lo + run, begin + n);
   const unsigned mask = (1u << a.bits) - 1;
-  auto get = [&](int i) { return a.in ? a.in[i] : item_of(a, i); };
-  digits_of_run<false>(rows[warp], lo, hi, a.shift, mask, get, [](unsigned, Item) {});
+  auto get = [&](int i) { return a.in ? a.in[i] : item_of<Item>(a, i); };
+  digits_of_run<Item, false>(rows[warp], lo, hi, a.shift, mask, get, [](unsigned, Item) {});
   __syncthreads();
   if (!MOVE) {
     if (threadIdx.x < kDigits) {
@@ -274,8 +334,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
     *all = sum;
     *before = mine;
   });
-  digits_of_run<true>(rows[warp], lo, hi, a.shift, mask, get,
-                      [&](unsigned at, Item x) { a.out[at] = x; });
+  digits_of_run<Item, true>(rows[warp], lo, hi, a.shift, mask, get,
+                            [&](unsigned at, Item x) { a.out[at] = x; });
 }
 
 // --------------------------------------------------------------------- sums
@@ -330,8 +390,26 @@ struct Slice {
     for (int i = 0; i < REP; ++i) {
       if (col(slice, i) >= a.dim) break;
 #pragma unroll
-      for (int j = 0; j < N; ++j) p[col(slice, i) + j] = sum[i][j];
+      for (int j = 0; j < N; j += kWide)
+        *reinterpret_cast<Wide*>(p + col(slice, i) + j) =
+            *reinterpret_cast<const Wide*>(&sum[i][j]);
     }
+  }
+  // (dim is a multiple of N, the partial sums begin at 16 bytes)
+  using Wide = typename Select<N % 4 == 0, float4, typename Select<N == 2, float2, float>::type>::type;
+  static constexpr int kWide = N % 4 == 0 ? 4 : N;
+  static __device__ __forceinline__ void add_part(const float* p, const SumArgs& a, int slice,
+                                                  float (&sum)[REP][N]) {
+#pragma unroll
+    for (int i = 0; i < REP; ++i)
+      if (col(slice, i) < a.dim) {
+#pragma unroll
+        for (int j = 0; j < N; j += kWide) {
+          const Wide w = *reinterpret_cast<const Wide*>(p + col(slice, i) + j);
+#pragma unroll
+          for (int k = 0; k < kWide; ++k) sum[i][j + k] += reinterpret_cast<const float*>(&w)[k];
+        }
+      }
   }
 };
 
@@ -435,6 +513,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
   pdl_wait();
   const long long step = (long long)gridDim.x * kWarps;
   const long long units = (long long)(a.chunks - 1) * a.slices;
+  const int lane = threadIdx.x % 32;
   for (long long u = (long long)blockIdx.x * kWarps + threadIdx.x / 32; u < units; u += step) {
     const int chunk = (int)(u / a.slices), slice = (int)(u - (long long)chunk * a.slices);
     const int lo = chunk * a.chunk, hi = lo + a.chunk;  // not the last chunk
@@ -442,25 +521,21 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     if (word >= (unsigned)a.vocab || word_of(a.items[hi]) != word) continue;
     // it begins in this chunk
     if (lo > 0 && word_of(a.items[lo]) == word && word_of(a.items[lo - 1]) == word) continue;
-    int from = hi + 1, to = a.tokens;  // the first item behind it
-    while (from < to) {
-      const int mid = (from + to) / 2;
-      if (word_of(a.items[mid]) == word) from = mid + 1;
-      else to = mid;
+    // the chunks that it goes on into: every lane looks at the end of one
+    int last = chunk + 1;
+    for (;; last += 32) {
+      const long long end = (long long)(last + lane + 1) * a.chunk;
+      const bool on = end < a.tokens && word_of(a.items[end]) == word;
+      const unsigned stops = ~__ballot_sync(0xffffffffu, on);
+      if (stops) {
+        last += __ffs(stops) - 1;
+        break;
+      }
     }
-    const int last = (from - 1) / a.chunk;
     float sum[REP][N] = {};
-    auto add = [&](const float* p) {
-#pragma unroll
-      for (int i = 0; i < REP; ++i)
-        if (S::col(slice, i) < a.dim) {
-#pragma unroll
-          for (int j = 0; j < N; ++j) sum[i][j] += p[S::col(slice, i) + j];
-        }
-    };
-    add(S::part(a, chunk, 1));
-#pragma unroll 4
-    for (int k = chunk + 1; k <= last; ++k) add(S::part(a, k, 0));
+    S::add_part(S::part(a, chunk, 1), a, slice, sum);
+#pragma unroll 8
+    for (int k = chunk + 1; k <= last; ++k) S::add_part(S::part(a, k, 0), a, slice, sum);
     S::write(a, word, slice, sum);
   }
 }
@@ -471,15 +546,25 @@ constexpr size_t kMostTokens = (size_t)1 << 30, kMostVocab = (size_t)1 << 30,
 constexpr int kMostCtas = 152;
 constexpr size_t kSortRun = 2048;  // the fewest tokens that a CTA of a large sort takes
 
-// The sorted tokens are cut into chunks of 32 or more, fewer than 4096.
-size_t chunk_of(size_t tokens) {
-  size_t c = 32;
-  while (tokens / c > 4096) c *= 2;
+int bits_of(size_t n) {
+  int b = 1;
+  while (n >> b) ++b;
+  return b;
+}
+
+// Items of a chunk: as few as four where that makes no more warps than are
+// resident at once (a warp writes the rows of its words one after the other: 777
+// tokens x 1000 columns in 7 us instead of 27 with 32).
+size_t chunk_of(size_t tokens, size_t dim) {
+  const size_t slices = (dim + 255) / 256;
+  size_t c = 4;
+  while (tokens / c * slices > 8192) c *= 2;
   return c;
 }
 
 struct EmbedPlan {
-  bool small;
+  bool small, narrow;  // one CTA sorts; with items of 32 bits
+  int passes, bits, tokenBits;
   size_t run, ctas, chunk, chunks;
   size_t items, other, counts, parts, bytes;  // offsets into the workspace
 };
@@ -488,10 +573,16 @@ bool make_plan(size_t tokens, size_t dim, size_t vocab, int dtype, EmbedPlan* p)
       vocab > kMostVocab)
     return false;
   *p = EmbedPlan{};
-  p->small = tokens <= (size_t)kSmallSort;
+  const int words = bits_of(vocab);  // of the words 0 .. vocab
+  p->passes = (words + kMaxBits - 1) / kMaxBits;
+  p->bits = (words + p->passes - 1) / p->passes;
+  p->tokenBits = bits_of(tokens ? tokens - 1 : 0);
+  p->narrow = tokens <= kSmallBytes / 4 && words + p->tokenBits <= 32;
+  p->small = p->narrow || tokens <= kSmallBytes / sizeof(Item);
+  if (!p->narrow) p->tokenBits = kItemBits;
   p->run = std::max(kSortRun, (tokens + kMostCtas - 1) / kMostCtas);
   p->ctas = (tokens + p->run - 1) / p->run;
-  p->chunk = chunk_of(tokens);
+  p->chunk = chunk_of(tokens, dim);
   p->chunks = (tokens + p->chunk - 1) / p->chunk;
   size_t at = 0;
   auto take = [&at](size_t n) {
@@ -515,7 +606,7 @@ int access_bytes(uintptr_t bits, size_t elem) {
 template <typename T, int N, int REP>
 vr_result_t launch_sums(const EmbedPlan& p, const OpDevice& dev, SumArgs& a, void* stream) {
   a.slices = (a.dim + Slice<T, N, REP>::kCols - 1) / Slice<T, N, REP>::kCols;
-  a.fillUnits = a.add ? 0 : ((long long)a.vocab + kFillRows - 1) / kFillRows;
+  a.fillUnits = a.add || p.small ? 0 : ((long long)a.vocab + kFillRows - 1) / kFillRows;
   a.units = a.fillUnits + (long long)p.chunks * a.slices;
   void* args[] = {&a};
   auto grid = [&](long long units) {
@@ -641,17 +732,25 @@ vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long lo
   s.tokens = (int)tokens;
   s.vocab = (int)vocab;
   s.status = dev.status;
-  int bits = 1;  // of the words 0 .. vocab
-  while (vocab >> bits) ++bits;
-  s.passes = (bits + kMaxBits - 1) / kMaxBits;
-  s.bits = (bits + s.passes - 1) / s.passes;
+  s.passes = p.passes;
+  s.bits = p.bits;
+  s.tokenBits = p.tokenBits;
+  const int access = access_bytes((uintptr_t)dOut | (uintptr_t)dWeight | (uintptr_t)(dim * E) |
+                                      (uintptr_t)(dOutStride * E),
+                                  E);
   Item* items = reinterpret_cast<Item*>(w + p.items);
   if (p.small) {
     s.out = items;
+    s.table = static_cast<char*>(dWeight);
+    s.rowBytes = (long long)(dim * E);
+    s.access = access;
     void* args[] = {&s};
-    const void* fn = (const void*)embed_sort_small_kernel;
+    const void* fn = p.narrow ? (const void*)embed_sort_small_kernel<unsigned>
+                              : (const void*)embed_sort_small_kernel<Item>;
+    const unsigned grid =
+        accumulate ? 1 : 1 + (unsigned)std::min<size_t>(std::max(dev.sms - 1, 1), vocab);
     if ((e = gemm_prepare(fn, dev.device, kSmallSmem)) != VR_SUCCESS ||
-        (e = op_launch(fn, dim3(1), dim3(kSortThreads), args, kSmallSmem, stream)) != VR_SUCCESS)
+        (e = op_launch(fn, dim3(grid), dim3(kSortThreads), args, kSmallSmem, stream)) != VR_SUCCESS)
       return e;
   } else {
     Item* other = reinterpret_cast<Item*>(w + p.other);
@@ -665,7 +764,7 @@ vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long lo
     s.ctas = (int)p.ctas;
     s.run = (int)p.run;
     for (int i = 0; i < s.passes; ++i) {
-      s.shift = i * s.bits;
+      s.shift = s.tokenBits + i * s.bits;
       // the last pass ends in `items`
       s.out = (s.passes - 1 - i) % 2 ? other : items;
       void* args[] = {&s};
@@ -690,9 +789,6 @@ vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long lo
   a.chunk = (int)p.chunk;
   a.chunks = (int)p.chunks;
   a.scale = scale;
-  const int access = access_bytes((uintptr_t)dOut | (uintptr_t)dWeight | (uintptr_t)(dim * E) |
-                                      (uintptr_t)(dOutStride * E),
-                                  E);
   return dtype == VR_FLOAT32   ? sums<float>(p, dev, a, access, stream)
          : dtype == VR_FLOAT16 ? sums<__half>(p, dev, a, access, stream)
                                : sums<__nv_bfloat16>(p, dev, a, access, stream);

@@ -62,7 +62,10 @@ vr_result_t gemm_prepare(const void* fn, int device, size_t smem) {
     const auto key = std::make_pair(fn, device);
     if (g_prepared.count(key)) return VR_SUCCESS;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+            cudaSuccess ||
+        // (as much shared memory as there is: all CTAs that it has room for)
+        cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared) != cudaSuccess)
       return VR_ERR_CUDA;
     g_prepared.insert(key);
     return VR_SUCCESS;

@@ -652,8 +652,8 @@ vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const vo
  * 1 - beta in fp32: the same bits wherever they are computed.
  * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, a bad dtype, gradDtype or
  * stateBits, masters with fp32 parameters, scales that do not go with
- * stateBits, a size above 2^40, beta1 or beta2 outside [0, 1), eps negative or
- * not finite, weightDecay or (without control) lr or gradScale not finite or
+ * stateBits, a size above 2^40, beta1 or beta2 outside [0, 1), eps negative,
+ * denormal or not finite, weightDecay or (without control) lr or gradScale not finite or
  * step < 1, a NULL or misaligned buffer, or any overlap. */
 vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const* m,
                      void* const* v, float* const* mScales, float* const* vScales,

@@ -104,7 +104,7 @@ def encode(kind, x, cut):
         if kind == "v":
             c = np.where(part > 0, np.maximum(c, 1), c)
         else:
-            c = np.where((part < 0) & (c > 0), c + 128, c)
+            c = np.where(np.signbit(part), c + 128, c)  # (a zero keeps its sign)
         codes[b * 256:b * 256 + len(part)] = c.astype(np.uint8)
     return codes, scales
 

@@ -144,7 +144,7 @@ def adamw_args(**kw):
     dict(dtype=vr.VR_FLOAT32), dict(mScales=None), dict(vScales=None), dict(stateBits=32),
     dict(params=None), dict(grads=None), dict(m=None), dict(v=None),
     dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=math.nan), dict(eps=-1.0),
-    dict(eps=math.inf), dict(lr=math.nan), dict(gradScale=math.inf), dict(weightDecay=math.inf),
+    dict(eps=math.inf), dict(eps=1e-40), dict(lr=math.nan), dict(gradScale=math.inf), dict(weightDecay=math.inf),
     dict(step=0), dict(step=-5), dict(sizes=[1000, 1 << 41]), dict(control=A + 50 * STEP + 2),
     dict(params=[A, 0]), dict(grads=[0, A + STEP]), dict(masters=[A + 12 * STEP, 0]),
     dict(mScales=[A + 8 * STEP, 0]), dict(params=[A + 1, A + STEP]),
