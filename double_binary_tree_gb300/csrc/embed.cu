@@ -398,18 +398,45 @@ struct Slice {
   // (dim is a multiple of N, the partial sums begin at 16 bytes)
   using Wide = typename Select<N % 4 == 0, float4, typename Select<N == 2, float2, float>::type>::type;
   static constexpr int kWide = N % 4 == 0 ? 4 : N;
-  static __device__ __forceinline__ void add_part(const float* p, const SumArgs& a, int slice,
-                                                  float (&sum)[REP][N]) {
+  // the partial sums of chunks `from` to `to` that begin with the word, in order,
+  // eight loads in flight
+  static __device__ __forceinline__ void add_parts(const SumArgs& a, int from, int to, int slice,
+                                                   float (&sum)[REP][N]) {
+    constexpr int kUnits = N / kWide, kAtOnce = 8 / kUnits > 4 ? 4 : 8 / kUnits;
+    const long long step = 2LL * a.dim;
 #pragma unroll
-    for (int i = 0; i < REP; ++i)
-      if (col(slice, i) < a.dim) {
+    for (int i = 0; i < REP; ++i) {
+      if (col(slice, i) >= a.dim) break;
+      const float* p = part(a, from, 0) + col(slice, i);
+      for (int k = from; k <= to; k += kAtOnce) {
+        Wide w[kAtOnce][kUnits];
 #pragma unroll
-        for (int j = 0; j < N; j += kWide) {
-          const Wide w = *reinterpret_cast<const Wide*>(p + col(slice, i) + j);
+        for (int q = 0; q < kAtOnce; ++q)
 #pragma unroll
-          for (int k = 0; k < kWide; ++k) sum[i][j + k] += reinterpret_cast<const float*>(&w)[k];
-        }
+          for (int j = 0; j < kUnits; ++j)
+            if (k + q <= to) w[q][j] = *reinterpret_cast<const Wide*>(p + q * step + j * kWide);
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q)
+          if (k + q <= to) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              sum[i][j] += reinterpret_cast<const float*>(&w[q][j / kWide])[j % kWide];
+          }
+        p += kAtOnce * step;
       }
+    }
+  }
+  static __device__ __forceinline__ void load_part(const SumArgs& a, int chunk, int end, int slice,
+                                                   float (&sum)[REP][N]) {
+    const float* p = part(a, chunk, end);
+#pragma unroll
+    for (int i = 0; i < REP; ++i) {
+      if (col(slice, i) >= a.dim) break;
+#pragma unroll
+      for (int j = 0; j < N; j += kWide)
+        *reinterpret_cast<Wide*>(&sum[i][j]) =
+            *reinterpret_cast<const Wide*>(p + col(slice, i) + j);
+    }
   }
 };
 
@@ -453,17 +480,22 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
     if (word >= (unsigned)a.vocab) continue;  // tokens that do not count are last
     bool head = lo > 0 && word_of(a.items[lo - 1]) == word;  // goes on from the last chunk
     float sum[REP][N] = {};
+    unsigned before = word;  // of the item before the next 32
     for (int i0 = lo; i0 < hi; i0 += 32) {
-      const Item mine = i0 + lane < hi ? a.items[i0 + lane] : (Item)~0u << 32;
-      const int n = min(32, hi - i0);
+      const Item mine = i0 + lane < hi ? a.items[i0 + lane] : (Item)~0u << kItemBits;
+      const unsigned w = word_of(mine);
+      const unsigned up = __shfl_up_sync(0xffffffffu, w, 1);
+      const unsigned starts = __ballot_sync(0xffffffffu, w != (lane ? up : before));
+      const int n = __popc(__ballot_sync(0xffffffffu, w < (unsigned)a.vocab));  // those first
+      before = __shfl_sync(0xffffffffu, w, 31);
       constexpr int kAhead = 8 / REP;
       for (int j0 = 0; j0 < n; j0 += kAhead) {
         Raw r[kAhead][REP];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const Item x = __shfl_sync(0xffffffffu, mine, (j0 + k) & 31);
-          if (j0 + k >= n || word_of(x) >= (unsigned)a.vocab) continue;
-          const T* in = static_cast<const T*>(a.dout) + (long long)token_of(x) * a.stride;
+          if (j0 + k >= n) break;
+          const unsigned token = __shfl_sync(0xffffffffu, token_of(mine), j0 + k);
+          const T* in = static_cast<const T*>(a.dout) + (long long)token * a.stride;
 #pragma unroll
           for (int i = 0; i < REP; ++i)
             if (S::col(slice, i) < a.dim)
@@ -471,21 +503,17 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const unsigned w = word_of(__shfl_sync(0xffffffffu, mine, (j0 + k) & 31));
-          if (j0 + k >= n) continue;
-          if (w != word) {
-            if (word < (unsigned)a.vocab) {
-              if (head) S::store_part(a, chunk, 0, slice, sum);
-              else S::write(a, word, slice, sum);
-            }
+          if (j0 + k >= n) break;
+          if (starts >> (j0 + k) & 1) {
+            if (head) S::store_part(a, chunk, 0, slice, sum);
+            else S::write(a, word, slice, sum);
             head = false;
-            word = w;
+            word = __shfl_sync(0xffffffffu, w, j0 + k);
 #pragma unroll
             for (int i = 0; i < REP; ++i)
 #pragma unroll
               for (int j = 0; j < N; ++j) sum[i][j] = 0.0f;
           }
-          if (w >= (unsigned)a.vocab) continue;
 #pragma unroll
           for (int i = 0; i < REP; ++i) {
             float x[N];
@@ -496,7 +524,6 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
         }
       }
     }
-    if (word >= (unsigned)a.vocab) continue;
     const bool tail = hi < a.tokens && word_of(a.items[hi]) == word;
     if (head) S::store_part(a, chunk, 0, slice, sum);
     else if (tail) S::store_part(a, chunk, 1, slice, sum);
@@ -533,9 +560,8 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
       }
     }
     float sum[REP][N] = {};
-    S::add_part(S::part(a, chunk, 1), a, slice, sum);
-#pragma unroll 8
-    for (int k = chunk + 1; k <= last; ++k) S::add_part(S::part(a, k, 0), a, slice, sum);
+    S::load_part(a, chunk, 1, slice, sum);
+    S::add_parts(a, chunk + 1, last, slice, sum);
     S::write(a, word, slice, sum);
   }
 }
