@@ -198,6 +198,24 @@ def test_many_groups():
     check(Case([0] * 1023 + [300], 64, 40, "bf16"))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("mean,K,N", [(9, 264, 520), (9, 72, 1040), (50, 64, 1600), (50, 520, 100),
+                                      (700, 1032, 2056)])
+def test_many_tiles(mean, K, N, dtype):
+    """Several tiles for every CTA; groups of very different sizes."""
+    g = torch.Generator()
+    g.manual_seed(mean)
+    n = 16 if mean == 700 else 300
+    counts = (torch.exp(torch.randn(n, generator=g)) * mean * 0.6).long().clamp(max=40 * mean)
+    counts[::7] = 0
+    case = Case(counts.tolist(), K, N, dtype, spare=5)
+    check(case)
+    again = [case.linear()[:case.used]] + list(case.grad())
+    got = [case.linear()[:case.used]] + list(case.grad())
+    assert torch.equal(again[0], got[0]) and torch.equal(again[2], got[2])
+    assert torch.equal(again[1][:case.used], got[1][:case.used])
+
+
 @pytest.mark.parametrize("counts", [[5, 0, 17], [100, 3, 200], [555, 600]],
                          ids=lambda c: "%dx%d" % (len(c), sum(c)))
 def test_streams_and_graphs(counts):
