@@ -57,17 +57,24 @@ struct GroupedArgs {
   unsigned long long timeoutNs;
 };
 
-template <int BN, bool PAIR>
+// dW's rows are stored through shared memory, a warp's 32 rows of 32 columns at a
+// time: a store then covers 64 bytes of eight rows, not 16 or 32 bytes of 32 (as
+// many lines as there are rows, which took a third of the time where groups have
+// a few hundred rows).
+constexpr int kStaged = 32 * 64;  // bytes of a warp
+
+template <int BN, bool PAIR, bool STAGED>
 struct GroupedShape {
   static constexpr int kABytes = kTileM * kTileK * 2;
   static constexpr int kBRows = PAIR ? BN / 2 : BN;
   static constexpr int kBBytes = kBRows * kTileK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kTileRows = PAIR ? 2 * kTileM : kTileM;
-  static constexpr int kStages = kGroupedSmem / kStageBytes;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes;
-  static constexpr int kTmem = 2 * BN;
   static constexpr int kWarps = BN >= 128 ? 16 : 4;  // of the epilogue
+  static constexpr int kStagedBytes = STAGED ? kWarps * kStaged : 0;
+  static constexpr int kStages = (kGroupedSmem - kStagedBytes) / kStageBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kStagedBytes;
+  static constexpr int kTmem = 2 * BN;
   static constexpr int kGrain = PAIR ? 32 : 16;      // columns of an instruction
 };
 
@@ -101,6 +108,47 @@ __device__ __forceinline__ void zero_rows(uint32_t stage, int from, int to, int 
   __syncwarp();
 }
 
+// 32 columns of a warp's `rows` (at most 32) rows, of which `cols` are there,
+// through its part of shared memory: out is the first row's.
+template <typename T>
+__device__ __forceinline__ void store_staged(uint32_t staged, T* out, long long ld,
+                                             const float (&v)[32], int rows, int cols, int align) {
+  const int lane = threadIdx.x % 32;
+  auto piece = [&](int row, int i) {  // swizzled: no bank twice in a phase either way
+    return staged + (unsigned)(row * 64 + ((i ^ (row >> 1 & 3)) << 4));
+  };
+  __syncwarp();  // (what was there has been read)
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, i)),
+                 "r"(pack2<T>(v[8 * i], v[8 * i + 1])), "r"(pack2<T>(v[8 * i + 2], v[8 * i + 3])),
+                 "r"(pack2<T>(v[8 * i + 4], v[8 * i + 5])), "r"(pack2<T>(v[8 * i + 6], v[8 * i + 7]))
+                 : "memory");
+  __syncwarp();
+  if (align < 16 || cols < 32) {  // an element a lane, row by row
+#pragma unroll 8
+    for (int row = 0; row < min(rows, 32); ++row) {
+      uint16_t x;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(x)
+                   : "r"(piece(row, lane / 8) + lane % 8 * 2)
+                   : "memory");
+      if (lane < cols) reinterpret_cast<uint16_t*>(out + row * ld)[lane] = x;
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = k * 8 + lane / 4;
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                 : "r"(piece(row, lane % 4))
+                 : "memory");
+    if (row < rows) *reinterpret_cast<uint4*>(out + row * ld + lane % 4 * 8) = q;
+  }
+}
+
 // A warp's 32 columns m of `rows` (at most 32) rows, 32 values a lane, one of
 // each row.  align >= 4: two columns of a row in one store, which a pair of
 // lanes make of each two rows.
@@ -126,10 +174,10 @@ __device__ __forceinline__ void store_columns(T* out, long long ld, const float 
 }
 
 template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
-__global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
+__global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGradWeight>::kWarps, 1)
     grouped_kernel(const __grid_constant__ GroupedArgs g) {
-  using Shape = GroupedShape<BN, PAIR>;
   using Is = KindOf<KIND>;
+  using Shape = GroupedShape<BN, PAIR, Is::kWeight>;
   constexpr bool AMN = Is::kAMn, BMN = Is::kBMn, kWeight = Is::kWeight;
   constexpr int kStages = Shape::kStages, kCtas = PAIR ? 2 : 1, kRows = Shape::kTileRows;
   constexpr int kEpilogueWarps = Shape::kWarps, kGroups = kEpilogueWarps / 4;
@@ -443,12 +491,15 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR>::kWarps, 1)
       if (++buf == 2) buf = 0, bufTurn ^= 1;
     };
     T* out = static_cast<T*>(g.out);
+    const uint32_t staged =
+        stage0 + (unsigned)(kStages * Shape::kStageBytes + (kWeight ? (warp - 4) * kStaged : 0));
     // 32 columns from c of the tile
     auto store = [&](const GroupTile& o, int c, const float(&v)[32]) {
       const int m = o.m0 + (int)rank * kTileM + row;
       if constexpr (kWeight) {
-        if (m < g.M)
-          store_row(out + ((long long)o.g * g.M + m) * g.ld + o.n0 + c, v, g.N - o.n0 - c, g.align);
+        const int first = m - lane;  // the warp's
+        store_staged(staged, out + ((long long)o.g * g.M + first) * g.ld + o.n0 + c, g.ld, v,
+                     g.M - first, g.N - o.n0 - c, g.align);
       } else {
         store_columns(out + (o.n0 + c) * g.ld, g.ld, v, min(o.hi - o.n0, o.width) - c, m, g.M,
                       g.align);
@@ -608,8 +659,8 @@ struct GroupedSize {
 template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
 vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, const GroupedSize& z,
                    int cap, const int* counts, void* out, size_t ld, void* stream) {
-  using Shape = GroupedShape<BN, PAIR>;
   using Is = KindOf<KIND>;
+  using Shape = GroupedShape<BN, PAIR, Is::kWeight>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const void* fn = (const void*)grouped_kernel<T, BN, KIND, PAIR, CHUNK>;
   GroupedArgs g = {};
