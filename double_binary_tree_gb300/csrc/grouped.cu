@@ -42,14 +42,11 @@ struct KindOf {
   // operands whose rows are the summed dimension
   static constexpr bool kAMn = KIND != kLinear, kBMn = kWeight;
 };
-constexpr int kBox = 32;  // rows that a tensor copy of a group's rows fetches
-
 struct GroupedArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b, c;  // c: dW, where its rows are 16-byte units
   const int* counts;
   int groups, rows;  // rows: that the buffers have
   int M, N, K;       // of the product; N (rows) or K (weight) is counted on the device
-  int cap;           // most columns of a tile of rows, a multiple of 32
   void* out;
   long long ld;      // elements between its rows
   int align;
@@ -58,9 +55,10 @@ struct GroupedArgs {
 };
 
 // dW's rows are stored through shared memory, a warp's 32 rows of 32 columns at a
-// time: a store then covers 64 bytes of eight rows, not 16 or 32 bytes of 32 (as
-// many lines as there are rows, which took a third of the time where groups have
-// a few hundred rows).
+// time, by a tensor copy, or, rows that are no 16-byte units, an element a lane.
+// (Straight from registers a store covers 16 or 32 bytes of 32 rows, as many lines
+// as there are rows, which took a third of the time where groups have a few hundred
+// rows.)
 constexpr int kStaged = 32 * 64;  // bytes of a warp
 
 template <int BN, bool PAIR, bool STAGED>
@@ -76,6 +74,7 @@ struct GroupedShape {
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kStagedBytes;
   static constexpr int kTmem = 2 * BN;
   static constexpr int kGrain = PAIR ? 32 : 16;      // columns of an instruction
+  static constexpr int kBox = BN < 128 ? 16 : 32;    // rows that a copy of a group's rows fetches
 };
 
 // A tile: its group, its place in the product and its columns, a multiple of
@@ -108,44 +107,53 @@ __device__ __forceinline__ void zero_rows(uint32_t stage, int from, int to, int 
   __syncwarp();
 }
 
-// 32 columns of a warp's `rows` (at most 32) rows, of which `cols` are there,
-// through its part of shared memory: out is the first row's.
+// 32 columns of a warp's 32 rows in its part of shared memory, as a 64-byte
+// swizzled tile (no bank twice in a phase, neither by rows nor along them).
+__device__ __forceinline__ uint32_t staged_piece(uint32_t staged, int row, int i) {
+  return staged + (unsigned)(row * 64 + ((i ^ (row >> 1 & 3)) << 4));
+}
 template <typename T>
-__device__ __forceinline__ void store_staged(uint32_t staged, T* out, long long ld,
-                                             const float (&v)[32], int rows, int cols, int align) {
+__device__ __forceinline__ void stage_rows(uint32_t staged, const float (&v)[32]) {
   const int lane = threadIdx.x % 32;
-  auto piece = [&](int row, int i) {  // swizzled: no bank twice in a phase either way
-    return staged + (unsigned)(row * 64 + ((i ^ (row >> 1 & 3)) << 4));
-  };
-  __syncwarp();  // (what was there has been read)
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, i)),
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staged_piece(staged, lane, i)),
                  "r"(pack2<T>(v[8 * i], v[8 * i + 1])), "r"(pack2<T>(v[8 * i + 2], v[8 * i + 3])),
                  "r"(pack2<T>(v[8 * i + 4], v[8 * i + 5])), "r"(pack2<T>(v[8 * i + 6], v[8 * i + 7]))
                  : "memory");
+}
+// From there to memory: the tile's place is x, y, z of the map (what is outside is
+// cut off).  The part may be written again after staged_free.
+__device__ __forceinline__ void store_staged(uint32_t staged, const CUtensorMap* map, int x, int y,
+                                             int z) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
-  if (align < 16 || cols < 32) {  // an element a lane, row by row
-#pragma unroll 8
-    for (int row = 0; row < min(rows, 32); ++row) {
-      uint16_t x;
-      asm volatile("ld.shared.u16 %0, [%1];"
-                   : "=h"(x)
-                   : "r"(piece(row, lane / 8) + lane % 8 * 2)
-                   : "memory");
-      if (lane < cols) reinterpret_cast<uint16_t*>(out + row * ld)[lane] = x;
-    }
-    return;
+  if (threadIdx.x % 32 == 0) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+        "r"(x), "r"(y), "r"(z), "r"(staged)
+        : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = k * 8 + lane / 4;
-    uint4 q;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                 : "r"(piece(row, lane % 4))
+}
+__device__ __forceinline__ void staged_free() {
+  if (threadIdx.x % 32 == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+// The same for rows that are no 16-byte units: `rows` and `cols` of them are there.
+template <typename T>
+__device__ __forceinline__ void store_staged(uint32_t staged, T* out, long long ld, int rows,
+                                             int cols) {
+  const int lane = threadIdx.x % 32;
+  __syncwarp();
+#pragma unroll 8
+  for (int row = 0; row < min(rows, 32); ++row) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];"
+                 : "=h"(x)
+                 : "r"(staged_piece(staged, row, lane / 8) + lane % 8 * 2)
                  : "memory");
-    if (row < rows) *reinterpret_cast<uint4*>(out + row * ld + lane % 4 * 8) = q;
+    if (lane < cols) reinterpret_cast<uint16_t*>(out + row * ld)[lane] = x;
   }
 }
 
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
   __shared__ alignas(8) uint64_t bars[2 * kStages + 5 + (kTails ? 2 * kStages : 0)];
   __shared__ uint32_t tmemBase;
   __shared__ volatile int abortFlag;
-  __shared__ int rowStart[kMostGroups + 1], tileStart[kMostGroups + 1];
+  __shared__ int rowStart[kMostGroups + 1], tileStart[kMostGroups + 1], chosenCap;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
@@ -234,6 +242,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
   if (warp == 1 && elected()) {
     prefetch_map(&g.a);
     prefetch_map(&g.b);
+    if (kWeight && g.align >= 16) prefetch_map(&g.c);
   }
   if (warp == 2) {
     if constexpr (PAIR) {
@@ -254,7 +263,10 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
   pdl_wait();
   const int tilesM = (g.M + kRows - 1) / kRows, tilesN = (g.N + BN - 1) / BN;
   if (warp == 3) {  // the groups' rows and tiles
-    int rows = 0, tiles = 0;
+    // Caps of a tile's columns, and the tiles of all groups with each.
+    constexpr int kCaps = kWeight || BN < 128 ? 1 : 4;
+    auto cap_of = [](int i) { return i == 0 ? BN : i == 1 ? 192 : i == 2 ? 128 : 64; };
+    int rows = 0, sums[kCaps] = {};
 #pragma unroll 4
     for (int e0 = 0; e0 < g.groups; e0 += 32) {
       const int e = e0 + lane;
@@ -271,28 +283,53 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
       if (given < 0 || end > g.rows) atomicCAS(g.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
       const int hi = (int)min(end, (long long)g.rows);
       const int up = __shfl_up_sync(0xffffffffu, hi, 1), lo = lane ? up : rows;
-      int sum = 0;
-      if (e < g.groups) sum = kWeight ? tilesM * tilesN : (hi - lo + g.cap - 1) / g.cap * tilesM;
+      if (e < g.groups) rowStart[e + 1] = hi;
+      if constexpr (!kWeight) {
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int more = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += more;
-      }
-      if (e < g.groups) {
-        rowStart[e + 1] = hi;
-        tileStart[e + 1] = tiles + sum;
+        for (int i = 0; i < kCaps; ++i) sums[i] += (hi - lo + cap_of(i) - 1) / cap_of(i);
       }
       rows = __shfl_sync(0xffffffffu, hi, 31);
-      tiles += __shfl_sync(0xffffffffu, sum, 31);
     }
     if (lane == 0) rowStart[0] = tileStart[0] = 0;
+    __syncwarp();
+    // Fewer than three rounds of tiles: the cap whose rounds take the least time.  (A
+    // slice takes about 0.13 us for the weight's copies and 0.0007 us a column; by the
+    // mean width.)
+    int cap = BN;
+    if constexpr (kCaps > 1) {
+      const float workers = (float)((int)gridDim.x / kCtas);
+      float best = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kCaps; ++i) {
+        const float across = (float)__reduce_add_sync(0xffffffffu, sums[i]);
+        const float rounds = ceilf(across * (float)tilesM / workers);
+        const float time = rounds * (0.13f + 0.0007f * (float)rows / fmaxf(across, 1.0f));
+        if (i == 0 || time < best) best = time, cap = cap_of(i);
+        if (i == 0 && rounds >= 3.0f) break;
+      }
+    }
+    int tiles = 0;
+    for (int e0 = 0; e0 < g.groups; e0 += 32) {
+      const int e = e0 + lane;
+      int sum = 0;
+      if (e < g.groups)
+        sum = kWeight ? tilesM * tilesN : (rowStart[e + 1] - rowStart[e] + cap - 1) / cap * tilesM;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (e < g.groups) tileStart[e + 1] = tiles + sum;
+      tiles += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) chosenCap = cap;
   }
   tmem_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();  // the peer's barriers are set up
   tmem_fence_after();
   const uint32_t tmem = tmemBase;
-  const int tiles = tileStart[g.groups];
+  const int tiles = tileStart[g.groups], cap = chosenCap;
   const int firstTile = (int)blockIdx.x / kCtas, tileStep = (int)gridDim.x / kCtas;
   // Tiles are walked upwards: `e` is the group of the last one.
   auto tile_at = [&](int t, int& e) {
@@ -303,7 +340,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     // the operands of the tiles in flight stay in L2
     constexpr int kHigh = 2048 / kRows;
     constexpr int G = Shape::kGrain;
-    const int n = o.hi - o.lo, across = kWeight ? tilesN : (n + g.cap - 1) / g.cap;
+    const int n = o.hi - o.lo, across = kWeight ? tilesN : (n + cap - 1) / cap;
     const int block = t / (kHigh * across), high = min(kHigh, tilesM - block * kHigh);
     t -= block * kHigh * across;
     o.m0 = (block * kHigh + t % high) * kRows;
@@ -331,8 +368,8 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
       const int slices = slices_of(o);
       const int mine = PAIR ? o.width / 2 : o.width;  // columns that this CTA holds
       const int m0 = o.m0 + (int)rank * kTileM, n0 = o.n0 + (int)rank * mine;
-      const int first = kWeight ? o.lo : 0, boxes = (mine + kBox - 1) / kBox;
-      const unsigned bytes = Shape::kABytes + (kWeight ? Shape::kBBytes : boxes * (kBox * 128));
+      const int first = kWeight ? o.lo : 0, boxes = (mine + Shape::kBox - 1) / Shape::kBox;
+      const unsigned bytes = Shape::kABytes + (kWeight ? Shape::kBBytes : boxes * (Shape::kBox * 128));
       for (int kb = 0; kb < slices; ++kb) {
         ok = all_wait(empty(s), turn ^ 1);
         if (!ok) break;
@@ -360,7 +397,8 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
               tensor_load<PAIR>(dst + Shape::kABytes + i * kSlab, &g.b, n0 + i * 64, k0, 0, landed);
           } else {
             for (int i = 0; i < boxes; ++i)
-              tensor_load<PAIR>(dst + Shape::kABytes + i * (kBox * 128), &g.b, k0, n0 + i * kBox, 0,
+              tensor_load<PAIR>(dst + Shape::kABytes + i * (Shape::kBox * 128), &g.b, k0,
+                                n0 + i * Shape::kBox, 0,
                                 landed);
           }
         }
@@ -497,9 +535,15 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     auto store = [&](const GroupTile& o, int c, const float(&v)[32]) {
       const int m = o.m0 + (int)rank * kTileM + row;
       if constexpr (kWeight) {
-        const int first = m - lane;  // the warp's
-        store_staged(staged, out + ((long long)o.g * g.M + first) * g.ld + o.n0 + c, g.ld, v,
-                     g.M - first, g.N - o.n0 - c, g.align);
+        const int first = m - lane, n = o.n0 + c;  // the warp's tile
+        staged_free();
+        stage_rows<T>(staged, v);
+        if (first >= g.M) return;
+        if (g.align >= 16)
+          store_staged(staged, &g.c, n, first, o.g);
+        else
+          store_staged(staged, out + ((long long)o.g * g.M + first) * g.ld + n, g.ld, g.M - first,
+                       g.N - n);
       } else {
         store_columns(out + (o.n0 + c) * g.ld, g.ld, v, min(o.hi - o.n0, o.width) - c, m, g.M,
                       g.align);
@@ -562,6 +606,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
         if (slices) release();
       }
     }
+    if (kWeight && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   tmem_fence_before();
@@ -658,7 +703,7 @@ struct GroupedSize {
 
 template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
 vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, const GroupedSize& z,
-                   int cap, const int* counts, void* out, size_t ld, void* stream) {
+                   const int* counts, void* out, size_t ld, void* stream) {
   using Is = KindOf<KIND>;
   using Shape = GroupedShape<BN, PAIR, Is::kWeight>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -669,7 +714,7 @@ vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, const 
                         m.stride * 2 * m.rows, boxRows);
   };
   vr_result_t e = map(&g.a, a, Is::kAMn ? kTileK : kTileM);
-  if (e != VR_SUCCESS || (e = map(&g.b, b, Is::kBMn ? kTileK : kBox)) != VR_SUCCESS ||
+  if (e != VR_SUCCESS || (e = map(&g.b, b, Is::kBMn ? kTileK : Shape::kBox)) != VR_SUCCESS ||
       (e = gemm_prepare(fn, dev.device, Shape::kSmem)) != VR_SUCCESS)
     return e;
   g.counts = counts;
@@ -678,18 +723,22 @@ vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, const 
   g.M = (int)z.M;
   g.N = (int)z.N;
   g.K = (int)z.K;
-  g.cap = cap;
   g.out = out;
   g.ld = (long long)ld;
   const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * ld);
-  g.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  g.align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  if (Is::kWeight && g.align == 16 &&
+      (e = gemm_operand(&g.c, out, bf16, z.N, z.M, (size_t)z.groups, ld * 2, ld * 2 * z.M, 32,
+                        kAuxCols)) != VR_SUCCESS)
+    return e;
   g.status = dev.status;
   g.timeoutNs = dev.timeoutNs;
-  // at most so many tiles: every group's last one may be cut
+  // at most so many tiles: every group's last one may be cut; with the smallest cap
+  constexpr int kCap = BN < 128 ? BN : 64;
   const size_t tm = (z.M + Shape::kTileRows - 1) / Shape::kTileRows;
   const size_t tiles =
       Is::kWeight ? (size_t)z.groups * tm * ((z.N + BN - 1) / BN)
-                  : (z.rows / cap + std::min<size_t>((size_t)z.groups, z.rows)) * tm;
+                  : (z.rows / kCap + std::min<size_t>((size_t)z.groups, z.rows)) * tm;
   constexpr size_t kCtas = PAIR ? 2 : 1;
   const size_t grid = std::min<size_t>(tiles, dev.sms / kCtas) * kCtas;
   void* args[] = {&g};
@@ -711,12 +760,12 @@ vr_result_t rows_product(const OpDevice& dev, const Matrix& w, const Matrix& x,
                          const GroupedSize& z, const int* counts, void* out, size_t ld,
                          void* stream) {
   const bool lng = z.K > kLongSum<T>;
-#define VR_GO(BN, PAIR, CAP)                                                                   \
-  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, w, x, z, CAP, counts, out, ld, stream)     \
-       : launch<T, BN, KIND, PAIR, 0>(dev, w, x, z, CAP, counts, out, ld, stream))
-  if (z.rows <= kFewRows * (size_t)z.groups) return VR_GO(32, false, 32);
-  if (z.M <= kTileM) return VR_GO(256, false, 256);
-  return VR_GO(256, true, 256);
+#define VR_GO(BN, PAIR)                                                              \
+  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, w, x, z, counts, out, ld, stream) \
+       : launch<T, BN, KIND, PAIR, 0>(dev, w, x, z, counts, out, ld, stream))
+  if (z.rows <= kFewRows * (size_t)z.groups) return VR_GO(32, false);
+  if (z.M <= kTileM) return VR_GO(256, false);
+  return VR_GO(256, true);
 #undef VR_GO
 }
 template <typename T>
@@ -736,11 +785,11 @@ template <typename T>
 vr_result_t grad_weight(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
                         size_t outDim, int groups, const int* counts, void* out, void* stream) {
   const GroupedSize z = {outDim, dim, rows, rows, groups};
-#define VR_GO(PAIR)                                                                               \
-  (rows > kLongSum<T>                                                                             \
-       ? launch<T, 256, kGradWeight, PAIR, kLongChunk>(dev, p.dy, p.x, z, 256, counts, out, dim,  \
-                                                       stream)                                    \
-       : launch<T, 256, kGradWeight, PAIR, 0>(dev, p.dy, p.x, z, 256, counts, out, dim, stream))
+#define VR_GO(PAIR)                                                                             \
+  (rows > kLongSum<T>                                                                           \
+       ? launch<T, 256, kGradWeight, PAIR, kLongChunk>(dev, p.dy, p.x, z, counts, out, dim,     \
+                                                       stream)                                  \
+       : launch<T, 256, kGradWeight, PAIR, 0>(dev, p.dy, p.x, z, counts, out, dim, stream))
   return outDim <= kTileM ? VR_GO(false) : VR_GO(true);
 #undef VR_GO
 }
