@@ -699,9 +699,8 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
   try {
     Spans spans;
     spans.v.reserve((size_t)count * 7 + 1);
-    std::vector<const void*> reach;
     for (int i = 0; i < count; ++i) {
-      const size_t n = sizes[i], blocks = (n + kBlock - 1) / kBlock;
+      const size_t n = sizes[i];
       if (n > kMostSize) return VR_ERR_INVALID_ARGUMENT;
       if (!n) continue;
       if (!params[i] || !grads[i] || !m[i] || !v[i] || (few && (!mScales[i] || !vScales[i])) ||
@@ -710,16 +709,18 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
           (few && ((uintptr_t)mScales[i] | (uintptr_t)vScales[i]) % 4) ||
           (masters && (uintptr_t)masters[i] % 4))
         return VR_ERR_INVALID_ARGUMENT;
-      spans.add(params[i], n * E, true);
-      spans.add(grads[i], n * GE, false);
-      spans.add(m[i], n * SE, true);
-      spans.add(v[i], n * SE, true);
-      if (few) {
-        spans.add(mScales[i], blocks * 4, true);
-        spans.add(vScales[i], blocks * 4, true);
-      }
-      if (masters) spans.add(masters[i], n * 4, true);
     }
+    auto list = [&](auto p, size_t elem, size_t per, bool write) {
+      for (int i = 0; p && i < count; ++i)
+        if (sizes[i]) spans.add(p[i], (sizes[i] + per - 1) / per * elem, write);
+    };
+    list(params, E, 1, true);
+    list(grads, GE, 1, false);
+    list(m, SE, 1, true);
+    list(v, SE, 1, true);
+    list(mScales, 4, kBlock, true);
+    list(vScales, 4, kBlock, true);
+    list(masters, 4, 1, true);
     spans.add(control, 12, false);
     if (!op_spans_ok(spans.v.data(), spans.v.size())) return VR_ERR_INVALID_ARGUMENT;
     OpDevice dev;
@@ -778,20 +779,25 @@ vr_result_t vr_adamw_values(const void* const* m, const void* const* v,
     Spans spans;
     spans.v.reserve((size_t)count * 6);
     for (int i = 0; i < count; ++i) {
-      const size_t n = sizes[i], blocks = (n + kBlock - 1) / kBlock;
+      const size_t n = sizes[i];
       if (n > kMostSize) return VR_ERR_INVALID_ARGUMENT;
-      auto one = [&](const void* const* codes, const float* const* scales, float* const* out) {
-        if (!n || !out) return true;
-        if (!codes[i] || !scales[i] || !out[i] ||
-            ((uintptr_t)scales[i] | (uintptr_t)out[i]) % 4)
-          return false;
-        spans.add(codes[i], n, false);
-        spans.add(scales[i], blocks * 4, false);
-        spans.add(out[i], n * 4, true);
-        return true;
+      auto bad = [&](const void* const* codes, const float* const* scales, float* const* out) {
+        return n && out &&
+               (!codes[i] || !scales[i] || !out[i] ||
+                ((uintptr_t)scales[i] | (uintptr_t)out[i]) % 4);
       };
-      if (!one(m, mScales, mValues) || !one(v, vScales, vValues)) return VR_ERR_INVALID_ARGUMENT;
+      if (bad(m, mScales, mValues) || bad(v, vScales, vValues)) return VR_ERR_INVALID_ARGUMENT;
     }
+    auto list = [&](auto p, auto out, size_t elem, size_t per, bool write) {
+      for (int i = 0; out && i < count; ++i)
+        if (sizes[i]) spans.add(p[i], (sizes[i] + per - 1) / per * elem, write);
+    };
+    list(m, mValues, 1, 1, false);
+    list(mScales, mValues, 4, kBlock, false);
+    list(mValues, mValues, 4, 1, true);
+    list(v, vValues, 1, 1, false);
+    list(vScales, vValues, 4, kBlock, false);
+    list(vValues, vValues, 4, 1, true);
     if (!op_spans_ok(spans.v.data(), spans.v.size())) return VR_ERR_INVALID_ARGUMENT;
     OpDevice dev;
     vr_result_t e = op_device(&dev);

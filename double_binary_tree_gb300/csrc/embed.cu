@@ -176,12 +176,13 @@ __device__ __forceinline__ void digits_of_run(unsigned* row, int lo, int hi, int
 // before this CTA's n items of the digit, as a whole sum over lower digits
 // (the CTAs' totals) and earlier CTAs.
 template <class Base>
-__device__ __forceinline__ void places(unsigned (*rows)[kDigits], unsigned* sScan, Base base) {
+__device__ __forceinline__ void places(unsigned (*rows)[kDigits], int warps, unsigned* sScan,
+                                       Base base) {
   const int d = threadIdx.x;
   unsigned total = 0;
   if (d < kDigits) {
 #pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const unsigned n = rows[w][d];
       rows[w][d] = total;
       total += n;
@@ -202,14 +203,15 @@ __device__ __forceinline__ void places(unsigned (*rows)[kDigits], unsigned* sSca
   if (d < kDigits) {
     unsigned start = sum - all + before;
     for (int w = 0; w < warp; ++w) start += sScan[w];
-    for (int w = 0; w < kSortWarps; ++w) rows[w][d] += start;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) rows[w][d] += start;
   }
   __syncthreads();
 }
 
-__device__ __forceinline__ void clear(unsigned (*rows)[kDigits]) {
+__device__ __forceinline__ void clear(unsigned (*rows)[kDigits], int warps) {
   unsigned* p = &rows[0][0];
-  for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) p[i] = 0;
+  for (int i = threadIdx.x; i < warps * kDigits; i += kSortThreads) p[i] = 0;
   __syncthreads();
 }
 
@@ -269,16 +271,18 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(
   }
   for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) from[t] = item_of<K>(a, t);
   const int warp = threadIdx.x / 32;
-  const int run = (a.tokens + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;
+  // (128 tokens a warp at least: every warp has counters to be added up)
+  const int run = max((a.tokens + kSortWarps * 32 - 1) / (kSortWarps * 32), 4) * 32;
+  const int warps = (a.tokens + run - 1) / run;
   const int lo = min(warp * run, a.tokens), hi = min(lo + run, a.tokens);
   const unsigned mask = (1u << a.bits) - 1;
   for (int p = 0; p < a.passes; ++p) {
-    clear(rows);
+    clear(rows, warps);
     const int shift = a.tokenBits + p * a.bits;
     auto get = [&](int i) { return from[i]; };
     digits_of_run<K, false>(rows[warp], lo, hi, shift, mask, get, [](unsigned, K) {});
     __syncthreads();
-    places(rows, sScan, [](int, unsigned*, unsigned*) {});
+    places(rows, warps, sScan, [](int, unsigned*, unsigned*) {});
     if (p + 1 == a.passes) {
       digits_of_run<K, true>(rows[warp], lo, hi, shift, mask, get, [&](unsigned at, K x) {
         a.out[at] = (Item)(x >> a.tokenBits) << kItemBits | (unsigned)(x & ((K)1 << a.tokenBits) - 1);
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
   __shared__ unsigned sScan[kSortWarps];
   unsigned(*rows)[kDigits] = reinterpret_cast<unsigned(*)[kDigits]>(smem);
   pdl_launch();
-  clear(rows);
+  clear(rows, kSortWarps);
   pdl_wait();
   const int warp = threadIdx.x / 32;
   const int begin = (int)min((long long)blockIdx.x * a.run, (long long)a.tokens);
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
     }
     return;
   }
-  places(rows, sScan, [&](int d, unsigned* all, unsigned* before) {
+  places(rows, kSortWarps, sScan, [&](int d, unsigned* all, unsigned* before) {
     unsigned sum = 0, mine = 0;
 #pragma unroll 16
     for (int c = 0; c < a.ctas; ++c) {

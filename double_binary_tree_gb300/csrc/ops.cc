@@ -57,15 +57,41 @@ bool op_buffers_ok(const OpBuffer* b, int n) {
 }
 
 bool op_spans_ok(OpSpan* v, size_t n) {
-  std::sort(v, v + n, [](const OpSpan& a, const OpSpan& b) { return a.lo < b.lo; });
   // the furthest end so far of any span, and of a written one
   size_t any = 0, written = 0;
-  for (const OpSpan* s = v; s < v + n; ++s) {
-    if (s->lo < written || (s->write && s->lo < any)) return false;
-    any = std::max(any, s->hi);
-    if (s->write) written = std::max(written, s->hi);
+  auto apart = [&](const OpSpan* s, size_t m) {
+    for (; m; --m, ++s) {
+      if (s->lo < written || (s->write && s->lo < any)) return false;
+      any = std::max(any, s->hi);
+      if (s->write) written = std::max(written, s->hi);
+    }
+    return true;
+  };
+  // Lists that ascend and lie one behind the other (slices of a few buffers) need
+  // no sorting, only their order.
+  struct Run {
+    size_t first, size;
+  };
+  constexpr int kMost = 16;
+  Run runs[kMost + 1];
+  int m = 0;
+  for (size_t i = 0; i < n && m <= kMost; ++i) {
+    if (i && v[i].lo >= v[i - 1].lo) ++runs[m - 1].size;
+    else runs[m++] = {i, 1};
   }
-  return true;
+  if (m <= kMost) {
+    std::sort(runs, runs + m, [v](const Run& a, const Run& b) { return v[a.first].lo < v[b.first].lo; });
+    bool sorted = true;
+    for (int i = 1; i < m && sorted; ++i)
+      sorted = v[runs[i - 1].first + runs[i - 1].size - 1].lo <= v[runs[i].first].lo;
+    if (sorted) {
+      for (int i = 0; i < m; ++i)
+        if (!apart(v + runs[i].first, runs[i].size)) return false;
+      return true;
+    }
+  }
+  std::sort(v, v + n, [](const OpSpan& a, const OpSpan& b) { return a.lo < b.lo; });
+  return apart(v, n);
 }
 
 bool op_lists_ok(const void* const* src, void* const* dst, int count, size_t bytes,
