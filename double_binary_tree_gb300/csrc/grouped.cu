@@ -14,9 +14,9 @@
 //           multiple of 16 (pairs of CTAs: 32) of those: a group's last tile costs what it
 //           holds.  (The other way round 64 groups of 512 rows on average pay
 //           for 640: 2048 x 4096 in 400 us instead of the 286 of the peak.)  A group's
-//           rows are cut into tiles of about the same size.  A thread then has
-//           one output column of many rows; pairs of lanes exchange values, so
-//           that a store is two columns of one row.
+//           rows are cut into tiles of about the same size.  The accumulator then
+//           holds the results transposed; they are turned on their way through
+//           shared memory (stmatrix), so that a store covers 64 bytes of eight rows.
 //   few     The same for few rows a group: up to 32 columns, so that nearly all
 //           of shared memory holds weights on their way.
 //   weight  (dW)  A sum over the group's rows.  The last slice of 64 reads on
@@ -54,14 +54,14 @@ struct GroupedArgs {
   unsigned long long timeoutNs;
 };
 
-// dW's rows are stored through shared memory, a warp's 32 rows of 32 columns at a
+// Results are stored through shared memory.  dW: a warp's 32 rows of 32 columns at a
 // time, by a tensor copy, or, rows that are no 16-byte units, an element a lane.
 // (Straight from registers a store covers 16 or 32 bytes of 32 rows, as many lines
 // as there are rows, which took a third of the time where groups have a few hundred
-// rows.)
-constexpr int kStaged = 32 * 64;  // bytes of a warp
+// rows.)  Rows: 16 rows of 32 columns, 64 bytes of eight rows to a store.
+constexpr int kStaged = 32 * 64;  // bytes of a warp's 32 rows
 
-template <int BN, bool PAIR, bool STAGED>
+template <int BN, bool PAIR, bool WEIGHT>
 struct GroupedShape {
   static constexpr int kABytes = kTileM * kTileK * 2;
   static constexpr int kBRows = PAIR ? BN / 2 : BN;
@@ -69,7 +69,7 @@ struct GroupedShape {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kTileRows = PAIR ? 2 * kTileM : kTileM;
   static constexpr int kWarps = BN >= 128 ? 16 : 4;  // of the epilogue
-  static constexpr int kStagedBytes = STAGED ? kWarps * kStaged : 0;
+  static constexpr int kStagedBytes = kWarps * (WEIGHT ? kStaged : kStaged / 2);
   static constexpr int kStages = (kGroupedSmem - kStagedBytes) / kStageBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kStagedBytes;
   static constexpr int kTmem = 2 * BN;
@@ -154,6 +154,76 @@ __device__ __forceinline__ void store_staged(uint32_t staged, T* out, long long 
                  : "r"(staged_piece(staged, row, lane / 8) + lane % 8 * 2)
                  : "memory");
     if (lane < cols) reinterpret_cast<uint16_t*>(out + row * ld)[lane] = x;
+  }
+}
+
+// 16 rows of the accumulator by 32 columns, as products hand them out: lane l has of
+// each eight columns 2 (l % 4) and the next, of row l / 4, then of row l / 4 + 8.
+__device__ __forceinline__ void tmem_issue_fragment(uint32_t addr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_fragment(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+// A warp's 32 rows of the accumulator by 32 columns, turned: its columns are `rows`
+// rows of the result, its rows `cols` columns (at most 32 of each).
+template <typename T>
+__device__ __forceinline__ void store_turned(uint32_t acc, uint32_t staged, T* out, long long ld,
+                                             int rows, int cols, int align) {
+  const int lane = threadIdx.x % 32;
+  float a[16], b[16];  // rows 0 to 15 and 16 to 31
+  tmem_issue_fragment(acc, a);
+  tmem_issue_fragment(acc + (16u << 16), b);
+  tmem_wait_fragment(a);
+  tmem_wait_fragment(b);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // 16 rows of the result
+    __syncwarp();                // (what was there has been read)
+#pragma unroll
+    for (int i = 8 * h; i < 8 * h + 8; i += 4)  // eight rows: four 8 x 8 matrices, transposed
+      asm volatile(
+          "stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+              staged_piece(staged, i % 8 * 2 + lane % 8, lane / 8)),
+          "r"(pack2<T>(a[i], a[i + 1])), "r"(pack2<T>(a[i + 2], a[i + 3])),
+          "r"(pack2<T>(b[i], b[i + 1])), "r"(pack2<T>(b[i + 2], b[i + 3]))
+          : "memory");
+    __syncwarp();
+    T* to = out + 16 * h * ld;
+    const int n = rows - 16 * h;
+    if (align >= 16 && cols >= 32) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = k * 8 + lane / 4;
+        uint4 q;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "r"(staged_piece(staged, row, lane % 4))
+                     : "memory");
+        if (row < n) *reinterpret_cast<uint4*>(to + row * ld + lane % 4 * 8) = q;
+      }
+    } else {
+#pragma unroll 8
+      for (int row = 0; row < min(n, 16); ++row) {
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(x)
+                     : "r"(staged_piece(staged, row, lane / 8) + lane % 8 * 2)
+                     : "memory");
+        if (lane < cols) reinterpret_cast<uint16_t*>(to + row * ld)[lane] = x;
+      }
+    }
   }
 }
 
@@ -530,7 +600,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     };
     T* out = static_cast<T*>(g.out);
     const uint32_t staged =
-        stage0 + (unsigned)(kStages * Shape::kStageBytes + (kWeight ? (warp - 4) * kStaged : 0));
+        stage0 + (unsigned)(kStages * Shape::kStageBytes + (warp - 4) * (kWeight ? kStaged : kStaged / 2));
     // 32 columns from c of the tile
     auto store = [&](const GroupTile& o, int c, const float(&v)[32]) {
       const int m = o.m0 + (int)rank * kTileM + row;
@@ -593,15 +663,22 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
         for (int i = 0; i < kUnits; ++i) {
           const int c = (part + i * kGroups) * 32;
           if (!there(o, c)) break;
-          float v[32];
           __syncwarp();
-          if (slices) {
-            tmem_load32(quadBase + (unsigned)(buf * BN + c), v);
-          } else {
+          if constexpr (kWeight) {
+            float v[32];
+            if (slices) {
+              tmem_load32(quadBase + (unsigned)(buf * BN + c), v);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+              for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            }
+            store(o, c, v);
+          } else {
+            const int m = o.m0 + (int)rank * kTileM + quad * 32;  // the warp's first
+            store_turned(quadBase + (unsigned)(buf * BN + c), staged,
+                         out + (o.n0 + c) * g.ld + m, g.ld, min(o.hi - o.n0, o.width) - c, g.M - m,
+                         g.align);
           }
-          store(o, c, v);
         }
         if (slices) release();
       }
