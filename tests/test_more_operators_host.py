@@ -2,6 +2,7 @@
 before anything is enqueued.  The pointers are never dereferenced."""
 
 import math
+import random
 
 import pytest
 
@@ -181,3 +182,37 @@ def values_args(**kw):
 ])
 def test_adamw_values_refusals(bad):
     assert code(vr.vr_adamw_values, *values_args(**bad)) == INV
+
+
+def test_adamw_overlaps_as_a_plain_statement_says():
+    """Random layouts: refused exactly when a written buffer touches another
+    one.  (What is not refused goes on to the device: none here.)"""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not real")
+    rng = random.Random(4)
+    seen = set()
+    for _ in range(3000):
+        n = rng.randint(1, 4)
+        sizes = [rng.randint(1, 900) for _ in range(n)]
+        space = rng.choice([20000, 60000, 400000])
+        if rng.random() < 0.5:  # slices of a few buffers, as programs have them
+            def place(unit):
+                at, out = A + rng.randint(0, space) * 256, []
+                for k in sizes:
+                    out.append(at)
+                    at += (k * unit + 255) // 256 * 256 + rng.choice([0, 0, 0, 256])
+                return out
+        else:
+            def place(unit):
+                return [A + rng.randint(0, space) * 4 for _ in sizes]
+        p, g, m, v = (place(4) for _ in range(4))
+        extents = [(a, a + 4 * k, w) for ps, w in ((p, True), (g, False), (m, True), (v, True))
+                   for a, k in zip(ps, sizes)]
+        bad = any((x[2] or y[2]) and x[0] < y[1] and y[0] < x[1]
+                  for i, x in enumerate(extents) for y in extents[:i])
+        got = code(vr.vr_adamw, p, g, m, v, None, None, None, sizes, n, vr.VR_FLOAT32,
+                   vr.VR_FLOAT32, 32, 1e-3, 0.9, 0.99, 1e-8, 0.1, 1, 1.0, 1, None)
+        assert (got == INV) == bad, (extents, got)
+        seen.add(bad)
+    assert seen == {True, False}
