@@ -633,7 +633,7 @@ constexpr size_t kMostSize = (size_t)1 << 40;
 struct Spans {
   std::vector<OpSpan> v;
   void add(const void* p, size_t bytes, bool write) {
-    if (p && bytes) v.push_back({(uintptr_t)p, (uintptr_t)p + bytes, write});
+    if (bytes && p) v.push_back({(uintptr_t)p, (uintptr_t)p + bytes, write});
   }
 };
 
@@ -704,32 +704,31 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
       if (n > kMostSize) return VR_ERR_INVALID_ARGUMENT;
       if (!n) continue;
       if (!params[i] || !grads[i] || !m[i] || !v[i] || (few && (!mScales[i] || !vScales[i])) ||
-          (masters && !masters[i]) || (uintptr_t)params[i] % E || (uintptr_t)grads[i] % GE ||
-          ((uintptr_t)m[i] | (uintptr_t)v[i]) % SE ||
-          (few && ((uintptr_t)mScales[i] | (uintptr_t)vScales[i]) % 4) ||
-          (masters && (uintptr_t)masters[i] % 4))
+          (masters && !masters[i]) || (uintptr_t)params[i] & (E - 1) ||
+          (uintptr_t)grads[i] & (GE - 1) || ((uintptr_t)m[i] | (uintptr_t)v[i]) & (SE - 1) ||
+          (few && ((uintptr_t)mScales[i] | (uintptr_t)vScales[i]) & 3) ||
+          (masters && (uintptr_t)masters[i] & 3))
         return VR_ERR_INVALID_ARGUMENT;
     }
-    auto list = [&](auto p, size_t elem, size_t per, bool write) {
-      for (int i = 0; p && i < count; ++i)
-        if (sizes[i]) spans.add(p[i], (sizes[i] + per - 1) / per * elem, write);
+    auto list = [&](auto p, size_t elem, bool write) {
+      for (int i = 0; p && i < count; ++i) spans.add(p[i], sizes[i] * elem, write);
     };
-    list(params, E, 1, true);
-    list(grads, GE, 1, false);
-    list(m, SE, 1, true);
-    list(v, SE, 1, true);
-    list(mScales, 4, kBlock, true);
-    list(vScales, 4, kBlock, true);
-    list(masters, 4, 1, true);
+    auto scales = [&](auto p) {
+      for (int i = 0; p && i < count; ++i) spans.add(p[i], (sizes[i] + kBlock - 1) / kBlock * 4, true);
+    };
+    list(params, E, true);
+    list(grads, GE, false);
+    list(m, SE, true);
+    list(v, SE, true);
+    scales(mScales);
+    scales(vScales);
+    list(masters, 4, true);
     spans.add(control, 12, false);
     if (!op_spans_ok(spans.v.data(), spans.v.size())) return VR_ERR_INVALID_ARGUMENT;
     OpDevice dev;
     vr_result_t e = op_device(&dev);
     if (e != VR_SUCCESS) return e;
-    for (const OpSpan& s : spans.v) {
-      const void* p = (const void*)s.lo;
-      if ((e = op_reachable(&p, 1, dev.device)) != VR_SUCCESS) return e;
-    }
+    if ((e = op_reachable(spans.v.data(), spans.v.size(), dev.device)) != VR_SUCCESS) return e;
     AdamArgs a;
     a.beta1 = beta1;
     a.beta2 = beta2;
@@ -760,8 +759,9 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
             masters ? masters[i] : nullptr,
             0,
             0};
-      return (uintptr_t)params[i] % (8 * E) == 0 && (uintptr_t)grads[i] % (8 * GE) == 0 &&
-             ((uintptr_t)m[i] | (uintptr_t)v[i]) % (8 * SE) == 0 && (uintptr_t)t->master % 32 == 0;
+      return !((uintptr_t)params[i] & (8 * E - 1)) && !((uintptr_t)grads[i] & (8 * GE - 1)) &&
+             !(((uintptr_t)m[i] | (uintptr_t)v[i]) & (8 * SE - 1)) &&
+             !((uintptr_t)t->master & 31);
     });
   } catch (...) {  // no host memory for the list
     return VR_ERR_INTERNAL;
@@ -802,10 +802,7 @@ vr_result_t vr_adamw_values(const void* const* m, const void* const* v,
     OpDevice dev;
     vr_result_t e = op_device(&dev);
     if (e != VR_SUCCESS) return e;
-    for (const OpSpan& s : spans.v) {
-      const void* p = (const void*)s.lo;
-      if ((e = op_reachable(&p, 1, dev.device)) != VR_SUCCESS) return e;
-    }
+    if ((e = op_reachable(spans.v.data(), spans.v.size(), dev.device)) != VR_SUCCESS) return e;
     AdamArgs a;
     return over_tensors({(const void*)adamw_values_kernel, 0}, a, sizes, count, dev, stream,
                         [&](int i, Tensor* t) {

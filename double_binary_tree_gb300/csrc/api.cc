@@ -695,6 +695,15 @@ vr_result_t op_reachable(const OpBuffer* b, int n, int device) {
   return VR_SUCCESS;
 }
 
+vr_result_t op_reachable(const OpSpan* v, size_t n, int device) {
+  for (size_t i = 0; i < n; ++i) {
+    const void* p = reinterpret_cast<const void*>(v[i].lo);
+    const vr_result_t e = check_reachable(&p, 1, device);
+    if (e != VR_SUCCESS) return e;
+  }
+  return VR_SUCCESS;
+}
+
 vr_result_t op_launch(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
                       void* stream, int cluster) {
   cudaLaunchConfig_t cfg = {};

@@ -54,6 +54,7 @@ bool op_spans_ok(OpSpan* v, size_t n);
 // reached from the current device.
 vr_result_t op_reachable(const OpBuffer* b, int n, int device);
 vr_result_t op_reachable(const void* const* p, int n, int device);
+vr_result_t op_reachable(const OpSpan* v, size_t n, int device);
 
 // Bytes rounded up to the alignment of a workspace's parts.
 constexpr size_t kOpAlign = 256;
