@@ -23,6 +23,7 @@
 //           into the next group; the rows behind the end, up to the next
 //           multiple of the 16 that a product takes, are zeroed in shared memory
 //           (in both operands: they may hold NaN).
+//   both    dW's tiles and then dX's in one launch, where they are few.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -35,21 +36,18 @@ namespace {
 constexpr int kMostGroups = 1024;
 constexpr int kGroupedSmem = 212 * 1024;  // the stages; the tables of the groups are beside them
 
-enum Kind : int { kLinear, kGradRows, kGradWeight };
-template <int KIND>
-struct KindOf {
-  static constexpr bool kWeight = KIND == kGradWeight;
-  // operands whose rows are the summed dimension
-  static constexpr bool kAMn = KIND != kLinear, kBMn = kWeight;
+enum Kind : int { kLinear, kGradRows, kGradWeight, kGradBoth };
+struct Product {
+  CUtensorMap a, b, c;  // c: dW, where its rows are 16-byte units
+  int M, N, K;          // N (rows) or K (weight) is counted on the device
+  int align;
+  void* out;
+  long long ld;         // elements between its rows
 };
 struct GroupedArgs {
-  CUtensorMap a, b, c;  // c: dW, where its rows are 16-byte units
+  Product rows, weight;  // those that the kind has
   const int* counts;
-  int groups, rows;  // rows: that the buffers have
-  int M, N, K;       // of the product; N (rows) or K (weight) is counted on the device
-  void* out;
-  long long ld;      // elements between its rows
-  int align;
+  int groups, most;      // most: rows that the buffers have
   unsigned* status;
   unsigned long long timeoutNs;
 };
@@ -88,6 +86,7 @@ __device__ __forceinline__ int quotient(int t, int d) {
 // what an instruction takes; the group's rows [lo, hi).
 struct GroupTile {
   int g, m0, n0, width, lo, hi;
+  bool weight;  // of dW
 };
 
 // The same arrive and wait as mbar_arrive and mbar_test for what another CTA of
@@ -259,11 +258,12 @@ __device__ __forceinline__ void store_columns(T* out, long long ld, const float 
 }
 
 template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
-__global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGradWeight>::kWarps, 1)
+__global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, (KIND >= kGradWeight)>::kWarps, 1)
     grouped_kernel(const __grid_constant__ GroupedArgs g) {
-  using Is = KindOf<KIND>;
-  using Shape = GroupedShape<BN, PAIR, Is::kWeight>;
-  constexpr bool AMN = Is::kAMn, BMN = Is::kBMn, kWeight = Is::kWeight;
+  constexpr bool kWeight = KIND >= kGradWeight, kRowsToo = KIND != kGradWeight;  // the tiles it has
+  using Shape = GroupedShape<BN, PAIR, kWeight>;
+  static_assert(!(kWeight && kRowsToo) || (PAIR && CHUNK == 0), "both: pairs, sums of one piece");
+  constexpr bool kTurned = KIND != kLinear;  // rows: the weight's rows are the summed dimension
   constexpr int kStages = Shape::kStages, kCtas = PAIR ? 2 : 1, kRows = Shape::kTileRows;
   constexpr int kEpilogueWarps = Shape::kWarps, kGroups = kEpilogueWarps / 4;
   constexpr int kUnits = BN / 32 / kGroups;  // of 32 columns, for each group of four warps
@@ -317,9 +317,15 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     asm volatile("fence.proxy.async;" ::: "memory");
   }
   if (warp == 1 && elected()) {
-    prefetch_map(&g.a);
-    prefetch_map(&g.b);
-    if (kWeight && g.align >= 16) prefetch_map(&g.c);
+    if (kRowsToo) {
+      prefetch_map(&g.rows.a);
+      prefetch_map(&g.rows.b);
+    }
+    if (kWeight) {
+      prefetch_map(&g.weight.a);
+      prefetch_map(&g.weight.b);
+      if (g.weight.align >= 16) prefetch_map(&g.weight.c);
+    }
   }
   if (warp == 2) {
     if constexpr (PAIR) {
@@ -338,10 +344,13 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
   }
   pdl_launch();
   pdl_wait();
-  const int tilesM = (g.M + kRows - 1) / kRows, tilesN = (g.N + BN - 1) / BN;
+  // tiles along the products' M, and along dW's N; dW's come first
+  const int rowsM = (g.rows.M + kRows - 1) / kRows, weightM = (g.weight.M + kRows - 1) / kRows;
+  const int weightN = (g.weight.N + BN - 1) / BN;
+  const int weightTiles = kWeight ? g.groups * weightM * weightN : 0;
   if (warp == 3) {  // the groups' rows and tiles
     // Caps of a tile's columns, and the tiles of all groups with each.
-    constexpr int kCaps = kWeight || BN < 128 ? 1 : 4;
+    constexpr int kCaps = kWeight || BN < 128 ? 1 : 4;  // (both: dW has tiles enough)
     auto cap_of = [](int i) { return i == 0 ? BN : i == 1 ? 192 : i == 2 ? 128 : 64; };
     int rows = 0, sums[kCaps] = {};
 #pragma unroll 4
@@ -357,11 +366,11 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
         if (lane >= o) end += up;
       }
       end += rows;
-      if (given < 0 || end > g.rows) atomicCAS(g.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
-      const int hi = (int)min(end, (long long)g.rows);
+      if (given < 0 || end > g.most) atomicCAS(g.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
+      const int hi = (int)min(end, (long long)g.most);
       const int up = __shfl_up_sync(0xffffffffu, hi, 1), lo = lane ? up : rows;
       if (e < g.groups) rowStart[e + 1] = hi;
-      if constexpr (!kWeight) {
+      if constexpr (kCaps > 1) {
 #pragma unroll
         for (int i = 0; i < kCaps; ++i) sums[i] += (hi - lo + cap_of(i) - 1) / cap_of(i);
       }
@@ -379,18 +388,17 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
 #pragma unroll
       for (int i = 0; i < kCaps; ++i) {
         const float across = (float)__reduce_add_sync(0xffffffffu, sums[i]);
-        const float rounds = ceilf(across * (float)tilesM / workers);
+        const float rounds = ceilf(across * (float)rowsM / workers);
         const float time = rounds * (0.13f + 0.0007f * (float)rows / fmaxf(across, 1.0f));
         if (i == 0 || time < best) best = time, cap = cap_of(i);
         if (i == 0 && rounds >= 3.0f) break;
       }
     }
     int tiles = 0;
-    for (int e0 = 0; e0 < g.groups; e0 += 32) {
+    for (int e0 = 0; kRowsToo && e0 < g.groups; e0 += 32) {
       const int e = e0 + lane;
       int sum = 0;
-      if (e < g.groups)
-        sum = kWeight ? tilesM * tilesN : (rowStart[e + 1] - rowStart[e] + cap - 1) / cap * tilesM;
+      if (e < g.groups) sum = (rowStart[e + 1] - rowStart[e] + cap - 1) / cap * rowsM;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
         const int up = __shfl_up_sync(0xffffffffu, sum, o);
@@ -406,23 +414,34 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
   if constexpr (PAIR) cluster_sync();  // the peer's barriers are set up
   tmem_fence_after();
   const uint32_t tmem = tmemBase;
-  const int tiles = tileStart[g.groups], cap = chosenCap;
+  const int tiles = weightTiles + (kRowsToo ? tileStart[g.groups] : 0), cap = chosenCap;
   const int firstTile = (int)blockIdx.x / kCtas, tileStep = (int)gridDim.x / kCtas;
-  // Tiles are walked upwards: `e` is the group of the last one.
+  // Tiles are walked upwards: `e` is the group of the last one of rows.
   auto tile_at = [&](int t, int& e) {
-    while (t >= tileStart[e + 1]) ++e;
-    GroupTile o = {e, 0, 0, BN, rowStart[e], rowStart[e + 1]};
-    t -= tileStart[e];
+    constexpr int kHigh = 2048 / kRows, G = Shape::kGrain;
+    const bool weight = kWeight && (!kRowsToo || t < weightTiles);
+    int of, high;
+    if (weight) {
+      of = quotient(t, weightM * weightN);
+      t -= of * weightM * weightN;
+      high = weightM;
+    } else {
+      t -= weightTiles;
+      while (t >= tileStart[e + 1]) ++e;
+      t -= tileStart[e];
+      of = e;
+      high = rowsM;
+    }
+    GroupTile o = {of, 0, 0, BN, rowStart[of], rowStart[of + 1], weight};
     // the tiles of a block of 2048 rows of the product column by column, so that
     // the operands of the tiles in flight stay in L2
-    constexpr int kHigh = 2048 / kRows;
-    constexpr int G = Shape::kGrain;
-    const int n = o.hi - o.lo, across = kWeight ? tilesN : quotient(n + cap - 1, cap);
-    const int block = quotient(t, kHigh * across), high = min(kHigh, tilesM - block * kHigh);
+    const int n = o.hi - o.lo, across = weight ? weightN : quotient(n + cap - 1, cap);
+    const int block = quotient(t, kHigh * across);
+    high = min(kHigh, high - block * kHigh);
     t -= block * kHigh * across;
     const int column = quotient(t, high);
     o.m0 = (block * kHigh + t - column * high) * kRows;
-    if constexpr (kWeight) {
+    if (weight) {
       o.n0 = column * BN;
     } else {  // columns in shares of about one size, none of them empty
       const int share = quotient((n + G - 1) / G + across - 1, across) * G, from = column * share;
@@ -431,8 +450,10 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     }
     return o;
   };
+  // (known where a kind has tiles of one sort only)
+  auto of_weight = [](const GroupTile& o) { return kWeight && (!kRowsToo || o.weight); };
   auto slices_of = [&](const GroupTile& o) {
-    return ((kWeight ? o.hi - o.lo : g.K) + kTileK - 1) / kTileK;
+    return ((of_weight(o) ? o.hi - o.lo : g.rows.K) + kTileK - 1) / kTileK;
   };
 
   if (warp == 0) {
@@ -444,14 +465,16 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     for (int t = firstTile; ok && t < tiles; t += tileStep) {
       const GroupTile o = tile_at(t, e);
       const int slices = slices_of(o);
+      const bool weight = of_weight(o);
       const int mine = PAIR ? o.width / 2 : o.width;  // columns that this CTA holds
       const int m0 = o.m0 + (int)rank * kTileM, n0 = o.n0 + (int)rank * mine;
-      const int first = kWeight ? o.lo : 0, boxes = (mine + Shape::kBox - 1) / Shape::kBox;
-      const unsigned bytes = Shape::kABytes + (kWeight ? Shape::kBBytes : boxes * (Shape::kBox * 128));
+      const int boxes = (mine + Shape::kBox - 1) / Shape::kBox;
+      const unsigned bytes =
+          Shape::kABytes + (weight ? Shape::kBBytes : boxes * (Shape::kBox * 128));
       for (int kb = 0; kb < slices; ++kb) {
         ok = all_wait(empty(s), turn ^ 1);
         if (!ok) break;
-        const bool tail = kTails && o.hi - o.lo < (kb + 1) * kTileK;
+        const bool tail = kTails && weight && o.hi - o.lo < (kb + 1) * kTileK;
         if (elected()) {
           uint32_t landed = landed0 + 8u * s;
           if (tail) {
@@ -460,23 +483,25 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
           } else if (leader) {
             mbar_arrive_expect_tx(full(s), kCtas * bytes);
           }
-          const uint32_t dst = stage0 + (unsigned)s * Shape::kStageBytes;
-          const int k0 = first + kb * kTileK, z = kWeight ? 0 : o.g;
-          if constexpr (AMN) {
+          const uint32_t a = stage0 + (unsigned)s * Shape::kStageBytes, b = a + Shape::kABytes;
+          const int k0 = kb * kTileK;
+          if (weight) {
 #pragma unroll
             for (int i = 0; i < kTileM / 64; ++i)
-              tensor_load<PAIR>(dst + i * kSlab, &g.a, m0 + i * 64, k0, z, landed);
-          } else {
-            tensor_load<PAIR>(dst, &g.a, k0, m0, z, landed);
-          }
-          if constexpr (BMN) {
+              tensor_load<PAIR>(a + i * kSlab, &g.weight.a, m0 + i * 64, o.lo + k0, 0, landed);
 #pragma unroll
             for (int i = 0; i < Shape::kBRows / 64; ++i)
-              tensor_load<PAIR>(dst + Shape::kABytes + i * kSlab, &g.b, n0 + i * 64, k0, 0, landed);
+              tensor_load<PAIR>(b + i * kSlab, &g.weight.b, n0 + i * 64, o.lo + k0, 0, landed);
           } else {
+            if constexpr (kTurned) {
+#pragma unroll
+              for (int i = 0; i < kTileM / 64; ++i)
+                tensor_load<PAIR>(a + i * kSlab, &g.rows.a, m0 + i * 64, k0, o.g, landed);
+            } else {
+              tensor_load<PAIR>(a, &g.rows.a, k0, m0, o.g, landed);
+            }
             for (int i = 0; i < boxes; ++i)
-              tensor_load<PAIR>(dst + Shape::kABytes + i * (Shape::kBox * 128), &g.b, k0,
-                                n0 + i * Shape::kBox, 0,
+              tensor_load<PAIR>(b + i * (Shape::kBox * 128), &g.rows.b, k0, n0 + i * Shape::kBox, 0,
                                 landed);
           }
         }
@@ -500,17 +525,24 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
       }
     }
   } else if (warp == 1 && leader) {
-    // (the number of columns is the tile's)
-    constexpr uint32_t idesc0 = mma_idesc<T>(kRows, 0, AMN, BMN);
-    constexpr unsigned aStep = (AMN ? 16 * 128 : 32) >> 4, bStep = (BMN ? 16 * 128 : 32) >> 4;
-    const uint64_t aDesc0 = operand_desc(stage0, AMN ? kSlab : 16, 1024);
-    const uint64_t bDesc0 = operand_desc(stage0 + Shape::kABytes, BMN ? kSlab : 16, 1024);
+    // MN-major operands: slabs of 64 columns, 16 rows of 128 bytes to a product;
+    // K-major ones: 32 bytes along a row
+    const uint64_t aMn = operand_desc(stage0, kSlab, 1024), aK = operand_desc(stage0, 16, 1024);
+    const uint64_t bMn = operand_desc(stage0 + Shape::kABytes, kSlab, 1024);
+    const uint64_t bK = operand_desc(stage0 + Shape::kABytes, 16, 1024);
+    constexpr unsigned kStepMn = 16 * 128 >> 4, kStepK = 32 >> 4;
     int s = 0, turn = 0, buf = 0, bufTurn = 0, e = 0;
     bool ok = true;
     for (int t = firstTile; ok && t < tiles; t += tileStep) {
       const GroupTile o = tile_at(t, e);
       const int slices = slices_of(o), chunk = CHUNK ? CHUNK : max(slices, 1);
-      const uint32_t idesc = idesc0 | (uint32_t)(o.width >> 3) << 17;
+      const bool weight = of_weight(o);
+      const uint32_t idesc = (weight ? mma_idesc<T>(kRows, 0, true, true)
+                                     : mma_idesc<T>(kRows, 0, kTurned, false)) |
+                             (uint32_t)(o.width >> 3) << 17;
+      const uint64_t aDesc0 = weight || kTurned ? aMn : aK, bDesc0 = weight ? bMn : bK;
+      const unsigned aStep = weight || kTurned ? kStepMn : kStepK;
+      const unsigned bStep = weight ? kStepMn : kStepK;
       for (int c0 = 0; ok && c0 < slices; c0 += chunk) {
         ok = all_wait(accEmpty(buf), bufTurn ^ 1);
         if (!ok) break;
@@ -521,12 +553,13 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
           ok = all_wait(full(s), turn);
           if (!ok) break;
           int steps = kTileK / 16;
-          if constexpr (kWeight) {
+          if (weight) {
             const int left = o.hi - o.lo - kb * kTileK;  // rows of the group in this slice
             if (left < kTileK) {
               steps = (left + 15) / 16;
-              if (!kTails) zero_rows<Shape::kStageBytes / (int)kSlab>(
-                  stage0 + (unsigned)s * Shape::kStageBytes, left, steps * 16, lane);
+              if (!kTails)
+                zero_rows<Shape::kStageBytes / (int)kSlab>(
+                    stage0 + (unsigned)s * Shape::kStageBytes, left, steps * 16, lane);
             }
           }
           tmem_fence_after();
@@ -566,7 +599,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
       const GroupTile o = tile_at(t, e);
       const int slices = slices_of(o), left = (o.hi - o.lo) % kTileK;
       done += slices;
-      if (!left) continue;
+      if (!of_weight(o) || !left) continue;
       const int s = (int)((done - 1) % kStages);
       const unsigned parity = tailTurn >> s & 1;
       tailTurn ^= 1u << s;
@@ -586,7 +619,6 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
     if (!ok) raise_error(g.status, &abortFlag, VR_ERR_TIMEOUT);
   } else if (warp >= 4) {
     const int quad = warp % 4, part = (warp - 4) / 4;
-    const int row = quad * 32 + lane;
     const uint32_t quadBase = tmem + ((uint32_t)(quad * 32) << 16);
     int buf = 0, bufTurn = 0, e = 0;
     auto next = [&]() {
@@ -606,30 +638,31 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
       }
       if (++buf == 2) buf = 0, bufTurn ^= 1;
     };
-    T* out = static_cast<T*>(g.out);
-    const uint32_t staged =
-        stage0 + (unsigned)(kStages * Shape::kStageBytes + (warp - 4) * (kWeight ? kStaged : kStaged / 2));
-    // 32 columns from c of the tile
-    auto store = [&](const GroupTile& o, int c, const float(&v)[32]) {
-      const int m = o.m0 + (int)rank * kTileM + row;
-      if constexpr (kWeight) {
-        const int first = m - lane, n = o.n0 + c;  // the warp's tile
-        staged_free();
-        stage_rows<T>(staged, v);
-        if (first >= g.M) return;
-        if (g.align >= 16)
-          store_staged(staged, &g.c, n, first, o.g);
-        else
-          store_staged(staged, out + ((long long)o.g * g.M + first) * g.ld + n, g.ld, g.M - first,
-                       g.N - n);
-      } else {
-        store_columns(out + (o.n0 + c) * g.ld, g.ld, v, min(o.hi - o.n0, o.width) - c, m, g.M,
-                      g.align);
-      }
+    const uint32_t staged = stage0 + (unsigned)(kStages * Shape::kStageBytes +
+                                                (warp - 4) * (kWeight ? kStaged : kStaged / 2));
+    const int m = (int)rank * kTileM + quad * 32;  // the warp's first row of a tile
+    // 32 columns from c of a tile of dW
+    auto store_weight = [&](const GroupTile& o, int c, const float(&v)[32]) {
+      const Product& p = g.weight;
+      const int first = o.m0 + m, n = o.n0 + c;
+      staged_free();
+      stage_rows<T>(staged, v);
+      if (first >= p.M) return;
+      if (p.align >= 16)
+        store_staged(staged, &p.c, n, first, o.g);
+      else
+        store_staged(staged, static_cast<T*>(p.out) + ((long long)o.g * p.M + first) * p.ld + n,
+                     p.ld, p.M - first, p.N - n);
     };
+    // and of one of rows: the first row's place
+    auto row_of = [&](const GroupTile& o, int c) {
+      return static_cast<T*>(g.rows.out) + (o.n0 + c) * g.rows.ld;
+    };
+    // rows that the tile has from its column c on
+    auto rows_of = [&](const GroupTile& o, int c) { return min(o.hi - o.n0, o.width) - c; };
     // whether the 32 columns from c are in the product
     auto there = [&](const GroupTile& o, int c) {
-      return kWeight ? o.n0 + c < g.N : c < o.width && o.n0 + c < o.hi;
+      return of_weight(o) ? o.n0 + c < g.weight.N : rows_of(o, c) > 0;
     };
     for (int t = firstTile; t < tiles; t += tileStep) {
       const GroupTile o = tile_at(t, e);
@@ -663,7 +696,12 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = sum[i * 32 + j];
-          if (there(o, c)) store(o, c, v);
+          if (!there(o, c)) break;
+          if constexpr (kWeight)
+            store_weight(o, c, v);
+          else
+            store_columns(row_of(o, c), g.rows.ld, v, rows_of(o, c), o.m0 + m + lane, g.rows.M,
+                          g.rows.align);
         }
       } else {
         if (slices && !next()) break;
@@ -672,7 +710,7 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
           const int c = (part + i * kGroups) * 32;
           if (!there(o, c)) break;
           __syncwarp();
-          if constexpr (kWeight) {
+          if (of_weight(o)) {
             float v[32];
             if (slices) {
               tmem_load32(quadBase + (unsigned)(buf * BN + c), v);
@@ -680,12 +718,11 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, KIND == kGra
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.0f;
             }
-            store(o, c, v);
+            store_weight(o, c, v);
           } else {
-            const int m = o.m0 + (int)rank * kTileM + quad * 32;  // the warp's first
-            store_turned(quadBase + (unsigned)(buf * BN + c), staged,
-                         out + (o.n0 + c) * g.ld + m, g.ld, min(o.hi - o.n0, o.width) - c, g.M - m,
-                         g.align);
+            if (kWeight) staged_free();
+            store_turned(quadBase + (unsigned)(buf * BN + c), staged, row_of(o, c) + o.m0 + m,
+                         g.rows.ld, rows_of(o, c), g.rows.M - o.m0 - m, g.rows.align);
           }
         }
         if (slices) release();
@@ -786,44 +823,58 @@ struct GroupedSize {
   int groups;
 };
 
-template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
-vr_result_t launch(const OpDevice& dev, const Matrix& a, const Matrix& b, const GroupedSize& z,
-                   const int* counts, void* out, size_t ld, void* stream) {
-  using Is = KindOf<KIND>;
-  using Shape = GroupedShape<BN, PAIR, Is::kWeight>;
-  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-  const void* fn = (const void*)grouped_kernel<T, BN, KIND, PAIR, CHUNK>;
-  GroupedArgs g = {};
+// The operands of a product and where its result goes.
+vr_result_t fill(Product* p, bool bf16, const Matrix& a, int aBox, const Matrix& b, int bBox,
+                 const GroupedSize& z, void* out, size_t ld, bool weight) {
   auto map = [&](CUtensorMap* to, const Matrix& m, int boxRows) {
     return gemm_operand(to, m.p, bf16, m.cols, m.rows, m.batch, m.stride * 2,
                         m.stride * 2 * m.rows, boxRows);
   };
-  vr_result_t e = map(&g.a, a, Is::kAMn ? kTileK : kTileM);
-  if (e != VR_SUCCESS || (e = map(&g.b, b, Is::kBMn ? kTileK : Shape::kBox)) != VR_SUCCESS ||
-      (e = gemm_prepare(fn, dev.device, Shape::kSmem)) != VR_SUCCESS)
-    return e;
-  g.counts = counts;
-  g.groups = z.groups;
-  g.rows = (int)z.rows;
-  g.M = (int)z.M;
-  g.N = (int)z.N;
-  g.K = (int)z.K;
-  g.out = out;
-  g.ld = (long long)ld;
+  vr_result_t e = map(&p->a, a, aBox);
+  if (e != VR_SUCCESS || (e = map(&p->b, b, bBox)) != VR_SUCCESS) return e;
+  p->M = (int)z.M;
+  p->N = (int)z.N;
+  p->K = (int)z.K;
+  p->out = out;
+  p->ld = (long long)ld;
   const uintptr_t bits = (uintptr_t)out | (uintptr_t)(2 * ld);
-  g.align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
-  if (Is::kWeight && g.align == 16 &&
-      (e = gemm_operand(&g.c, out, bf16, z.N, z.M, (size_t)z.groups, ld * 2, ld * 2 * z.M, 32,
-                        kAuxCols)) != VR_SUCCESS)
-    return e;
+  p->align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  if (!weight || p->align < 16) return VR_SUCCESS;
+  return gemm_operand(&p->c, out, bf16, z.N, z.M, (size_t)z.groups, ld * 2, ld * 2 * z.M, 32,
+                      kAuxCols);
+}
+template <int BN, bool PAIR, int KIND>
+vr_result_t fill_rows(GroupedArgs* g, bool bf16, const Matrix& w, const Matrix& x,
+                      const GroupedSize& z, void* out, size_t ld) {
+  return fill(&g->rows, bf16, w, KIND == kLinear ? kTileM : kTileK, x,
+              GroupedShape<BN, PAIR, false>::kBox, z, out, ld, false);
+}
+vr_result_t fill_weight(GroupedArgs* g, bool bf16, const Matrix& dy, const Matrix& x,
+                        const GroupedSize& z, void* out, size_t ld) {
+  return fill(&g->weight, bf16, dy, kTileK, x, kTileK, z, out, ld, true);
+}
+
+template <typename T, int BN, int KIND, bool PAIR, int CHUNK>
+vr_result_t launch(const OpDevice& dev, GroupedArgs& g, size_t rows, int groups, const int* counts,
+                   void* stream) {
+  using Shape = GroupedShape<BN, PAIR, (KIND >= kGradWeight)>;
+  const void* fn = (const void*)grouped_kernel<T, BN, KIND, PAIR, CHUNK>;
+  const vr_result_t e = gemm_prepare(fn, dev.device, Shape::kSmem);
+  if (e != VR_SUCCESS) return e;
+  g.counts = counts;
+  g.groups = groups;
+  g.most = (int)rows;
   g.status = dev.status;
   g.timeoutNs = dev.timeoutNs;
   // at most so many tiles: every group's last one may be cut; with the smallest cap
-  constexpr int kCap = BN < 128 ? BN : 64;
-  const size_t tm = (z.M + Shape::kTileRows - 1) / Shape::kTileRows;
-  const size_t tiles =
-      Is::kWeight ? (size_t)z.groups * tm * ((z.N + BN - 1) / BN)
-                  : (z.rows / kCap + std::min<size_t>((size_t)z.groups, z.rows)) * tm;
+  constexpr size_t kCap = BN < 128 ? BN : 64;
+  auto along = [](int n, int tile) { return (size_t)((n + tile - 1) / tile); };
+  size_t tiles = 0;
+  if (KIND != kGradWeight)
+    tiles += (rows / kCap + std::min<size_t>((size_t)groups, rows)) *
+             along(g.rows.M, Shape::kTileRows);
+  if (KIND >= kGradWeight)
+    tiles += (size_t)groups * along(g.weight.M, Shape::kTileRows) * along(g.weight.N, BN);
   constexpr size_t kCtas = PAIR ? 2 : 1;
   const size_t grid = std::min<size_t>(tiles, dev.sms / kCtas) * kCtas;
   void* args[] = {&g};
@@ -838,20 +889,30 @@ template <typename T>
 constexpr size_t kLongSum = std::is_same<T, __half>::value ? 32768 : 262144;
 
 constexpr size_t kFewRows = 32;  // a group on average
+constexpr size_t kBothMost = 4;  // tiles for each SM: eight rounds of pairs
+
+bool few_rows(size_t rows, int groups) { return rows <= kFewRows * (size_t)groups; }
 
 // out or dX: w's rows by a group's rows.
 template <typename T, int KIND>
 vr_result_t rows_product(const OpDevice& dev, const Matrix& w, const Matrix& x,
                          const GroupedSize& z, const int* counts, void* out, size_t ld,
                          void* stream) {
-  const bool lng = z.K > kLongSum<T>;
-#define VR_GO(BN, PAIR)                                                              \
-  (lng ? launch<T, BN, KIND, PAIR, kLongChunk>(dev, w, x, z, counts, out, ld, stream) \
-       : launch<T, BN, KIND, PAIR, 0>(dev, w, x, z, counts, out, ld, stream))
-  if (z.rows <= kFewRows * (size_t)z.groups) return VR_GO(32, false);
-  if (z.M <= kTileM) return VR_GO(256, false);
-  return VR_GO(256, true);
-#undef VR_GO
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  GroupedArgs g = {};
+  auto go = [&](auto bn, auto pair) {
+    constexpr int BN = decltype(bn)::value;
+    constexpr bool PAIR = decltype(pair)::value;
+    const vr_result_t e = fill_rows<BN, PAIR, KIND>(&g, bf16, w, x, z, out, ld);
+    if (e != VR_SUCCESS) return e;
+    if (z.K > kLongSum<T>)
+      return launch<T, BN, KIND, PAIR, kLongChunk>(dev, g, z.rows, z.groups, counts, stream);
+    return launch<T, BN, KIND, PAIR, 0>(dev, g, z.rows, z.groups, counts, stream);
+  };
+  using std::integral_constant;
+  if (few_rows(z.rows, z.groups)) return go(integral_constant<int, 32>(), std::false_type());
+  if (z.M <= kTileM) return go(integral_constant<int, 256>(), std::false_type());
+  return go(integral_constant<int, 256>(), std::true_type());
 }
 template <typename T>
 vr_result_t linear(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
@@ -861,22 +922,43 @@ vr_result_t linear(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_
                                   ld, stream);
 }
 template <typename T>
-vr_result_t grad_rows(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
-                      size_t outDim, int groups, const int* counts, void* out, void* stream) {
-  return rows_product<T, kGradRows>(dev, p.w, p.dy, {dim, rows, outDim, rows, groups}, counts, out,
-                                    dim, stream);
+vr_result_t weight_product(const OpDevice& dev, const Matrix& dy, const Matrix& x,
+                           const GroupedSize& z, const int* counts, void* out, void* stream) {
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  GroupedArgs g = {};
+  const vr_result_t e = fill_weight(&g, bf16, dy, x, z, out, z.N);
+  if (e != VR_SUCCESS) return e;
+#define VR_GO(PAIR, CHUNK) \
+  launch<T, 256, kGradWeight, PAIR, CHUNK>(dev, g, z.rows, z.groups, counts, stream)
+  if (z.K > kLongSum<T>) return z.M <= kTileM ? VR_GO(false, kLongChunk) : VR_GO(true, kLongChunk);
+  return z.M <= kTileM ? VR_GO(false, 0) : VR_GO(true, 0);
+#undef VR_GO
 }
 template <typename T>
-vr_result_t grad_weight(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim,
-                        size_t outDim, int groups, const int* counts, void* out, void* stream) {
-  const GroupedSize z = {outDim, dim, rows, rows, groups};
-#define VR_GO(PAIR)                                                                             \
-  (rows > kLongSum<T>                                                                           \
-       ? launch<T, 256, kGradWeight, PAIR, kLongChunk>(dev, p.dy, p.x, z, counts, out, dim,     \
-                                                       stream)                                  \
-       : launch<T, 256, kGradWeight, PAIR, 0>(dev, p.dy, p.x, z, counts, out, dim, stream))
-  return outDim <= kTileM ? VR_GO(false) : VR_GO(true);
-#undef VR_GO
+vr_result_t grad(const GroupedPlan& p, const OpDevice& dev, size_t rows, size_t dim, size_t outDim,
+                 int groups, const int* counts, void* dx, void* dw, void* stream) {
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const GroupedSize zx = {dim, rows, outDim, rows, groups}, zw = {outDim, dim, rows, rows, groups};
+  vr_result_t e = VR_SUCCESS;
+  // One launch where both take pairs and sums of one piece, and few tiles.  It saves
+  // the second one's start and a round that is not full (12 groups of 250 rows, 1000 x
+  // 1512: 37 us instead of 46); with many tiles the epilogues of dW beside dX's
+  // cost more (64 groups of 128 rows, 2048 x 4096: 450 us instead of 438; 32 of 2048
+  // rows 1302 instead of 1285).
+  const size_t tiles = (rows / 256 + std::min<size_t>((size_t)groups, rows)) * (up(dim, 256) / 256) +
+                       (size_t)groups * (up(dim, 256) / 256) * (up(outDim, 256) / 256);
+  if (dx && dw && !few_rows(rows, groups) && dim > kTileM && outDim > kTileM &&
+      rows <= kLongSum<T> && outDim <= kLongSum<T> && tiles <= kBothMost * (size_t)dev.sms) {
+    GroupedArgs g = {};
+    if ((e = fill_rows<256, true, kGradRows>(&g, bf16, p.w, p.dy, zx, dx, dim)) != VR_SUCCESS ||
+        (e = fill_weight(&g, bf16, p.dy, p.x, zw, dw, dim)) != VR_SUCCESS)
+      return e;
+    return launch<T, 256, kGradBoth, true, 0>(dev, g, rows, groups, counts, stream);
+  }
+  if (dx && (e = rows_product<T, kGradRows>(dev, p.w, p.dy, zx, counts, dx, dim, stream)) !=
+                VR_SUCCESS)
+    return e;
+  return dw ? weight_product<T>(dev, p.dy, p.x, zw, counts, dw, stream) : VR_SUCCESS;
 }
 
 }  // namespace
@@ -977,16 +1059,9 @@ vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const vo
       (dWeight && (e = pad_matrix(&p.x, w, dev, stream)) != VR_SUCCESS) ||
       (dX && (e = pad_matrix(&p.w, w, dev, stream)) != VR_SUCCESS))
     return e;
-  const bool bf16 = dtype == VR_BFLOAT16;
-  if (dX && (e = bf16 ? grad_rows<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts, dX,
-                                                 stream)
-                      : grad_rows<__half>(p, dev, rows, dim, outDim, groups, counts, dX,
-                                          stream)) != VR_SUCCESS)
-    return e;
-  if (!dWeight) return VR_SUCCESS;
-  return bf16 ? grad_weight<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts, dWeight,
-                                           stream)
-              : grad_weight<__half>(p, dev, rows, dim, outDim, groups, counts, dWeight, stream);
+  return dtype == VR_BFLOAT16
+             ? grad<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts, dX, dWeight, stream)
+             : grad<__half>(p, dev, rows, dim, outDim, groups, counts, dX, dWeight, stream);
 }
 
 }  // extern "C"
