@@ -3,7 +3,9 @@
 //
 //   out_t = scale w[id_t];  dw_v (+)= scale sum_{t: id_t = v} dout_t
 //
-// The lookup is a gather: a warp takes a piece of a token's row.
+// The lookup is a gather: a warp takes a piece of a token's row.  16384 tokens of
+// 4096 in bf16, of 131072 words, take 32.6 us; the distinct rows once and the
+// result are 191 MB, 28.6 us at the copy bandwidth.
 //
 // The gradient sorts the tokens by word, stably, by the words' digits from the
 // lowest up (each pass counts the digits of every warp's run of tokens, adds
@@ -20,6 +22,11 @@
 // by the CTAs beside the one that sorts, each of which marks the words of its
 // part of the table for itself; after a sort over all SMs, by the launch that
 // sums, where a lane looks its word up among the sorted ones.
+//
+// The same 16384 tokens: 217 us, 180 us of them its 1.2 GB at the copy bandwidth.
+// 159 us zero rows (6.0 TB/s to DRAM, the sort beside them), 37 us sum (bound by
+// latency: 78 registers, a third of the warps), 11 us join.  777 tokens x 1000 added
+// to a table: 14 us, the three launches' latencies (9, 6 and 5 us by themselves).
 #include <algorithm>
 #include <climits>
 #include <cstdint>

@@ -427,9 +427,9 @@ vr_result_t vr_allreduce_ring_stepwise_noalloc(const void* const* sendbufs, void
  * The pages stop at the collective; these have no counterpart there.  The
  * conventions at the top of this header hold: asynchronous on `stream`,
  * arguments checked before anything is enqueued, no device memory allocated
- * (each call takes a workspace of the caller's, at least as large as its
- * ..._workspace_bytes says and 16-byte aligned, whose contents need no
- * initial value and are overwritten; calls that run at the same time need
+ * (a call that needs memory takes a workspace of the caller's, at least as
+ * large as its ..._workspace_bytes says and 16-byte aligned, whose contents need
+ * no initial value and are overwritten; calls that run at the same time need
  * one each), the same bits on every run.  A written buffer may overlap no
  * other buffer of the call unless stated. */
 
@@ -563,8 +563,8 @@ vr_result_t vr_embedding(const void* weight, size_t weightStride, const long lon
  * dim): contiguous; both of dtype.  Without accumulate every row is written,
  * zeros for words that do not occur; with it their rows are neither read nor
  * written (the gradient of an output layer that shares the table goes first).
- * Sums are fp32 in token order (more than 32 equal tokens: of 32 or more at a
- * time), rounded once to dtype.  Ignored tokens and indices outside the
+ * Sums are fp32 in token order (many equal tokens: in runs of four or more,
+ * by the numbers of tokens and columns), rounded once to dtype.  Ignored tokens and indices outside the
  * vocabulary as above; what their rows of dOut hold is not read.
  * Errors: those of vr_embedding, or a short workspace. */
 vr_result_t vr_embedding_grad_workspace_bytes(size_t tokens, size_t dim, size_t vocab,
@@ -646,10 +646,12 @@ vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const vo
  *     states before that rounding.  A NaN or an infinity in a block makes its
  *     scale NaN.
  *   control: NULL, or three floats in device memory, read when the kernel runs:
- *     lr, step and gradScale in place of the arguments, which a captured step
- *     needs.  A gradScale there that is not finite leaves everything as it was.
+ *     lr, step (1 or more) and gradScale in place of the arguments, which a
+ *     captured step needs.  A gradScale there that is not finite leaves
+ *     everything as it was.
  * States are fp32 operations each rounded by itself, in the order written, with
  * 1 - beta in fp32: the same bits wherever they are computed.
+ * With eps = 0 an element that never had a gradient becomes NaN (0 / 0).
  * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, a bad dtype, gradDtype or
  * stateBits, masters with fp32 parameters, scales that do not go with
  * stateBits, a size above 2^40, beta1 or beta2 outside [0, 1), eps negative,
