@@ -603,7 +603,9 @@ __global__ void __launch_bounds__(128 + 32 * GroupedShape<BN, PAIR, (KIND >= kGr
       const int s = (int)((done - 1) % kStages);
       const unsigned parity = tailTurn >> s & 1;
       tailTurn ^= 1u << s;
-      ok = all_wait(tailFull(s), parity);
+      // (the whole tile before it: one limit for each 65536 slices)
+      for (int i = 0; !(ok = all_wait(tailFull(s), parity)) && i < slices >> 16 && !abortFlag; ++i) {
+      }
       if (!ok) break;
       zero_rows<Shape::kStageBytes / (int)kSlab>(stage0 + (unsigned)s * Shape::kStageBytes, left,
                                                  (left + 15) / 16 * 16, lane);
@@ -804,16 +806,19 @@ bool plan_grad(const void* dy, size_t dyStride, const void* x, size_t xStride, c
   return true;
 }
 
-vr_result_t pad_matrix(Matrix* m, char* w, const OpDevice& dev, void* stream) {
+// `counts`: of the groups whose matrices m holds; the others are not read.
+vr_result_t pad_matrix(Matrix* m, char* w, const OpDevice& dev, void* stream,
+                       const int* counts = nullptr) {
   if (!m->pad || !m->rows) return VR_SUCCESS;
   const size_t ld = up(m->cols, 16), rows = m->batch * m->rows;
   PadArgs a = {static_cast<const uint16_t*>(m->p), (long long)m->stride, (long long)rows,
-               (int)m->cols, (int)ld, reinterpret_cast<uint16_t*>(w + m->copy)};
+               (int)m->cols, (int)ld, reinterpret_cast<uint16_t*>(w + m->copy), counts,
+               (long long)m->rows};
   void* args[] = {&a};
   m->p = w + m->copy;
   m->stride = ld;
   return op_launch((const void*)pad_kernel,
-                   dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 8)),
+                   dim3((unsigned)std::min<size_t>((rows + 7) / 8, (size_t)dev.sms * 32)),
                    dim3(256), args, 0, stream);
 }
 
@@ -1002,7 +1007,7 @@ vr_result_t vr_grouped_linear(const void* x, size_t xStride, const void* weight,
   if (!rows) return VR_SUCCESS;
   char* w = op_workspace(workspace);
   if ((e = pad_matrix(&p.x, w, dev, stream)) != VR_SUCCESS ||
-      (e = pad_matrix(&p.w, w, dev, stream)) != VR_SUCCESS)
+      (e = pad_matrix(&p.w, w, dev, stream, counts)) != VR_SUCCESS)
     return e;
   return dtype == VR_BFLOAT16 ? linear<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts,
                                                       out, outStride, stream)
@@ -1057,7 +1062,7 @@ vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const vo
   char* w = op_workspace(workspace);
   if ((e = pad_matrix(&p.dy, w, dev, stream)) != VR_SUCCESS ||
       (dWeight && (e = pad_matrix(&p.x, w, dev, stream)) != VR_SUCCESS) ||
-      (dX && (e = pad_matrix(&p.w, w, dev, stream)) != VR_SUCCESS))
+      (dX && (e = pad_matrix(&p.w, w, dev, stream, counts)) != VR_SUCCESS))
     return e;
   return dtype == VR_BFLOAT16
              ? grad<__nv_bfloat16>(p, dev, rows, dim, outDim, groups, counts, dX, dWeight, stream)

@@ -49,6 +49,10 @@ struct PadArgs {
   long long stride, rows;
   int cols, ld;
   uint16_t* dst;
+  // in: batches of so many rows, of which those with a positive count are copied
+  // (null: all)
+  const int* counts;
+  long long perCount;
 };
 __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadArgs a) {
   pdl_launch();
@@ -56,6 +60,7 @@ __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadArg
   const int lane = threadIdx.x % 32;
   for (long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32; r < a.rows;
        r += (long long)gridDim.x * 8) {
+    if (a.counts && a.counts[r / a.perCount] <= 0) continue;
     const uint16_t* in = a.src + r * a.stride;
     uint4* out = reinterpret_cast<uint4*>(a.dst + r * a.ld);
 #pragma unroll 2
