@@ -23,10 +23,11 @@
 // part of the table for itself; after a sort over all SMs, by the launch that
 // sums, where a lane looks its word up among the sorted ones.
 //
-// The same 16384 tokens: 217 us, 180 us of them its 1.2 GB at the copy bandwidth.
-// 159 us zero rows (6.0 TB/s to DRAM, the sort beside them), 37 us sum (bound by
-// latency: 78 registers, a third of the warps), 11 us join.  777 tokens x 1000 added
-// to a table: 14 us, the three launches' latencies (9, 6 and 5 us by themselves).
+// The same 16384 tokens: 208 us, 180 us of them its 1.2 GB at the copy bandwidth.
+// 159 us zero rows (6.0 TB/s to DRAM, the sort beside them), 40 us sum (rows on
+// their way through shared memory; 43 us with eight of them in registers, which
+// leaves room for half the warps), 11 us join.  777 tokens x 1000 added to a table:
+// 14 us, the three launches' latencies (9, 6 and 5 us by themselves).
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -368,6 +369,8 @@ template <typename T, int N, int REP>
 struct Slice {
   using Raw = typename Pack<T, N>::Raw;
   static constexpr int kCols = 32 * N * REP;
+  // rows of a warp on their way, where they are whole 16-byte units
+  static constexpr int kRing = sizeof(Raw) == 16 ? 8 / REP : 0;
   static __device__ __forceinline__ int col(int slice, int i) {
     return slice * kCols + (i * 32 + (int)threadIdx.x % 32) * N;
   }
@@ -466,6 +469,7 @@ template <typename T, int N, int REP>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ SumArgs a) {
   using S = Slice<T, N, REP>;
   using Raw = typename S::Raw;
+  __shared__ uint4 rings[S::kRing ? kWarps : 1][S::kRing ? S::kRing : 1][REP][32];
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x % 32;
@@ -499,38 +503,77 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_consta
       const unsigned starts = __ballot_sync(0xffffffffu, w != (lane ? up : before));
       const int n = __popc(__ballot_sync(0xffffffffu, w < (unsigned)a.vocab));  // those first
       before = __shfl_sync(0xffffffffu, w, 31);
-      constexpr int kAhead = 8 / REP;
-      for (int j0 = 0; j0 < n; j0 += kAhead) {
-        Raw r[kAhead][REP];
+      auto start = [&](int j) {  // item j begins a word: the last one is written
+        if (head) S::store_part(a, chunk, 0, slice, sum);
+        else S::write(a, word, slice, sum);
+        head = false;
+        word = __shfl_sync(0xffffffffu, w, j);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (j0 + k >= n) break;
-          const unsigned token = __shfl_sync(0xffffffffu, token_of(mine), j0 + k);
-          const T* in = static_cast<const T*>(a.dout) + (long long)token * a.stride;
+        for (int i = 0; i < REP; ++i)
 #pragma unroll
-          for (int i = 0; i < REP; ++i)
-            if (S::col(slice, i) < a.dim)
-              r[k][i] = *reinterpret_cast<const Raw*>(in + S::col(slice, i));
+          for (int k = 0; k < N; ++k) sum[i][k] = 0.0f;
+      };
+      auto add = [&](const Raw(&r)[REP]) {
+#pragma unroll
+        for (int i = 0; i < REP; ++i) {
+          float x[N];
+          Pack<T, N>::widen(r[i], x);
+#pragma unroll
+          for (int k = 0; k < N; ++k) sum[i][k] += x[k];
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (j0 + k >= n) break;
-          if (starts >> (j0 + k) & 1) {
-            if (head) S::store_part(a, chunk, 0, slice, sum);
-            else S::write(a, word, slice, sum);
-            head = false;
-            word = __shfl_sync(0xffffffffu, w, j0 + k);
+      };
+      auto row_of = [&](int j) {
+        const unsigned token = __shfl_sync(0xffffffffu, token_of(mine), j);
+        return static_cast<const T*>(a.dout) + (long long)token * a.stride;
+      };
+      if constexpr (S::kRing > 0) {
+        // a lane's 16 bytes of the next rows on their way through shared memory
+        uint4(*ring)[REP][32] = rings[threadIdx.x / 32];
+        auto fetch = [&](int j) {
+          if (j < n) {
+            const T* in = row_of(j);
 #pragma unroll
             for (int i = 0; i < REP; ++i)
+              if (S::col(slice, i) < a.dim)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_addr(&ring[j % S::kRing][i][lane])),
+                             "l"(in + S::col(slice, i))
+                             : "memory");
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
 #pragma unroll
-              for (int j = 0; j < N; ++j) sum[i][j] = 0.0f;
+        for (int j = 0; j < S::kRing - 1; ++j) fetch(j);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          fetch(j + S::kRing - 1);  // (into the place that was read in the last round)
+          asm volatile("cp.async.wait_group %0;" ::"n"(S::kRing - 1) : "memory");
+          if (starts >> j & 1) start(j);
+          Raw r[REP];
+#pragma unroll
+          for (int i = 0; i < REP; ++i)
+            r[i] = *reinterpret_cast<const Raw*>(&ring[j % S::kRing][i][lane]);
+          add(r);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      } else {
+        constexpr int kAhead = 8 / REP;
+        for (int j0 = 0; j0 < n; j0 += kAhead) {
+          Raw r[kAhead][REP];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (j0 + k >= n) break;
+            const T* in = row_of(j0 + k);
+#pragma unroll
+            for (int i = 0; i < REP; ++i)
+              if (S::col(slice, i) < a.dim)
+                r[k][i] = *reinterpret_cast<const Raw*>(in + S::col(slice, i));
           }
 #pragma unroll
-          for (int i = 0; i < REP; ++i) {
-            float x[N];
-            Pack<T, N>::widen(r[k][i], x);
-#pragma unroll
-            for (int j = 0; j < N; ++j) sum[i][j] += x[j];
+          for (int k = 0; k < kAhead; ++k) {
+            if (j0 + k >= n) break;
+            if (starts >> (j0 + k) & 1) start(j0 + k);
+            add(r[k]);
           }
         }
       }
