@@ -19,9 +19,10 @@
 // three.  Both are a 32-bit number, multiplied so that the format's lowest
 // exponent becomes a denormal's, without its last 20 bits: the codes are the
 // remaining ones.  A random number is added before they are cut off (16 bits, at
-// the upper end of the 20), so that a code is the value on average.  (Rounded to the nearest, v would never move:
-// one step changes it by 1 - b2 of itself, a thousandth, and its neighbours are
-// a sixteenth away.)  The random bits are a function of seed, step and element.
+// the upper end of the 20), so that a code is the value on average.  (Rounded to
+// the nearest, v would never move: one step changes it by 1 - b2 of itself, a
+// thousandth, and its neighbours are a sixteenth away.)  The random bits are a
+// function of seed, step and element.
 // A positive v does not become zero: its code is 1 at least, or m, whose
 // smallest code is about as large against sqrt(v)'s, would be divided by eps.
 //

@@ -26,11 +26,15 @@
 // The same 16384 tokens: 208 us, 180 us of them its 1.2 GB at the copy bandwidth.
 // 159 us zero rows (6.0 TB/s to DRAM, the sort beside them), 40 us sum (rows on
 // their way through shared memory; 43 us with eight of them in registers, which
-// leaves room for half the warps), 11 us join.  777 tokens x 1000 added to a table:
-// 14 us, the three launches' latencies (9, 6 and 5 us by themselves).
+// leaves room for half the warps), 11 us join.
+//
+// Few tokens are summed by one launch without sorting (embed_few_kernel): 777 tokens
+// x 1000 added to a table take 7.7 us of a call, 6.3 us in a graph; 10 us where a few
+// words are frequent.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.h"
 #include "fold.cuh"
@@ -135,7 +139,7 @@ struct SortArgs {
   Item* out;
   int* counts;        // large: [ctas][kDigits]
   unsigned* status;
-  // small: the table, whose rows of words that do not occur are zeroed (null: not)
+  // the table, whose rows of words that do not occur are zeroed (not large)
   char* table;
   long long rowBytes;
   int access;
@@ -240,28 +244,29 @@ __device__ __forceinline__ void zero_row(char* row, long long bytes, int access)
       *reinterpret_cast<unsigned short*>(row + i) = 0;
   }
 }
+template <int THREADS>
 __device__ __forceinline__ void zero_rows(const SortArgs& a, unsigned* marks, int part, int parts) {
   const int lo = (int)((long long)a.vocab * part / parts);
   const int hi = (int)((long long)a.vocab * (part + 1) / parts);
   for (int v0 = lo; v0 < hi; v0 += kMarked) {
     const int n = min(kMarked, hi - v0);
-    for (int i = threadIdx.x; i < kMarked / 32; i += kSortThreads) marks[i] = 0;
+    for (int i = threadIdx.x; i < kMarked / 32; i += THREADS) marks[i] = 0;
     __syncthreads();
 #pragma unroll 4
-    for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) {
+    for (int t = threadIdx.x; t < a.tokens; t += THREADS) {
       const long long id = a.ids[t];
       if (id >= v0 && id < v0 + n && id != a.ignore)
         atomicOr(&marks[(id - v0) / 32], 1u << ((id - v0) % 32));
     }
     __syncthreads();
-    for (int i = threadIdx.x / 32; i < n; i += kSortWarps)
+    for (int i = threadIdx.x / 32; i < n; i += THREADS / 32)
       if (!(marks[i / 32] >> (i % 32) & 1))
         zero_row(a.table + (long long)(v0 + i) * a.rowBytes, a.rowBytes, a.access);
     __syncthreads();
   }
 }
 
-// Few tokens: CTA 0 sorts them in shared memory, the others zero rows.
+// CTA 0 sorts the tokens in shared memory, the others zero rows.
 constexpr size_t kSmallSmem = 2 * kSmallBytes + kSortWarps * kDigits * 4;
 template <typename K>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(
   pdl_launch();
   pdl_wait();
   if (blockIdx.x > 0) {
-    zero_rows(a, &rows[0][0], (int)blockIdx.x - 1, (int)gridDim.x - 1);
+    zero_rows<kSortThreads>(a, &rows[0][0], (int)blockIdx.x - 1, (int)gridDim.x - 1);
     return;
   }
   for (int t = threadIdx.x; t < a.tokens; t += kSortThreads) from[t] = item_of<K>(a, t);
@@ -375,15 +380,18 @@ struct Slice {
     return slice * kCols + (i * 32 + (int)threadIdx.x % 32) * N;
   }
   // the final row of a word: scaled, added to what is there, rounded once
-  static __device__ __forceinline__ void write(const SumArgs& a, unsigned word, int slice,
-                                               const float (&sum)[REP][N]) {
-    T* out = static_cast<T*>(a.dweight) + (long long)word * a.dim;
-    Raw old[REP];
-    if (a.add) {
+  static __device__ __forceinline__ T* row(const SumArgs& a, unsigned word) {
+    return static_cast<T*>(a.dweight) + (long long)word * a.dim;
+  }
+  static __device__ __forceinline__ void load_old(const SumArgs& a, unsigned word, int slice,
+                                                  Raw (&old)[REP]) {
+    if (!a.add) return;
 #pragma unroll
-      for (int i = 0; i < REP; ++i)
-        if (col(slice, i) < a.dim) old[i] = *reinterpret_cast<const Raw*>(out + col(slice, i));
-    }
+    for (int i = 0; i < REP; ++i)
+      if (col(slice, i) < a.dim) old[i] = *reinterpret_cast<const Raw*>(row(a, word) + col(slice, i));
+  }
+  static __device__ __forceinline__ void write(const SumArgs& a, unsigned word, int slice,
+                                               const float (&sum)[REP][N], const Raw (&old)[REP]) {
 #pragma unroll
     for (int i = 0; i < REP; ++i) {
       if (col(slice, i) >= a.dim) break;
@@ -391,8 +399,14 @@ struct Slice {
       if (a.add) Pack<T, N>::widen(old[i], x);
 #pragma unroll
       for (int j = 0; j < N; ++j) x[j] = fmaf(sum[i][j], a.scale, a.add ? x[j] : 0.0f);
-      *reinterpret_cast<Raw*>(out + col(slice, i)) = Pack<T, N>::narrow(x);
+      *reinterpret_cast<Raw*>(row(a, word) + col(slice, i)) = Pack<T, N>::narrow(x);
     }
+  }
+  static __device__ __forceinline__ void write(const SumArgs& a, unsigned word, int slice,
+                                               const float (&sum)[REP][N]) {
+    Raw old[REP];
+    load_old(a, word, slice, old);
+    write(a, word, slice, sum, old);
   }
   static __device__ __forceinline__ float* part(const SumArgs& a, int chunk, int end) {
     return a.parts + ((long long)chunk * 2 + end) * a.dim;
@@ -620,6 +634,159 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
   }
 }
 
+// ---------------------------------------------------------------- few tokens
+// No sorting: a warp takes a slice of a token's columns, compares the token's word
+// with all others, and where the token is the first that has it, adds up the
+// rows of those that do, in token order.  A word that more than kHot tokens have
+// is left to all warps of the CTA, an eighth of the tokens each, whose sums are
+// added in order.  The first CTAs zero rows.
+//
+// One launch instead of three, and no partial sums in memory.  Comparisons grow
+// with the tokens' square: 1024 tokens x 4096 columns added to a table take 17 us
+// (sorted: 16; half of them one word: 22 and 27), x 8192 29 us (20), which is
+// sorted; 777 x 1000 6.3 us (14.7), all of one word 16 us (30), 64 x 1024 2.5 us
+// (10).  (With several slices a warp, to compare once for them, a frequent word's
+// are summed by few CTAs: 64 us instead of 21.)
+constexpr size_t kFewTokens = 1024, kFewSlices = 16384;  // slices of 256 columns of all tokens
+constexpr int kHot = 32;
+struct FewArgs {
+  SortArgs sort;
+  SumArgs sum;
+  int zeroing;  // CTAs that zero rows
+};
+
+template <typename T, int N, int REP>
+__global__ void __launch_bounds__(kThreads) embed_few_kernel(const __grid_constant__ FewArgs f) {
+  using S = Slice<T, N, REP>;
+  using Raw = typename S::Raw;
+  __shared__ unsigned words[kFewTokens];  // of the tokens; of one that does not count: vocab
+  __shared__ alignas(16) float parts[kWarps][S::kCols];
+  __shared__ long long hot[kWarps];
+  static_assert(sizeof(parts) >= kMarked / 8, "the marks of the words");
+  const SumArgs& a = f.sum;
+  pdl_launch();
+  pdl_wait();
+  if ((int)blockIdx.x < f.zeroing) {
+    zero_rows<kThreads>(f.sort, reinterpret_cast<unsigned*>(&parts[0][0]), (int)blockIdx.x,
+                        f.zeroing);
+    return;
+  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int cta = (int)blockIdx.x - f.zeroing, ctas = (int)gridDim.x - f.zeroing;
+  const int blocks = (a.tokens + 31) / 32;  // of 32 tokens: at most one for each lane
+  for (int t = threadIdx.x; t < blocks * 32; t += kThreads) {
+    const long long id = t < a.tokens ? f.sort.ids[t] : f.sort.ignore;
+    const bool there = counts_as_word(f.sort, id);
+    if (!there && id != f.sort.ignore && cta == 0)
+      atomicCAS(f.sort.status, 0u, (unsigned)VR_ERR_INVALID_ARGUMENT);
+    words[t] = there ? (unsigned)id : (unsigned)a.vocab;
+  }
+  __syncthreads();
+  // the tokens that have the word: lane b has those of block b, in [from, to)
+  auto tokens_of = [&](unsigned word, int from, int to) {
+    unsigned mine = 0;
+#pragma unroll 8
+    for (int b = from; b < to; ++b) {
+      const unsigned same = __ballot_sync(0xffffffffu, words[b * 32 + lane] == word);
+      if (lane == b) mine = same;
+    }
+    return mine;
+  };
+  // the sum of their rows
+  auto add_rows = [&](unsigned mine, int slice, float(&sum)[REP][N]) {
+    constexpr int kRows = 8 / REP;  // on their way
+    unsigned left = __ballot_sync(0xffffffffu, mine != 0), bits = 0;
+    int block = 0;
+    for (bool more = left != 0; more;) {
+      Raw r[kRows][REP];
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (!bits) {
+          if (!left) break;
+          block = __ffs(left) - 1;
+          left &= left - 1;
+          bits = __shfl_sync(0xffffffffu, mine, block);
+        }
+        const int token = block * 32 + __ffs(bits) - 1;
+        bits &= bits - 1;
+        const T* in = static_cast<const T*>(a.dout) + (long long)token * a.stride;
+#pragma unroll
+        for (int i = 0; i < REP; ++i)
+          if (S::col(slice, i) < a.dim) r[k][i] = *reinterpret_cast<const Raw*>(in + S::col(slice, i));
+        n = k + 1;
+      }
+      more = bits || left;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (k >= n) break;
+#pragma unroll
+        for (int i = 0; i < REP; ++i) {
+          float x[N];
+          Pack<T, N>::widen(r[k][i], x);
+#pragma unroll
+          for (int j = 0; j < N; ++j) sum[i][j] += x[j];
+        }
+      }
+    }
+  };
+  const long long step = (long long)ctas * kWarps;
+  for (long long u0 = 0; u0 < a.units; u0 += step) {
+    // (the slices of a token in CTAs beside each other)
+    const long long u = u0 + (long long)warp * ctas + cta;
+    bool whole = false;
+    if (u < a.units) {
+      const int t = (int)(u / a.slices), slice = (int)(u - (long long)t * a.slices);
+      const unsigned word = words[t];
+      if (word < (unsigned)a.vocab) {
+        const unsigned mine = tokens_of(word, 0, blocks);
+        const int count = (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(mine));
+        // the first token that has it: in the first block that has one
+        const bool earlier = lane < t / 32 ? mine != 0
+                                           : lane == t / 32 && (mine & ((1u << (t % 32)) - 1)) != 0;
+        const bool first = !__any_sync(0xffffffffu, earlier);
+        whole = first && count > kHot;
+        if (first && !whole) {
+          Raw old[REP];
+          float sum[REP][N] = {};
+          S::load_old(a, word, slice, old);
+          add_rows(mine, slice, sum);
+          S::write(a, word, slice, sum, old);
+        }
+      }
+    }
+    if (lane == 0) hot[warp] = whole ? u : -1;
+    if (!__syncthreads_or(whole)) continue;  // (nobody reads `hot`)
+    for (int w = 0; w < kWarps; ++w) {
+      const long long h = hot[w];
+      if (h < 0) continue;
+      const int t = (int)(h / a.slices), slice = (int)(h - (long long)t * a.slices);
+      const unsigned word = words[t];
+      float sum[REP][N] = {};
+      add_rows(tokens_of(word, blocks * warp / kWarps, blocks * (warp + 1) / kWarps), slice, sum);
+#pragma unroll
+      for (int i = 0; i < REP; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) parts[warp][(i * N + j) * 32 + lane] = sum[i][j];
+      __syncthreads();
+      if (warp == w) {
+#pragma unroll
+        for (int i = 0; i < REP; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            float x = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) x += parts[k][(i * N + j) * 32 + lane];
+            sum[i][j] = x;
+          }
+        S::write(a, word, slice, sum);
+      }
+      __syncthreads();
+    }
+    __syncthreads();  // (all have read `hot`)
+  }
+}
+
 // ------------------------------------------------------------- host side
 constexpr size_t kMostTokens = (size_t)1 << 30, kMostVocab = (size_t)1 << 30,
                  kMostDim = (size_t)1 << 24, kMostStride = (size_t)1 << 31;
@@ -634,7 +801,7 @@ int bits_of(size_t n) {
 
 // Items of a chunk: as few as four where that makes no more warps than are
 // resident at once (a warp writes the rows of its words one after the other: 777
-// tokens x 1000 columns in 7 us instead of 27 with 32).
+// tokens x 1000 columns, sorted, in 7 us instead of 27 with 32).
 size_t chunk_of(size_t tokens, size_t dim) {
   const size_t slices = (dim + 255) / 256;
   size_t c = 4;
@@ -643,6 +810,7 @@ size_t chunk_of(size_t tokens, size_t dim) {
 }
 
 struct EmbedPlan {
+  bool few;            // no sorting
   bool small, narrow;  // one CTA sorts; with items of 32 bits
   int passes, bits, tokenBits;
   size_t run, ctas, chunk, chunks;
@@ -653,6 +821,8 @@ bool make_plan(size_t tokens, size_t dim, size_t vocab, int dtype, EmbedPlan* p)
       vocab > kMostVocab)
     return false;
   *p = EmbedPlan{};
+  // (a workspace of the same size either way: which way is no caller's concern)
+  p->few = tokens <= kFewTokens && tokens * ((dim + 255) / 256) <= kFewSlices;
   const int words = bits_of(vocab);  // of the words 0 .. vocab
   p->passes = (words + kMaxBits - 1) / kMaxBits;
   p->bits = (words + p->passes - 1) / p->passes;
@@ -699,13 +869,32 @@ vr_result_t launch_sums(const EmbedPlan& p, const OpDevice& dev, SumArgs& a, voi
                    grid((long long)(p.chunks - 1) * a.slices), dim3(kThreads), args, 0, stream);
 }
 
+template <typename T, int N, int REP>
+vr_result_t launch_few(const SortArgs& s, const OpDevice& dev, SumArgs& a, void* stream) {
+  FewArgs f = {s, a, 0};
+  f.sum.slices = (a.dim + Slice<T, N, REP>::kCols - 1) / Slice<T, N, REP>::kCols;
+  f.sum.units = (long long)a.tokens * f.sum.slices;
+  if (!a.add) f.zeroing = std::min(dev.sms * 4, a.vocab);
+  const long long ctas = std::min<long long>((f.sum.units + kWarps - 1) / kWarps, dev.sms * 4LL);
+  void* args[] = {&f};
+  return op_launch((const void*)embed_few_kernel<T, N, REP>, dim3((unsigned)(f.zeroing + ctas)),
+                   dim3(kThreads), args, 0, stream);
+}
+
 template <typename T>
-vr_result_t sums(const EmbedPlan& p, const OpDevice& dev, SumArgs& a, int access, void* stream) {
+vr_result_t sums(const EmbedPlan& p, const SortArgs& s, const OpDevice& dev, SumArgs& a, int access,
+                 void* stream) {
+  auto go = [&](auto n, auto rep) {
+    constexpr int N = decltype(n)::value, REP = decltype(rep)::value;
+    return p.few ? launch_few<T, N, REP>(s, dev, a, stream)
+                 : launch_sums<T, N, REP>(p, dev, a, stream);
+  };
+  using std::integral_constant;
   constexpr int kElem = (int)sizeof(T), kWide = 16 / kElem;
-  if (access == 16) return launch_sums<T, kWide, 8 / kWide>(p, dev, a, stream);
+  if (access == 16) return go(integral_constant<int, kWide>(), integral_constant<int, 8 / kWide>());
   if constexpr (kElem == 2)
-    if (access == 4) return launch_sums<T, 2, 4>(p, dev, a, stream);
-  return launch_sums<T, 1, 4>(p, dev, a, stream);
+    if (access == 4) return go(integral_constant<int, 2>(), integral_constant<int, 4>());
+  return go(integral_constant<int, 1>(), integral_constant<int, 4>());
 }
 
 template <typename T>
@@ -819,11 +1008,12 @@ vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long lo
                                       (uintptr_t)(dOutStride * E),
                                   E);
   Item* items = reinterpret_cast<Item*>(w + p.items);
-  if (p.small) {
+  s.table = static_cast<char*>(dWeight);
+  s.rowBytes = (long long)(dim * E);
+  s.access = access;
+  if (p.few) {  // (the launch that sums is all)
+  } else if (p.small) {
     s.out = items;
-    s.table = static_cast<char*>(dWeight);
-    s.rowBytes = (long long)(dim * E);
-    s.access = access;
     void* args[] = {&s};
     const void* fn = p.narrow ? (const void*)embed_sort_small_kernel<unsigned>
                               : (const void*)embed_sort_small_kernel<Item>;
@@ -869,9 +1059,9 @@ vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long lo
   a.chunk = (int)p.chunk;
   a.chunks = (int)p.chunks;
   a.scale = scale;
-  return dtype == VR_FLOAT32   ? sums<float>(p, dev, a, access, stream)
-         : dtype == VR_FLOAT16 ? sums<__half>(p, dev, a, access, stream)
-                               : sums<__nv_bfloat16>(p, dev, a, access, stream);
+  return dtype == VR_FLOAT32   ? sums<float>(p, s, dev, a, access, stream)
+         : dtype == VR_FLOAT16 ? sums<__half>(p, s, dev, a, access, stream)
+                               : sums<__nv_bfloat16>(p, s, dev, a, access, stream);
 }
 
 }  // extern "C"

@@ -563,9 +563,9 @@ vr_result_t vr_embedding(const void* weight, size_t weightStride, const long lon
  * dim): contiguous; both of dtype.  Without accumulate every row is written,
  * zeros for words that do not occur; with it their rows are neither read nor
  * written (the gradient of an output layer that shares the table goes first).
- * Sums are fp32 in token order (many equal tokens: in runs of four or more,
- * by the numbers of tokens and columns), rounded once to dtype.  Ignored tokens and indices outside the
- * vocabulary as above; what their rows of dOut hold is not read.
+ * Sums are fp32 in token order (many equal tokens: in runs of them, by the numbers
+ * of tokens and columns), rounded once to dtype.  Ignored tokens and indices outside
+ * the vocabulary as above; what their rows of dOut hold is not read.
  * Errors: those of vr_embedding, or a short workspace. */
 vr_result_t vr_embedding_grad_workspace_bytes(size_t tokens, size_t dim, size_t vocab,
                                               vr_dtype_t dtype, size_t* bytes);

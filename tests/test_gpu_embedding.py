@@ -118,6 +118,31 @@ def test_gradient_of_one_word(T, dtype):
         check_grad(dout, two.flip(0), 7, dtype, 1.0, True)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("T,D", [(1, 600), (33, 520), (1023, 41), (1024, 1032), (1025, 1032),
+                                 (1024, 262), (900, 3), (3001, 40), (1024, 4096), (1024, 4100),
+                                 (20, 1), (8200, 33)])
+@pytest.mark.parametrize("add", [False, True])
+def test_gradient_of_frequent_words(T, D, dtype, add):
+    """Words of 32 and 33 tokens, of a third of all and of one, a table of a few
+    thousand rows, for each way of summing."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + D)
+    ids = torch.randint(0, 9000, (T,), generator=g, device="cuda")
+    ids[:T // 3], ids[T // 3:][:32], ids[T // 3 + 32:][:33] = 77, 8999, 0
+    ids = ids[torch.randperm(T, generator=g, device="cuda")]
+    ids[T - 1:] = IGNORE if T % 2 else 8999
+    check_grad(rand((T, D), DT[dtype][1], T), ids, 9000, dtype, 0.7, add)
+
+
+def test_more_units_than_the_grid_has_warps():
+    """Few tokens of many columns: several rounds, frequent words in each."""
+    ids = torch.arange(700, device="cuda") % 11
+    check_grad(rand((700, 4000), torch.bfloat16, 1), ids, 12, "bf16", 1.0, False)
+    check_grad(rand((900, 4001), torch.bfloat16, 2), torch.arange(900, device="cuda") % 23, 23,
+               "bf16", 1.0, True)
+
+
 def test_words_of_many_bits():
     V = (1 << 20) + 3  # three passes
     ids = torch.randint(0, V, (9001,), device="cuda")
