@@ -11,8 +11,8 @@
 // lowest up (each pass counts the digits of every warp's run of tokens, adds
 // the counts up and moves the tokens), so that a word's rows are summed in
 // token order: the same bits on every run, without atomic additions.  Up to 8192
-// tokens (16384 where word and token fit 32 bits) are sorted by one CTA in
-// shared memory; more take two launches a pass.  The sorted tokens are cut into
+// tokens (16384 where word and token fit 32 bits) can be sorted by one CTA in
+// shared memory; else two launches make a pass.  The sorted tokens are cut into
 // chunks; a warp sums a slice of the columns of a chunk in fp32 and writes each
 // word's row that lies in the chunk as a whole; a word that goes on over the
 // chunk's end leaves a partial sum, and a last launch adds the partial sums up in
@@ -29,7 +29,7 @@
 // leaves room for half the warps), 11 us join.
 //
 // Few tokens are summed by one launch without sorting (embed_few_kernel): 777 tokens
-// x 1000 added to a table take 7.7 us of a call, 6.3 us in a graph; 10 us where a few
+// x 1000 added to a table take 6.3 us in a graph, 7.5 us where a few
 // words are frequent.
 #include <algorithm>
 #include <climits>
@@ -167,8 +167,15 @@ __device__ __forceinline__ void digits_of_run(unsigned* row, int lo, int hi, int
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const bool live = i0 + lane < hi;
     const K x = live ? get(i0 + lane) : 0;
-    const unsigned d = live ? (unsigned)(x >> shift) & mask : kDigits;
-    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const unsigned d = (unsigned)(x >> shift) & mask;
+    // the live lanes with the same digit, bit by bit (__match_any_sync: 43 us instead
+    // of 28 for 8192 tokens)
+    unsigned same = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+    for (int b = 0; b < kMaxBits; ++b) {
+      const unsigned set = __ballot_sync(0xffffffffu, d >> b & 1);
+      same &= d >> b & 1 ? set : ~set;
+    }
     const int first = __ffs(same) - 1;
     unsigned base = 0;
     if (live && lane == first) {
@@ -427,10 +434,10 @@ struct Slice {
   using Wide = typename Select<N % 4 == 0, float4, typename Select<N == 2, float2, float>::type>::type;
   static constexpr int kWide = N % 4 == 0 ? 4 : N;
   // the partial sums of chunks `from` to `to` that begin with the word, in order,
-  // eight loads in flight
+  // up to eight of them on their way
   static __device__ __forceinline__ void add_parts(const SumArgs& a, int from, int to, int slice,
                                                    float (&sum)[REP][N]) {
-    constexpr int kUnits = N / kWide, kAtOnce = 8 / kUnits > 4 ? 4 : 8 / kUnits;
+    constexpr int kUnits = N / kWide, kAtOnce = 8;
     const long long step = 2LL * a.dim;
 #pragma unroll
     for (int i = 0; i < REP; ++i) {
@@ -811,7 +818,7 @@ size_t chunk_of(size_t tokens, size_t dim) {
 
 struct EmbedPlan {
   bool few;            // no sorting
-  bool small, narrow;  // one CTA sorts; with items of 32 bits
+  bool small, narrow;  // one CTA may sort; with items of 32 bits
   int passes, bits, tokenBits;
   size_t run, ctas, chunk, chunks;
   size_t items, other, counts, parts, bytes;  // offsets into the workspace
@@ -829,7 +836,6 @@ bool make_plan(size_t tokens, size_t dim, size_t vocab, int dtype, EmbedPlan* p)
   p->tokenBits = bits_of(tokens ? tokens - 1 : 0);
   p->narrow = tokens <= kSmallBytes / 4 && words + p->tokenBits <= 32;
   p->small = p->narrow || tokens <= kSmallBytes / sizeof(Item);
-  if (!p->narrow) p->tokenBits = kItemBits;
   p->run = std::max(kSortRun, (tokens + kMostCtas - 1) / kMostCtas);
   p->ctas = (tokens + p->run - 1) / p->run;
   p->chunk = chunk_of(tokens, dim);
@@ -841,11 +847,23 @@ bool make_plan(size_t tokens, size_t dim, size_t vocab, int dtype, EmbedPlan* p)
     return here;
   };
   p->items = take(tokens * sizeof(Item));
-  p->other = p->small ? 0 : take(tokens * sizeof(Item));
-  p->counts = p->small ? 0 : take(p->ctas * kDigits * 4);
+  p->other = take(tokens * sizeof(Item));
+  p->counts = take(p->ctas * kDigits * 4);
   p->parts = take(p->chunks * 2 * dim * 4);
   p->bytes = at + kOpSlack;
   return true;
+}
+
+// Which sort.  One CTA's takes 28 us for 8192 tokens, 47 us for 16384 (two passes), the
+// other way 21 and 23 us, but nothing is zeroed meanwhile.
+// So it goes by whether the difference is more than zeroing `bytes` at 6 TB/s takes:
+// 16384 x 1024 added to a table 43 us instead of the one CTA's 68, the gradient of
+// 32768 words written whole 52 instead of 67, of 131072 words 83 instead of 69.
+void choose_sort(EmbedPlan* p, size_t tokens, double bytes) {
+  const double longer = 1.05e-3 * p->passes * ((double)tokens - 4900.0);  // us
+  p->small = p->small && longer <= bytes / 6e6;
+  p->narrow = p->narrow && p->small;
+  if (!p->narrow) p->tokenBits = kItemBits;
 }
 
 // The widest access that all rows allow: 16 bytes, 4 or one element.
@@ -994,6 +1012,7 @@ vr_result_t vr_embedding_grad(const void* dOut, size_t dOutStride, const long lo
                ? VR_SUCCESS
                : VR_ERR_CUDA;
   }
+  choose_sort(&p, tokens, accumulate ? 0.0 : (double)vocab * (double)(dim * E));
   char* w = op_workspace(workspace);
   SortArgs s = {};
   s.ids = ids;

@@ -143,6 +143,17 @@ def test_more_units_than_the_grid_has_warps():
                "bf16", 1.0, True)
 
 
+@pytest.mark.parametrize("T,D,V", [(16384, 512, 200000), (16384, 40, 300), (12000, 33, 70000),
+                                   (6000, 1024, 90000)])
+@pytest.mark.parametrize("add", [False, True])
+def test_gradient_by_either_sort(T, D, V, add):
+    """Thousands of tokens, of a table that takes longer to zero than they take
+    one CTA to sort, and of others."""
+    ids = words(T, V, T + D, 0.05)
+    ids[::20] = 3
+    check_grad(rand((T, D), torch.float32, T), ids, V, "fp32", 1.0, add)
+
+
 def test_words_of_many_bits():
     V = (1 << 20) + 3  # three passes
     ids = torch.randint(0, V, (9001,), device="cuda")
