@@ -213,7 +213,8 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 // A warp's block by its largest absolute value: its scale, 2^(exponent - top),
 // and x multiplied so that the codes' digits are those of 32-bit numbers from
 // bit 20 on.  (One factor, which may be a denormal; where it would be less, x
-// goes down by 2^64 first.)  An infinity or a NaN makes the scale NaN.
+// goes down by 2^100 first.  What that rounds is below 2^-126 of a block above
+// 2^36, nothing in its codes.)  An infinity or a NaN makes the scale NaN.
 template <int TOP, int LIFT>
 __device__ __forceinline__ float block_scale(const float (&x)[kLane], float (&y)[kLane]) {
   float largest = 0.0f;
@@ -222,10 +223,12 @@ __device__ __forceinline__ float block_scale(const float (&x)[kLane], float (&y)
   const unsigned all = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
   int e = max((int)(all >> 23) - 127, -110);
   const float scale = all >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : power(e - TOP);
+  constexpr int kDown = 100;
+  static_assert(TOP - LIFT - (127 - kDown) >= -149, "the factor of the largest blocks");
   if (e > 149 + TOP - LIFT) {
-    e -= 64;
+    e -= kDown;
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) y[i] = __fmul_rn(x[i], power(-64));
+    for (int i = 0; i < kLane; ++i) y[i] = __fmul_rn(x[i], power(-kDown));
   } else {
 #pragma unroll
     for (int i = 0; i < kLane; ++i) y[i] = x[i];

@@ -1,0 +1,83 @@
+"""vr_adamw over its whole range: blocks of 8-bit states with every exponent."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import double_binary_tree_gb300 as vr  # noqa: E402
+from tests import more_refs, operator_refs as refs  # noqa: E402
+from tests.test_gpu_adamw import HYPER, SEED, Model, same  # noqa: E402
+
+EXPONENTS = torch.arange(-110, 128)
+
+
+def check_blocks(model, before, **hyper):
+    """8-bit states bit for bit; parameters as `check` has them where they are
+    32-bit numbers.  (A loaded v of code 0 beside an m of 2^100 moves a parameter
+    by lr m / eps: what is 2^128 and more in 64 bits is infinite in 32, and what is
+    above 2^127 may be, with the bound's 16 roundings.)"""
+    h = dict(HYPER, **hyper)
+    assert vr.vr_stream_status() == 0 and model.arena.intact()
+    p, g, m, v, ms, vs, _ = (x and x[0] for x in before)
+    after = [x and x[0] for x in model.host()]
+    m0, v0 = (more_refs.values(*x).astype(np.float32) for x in (("m", m, ms), ("v", v, vs)))
+    want, bound, m1, v1 = more_refs.adamw(p, g, m0, v0, **h)
+    bits = more_refs.random_bits(SEED, h["step"], 0, len(p))
+    for kind, x, cut, code, scale in (("m", m1, bits & np.uint64(0xffff), 2, 4),
+                                      ("v", v1, bits >> np.uint64(16), 3, 5)):
+        codes, scales = more_refs.encode(kind, x, cut)
+        assert same(after[code], codes) and same(after[scale], scales), kind
+    small, large = np.abs(want) <= 2.0 ** 127, np.abs(want) >= 2.0 ** 128 * (1 + 2.0 ** -18)
+    assert np.isinf(after[0][large]).all()
+    assert np.array_equal(np.sign(after[0][large]), np.sign(want[large]))
+    refs.assert_close(torch.from_numpy(after[0][small]), torch.from_numpy(want[small]),
+                      torch.from_numpy(bound[small]), torch.float32, "parameters")
+    return after
+
+
+def test_loaded_blocks_of_every_exponent():
+    """States whose largest values begin at 2^-110 to 2^127, kept by a step
+    without a gradient.  (A step number at which 1 - beta^t is 1.)"""
+    n = len(EXPONENTS)
+    model = Model([256 * n], "fp32", "fp32", 8, False)
+    model.ms[0].copy_(torch.exp2(EXPONENTS.double() - 7))
+    model.vs[0].copy_(torch.exp2(EXPONENTS.double() - 15))
+    model.g[0].zero_()
+    before = model.host()
+    model.step(step=1 << 20)
+    after = check_blocks(model, before, step=1 << 20)
+    assert all(np.isfinite(after[i]).all() for i in (4, 5))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_blocks_of_gradients_of_every_exponent(wide):
+    """v = g^2 and m = g (both betas 0): the largest squares begin at 2^-110 to
+    2^127, none of them infinite; the others as large, or smaller by up to 2^40."""
+    n = len(EXPONENTS)
+    model = Model([256 * n], "fp32", "fp32", 8, False)
+    g = torch.Generator()
+    g.manual_seed(7)
+    u = torch.rand(n, 256, generator=g, dtype=torch.float64)
+    square = torch.exp2(EXPONENTS.double())[:, None] * (1.0 + 0.7 * u)
+    if wide:
+        square[:, 1:] *= torch.exp2(-40 * torch.rand(n, 255, generator=g, dtype=torch.float64))
+    sign = torch.randint(0, 2, (n, 256), generator=g) * 2 - 1
+    model.g[0].copy_((square.sqrt() * sign).reshape(-1))
+    before = model.host()
+    assert np.isfinite(before[1][0] * before[1][0]).all()
+    model.step(b1=0.0, b2=0.0, gs=1.0, step=1)
+    after = check_blocks(model, before, b1=0.0, b2=0.0, gs=1.0, step=1)
+    assert np.isfinite(after[5]).all()
+    # a second moment is its code's value, an eighth of it above or below at most
+    # (from 8 of the lowest code on, where codes are 1 apart, an eighth; what is just
+    # below may be rounded up to code 8, a seventh)
+    v = more_refs.values("v", after[3], after[5])
+    x = np.square(before[1][0].astype(np.float64))
+    live = after[3] > 8
+    assert live.any() and (np.abs(v - x)[live] <= x[live] / 8).all()
