@@ -239,6 +239,16 @@ __device__ __forceinline__ float block_scale(const float (&x)[kLane], float (&y)
   for (int i = 0; i < kLane; ++i) y[i] = __fmul_rn(y[i], by);
   return scale;
 }
+// A block's largest values may be rounded up to the next power of two, but not
+// to 2^128: they keep the code below, 1.875 2^127.
+template <int TOP>
+__device__ __forceinline__ void hold_finite(unsigned (&u)[kLane], float scale) {
+  if (scale == power(127 - TOP)) {
+    constexpr unsigned kMost = ((unsigned)(2 * TOP + 1) << 3) << 24;  // code of 2^(TOP + 1)
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) u[i] = min(u[i], kMost - 1);
+  }
+}
 // New codes; `cut`: 16 random bits each, from bit 8.  (Shifted up by 4, a code
 // is a word's top byte.)
 __device__ __forceinline__ uint2 encode_m(const float (&x)[kLane], const unsigned (&cut)[kLane],
@@ -251,6 +261,7 @@ __device__ __forceinline__ uint2 encode_m(const float (&x)[kLane], const unsigne
     t[i] = __float_as_uint(y[i]);
     u[i] = t[i] * 16u + cut[i];
   }
+  hold_finite<kTopM>(u, *scale);
   if (*scale != *scale) return make_uint2(0, 0);
   return make_uint2((top_bytes(t, 0) & 0x80808080u) | top_bytes(u, 0),
                     (top_bytes(t, 4) & 0x80808080u) | top_bytes(u, 4));
@@ -272,6 +283,7 @@ __device__ __forceinline__ uint2 encode_v(const float (&x)[kLane], const unsigne
   }
 #pragma unroll
   for (int i = 0; i < kLane; ++i) u[i] = t[i] * 16u + cut[i];
+  hold_finite<kTopV>(u, *scale);
   if (*scale != *scale) return make_uint2(0, 0);
   return make_uint2(top_bytes(u, 0), top_bytes(u, 4));
 }

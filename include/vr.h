@@ -644,7 +644,7 @@ vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const vo
  *     random bits that are a function of seed, step and the element's place
  *     among the call's tensors.  A positive v keeps a code above 0.  p is made of the
  *     states before that rounding.  A NaN or an infinity in a block makes its
- *     scale NaN.
+ *     scale NaN; finite states stay finite (none is rounded up to 2^128).
  *   control: NULL, or three floats in device memory, read when the kernel runs:
  *     lr, step (1 or more) and gradScale in place of the arguments, which a
  *     captured step needs.  A gradScale there that is not finite leaves

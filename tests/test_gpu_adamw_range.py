@@ -1,4 +1,5 @@
-"""vr_adamw over its whole range: blocks of 8-bit states with every exponent."""
+"""vr_adamw over its whole range: blocks of 8-bit states with every exponent,
+and none that becomes infinite."""
 
 import numpy as np
 import pytest
@@ -81,3 +82,39 @@ def test_blocks_of_gradients_of_every_exponent(wide):
     x = np.square(before[1][0].astype(np.float64))
     live = after[3] > 8
     assert live.any() and (np.abs(v - x)[live] <= x[live] / 8).all()
+
+
+def test_finite_states_stay_finite():
+    """Values between the largest code's below 2^128 and 2^128 are not rounded
+    up to infinity."""
+    model = Model([512], "fp32", "fp32", 8, False)
+    for t in (model.m[0], model.v[0], model.ms[0], model.vs[0]):
+        t.zero_()
+    g = torch.Generator()
+    g.manual_seed(8)
+    u = 1.88 + 0.11 * torch.rand(512, generator=g, dtype=torch.float64)
+    x = torch.cat([(u[:256] * 2.0 ** 127).sqrt(), u[256:] * 2.0 ** 127])  # v's block, m's block
+    sign = torch.randint(0, 2, (512,), generator=g) * 2 - 1
+    model.g[0].copy_(x * sign)
+    grad = model.g[0].cpu().numpy()
+    with np.errstate(over="ignore"):
+        assert np.isfinite((grad * grad)[:256]).all()
+    model.step(b1=0.0, b2=0.0, gs=1.0, step=1)
+    out = [torch.empty(512, device="cuda") for _ in range(2)]
+    vr.vr_adamw_values(model.m, model.v, model.ms, model.vs, [512], 1, out[:1], out[1:],
+                       torch.cuda.current_stream())
+    assert vr.vr_stream_status() == 0 and model.arena.intact()
+    assert bool(torch.isfinite(out[0]).all()) and bool(torch.isfinite(out[1][:256]).all())
+    # otherwise as the definition says: its code above the largest becomes that
+    bits = more_refs.random_bits(SEED, 1, 0, 512)
+    with np.errstate(over="ignore"):
+        for kind, x, cut, got, most in (("m", grad, bits & np.uint64(0xffff), model.m[0], 0x77),
+                                        ("v", (grad * grad)[:256], (bits >> np.uint64(16))[:256],
+                                         model.v[0][:256], 0xf7)):
+            codes, _ = more_refs.encode(kind, x, cut)
+            digits = codes & 0x7f if kind == "m" else codes
+            # (m's first block lies lower and keeps its codes)
+            top = np.abs(x) >= 2.0 ** 127
+            assert (digits[top] > most).any()
+            want = np.where(top, np.minimum(digits, most), digits) + (codes - digits)
+            assert same(got.cpu().numpy(), want.astype(np.uint8)), kind
