@@ -65,7 +65,7 @@ struct AdamArgs {
   int count;
   unsigned vec[2];          // tensors whose rows allow vector accesses
   float beta1, beta2, eps, weightDecay;
-  float gradScale, up, down, keep;  // up: lr / (1 - b1^t); down: 1 / (1 - b2^t)
+  float gradScale, up, down, keep;  // up: lr / (1 - b1^t); down: (1 - b2^t)^(-1/2)
   float logBeta1, logBeta2;
   const float* control;
   unsigned seedKey;
@@ -484,10 +484,11 @@ __device__ __forceinline__ void update_block(const AdamArgs& a, const Step& s,
     const float x = __fmul_rn(g[i], s.gradScale);
     m[i] = __fadd_rn(__fmul_rn(m[i], a.beta1), __fmul_rn(x, rest1));
     v[i] = __fadd_rn(__fmul_rn(v[i], a.beta2), __fmul_rn(__fmul_rn(x, x), rest2));
-    // (root + eps is 0 or above 2^-75: no denormal to be flushed)
+    // (root + eps is 0 or above 2^-75: no denormal to be flushed; v / (1 - b2^t)
+    // could pass 2^128)
     float root, inv;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i] * s.down));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(root + a.eps));
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i]));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, s.down, a.eps)));
     p[i] = p[i] * s.keep - s.up * m[i] * inv;
   }
   if (MASTER) Eight<Read>::store(l.read + off, n, WHOLE, p);
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 2 : 4) adamw_kernel(cons
     if (!(fabsf(s.gradScale) < INFINITY)) return;  // no step
     step = (long long)t;
     s.up = lr / -expm1f(t * a.logBeta1);
-    s.down = 1.0f / -expm1f(t * a.logBeta2);
+    s.down = sqrtf(1.0f / -expm1f(t * a.logBeta2));
     s.keep = 1.0f - lr * a.weightDecay;
   }
   if (BITS == 8) s.key = mix(mix(a.seedKey ^ (unsigned)step) ^ (unsigned)(step >> 32));
@@ -755,7 +756,7 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
     a.logBeta1 = (float)log1;
     a.logBeta2 = (float)log2;
     a.up = (float)((double)lr / -std::expm1((double)step * log1));
-    a.down = (float)(1.0 / -std::expm1((double)step * log2));
+    a.down = (float)std::sqrt(1.0 / -std::expm1((double)step * log2));
     a.keep = (float)(1.0 - (double)lr * (double)weightDecay);
     a.control = control;
     a.seedKey = mix(mix((unsigned)seed) ^ (unsigned)(seed >> 32));

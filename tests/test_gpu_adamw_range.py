@@ -1,5 +1,5 @@
 """vr_adamw over its whole range: blocks of 8-bit states with every exponent,
-and none that becomes infinite."""
+none that becomes infinite, and second moments near the largest number."""
 
 import numpy as np
 import pytest
@@ -13,7 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 import double_binary_tree_gb300 as vr  # noqa: E402
 from tests import more_refs, operator_refs as refs  # noqa: E402
-from tests.test_gpu_adamw import HYPER, SEED, Model, same  # noqa: E402
+from tests.test_gpu_adamw import HYPER, SEED, Model, check, same  # noqa: E402
 
 EXPONENTS = torch.arange(-110, 128)
 
@@ -118,3 +118,15 @@ def test_finite_states_stay_finite():
             assert (digits[top] > most).any()
             want = np.where(top, np.minimum(digits, most), digits) + (codes - digits)
             assert same(got.cpu().numpy(), want.astype(np.uint8)), kind
+
+
+def test_second_moments_near_the_largest_number():
+    """v / (1 - beta2^t) may pass 2^128 in the first steps; its root does not."""
+    model = Model([5000], "fp32", "fp32", 32, False)
+    model.v[0].copy_(2.0 ** 127 * (0.4 + 1.5 * torch.rand(5000, device="cuda")))
+    model.m[0].mul_(2.0 ** 62)
+    model.g[0].zero_()
+    before = model.host()
+    model.step(step=1)
+    after = check(model, before, step=1)
+    assert float(np.abs(after[0][0] - before[0][0]).mean()) > 1e-4
