@@ -65,7 +65,7 @@ struct AdamArgs {
   int count;
   unsigned vec[2];          // tensors whose rows allow vector accesses
   float beta1, beta2, eps, weightDecay;
-  float gradScale, up, down, keep;  // up: lr / (1 - b1^t); down: (1 - b2^t)^(-1/2)
+  float gradScale, up, down, decay;  // up: lr / (1 - b1^t); down: (1 - b2^t)^(-1/2)
   float logBeta1, logBeta2;
   const float* control;
   unsigned seedKey;
@@ -414,7 +414,7 @@ struct Slot {
 
 // What a step multiplies by.
 struct Step {
-  float gradScale, up, down, keep;
+  float gradScale, up, down, decay;
   unsigned key;
 };
 
@@ -489,7 +489,11 @@ __device__ __forceinline__ void update_block(const AdamArgs& a, const Step& s,
     float root, inv;
     asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[i]));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, s.down, a.eps)));
-    p[i] = p[i] * s.keep - s.up * m[i] * inv;
+    // What p loses by its decay, lr wd p, is added to its move before the one
+    // rounding of p: 1 - lr wd in 32 bits would be 1, or off by a half, where lr wd is
+    // about 2^-24.  (A parameter that is infinite, a mask, has no decay.)
+    const float shrink = fabsf(p[i]) < INFINITY ? p[i] : 0.0f;
+    p[i] -= fmaf(s.decay, shrink, s.up * m[i] * inv);
   }
   if (MASTER) Eight<Read>::store(l.read + off, n, WHOLE, p);
   Eight<P>::store(l.param + off, n, WHOLE, p);
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 2 : 4) adamw_kernel(cons
   extern __shared__ uint4 smem[];
   pdl_launch();
   pdl_wait();
-  Step s = {a.gradScale, a.up, a.down, a.keep, 0};
+  Step s = {a.gradScale, a.up, a.down, a.decay, 0};
   long long step = a.step;
   if (a.control) {
     const float lr = a.control[0], t = a.control[1];
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 2 : 4) adamw_kernel(cons
     step = (long long)t;
     s.up = lr / -expm1f(t * a.logBeta1);
     s.down = sqrtf(1.0f / -expm1f(t * a.logBeta2));
-    s.keep = 1.0f - lr * a.weightDecay;
+    s.decay = lr * a.weightDecay;
   }
   if (BITS == 8) s.key = mix(mix(a.seedKey ^ (unsigned)step) ^ (unsigned)(step >> 32));
   constexpr unsigned kSlot = kParts * S::kBytes;
@@ -757,7 +761,7 @@ vr_result_t vr_adamw(void* const* params, const void* const* grads, void* const*
     a.logBeta2 = (float)log2;
     a.up = (float)((double)lr / -std::expm1((double)step * log1));
     a.down = (float)std::sqrt(1.0 / -std::expm1((double)step * log2));
-    a.keep = (float)(1.0 - (double)lr * (double)weightDecay);
+    a.decay = (float)((double)lr * (double)weightDecay);
     a.control = control;
     a.seedKey = mix(mix((unsigned)seed) ^ (unsigned)(seed >> 32));
     a.step = step;

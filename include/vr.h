@@ -651,6 +651,7 @@ vr_result_t vr_grouped_linear_grad(const void* dOut, size_t dOutStride, const vo
  *     everything as it was.
  * States are fp32 operations each rounded by itself, in the order written, with
  * 1 - beta in fp32: the same bits wherever they are computed.
+ * The parameter is rounded once: its decay and its move are added first.
  * With eps = 0 an element that never had a gradient becomes NaN (0 / 0).
  * Errors: VR_ERR_INVALID_ARGUMENT for count < 1, a bad dtype, gradDtype or
  * stateBits, masters with fp32 parameters, scales that do not go with

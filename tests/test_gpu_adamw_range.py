@@ -1,5 +1,8 @@
 """vr_adamw over its whole range: blocks of 8-bit states with every exponent,
-none that becomes infinite, and second moments near the largest number."""
+none that becomes infinite, second moments near the largest number, decays far
+below an ulp of 1."""
+
+import math
 
 import numpy as np
 import pytest
@@ -130,3 +133,63 @@ def test_second_moments_near_the_largest_number():
     model.step(step=1)
     after = check(model, before, step=1)
     assert float(np.abs(after[0][0] - before[0][0]).mean()) > 1e-4
+
+
+@pytest.mark.parametrize("control", [False, True])
+@pytest.mark.parametrize("dtype,bits,master", [("fp32", 32, False), ("bf16", 32, True),
+                                               ("bf16", 8, True)])
+@pytest.mark.parametrize("lr,wd", [(1e-6, 0.01), (3e-6, 0.01), (1e-5, 0.01), (2e-7, 0.1)])
+def test_small_decays(lr, wd, dtype, bits, master, control):
+    """lr * weightDecay below or about an ulp of 1: a parameter's change is
+    right on average."""
+    n = 1 << 20
+    model = Model([n], dtype, dtype, bits, master)
+    start = (model.master or model.p)[0]
+    start.copy_(0.5 + 0.5 * torch.rand(n, device="cuda"))
+    if bits == 8:  # (the steps are a few lr, hundreds of ulp at most)
+        model.m[0].copy_(0x30 + 128 * torch.randint(0, 2, (n,), device="cuda"))
+        model.v[0].copy_(0x70 + torch.randint(0, 8, (n,), device="cuda"))
+        model.ms[0].fill_(1.0)
+        model.vs[0].fill_(1.0)
+    else:
+        model.v[0].add_(0.1)
+    model.g[0].copy_(torch.randn(n, device="cuda"))
+    before = model.host()
+    hyper = dict(lr=lr, wd=wd, step=5000, gs=1.0)
+    block = torch.tensor([lr, 5000.0, 1.0], device="cuda") if control else None
+    model.step(control=block, **hyper)
+    assert vr.vr_stream_status() == 0
+    after = model.host()
+    p = (before[6] or before[0])[0].astype(np.float64)
+    if bits == 8:
+        m, v = (more_refs.values(k, c[0], s[0]).astype(np.float32)
+                for k, c, s in (("m", before[2], before[4]), ("v", before[3], before[5])))
+    else:
+        m, v = before[2][0], before[3][0]
+    want, *_ = more_refs.adamw(p.astype(np.float32), before[1][0], m, v, lr, 0.9, 0.99, 1e-8, wd,
+                               5000, 1.0)
+    off = float(np.mean((after[6] or after[0])[0].astype(np.float64) - want))
+    # p is rounded once: to 2^-24 below 1 (2^-23 for what passes 1), an error between
+    # -2^-25 and 2^-25 with a deviation of 2^-25 / sqrt(3), of the mean's 2^10
+    # times less: six of those, and 20 roundings of the step's terms (the control
+    # block's factors are made in 32 bits: 2^-20)
+    move = float(np.mean(np.abs(want - p)))
+    assert abs(off) <= 6 * 2.0 ** -24 / math.sqrt(3 * n) + 2.0 ** -19 * move
+    assert 6 * 2.0 ** -24 / math.sqrt(3 * n) + 2.0 ** -19 * move < 0.2 * lr * wd * 0.75
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_infinite_parameters_stay(bits):
+    """A parameter of minus infinity (a mask) without a gradient stays one."""
+    model = Model([600], "fp32", "fp32", bits, False)
+    model.p[0][5:300:7] = -math.inf
+    model.p[0][1] = math.inf
+    for t in (model.m[0], model.g[0]):
+        t[:300].zero_()
+    before = model.host()
+    for wd in (0.1, 0.0):
+        model.step(wd=wd)
+        got = model.host()[0][0]
+        for x in (math.inf, -math.inf):
+            assert np.array_equal(got == x, before[0][0] == x)
+        assert not np.isnan(got).any()
