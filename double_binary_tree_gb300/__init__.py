@@ -154,7 +154,7 @@ def _ptr(x):
 
 
 def _ptrs(bufs):
-    if bufs is None or isinstance(bufs, ctypes.Array):
+    if bufs is None or (isinstance(bufs, ctypes.Array) and bufs._type_ is VP):
         return bufs
     return (VP * len(bufs))(*[b if b is None or isinstance(b, int) else b.data_ptr()
                               for b in bufs])
@@ -168,7 +168,7 @@ def pointer_array(bufs):
 
 def size_array(sizes):
     """A list of sizes in the same way."""
-    return sizes if isinstance(sizes, ctypes.Array) else (S * len(sizes))(*sizes)
+    return sizes if isinstance(sizes, ctypes.Array) and sizes._type_ is S else (S * len(sizes))(*sizes)
 
 
 def _stream(s):
