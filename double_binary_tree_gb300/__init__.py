@@ -168,7 +168,24 @@ def pointer_array(bufs):
 
 def size_array(sizes):
     """A list of sizes in the same way."""
-    return sizes if isinstance(sizes, ctypes.Array) and sizes._type_ is S else (S * len(sizes))(*sizes)
+    if isinstance(sizes, ctypes.Array) and sizes._type_ is S:
+        return sizes
+    return (S * len(sizes))(*sizes)
+
+
+def _lists(where, count, *lists):
+    """Lists of buffers as the library takes them; it reads `count` of each."""
+    out = [_ptrs(x) for x in lists]
+    if any(x is not None and len(x) < count for x in out):
+        raise VrError(VR_ERR_INVALID_ARGUMENT, where)
+    return out
+
+
+def _sizes(where, count, sizes):
+    sizes = size_array(sizes)
+    if len(sizes) < count:
+        raise VrError(VR_ERR_INVALID_ARGUMENT, where)
+    return sizes
 
 
 def _stream(s):
@@ -412,17 +429,23 @@ def vr_adamw(params, grads, m, v, mScales, vScales, masters, sizes, count, dtype
     """Sequences of `count` buffers (mScales / vScales None with 32-bit
     states, masters None without master copies) and of their sizes, or what
     pointer_array and size_array made of them; control may be None."""
-    _check(_L().vr_adamw(_ptrs(params), _ptrs(grads), _ptrs(m), _ptrs(v), _ptrs(mScales),
-                         _ptrs(vScales), _ptrs(masters), size_array(sizes), count, dtype, gradDtype,
+    lists = _lists("vr_adamw", count, params, grads, m, v, mScales, vScales, masters)
+    _check(_L().vr_adamw(*lists, _sizes("vr_adamw", count, sizes), count, dtype, gradDtype,
                          stateBits, lr, beta1, beta2, eps, weightDecay, step, gradScale, seed,
                          _ptr(control), _stream(stream)), "vr_adamw")
 
 
 def vr_adamw_values(m, v, mScales, vScales, sizes, count, mValues, vValues, stream=None):
     """m, mScales, mValues or v, vScales, vValues may be None."""
-    _check(_L().vr_adamw_values(_ptrs(m), _ptrs(v), _ptrs(mScales), _ptrs(vScales),
-                                size_array(sizes), count, _ptrs(mValues), _ptrs(vValues),
-                                _stream(stream)), "vr_adamw_values")
+    where = "vr_adamw_values"
+    if mValues is None:  # (not read then)
+        m = mScales = None
+    if vValues is None:
+        v = vScales = None
+    m, v, mScales, vScales, mValues, vValues = _lists(where, count, m, v, mScales, vScales, mValues,
+                                                      vValues)
+    _check(_L().vr_adamw_values(m, v, mScales, vScales, _sizes(where, count, sizes), count, mValues,
+                                vValues, _stream(stream)), where)
 
 
 # ------------------------------------------------------------- cost model

@@ -7,7 +7,7 @@ import ctypes
 import pytest
 
 import double_binary_tree_gb300 as vr
-from tests.test_more_operators_host import adamw_args
+from tests.test_more_operators_host import adamw_args, values_args
 from tests.test_operators_host import A, INV, STEP, code
 
 KINDS = [list, tuple, lambda x: (ctypes.c_void_p * 2)(*x), lambda x: (ctypes.c_size_t * 2)(*x),
@@ -39,3 +39,26 @@ def test_prepared_lists_are_taken_as_they_are():
         again = vr._ptrs(prepared) if prepared._type_ is ctypes.c_void_p else vr.size_array(prepared)
         assert again is prepared
     assert vr.pointer_array(None) is None
+
+
+def test_lists_shorter_than_the_count():
+    """Refused instead of read on."""
+    for name in ("params", "grads", "m", "v", "mScales", "vScales", "masters", "sizes"):
+        short = adamw_args()
+        at = ["params", "grads", "m", "v", "mScales", "vScales", "masters", "sizes"].index(name)
+        for cut in (short[at][:1], [],
+                    (vr.size_array if name == "sizes" else vr.pointer_array)(short[at][:1])):
+            args = list(short)
+            args[at] = cut
+            assert code(vr.vr_adamw, *args) == INV, name
+    for at in range(4):
+        args = values_args()
+        args[at] = args[at][:1]
+        assert code(vr.vr_adamw_values, *args) == INV
+    for at in (6, 7):
+        args = values_args()
+        args[at] = args[at][:1]
+        assert code(vr.vr_adamw_values, *args) == INV
+    # what is not read may be any list (the refusal is the sizes')
+    args = values_args(mValues=None, m=[], mScales=[], sizes=[1 << 41, 1])
+    assert code(vr.vr_adamw_values, *args) == INV
