@@ -1,6 +1,6 @@
 """vr_adamw over its whole range: blocks of 8-bit states with every exponent,
 none that becomes infinite, second moments near the largest number, decays far
-below an ulp of 1."""
+below an ulp of 1, and what a control block may change."""
 
 import math
 
@@ -193,3 +193,29 @@ def test_infinite_parameters_stay(bits):
         for x in (math.inf, -math.inf):
             assert np.array_equal(got == x, before[0][0] == x)
         assert not np.isnan(got).any()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("dtype,grad", [("bf16", "bf16"), ("fp16", "fp32")])
+def test_control_changes_factors_only(dtype, grad, bits):
+    """Steps with their numbers in device memory and as arguments: the same
+    states bit for bit, masters within the factors' precision."""
+    model, other = (Model([5000, 77, 300], dtype, grad, bits, True) for _ in range(2))
+    moved = [torch.zeros_like(w) for w in other.master]
+    for step, lr, gs in ((1, 1e-3, 1.0), (2, 1e-3, 0.5), (3, 2e-3, 2.0), (4, 5e-4, 0.25)):
+        old = [w.clone() for w in other.master]
+        model.step(control=torch.tensor([lr, float(step), gs], device="cuda"))
+        other.step(lr=lr, step=step, gs=gs)
+        for a, w, o in zip(moved, other.master, old):
+            a.add_((w - o).abs())
+    assert vr.vr_stream_status() == 0
+    for i in (2, 3, 4, 5):
+        for x, y in zip(model.host()[i] or [], other.host()[i] or []):
+            assert same(x, y), i
+    for i, (x, y) in enumerate(zip(model.master, other.master)):
+        # 1 - beta^t: the logarithm, its product with t, expm1 (1 ulp) and the
+        # division, 2^-21 in all, of the two factors; decay's factor one
+        # rounding; a rounding of p each step on both sides
+        bound = moved[i] * 2.0 ** -20 + 8 * 2.0 ** -24 * (y.abs() + moved[i])
+        assert bool(((x - y).abs() <= bound).all())
+        assert torch.equal(model.p[i], x.to(model.p[i].dtype))
