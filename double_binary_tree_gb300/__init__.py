@@ -173,19 +173,19 @@ def size_array(sizes):
     return (S * len(sizes))(*sizes)
 
 
-def _lists(where, count, *lists):
-    """Lists of buffers as the library takes them; it reads `count` of each."""
-    out = [_ptrs(x) for x in lists]
-    if any(x is not None and len(x) < count for x in out):
+def _lists(where, count, sizes, *lists):
+    """Sizes and lists of buffers as the library takes them; it reads `count` of
+    each."""
+    out = [size_array(sizes)]
+    short = len(out[0]) < count
+    for bufs in lists:
+        if bufs is not None:
+            bufs = _ptrs(bufs)
+            short |= len(bufs) < count
+        out.append(bufs)
+    if short:
         raise VrError(VR_ERR_INVALID_ARGUMENT, where)
     return out
-
-
-def _sizes(where, count, sizes):
-    sizes = size_array(sizes)
-    if len(sizes) < count:
-        raise VrError(VR_ERR_INVALID_ARGUMENT, where)
-    return sizes
 
 
 def _stream(s):
@@ -429,10 +429,10 @@ def vr_adamw(params, grads, m, v, mScales, vScales, masters, sizes, count, dtype
     """Sequences of `count` buffers (mScales / vScales None with 32-bit
     states, masters None without master copies) and of their sizes, or what
     pointer_array and size_array made of them; control may be None."""
-    lists = _lists("vr_adamw", count, params, grads, m, v, mScales, vScales, masters)
-    _check(_L().vr_adamw(*lists, _sizes("vr_adamw", count, sizes), count, dtype, gradDtype,
-                         stateBits, lr, beta1, beta2, eps, weightDecay, step, gradScale, seed,
-                         _ptr(control), _stream(stream)), "vr_adamw")
+    sizes, *lists = _lists("vr_adamw", count, sizes, params, grads, m, v, mScales, vScales, masters)
+    _check(_L().vr_adamw(*lists, sizes, count, dtype, gradDtype, stateBits, lr, beta1, beta2, eps,
+                         weightDecay, step, gradScale, seed, _ptr(control), _stream(stream)),
+           "vr_adamw")
 
 
 def vr_adamw_values(m, v, mScales, vScales, sizes, count, mValues, vValues, stream=None):
@@ -442,10 +442,9 @@ def vr_adamw_values(m, v, mScales, vScales, sizes, count, mValues, vValues, stre
         m = mScales = None
     if vValues is None:
         v = vScales = None
-    m, v, mScales, vScales, mValues, vValues = _lists(where, count, m, v, mScales, vScales, mValues,
-                                                      vValues)
-    _check(_L().vr_adamw_values(m, v, mScales, vScales, _sizes(where, count, sizes), count, mValues,
-                                vValues, _stream(stream)), where)
+    sizes, *lists, mValues, vValues = _lists(where, count, sizes, m, v, mScales, vScales, mValues,
+                                             vValues)
+    _check(_L().vr_adamw_values(*lists, sizes, count, mValues, vValues, _stream(stream)), where)
 
 
 # ------------------------------------------------------------- cost model
