@@ -210,6 +210,14 @@ __device__ __forceinline__ float max_abs(float a, float b) {
       : "f"(a), "f"(b));
   return r;
 }
+// x, an infinity made the largest number.  (One instruction: two of min and max, or a
+// comparison and a choice, take 1 % of the step with 8-bit states, and a comparison
+// 0.3 us of the shortest one's 4.)
+__device__ __forceinline__ float finite(float x) {
+  float r;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(FLT_MAX));
+  return r;
+}
 // A warp's block by its largest absolute value: its scale, 2^(exponent - top),
 // and x multiplied so that the codes' digits are those of 32-bit numbers from
 // bit 20 on.  (One factor, which may be a denormal; where it would be less, x
@@ -491,9 +499,9 @@ __device__ __forceinline__ void update_block(const AdamArgs& a, const Step& s,
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, s.down, a.eps)));
     // What p loses by its decay, lr wd p, is added to its move before the one
     // rounding of p: 1 - lr wd in 32 bits would be 1, or off by a half, where lr wd is
-    // about 2^-24.  (A parameter that is infinite, a mask, has no decay.)
-    const float shrink = fabsf(p[i]) < INFINITY ? p[i] : 0.0f;
-    p[i] -= fmaf(s.decay, shrink, s.up * m[i] * inv);
+    // about 2^-24.  (A parameter that is infinite, a mask, stays so: its decay is
+    // that of the largest number.)
+    p[i] -= fmaf(s.decay, finite(p[i]), s.up * m[i] * inv);
   }
   if (MASTER) Eight<Read>::store(l.read + off, n, WHOLE, p);
   Eight<P>::store(l.param + off, n, WHOLE, p);
