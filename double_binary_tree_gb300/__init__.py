@@ -153,11 +153,16 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _ptrs(bufs):
-    if bufs is None or (isinstance(bufs, ctypes.Array) and bufs._type_ is VP):
-        return bufs
-    return (VP * len(bufs))(*[b if b is None or isinstance(b, int) else b.data_ptr()
-                              for b in bufs])
+def _ptrs(bufs, least=0):
+    """Pointers of a list of buffers, of which the library reads `least`."""
+    if bufs is None:
+        return None
+    if not (isinstance(bufs, ctypes.Array) and bufs._type_ is VP):
+        bufs = (VP * len(bufs))(*[b if b is None or isinstance(b, int) else b.data_ptr()
+                                  for b in bufs])
+    if len(bufs) < least:
+        raise VrError(VR_ERR_INVALID_ARGUMENT, "a list of %d buffers" % len(bufs))
+    return bufs
 
 
 def pointer_array(bufs):
@@ -166,26 +171,17 @@ def pointer_array(bufs):
     return _ptrs(bufs)
 
 
+def _sizes(sizes, least=0):
+    if not (isinstance(sizes, ctypes.Array) and sizes._type_ is S):
+        sizes = (S * len(sizes))(*sizes)
+    if len(sizes) < least:
+        raise VrError(VR_ERR_INVALID_ARGUMENT, "a list of %d sizes" % len(sizes))
+    return sizes
+
+
 def size_array(sizes):
     """A list of sizes in the same way."""
-    if isinstance(sizes, ctypes.Array) and sizes._type_ is S:
-        return sizes
-    return (S * len(sizes))(*sizes)
-
-
-def _lists(where, count, sizes, *lists):
-    """Sizes and lists of buffers as the library takes them; it reads `count` of
-    each."""
-    out = [size_array(sizes)]
-    short = len(out[0]) < count
-    for bufs in lists:
-        if bufs is not None:
-            bufs = _ptrs(bufs)
-            short |= len(bufs) < count
-        out.append(bufs)
-    if short:
-        raise VrError(VR_ERR_INVALID_ARGUMENT, where)
-    return out
+    return _sizes(sizes)
 
 
 def _stream(s):
@@ -429,22 +425,23 @@ def vr_adamw(params, grads, m, v, mScales, vScales, masters, sizes, count, dtype
     """Sequences of `count` buffers (mScales / vScales None with 32-bit
     states, masters None without master copies) and of their sizes, or what
     pointer_array and size_array made of them; control may be None."""
-    sizes, *lists = _lists("vr_adamw", count, sizes, params, grads, m, v, mScales, vScales, masters)
-    _check(_L().vr_adamw(*lists, sizes, count, dtype, gradDtype, stateBits, lr, beta1, beta2, eps,
-                         weightDecay, step, gradScale, seed, _ptr(control), _stream(stream)),
-           "vr_adamw")
+    n = count
+    _check(_L().vr_adamw(_ptrs(params, n), _ptrs(grads, n), _ptrs(m, n), _ptrs(v, n),
+                         _ptrs(mScales, n), _ptrs(vScales, n), _ptrs(masters, n), _sizes(sizes, n),
+                         n, dtype, gradDtype, stateBits, lr, beta1, beta2, eps, weightDecay, step,
+                         gradScale, seed, _ptr(control), _stream(stream)), "vr_adamw")
 
 
 def vr_adamw_values(m, v, mScales, vScales, sizes, count, mValues, vValues, stream=None):
     """m, mScales, mValues or v, vScales, vValues may be None."""
-    where = "vr_adamw_values"
+    n = count
     if mValues is None:  # (not read then)
         m = mScales = None
     if vValues is None:
         v = vScales = None
-    sizes, *lists, mValues, vValues = _lists(where, count, sizes, m, v, mScales, vScales, mValues,
-                                             vValues)
-    _check(_L().vr_adamw_values(*lists, sizes, count, mValues, vValues, _stream(stream)), where)
+    _check(_L().vr_adamw_values(_ptrs(m, n), _ptrs(v, n), _ptrs(mScales, n), _ptrs(vScales, n),
+                                _sizes(sizes, n), n, _ptrs(mValues, n), _ptrs(vValues, n),
+                                _stream(stream)), "vr_adamw_values")
 
 
 # ------------------------------------------------------------- cost model
