@@ -856,9 +856,14 @@ bool make_plan(size_t tokens, size_t dim, size_t vocab, int dtype, EmbedPlan* p)
 
 // Which sort.  One CTA's takes 28 us for 8192 tokens, 47 us for 16384 (two passes), the
 // other way 21 and 23 us, but nothing is zeroed meanwhile.
-// So it goes by whether the difference is more than zeroing `bytes` at 6 TB/s takes:
-// 16384 x 1024 added to a table 43 us instead of the one CTA's 68, the gradient of
-// 32768 words written whole 52 instead of 67, of 131072 words 83 instead of 69.
+// So it goes by whether the difference is more than zeroing `bytes` at 6 TB/s takes.
+// Whole gradients in a graph, one CTA / all SMs (us, bf16):
+//                                  2048     4096     6000     8192    12000    16384 tokens
+//   x 1024, added, 5 % one word  17 / 24  26 / 27  34 / 31  43 / 36  53 / 35  67 / 42
+//   x 4096, added                22 / 29  34 / 35  44 / 40  71 / 62  91 / 72  127 / 98
+//   x 1024 of 32000, whole       17 / 32  24 / 33  29 / 34  37 / 36  48 / 38  62 / 41
+//   x 1024 of 131072, whole      50 / 64  52 / 67  55 / 71  59 / 78  59 / 78  69 / 82
+// The rule takes the quicker one everywhere but at 8192 of 32000 (37).
 void choose_sort(EmbedPlan* p, size_t tokens, double bytes) {
   const double longer = 1.05e-3 * p->passes * ((double)tokens - 4900.0);  // us
   p->small = p->small && longer <= bytes / 6e6;

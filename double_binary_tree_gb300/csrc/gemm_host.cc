@@ -62,7 +62,7 @@ vr_result_t gemm_prepare(const void* fn, int device, size_t smem) {
     const auto key = std::make_pair(fn, device);
     if (g_prepared.count(key)) return VR_SUCCESS;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess)
+        cudaSuccess)
       return VR_ERR_CUDA;
     g_prepared.insert(key);
     return VR_SUCCESS;

@@ -765,14 +765,13 @@ struct GroupedPlan {
   size_t bytes;
 };
 
-bool plan_matrix(const void* p, size_t rows, size_t cols, size_t stride, size_t batch, Matrix* m,
+void plan_matrix(const void* p, size_t rows, size_t cols, size_t stride, size_t batch, Matrix* m,
                  size_t* at) {
   *m = {p, rows, cols, stride, batch, 0, !packed_rows(p, stride)};
   if (m->pad) {
     m->copy = *at;
     *at += op_round(batch * rows * up(cols, 16) * 2);
   }
-  return true;
 }
 
 bool sizes_ok(size_t rows, size_t dim, size_t outDim, int groups, int dtype) {
@@ -888,12 +887,24 @@ vr_result_t launch(const OpDevice& dev, GroupedArgs& g, size_t rows, int groups,
 }
 
 // Sums longer than these are taken in chunks of 2048: the tensor cores truncate
-// where a product is added, 1.6e-8 of the sum per 16 k (xent.cu).
+// where a product is added, 1.6e-8 of the sum per 16 k (xent.cu).  So the longest sum
+// of one piece is off by about 3.3e-5 (fp16) or 2.6e-4 (bf16) of the running sum, a
+// fifteenth of the result's rounding.  For dW the host knows the rows of all groups together
+// only: fp16 in a buffer of 32769 rows, 12 groups, instead of 32768 takes 91 us
+// instead of 79 for dW of 1024 x 1536, both gradients 143.5 instead of 143, those of
+// 512 x 512, which share a launch otherwise, 57 instead of 48.
 constexpr int kLongChunk = 32;
 template <typename T>
 constexpr size_t kLongSum = std::is_same<T, __half>::value ? 32768 : 262144;
 
-constexpr size_t kFewRows = 32;  // a group on average
+// A group on average: the counts are not known here.  Tiles of 32 / of up to 256
+// columns, 64 groups of 2048 x 4096 in bf16 (us):
+//   every group has 8, 16, 24, 32 rows      183/183, 184/185, 187/185, 189/185
+//   8 groups have 8, 32, 64, 120, 240 rows  38/40, 38/42, 42/42, 54/42, 91/46
+//   16 groups have 8, 32, 64, 120 rows      62/66, 63/66, 64/66, 95/68
+// Few columns are quicker where few groups have few rows each, a step that decodes
+// some tokens, and cost up to twice the time where few have many.
+constexpr size_t kFewRows = 32;
 constexpr size_t kBothMost = 4;  // tiles for each SM: eight rounds of pairs
 
 bool few_rows(size_t rows, int groups) { return rows <= kFewRows * (size_t)groups; }
