@@ -167,7 +167,9 @@ def _ptrs(bufs, least=0):
 
 def pointer_array(bufs):
     """The pointers of a list of buffers, to pass instead of the list in calls
-    that repeat: the buffers must stay where they are.  None gives None."""
+    that repeat: the buffers must stay where they are.  None gives None.  (A
+    vr_adamw of 48 tensors takes 13 us with prepared lists, 62 with lists, 25 with
+    a list of gradients only.)"""
     return _ptrs(bufs)
 
 

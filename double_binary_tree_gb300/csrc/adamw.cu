@@ -8,10 +8,14 @@
 // warp updates blocks of 256 elements, eight consecutive ones a lane, in one
 // pass over every array.  With states of 32 bits that is bound by memory: 147 M
 // parameters in bf16 with masters, 28 bytes each, take 620 to 638 us (6.4 to 6.6
-// TB/s).  With states of 8 bits it is 16 bytes and 65 instructions an element: 122
-// M take 365 to 380 us (5.2 to 5.4 TB/s), the issue slots 57 to 60 % busy (82
+// TB/s).  With states of 8 bits it is 16 bytes and 67 instructions an element: 122
+// M take 365 to 370 us (5.2 to 5.3 TB/s), the issue slots 61 % busy (82
 // instructions and 430 us before codes were packed four at a time and decoded by
 // conversions).
+//
+// Tensors of which a buffer does not begin at a multiple of eight elements go
+// element by element, as ends of tensors do: 100 M in bf16 with masters take 865 to
+// 1050 us instead of 440 (states of 32 bits), 660 to 800 instead of 298 (8 bits).
 //
 // States of 8 bits.  256 elements share a power of two as scale, by the
 // largest of them.  m keeps a sign, four bits of exponent and three of
